@@ -313,6 +313,134 @@ CART_API int cart_attn_decode_noalloc(int B, int Hq, int Hkv, int d, int p, floa
                                       void* k_cache, void* v_cache, int cache_rows,
                                       const int* priv_len, void* o, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged private caches.  A conversation's private rows may lie in pages of a
+ * pool instead of in a dense [B, cache_rows] cache, so that conversations
+ * hold only the rows they have, and branches of one conversation share their
+ * common rows.  One set of tables serves every layer's pool:
+ *   k_pages, v_pages [layers, n_pages, page_rows, Hkv, d]: the pools.
+ *          page_rows is 16, 32, 64 or 128.  (cart_attn_decode_tree takes one
+ *          layer's [n_pages, page_rows, Hkv, d].)
+ *   table  [B, max_pages] int32: row r of conversation b is row
+ *          r % page_rows of page table[b][r / page_rows].  An entry outside
+ *          0 .. n_pages - 1 (-1 by convention) is no page: its rows are not
+ *          there, which is never an error (pages that a sliding window has
+ *          left behind may be taken out).
+ *   lens   [B] int32: rows that the conversation holds; < 0 an idle slot.
+ *   refs   [n_pages] int32: how many table entries name the page (a caller
+ *          may add its own holds); <= 0 is free.
+ * All tables are DEVICE memory, 4-byte aligned, max_pages * page_rows +
+ * p < 2^24, and a call reads and updates them on the stream: a step of reserve, tree
+ * attention, accept and fork never waits for the host and can be captured.
+ * Two calls that touch one table or pool must be ordered by the caller.   */
+
+/* ------------------------------------------------------------------------
+ * cart_attn_decode_tree -- one step over a tree of drafted tokens per
+ * conversation, behind the shared cartridge, with paged private rows: the
+ * span verify of cart_attn_decode_span for drafts that branch.
+ *   nodes  tokens per conversation, 1 <= nodes <= CART_MAX_TREE_NODES
+ *   parents [B, nodes] int32 (device): parents[b][t] = the node that t
+ *          follows, an earlier one (< t), or -1: t follows the cached rows.
+ *          NULL: a chain (node t follows node t - 1), which with nodes == 1
+ *          is the single-token step.
+ *   q      [B, nodes, Hq, d], k_new, v_new [B, nodes, Hkv, d] bf16, q and
+ *          k_new NOT rotated
+ *   kc, vc [p, Hkv, d] bf16 (NULL when p == 0); a non-finite cartridge value
+ *          reaches every conversation
+ *   o      [B, nodes, Hq, d] bf16 (output)
+ * Node t with D ancestors sits at position p + lens[b] + D.  Its rotated key
+ * and its value are written to private row lens[b] + t, and it attends to
+ * the cartridge, private rows 0 .. lens[b] - 1 (at positions p + row), its
+ * ancestors and itself; with window > 0, to those of them at its last
+ * `window` positions (as in cart_geom).  Other nodes' values, whatever they
+ * hold, do not reach it.
+ * A node is unused when its row has no page, or its parent is neither -1
+ * nor an earlier used node (-2 by convention pads a ragged tree): its o is
+ * 0, its row is not written, and no node attends to it.  An unused node
+ * that has a valid parent but no page sets device status bit 7.  All nodes
+ * of an idle conversation are unused.  lens[b] above max_pages * page_rows
+ * counts as that.  The rows lens[b] .. lens[b] + nodes - 1 must lie in pages
+ * that no other conversation uses (cart_pages_reserve sees to it).
+ * Hq / Hkv must be 1, 2, 4 or 8, d 64 or 128, B * nodes <= 65535.
+ * Workspace: cart_attn_decode_tree_workspace_size(); its contents need no
+ * initial value and nothing in it outlives the call.                      */
+#define CART_MAX_TREE_NODES 64
+CART_API size_t cart_attn_decode_tree_workspace_size(int B, int nodes, int Hq, int Hkv, int d,
+                                                     int p, int page_rows, int max_pages);
+CART_API int cart_attn_decode_tree(int B, int nodes, int window, int Hq, int Hkv, int d, int p,
+                                   float scale, double rope_theta, const void* q,
+                                   const void* k_new, const void* v_new, const void* kc,
+                                   const void* vc, void* k_pages, void* v_pages, int n_pages,
+                                   int page_rows, const int* table, int max_pages,
+                                   const int* lens, const int* parents, void* o,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * cart_pages_fork -- conversation dst[f] becomes the first rows[f] rows of
+ * conversation src[f], sharing its pages (no row is copied).
+ *   src, dst, rows [forks] int32 (device); rows may be NULL: all rows.
+ *          rows[f] above lens[src[f]] counts as that, below 0 as 0.
+ *   done   [forks] int32 (output): 1, or 0 for a fork that was left out: src
+ *          or dst outside 0 .. B - 1, dst[f] also named by another fork of
+ *          the call as its dst, or by any as its src.
+ * The pages that dst held before are given back.  lens[dst] is set; rows
+ * of dst's table row behind its last page are set to -1.
+ * 1 <= forks <= 8192.                                                     */
+CART_API int cart_pages_fork(int B, int* table, int max_pages, int* lens, int* refs, int n_pages,
+                             int page_rows, const int* src, const int* dst, const int* rows,
+                             int forks, int* done, void* stream);
+
+/* ------------------------------------------------------------------------
+ * cart_pages_reserve -- gives every conversation room for rows[b] rows in
+ * all: what comes before a step that appends.
+ *   rows   [B] int32 (device).  < 0, or more than max_pages * page_rows:
+ *          the conversation is left as it is.  0 gives all its pages back.
+ *   done   [B] int32 (output): 1 where rows[b] rows have room
+ * lens[b] becomes min(max(lens[b], 0), rows[b]).  Pages behind the last of
+ * rows[b] rows are given back first, of all conversations.  Then the rows
+ * lens[b] .. rows[b] - 1 come to lie in pages that b alone holds: missing
+ * ones are taken from the pool (lowest free page first, conversations in
+ * order), and in the place of one that is shared (refs > 1) a free one is
+ * taken, with the rows of b that it holds (below lens[b]) copied in every
+ * layer.  When the pool runs out, the conversation that finds too few free
+ * pages and all later ones that need any keep what they have, done 0.
+ * Pages that lose their last holder to such a copy are free from the next
+ * call on.
+ *   k_pages, v_pages: dtype CART_BF16 or CART_F32, row = Hkv * d elements
+ * Workspace: cart_pages_workspace_size().                                 */
+CART_API size_t cart_pages_workspace_size(int B, int max_pages, int n_pages);
+CART_API int cart_pages_reserve(int B, int layers, int Hkv, int d, cart_dtype dtype, void* k_pages,
+                                void* v_pages, int n_pages, int page_rows, int* table,
+                                int max_pages, int* lens, int* refs, const int* rows, int* done,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * cart_pages_accept -- keeps the accepted path of each conversation's tree:
+ * its rows are moved to follow the cached rows, in every layer.
+ *   parents [B, nodes] as in cart_attn_decode_tree (NULL: chains)
+ *   node   [B] int32 (device): the last accepted node; its ancestors are
+ *          accepted with it.  -1, or an unused node: nothing is.
+ *   new_lens [B] int32 (output, not lens itself): lens[b] + accepted nodes
+ * Row lens[b] + (i-th node of the path) goes to row lens[b] + i.  The rows
+ * behind new_lens[b] are left as they are.                                */
+CART_API int cart_pages_accept(int B, int nodes, int layers, int Hkv, int d, cart_dtype dtype,
+                               void* k_pages, void* v_pages, int n_pages, int page_rows,
+                               const int* table, int max_pages, const int* lens,
+                               const int* parents, const int* node, int* new_lens, void* stream);
+
+/* ------------------------------------------------------------------------
+ * cart_pages_compact -- moves the pool's live pages to its front, so that it
+ * can be cut or saved: with n live pages, the live pages numbered n and
+ * above go, in order, to the free numbers below n, in every layer.
+ *   moved  [n_pages] int32 (output): the page's new number, -1 if it was free
+ *   live   [1] int32 (output): n
+ * table (entries that name a free page become -1) and refs follow.
+ * Workspace: cart_pages_workspace_size().                                 */
+CART_API int cart_pages_compact(int B, int layers, int Hkv, int d, cart_dtype dtype, void* k_pages,
+                                void* v_pages, int n_pages, int page_rows, int* table,
+                                int max_pages, int* refs, int* moved, int* live, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a cart_status value (static string). */
 CART_API const char* cart_status_string(int status);
 
@@ -320,8 +448,9 @@ CART_API const char* cart_status_string(int status);
  * when a bounded wait gives up (bit 0: a TMA copy, 1: an MMA, 2: the softmax
  * warps, 3: the epilogue), when a work schedule is inconsistent (bit 4), or
  * when the dynamic shared memory does not start 1024-byte aligned (bit 5;
- * the kernel then does nothing), or when a packed segment table breaks its
- * rules (bit 6).  Synchronizes the current device.  Writes
+ * the kernel then does nothing), when a packed segment table breaks its
+ * rules (bit 6), or when a drafted token's row has no page (bit 7).
+ * Synchronizes the current device.  Writes
  * the bits to *bits_out (may be NULL); returns CART_OK, CART_ERR_TIMEOUT when
  * any bit is set, or CART_ERR_CUDA. */
 CART_API int cart_device_status(unsigned* bits_out, int clear);

@@ -91,6 +91,19 @@ def lib():
             L.cart_attn_bwd_packed.argtypes = [G, i, vp, i, i, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                                vp, vp, vp, vp, ctypes.POINTER(ctypes.c_int), i, i,
                                                vp, sz, vp]
+            L.cart_attn_decode_tree_workspace_size.argtypes = [i] * 8
+            L.cart_attn_decode_tree_workspace_size.restype = sz
+            L.cart_attn_decode_tree.argtypes = [i, i, i, i, i, i, i, f, d, vp, vp, vp, vp, vp, vp,
+                                                vp, i, i, vp, i, vp, vp, vp, vp, sz, vp]
+            L.cart_pages_fork.argtypes = [i, vp, i, vp, vp, i, i, vp, vp, vp, i, vp, vp]
+            L.cart_pages_workspace_size.argtypes = [i, i, i]
+            L.cart_pages_workspace_size.restype = sz
+            L.cart_pages_reserve.argtypes = [i, i, i, i, i, vp, vp, i, i, vp, i, vp, vp, vp, vp,
+                                             vp, sz, vp]
+            L.cart_pages_accept.argtypes = [i, i, i, i, i, i, vp, vp, i, i, vp, i, vp, vp, vp, vp,
+                                            vp]
+            L.cart_pages_compact.argtypes = [i, i, i, i, i, vp, vp, i, i, vp, i, vp, vp, vp, vp,
+                                             sz, vp]
             L.cart_status_string.argtypes = [i]
             L.cart_status_string.restype = ctypes.c_char_p
             L.cart_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i]
@@ -103,6 +116,8 @@ def lib():
                          "cart_attn_bwd_reuse",
                          "cart_attn_fwd_packed", "cart_attn_bwd_packed",
                          "cart_attn_decode", "cart_attn_decode_span", "cart_device_status",
+                         "cart_attn_decode_tree", "cart_pages_fork", "cart_pages_reserve",
+                         "cart_pages_accept", "cart_pages_compact",
                          "cart_trace_enable",
                          "cart_trace_count", "cart_trace_get"):
                 getattr(L, name).restype = ctypes.c_int
@@ -118,7 +133,10 @@ EXPORTS = ("cart_write_to_cache", "cart_attn_fwd_workspace_size", "cart_attn_fwd
            "cart_trace_count", "cart_trace_get", "cart_attn_decode_noalloc",
            "cart_attn_decode_span_workspace_size", "cart_attn_decode_span",
            "cart_attn_fwd_packed_workspace_size", "cart_attn_fwd_packed",
-           "cart_attn_bwd_packed_workspace_size", "cart_attn_bwd_packed", "cart_release")
+           "cart_attn_bwd_packed_workspace_size", "cart_attn_bwd_packed", "cart_release",
+           "cart_attn_decode_tree_workspace_size", "cart_attn_decode_tree", "cart_pages_fork",
+           "cart_pages_workspace_size", "cart_pages_reserve", "cart_pages_accept",
+           "cart_pages_compact")
 
 
 def _check(fn: str, rc: int):
@@ -399,6 +417,220 @@ def cart_attn_decode_span(q, k_new, v_new, kc, vc, k_cache, v_cache, lens, *, sc
                                      _ptr(ws), ws.numel(), _stream(stream, q.device))
     _check("cart_attn_decode_span", rc)
     return o
+
+
+# ------------------------------------------------- paged private caches ----
+class _On:
+    """The calls on a paged cache run on ``device`` (made current when it is
+    not) and on ``stream``, or its current stream; what they allocate is kept
+    for the stream that uses it."""
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.guard = None
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+            self.guard.__enter__()
+        now = torch.cuda.current_stream(device)
+        self.foreign = stream is not None and stream.cuda_stream != now.cuda_stream
+        self.stream = stream if stream is not None else now
+        self.handle = self.stream.cuda_stream
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.foreign:
+            t.record_stream(self.stream)
+        return t
+
+    def close(self):
+        if self.guard is not None:
+            self.guard.__exit__(None, None, None)
+
+
+def _check_like(name, t, dtype, shape, device):
+    """Data pointer of a contiguous tensor that has to have this dtype, shape
+    and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _pools(k_pages, v_pages):
+    """(layers, pages, rows, Hkv, d, dtype code, k pointer, v pointer) of a
+    pair of pools ``[layers, pages, rows, Hkv, d]`` (or one layer of them)."""
+    if k_pages.dim() not in (4, 5):
+        raise ValueError("pools are [layers, pages, rows, Hkv, d] or one layer of it")
+    shape = tuple(k_pages.shape)
+    layers = shape[0] if len(shape) == 5 else 1
+    kp = _check_like("k_pages", k_pages, k_pages.dtype, shape, k_pages.device)
+    vp = _check_like("v_pages", v_pages, k_pages.dtype, shape, k_pages.device)
+    return (layers, *shape[-4:], _dt(k_pages), kp, vp)
+
+
+def decode_tree_workspace_size(B, nodes, Hq, Hkv, d, p, page_rows, max_pages) -> int:
+    return int(lib().cart_attn_decode_tree_workspace_size(B, nodes, Hq, Hkv, d, p, page_rows,
+                                                          max_pages))
+
+
+def cart_attn_decode_tree(q, k_new, v_new, kc, vc, k_pages, v_pages, table, lens, parents=None, *,
+                          scale=None, theta=1.0e6, window=0, o=None, workspace=None, stream=None):
+    """One step over a tree of drafted tokens per conversation, its private
+    rows in pages.  q ``[B, nodes, Hq, d]``, k_new/v_new ``[B, nodes, Hkv,
+    d]`` (bf16, not rotated), kc/vc ``[p, Hkv, d]`` bf16 shared cartridge,
+    k_pages/v_pages ``[pages, page_rows, Hkv, d]`` bf16 pools (the rows
+    lens[b] + t of the used nodes t are written), table ``[B, max_pages]``
+    and lens ``[B]`` int32.  parents ``[B, nodes]`` int32: the node that each
+    node follows, an earlier one, -1 for the cached rows, -2 for an unused
+    node; None: chains.  Returns o ``[B, nodes, Hq, d]`` bf16, 0 for unused
+    nodes.  ``window`` as in ``cart_attn_decode_span``."""
+    B, T, Hq, d = q.shape
+    Hkv, p = k_new.shape[2], kc.shape[0]
+    N, P = k_pages.shape[0], k_pages.shape[1]
+    M, dev, bf, i32 = table.shape[-1], q.device, torch.bfloat16, torch.int32
+    new = (B, T, Hkv, d)
+    args = (_check_like("q", q, bf, (B, T, Hq, d), dev),
+            _check_like("k_new", k_new, bf, new, dev), _check_like("v_new", v_new, bf, new, dev),
+            _check_like("kc", kc, bf, (p, Hkv, d), dev), _check_like("vc", vc, bf, (p, Hkv, d), dev),
+            _check_like("k_pages", k_pages, bf, (N, P, Hkv, d), dev),
+            _check_like("v_pages", v_pages, bf, (N, P, Hkv, d), dev), N, P,
+            _check_like("table", table, i32, (B, M), dev), M,
+            _check_like("lens", lens, i32, (B,), dev),
+            None if parents is None else _check_like("parents", parents, i32, (B, T), dev))
+    L = lib()
+    need = L.cart_attn_decode_tree_workspace_size(B, T, Hq, Hkv, d, p, P, M)
+    on = _On(dev, stream)
+    try:
+        if o is None:
+            o = on.empty((B, T, Hq, d), bf)
+        if workspace is None:
+            workspace = on.empty((max(need, 16),), torch.uint8)
+        rc = L.cart_attn_decode_tree(
+            B, T, int(window), Hq, Hkv, d, p, 1.0 / math.sqrt(d) if scale is None else float(scale),
+            float(theta), *args, _check_like("o", o, bf, (B, T, Hq, d), dev),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), on.handle)
+    finally:
+        on.close()
+    _check("cart_attn_decode_tree", rc)
+    return o
+
+
+def pages_workspace_size(B, max_pages, n_pages) -> int:
+    return int(lib().cart_pages_workspace_size(B, max_pages, n_pages))
+
+
+def cart_pages_fork(table, lens, refs, src, dst, rows=None, *, page_rows, done=None, stream=None):
+    """Conversation dst[f] becomes the first rows[f] (None: all) rows of
+    conversation src[f], sharing its pages.  table ``[B, max_pages]``, lens
+    ``[B]`` and refs ``[pages]`` int32 are updated; src, dst, rows
+    ``[forks]`` int32, all on the device.  Returns done ``[forks]`` int32: 0
+    for a fork that was left out (dst also named by another fork)."""
+    B, M = table.shape
+    dev, i32, F = table.device, torch.int32, src.shape[0]
+    t, n, r, s, z = (_check_like(name, x, i32, shape, dev) for name, x, shape in (
+        ("table", table, (B, M)), ("lens", lens, (B,)), ("refs", refs, (refs.numel(),)),
+        ("src", src, (F,)), ("dst", dst, (F,))))
+    k = None if rows is None else _check_like("rows", rows, i32, (F,), dev)
+    on = _On(dev, stream)
+    try:
+        if done is None:
+            done = on.empty((F,), i32)
+        rc = lib().cart_pages_fork(B, t, M, n, r, refs.numel(), int(page_rows), s, z, k, F,
+                                   _check_like("done", done, i32, (F,), dev), on.handle)
+    finally:
+        on.close()
+    _check("cart_pages_fork", rc)
+    return done
+
+
+def cart_pages_reserve(k_pages, v_pages, table, lens, refs, rows, *, done=None, workspace=None,
+                       stream=None):
+    """Room for rows[b] rows in all of every conversation: pages behind them
+    are given back, and rows lens[b] .. rows[b] - 1 come to lie in pages that
+    b alone holds (a shared one is copied in every layer).  rows ``[B]``
+    int32 on the device, < 0: left as it is, 0: everything is given back.
+    Pools ``[layers, pages, page_rows, Hkv, d]`` (bf16 or f32); table, lens
+    and refs are updated.  Returns done ``[B]`` int32: 1 where there is
+    room."""
+    layers, N, P, Hkv, d, dt, kp, vp = _pools(k_pages, v_pages)
+    B, M = table.shape
+    dev, i32 = k_pages.device, torch.int32
+    t, n, r, w = (_check_like(name, x, i32, shape, dev) for name, x, shape in (
+        ("table", table, (B, M)), ("lens", lens, (B,)), ("refs", refs, (N,)), ("rows", rows, (B,))))
+    L = lib()
+    on = _On(dev, stream)
+    try:
+        if done is None:
+            done = on.empty((B,), i32)
+        if workspace is None:
+            workspace = on.empty((max(L.cart_pages_workspace_size(B, M, N), 16),), torch.uint8)
+        rc = L.cart_pages_reserve(B, layers, Hkv, d, dt, kp, vp, N, P, t, M, n, r, w,
+                                  _check_like("done", done, i32, (B,), dev),
+                                  workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), on.handle)
+    finally:
+        on.close()
+    _check("cart_pages_reserve", rc)
+    return done
+
+
+def cart_pages_accept(k_pages, v_pages, table, lens, parents, node, *, new_lens=None, stream=None):
+    """Keeps the path to node[b] (``[B]`` int32; -1: nothing) of each
+    conversation's tree: its rows are moved to lens[b], lens[b] + 1, ... in
+    every layer.  parents as in ``cart_attn_decode_tree`` (a tensor, or the
+    number of nodes of chains).  Returns new_lens ``[B]`` int32."""
+    layers, N, P, Hkv, d, dt, kp, vp = _pools(k_pages, v_pages)
+    B, M = table.shape
+    dev, i32 = k_pages.device, torch.int32
+    T = parents if isinstance(parents, int) else parents.shape[-1]
+    t, n, x = (_check_like(name, y, i32, shape, dev) for name, y, shape in (
+        ("table", table, (B, M)), ("lens", lens, (B,)), ("node", node, (B,))))
+    up = None if isinstance(parents, int) else _check_like("parents", parents, i32, (B, T), dev)
+    on = _On(dev, stream)
+    try:
+        if new_lens is None:
+            new_lens = on.empty((B,), i32)
+        rc = lib().cart_pages_accept(B, T, layers, Hkv, d, dt, kp, vp, N, P, t, M, n, up, x,
+                                     _check_like("new_lens", new_lens, i32, (B,), dev), on.handle)
+    finally:
+        on.close()
+    _check("cart_pages_accept", rc)
+    return new_lens
+
+
+def cart_pages_compact(k_pages, v_pages, table, refs, *, moved=None, live=None, workspace=None,
+                       stream=None):
+    """Moves the pool's live pages to its front, in every layer; table and
+    refs are updated.  Returns ``(moved [pages], live [1])`` int32: each
+    page's new number (-1: it was free) and the number of live pages."""
+    layers, N, P, Hkv, d, dt, kp, vp = _pools(k_pages, v_pages)
+    B, M = table.shape
+    dev, i32 = k_pages.device, torch.int32
+    t = _check_like("table", table, i32, (B, M), dev)
+    r = _check_like("refs", refs, i32, (N,), dev)
+    L = lib()
+    on = _On(dev, stream)
+    try:
+        if moved is None:
+            moved = on.empty((N,), i32)
+        if live is None:
+            live = on.empty((1,), i32)
+        if workspace is None:
+            workspace = on.empty((max(L.cart_pages_workspace_size(B, M, N), 16),), torch.uint8)
+        rc = L.cart_pages_compact(B, layers, Hkv, d, dt, kp, vp, N, P, t, M, r,
+                                  _check_like("moved", moved, i32, (N,), dev),
+                                  _check_like("live", live, i32, (1,), dev),
+                                  workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), on.handle)
+    finally:
+        on.close()
+    _check("cart_pages_compact", rc)
+    return moved, live
 
 
 def release() -> None:

@@ -226,6 +226,16 @@ bool make_rows_map(CUtensorMap* m, const void* base, int blocks, int rows, int H
 
 }  // namespace
 
+int check_device() {
+  int dev = 0, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CART_ERR_CUDA;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+    return CART_ERR_CUDA;
+  if (major != 10 || minor != 3) return CART_ERR_DEVICE;
+  return CART_OK;
+}
+
 bool make_bf16_rows_map(CUtensorMap* m, const void* base, int blocks, int rows, int H, int d,
                         unsigned box_rows) {
   return make_rows_map(m, base, blocks, rows, H, d, box_rows);
@@ -279,16 +289,6 @@ SideStream* side_stream() {
     }
   }
   return &x;
-}
-
-int check_device() {
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return CART_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return CART_ERR_CUDA;
-  if (major != 10 || minor != 3) return CART_ERR_DEVICE;
-  return CART_OK;
 }
 
 int check_geom(const cart_geom* g) {

@@ -70,6 +70,9 @@ struct TraceScope {
   TraceScope& operator=(const TraceScope&) = delete;
 };
 
+// CART_OK if the current device is one the kernels are built for (api.cu).
+int check_device();
+
 // 4D bf16 TMA map over a [blocks, rows, H, d] tensor as (d, H, rows, blocks)
 // with a 64 x 1 x box_rows x 1 box and 128-byte swizzle (api.cu).
 bool make_bf16_rows_map(CUtensorMap* m, const void* base, int blocks, int rows, int H, int d,

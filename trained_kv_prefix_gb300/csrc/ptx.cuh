@@ -19,6 +19,7 @@ enum : uint32_t {
   kDevErrBadSchedule = 1u << 4,
   kDevErrSmemLayout = 1u << 5,  // dynamic shared memory not 1024-byte aligned
   kDevErrSegments = 1u << 6,    // a packed segment table breaks its rules
+  kDevErrNoPage = 1u << 7,      // a drafted token's row has no page
 };
 
 // Longest legitimate wait inside one kernel is microseconds; give up after
