@@ -11,6 +11,17 @@ namespace cart {
 constexpr int kMaxNodes = CART_MAX_TREE_NODES;
 static_assert(kMaxNodes == 64, "ancestor sets are 64-bit words");
 
+// log2 of a page's rows, -1 for a size that is not offered.
+inline int page_log2_of(int page_rows) {
+  for (int l = 4; l <= 7; ++l)
+    if (page_rows == 1 << l) return l;
+  return -1;
+}
+
+inline bool aligned_to(const void* p, unsigned bytes) {
+  return p && (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
 // Page tables of one call (see cartattn.h): row r of conversation b lies in
 // page table[b * max_pages + (r >> page_log2)].
 struct PageTable {

@@ -446,16 +446,6 @@ __global__ void __launch_bounds__(128) accept_kernel(const AcceptArgs a) {
 }
 
 // ----------------------------------------------------------- arguments ----
-bool al(const void* p, unsigned bytes) {
-  return p && (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
-}
-
-int page_log2_of(int page_rows) {
-  for (int l = 4; l <= 7; ++l)
-    if (page_rows == 1 << l) return l;
-  return -1;
-}
-
 int check_tables(int B, int max_pages, int n_pages, int page_rows) {
   if (B < 1 || B > 65535 || max_pages < 1 || n_pages < 1 || n_pages > (1 << 30) ||
       page_log2_of(page_rows) < 0)
@@ -470,7 +460,7 @@ int check_pool(int layers, int Hkv, int d, cart_dtype dtype, const void* k, cons
   if (dtype != CART_BF16 && dtype != CART_F32) return CART_ERR_DTYPE;
   const long long row = static_cast<long long>(Hkv) * d * (dtype == CART_BF16 ? 2 : 4);
   if (row % 16 != 0 || row > (1 << 24)) return CART_ERR_GEOMETRY;
-  if (!al(k, 16) || !al(v, 16)) return CART_ERR_POINTER;
+  if (!aligned_to(k, 16) || !aligned_to(v, 16)) return CART_ERR_POINTER;
   return CART_OK;
 }
 
@@ -493,8 +483,8 @@ int cart_pages_fork(int B, int* table, int max_pages, int* lens, int* refs, int 
   int rc = check_tables(B, max_pages, n_pages, page_rows);
   if (rc) return rc;
   if (forks < 1 || forks > kMaxForks) return CART_ERR_GEOMETRY;
-  if (!al(table, 4) || !al(lens, 4) || !al(refs, 4) || !al(src, 4) || !al(dst, 4) ||
-      (rows && !al(rows, 4)) || !al(done, 4))
+  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(refs, 4) || !aligned_to(src, 4) || !aligned_to(dst, 4) ||
+      (rows && !aligned_to(rows, 4)) || !aligned_to(done, 4))
     return CART_ERR_POINTER;
   rc = check_device();
   if (rc) return rc;
@@ -517,10 +507,10 @@ int cart_pages_reserve(int B, int layers, int Hkv, int d, cart_dtype dtype, void
   int rc = check_tables(B, max_pages, n_pages, page_rows);
   if (!rc) rc = check_pool(layers, Hkv, d, dtype, k_pages, v_pages);
   if (rc) return rc;
-  if (!al(table, 4) || !al(lens, 4) || !al(refs, 4) || !al(rows, 4) || !al(done, 4))
+  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(refs, 4) || !aligned_to(rows, 4) || !aligned_to(done, 4))
     return CART_ERR_POINTER;
   const PagesWs w = pages_ws(B, n_pages);
-  if (!al(workspace, 16) || workspace_bytes < w.total) return CART_ERR_WORKSPACE;
+  if (!aligned_to(workspace, 16) || workspace_bytes < w.total) return CART_ERR_WORKSPACE;
   rc = check_device();
   if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -564,8 +554,8 @@ int cart_pages_accept(int B, int nodes, int layers, int Hkv, int d, cart_dtype d
   if (!rc) rc = check_pool(layers, Hkv, d, dtype, k_pages, v_pages);
   if (rc) return rc;
   if (nodes < 1 || nodes > kMaxNodes) return CART_ERR_GEOMETRY;
-  if (!al(table, 4) || !al(lens, 4) || (parents && !al(parents, 4)) || !al(node, 4) ||
-      !al(new_lens, 4) || new_lens == lens)
+  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || (parents && !aligned_to(parents, 4)) || !aligned_to(node, 4) ||
+      !aligned_to(new_lens, 4) || new_lens == lens)
     return CART_ERR_POINTER;
   rc = check_device();
   if (rc) return rc;
@@ -595,9 +585,9 @@ int cart_pages_compact(int B, int layers, int Hkv, int d, cart_dtype dtype, void
   int rc = check_tables(B, max_pages, n_pages, page_rows);
   if (!rc) rc = check_pool(layers, Hkv, d, dtype, k_pages, v_pages);
   if (rc) return rc;
-  if (!al(table, 4) || !al(refs, 4) || !al(moved, 4) || !al(live, 4)) return CART_ERR_POINTER;
+  if (!aligned_to(table, 4) || !aligned_to(refs, 4) || !aligned_to(moved, 4) || !aligned_to(live, 4)) return CART_ERR_POINTER;
   const PagesWs w = pages_ws(B, n_pages);
-  if (!al(workspace, 16) || workspace_bytes < w.total) return CART_ERR_WORKSPACE;
+  if (!aligned_to(workspace, 16) || workspace_bytes < w.total) return CART_ERR_WORKSPACE;
   rc = check_device();
   if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
