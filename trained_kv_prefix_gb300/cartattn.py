@@ -420,25 +420,35 @@ def cart_attn_decode_span(q, k_new, v_new, kc, vc, k_cache, v_cache, lens, *, sc
 
 
 # ------------------------------------------------- paged private caches ----
+# The calls below are a few microseconds of GPU time for a small batch, so
+# their bindings keep to a few checks per tensor.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _On:
-    """The calls on a paged cache run on ``device`` (made current when it is
-    not) and on ``stream``, or its current stream; what they allocate is kept
-    for the stream that uses it."""
+    """Where a call on a paged cache runs: on ``device``, made current while
+    it is not, and on ``stream`` or the device's current one.  What the call
+    allocates is kept for the stream that uses it."""
+
+    __slots__ = ("device", "guard", "stream", "handle")
 
     def __init__(self, device, stream):
         self.device = device
         self.guard = None
-        if device.index is not None and device.index != torch.cuda.current_device():
+        index = device.index
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU, not on {device}")
+        if index != torch.cuda.current_device():
             self.guard = torch.cuda.device(device)
             self.guard.__enter__()
-        now = torch.cuda.current_stream(device)
-        self.foreign = stream is not None and stream.cuda_stream != now.cuda_stream
-        self.stream = stream if stream is not None else now
-        self.handle = self.stream.cuda_stream
+        self.handle = _raw_stream(index)
+        self.stream = None
+        if stream is not None and stream.cuda_stream != self.handle:
+            self.stream, self.handle = stream, stream.cuda_stream
 
     def empty(self, shape, dtype):
         t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.foreign:
+        if self.stream is not None:
             t.record_stream(self.stream)
         return t
 
@@ -447,30 +457,40 @@ class _On:
             self.guard.__exit__(None, None, None)
 
 
-def _check_like(name, t, dtype, shape, device):
+def _arg(name, t, dtype, shape, device):
     """Data pointer of a contiguous tensor that has to have this dtype, shape
     and device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, not on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _scratch(on, workspace, need):
+    """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
+    if workspace is None:
+        need = max(need, 16)
+        workspace = on.empty((need,), torch.uint8)
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != on.device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous and on {on.device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _pools(k_pages, v_pages):
-    """(layers, pages, rows, Hkv, d, dtype code, k pointer, v pointer) of a
-    pair of pools ``[layers, pages, rows, Hkv, d]`` (or one layer of them)."""
-    if k_pages.dim() not in (4, 5):
+    """(layers, pages, rows, Hkv, d, dtype code, k pointer, v pointer, device)
+    of a pair of pools ``[layers, pages, rows, Hkv, d]`` or one layer of it."""
+    shape = k_pages.shape
+    if len(shape) not in (4, 5):
         raise ValueError("pools are [layers, pages, rows, Hkv, d] or one layer of it")
-    shape = tuple(k_pages.shape)
-    layers = shape[0] if len(shape) == 5 else 1
-    kp = _check_like("k_pages", k_pages, k_pages.dtype, shape, k_pages.device)
-    vp = _check_like("v_pages", v_pages, k_pages.dtype, shape, k_pages.device)
-    return (layers, *shape[-4:], _dt(k_pages), kp, vp)
+    dev, dt = k_pages.device, k_pages.dtype
+    return (shape[0] if len(shape) == 5 else 1, *shape[-4:], _dt(k_pages),
+            _arg("k_pages", k_pages, dt, shape, dev), _arg("v_pages", v_pages, dt, shape, dev), dev)
 
 
 def decode_tree_workspace_size(B, nodes, Hq, Hkv, d, p, page_rows, max_pages) -> int:
@@ -494,26 +514,24 @@ def cart_attn_decode_tree(q, k_new, v_new, kc, vc, k_pages, v_pages, table, lens
     N, P = k_pages.shape[0], k_pages.shape[1]
     M, dev, bf, i32 = table.shape[-1], q.device, torch.bfloat16, torch.int32
     new = (B, T, Hkv, d)
-    args = (_check_like("q", q, bf, (B, T, Hq, d), dev),
-            _check_like("k_new", k_new, bf, new, dev), _check_like("v_new", v_new, bf, new, dev),
-            _check_like("kc", kc, bf, (p, Hkv, d), dev), _check_like("vc", vc, bf, (p, Hkv, d), dev),
-            _check_like("k_pages", k_pages, bf, (N, P, Hkv, d), dev),
-            _check_like("v_pages", v_pages, bf, (N, P, Hkv, d), dev), N, P,
-            _check_like("table", table, i32, (B, M), dev), M,
-            _check_like("lens", lens, i32, (B,), dev),
-            None if parents is None else _check_like("parents", parents, i32, (B, T), dev))
-    L = lib()
-    need = L.cart_attn_decode_tree_workspace_size(B, T, Hq, Hkv, d, p, P, M)
+    args = (_arg("q", q, bf, q.shape, dev),
+            _arg("k_new", k_new, bf, new, dev), _arg("v_new", v_new, bf, new, dev),
+            _arg("kc", kc, bf, (p, Hkv, d), dev), _arg("vc", vc, bf, (p, Hkv, d), dev),
+            _arg("k_pages", k_pages, bf, (N, P, Hkv, d), dev),
+            _arg("v_pages", v_pages, bf, (N, P, Hkv, d), dev), N, P,
+            _arg("table", table, i32, (B, M), dev), M,
+            _arg("lens", lens, i32, (B,), dev),
+            None if parents is None else _arg("parents", parents, i32, (B, T), dev))
+    L = _lib or lib()
     on = _On(dev, stream)
     try:
         if o is None:
-            o = on.empty((B, T, Hq, d), bf)
-        if workspace is None:
-            workspace = on.empty((max(need, 16),), torch.uint8)
+            o = on.empty(q.shape, bf)
+        ws, wp, wn = _scratch(on, workspace, L.cart_attn_decode_tree_workspace_size(
+            B, T, Hq, Hkv, d, p, P, M))
         rc = L.cart_attn_decode_tree(
-            B, T, int(window), Hq, Hkv, d, p, 1.0 / math.sqrt(d) if scale is None else float(scale),
-            float(theta), *args, _check_like("o", o, bf, (B, T, Hq, d), dev),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), on.handle)
+            B, T, window, Hq, Hkv, d, p, d ** -0.5 if scale is None else scale, theta, *args,
+            _arg("o", o, bf, q.shape, dev), wp, wn, on.handle)
     finally:
         on.close()
     _check("cart_attn_decode_tree", rc)
@@ -531,17 +549,17 @@ def cart_pages_fork(table, lens, refs, src, dst, rows=None, *, page_rows, done=N
     ``[forks]`` int32, all on the device.  Returns done ``[forks]`` int32: 0
     for a fork that was left out (dst also named by another fork)."""
     B, M = table.shape
-    dev, i32, F = table.device, torch.int32, src.shape[0]
-    t, n, r, s, z = (_check_like(name, x, i32, shape, dev) for name, x, shape in (
-        ("table", table, (B, M)), ("lens", lens, (B,)), ("refs", refs, (refs.numel(),)),
-        ("src", src, (F,)), ("dst", dst, (F,))))
-    k = None if rows is None else _check_like("rows", rows, i32, (F,), dev)
+    F, N = src.shape[0], refs.shape[0]
+    dev, i32 = table.device, torch.int32
+    args = (B, _arg("table", table, i32, (B, M), dev), M, _arg("lens", lens, i32, (B,), dev),
+            _arg("refs", refs, i32, (N,), dev), N, page_rows, _arg("src", src, i32, (F,), dev),
+            _arg("dst", dst, i32, (F,), dev),
+            None if rows is None else _arg("rows", rows, i32, (F,), dev), F)
     on = _On(dev, stream)
     try:
         if done is None:
             done = on.empty((F,), i32)
-        rc = lib().cart_pages_fork(B, t, M, n, r, refs.numel(), int(page_rows), s, z, k, F,
-                                   _check_like("done", done, i32, (F,), dev), on.handle)
+        rc = (_lib or lib()).cart_pages_fork(*args, _arg("done", done, i32, (F,), dev), on.handle)
     finally:
         on.close()
     _check("cart_pages_fork", rc)
@@ -557,22 +575,19 @@ def cart_pages_reserve(k_pages, v_pages, table, lens, refs, rows, *, done=None, 
     Pools ``[layers, pages, page_rows, Hkv, d]`` (bf16 or f32); table, lens
     and refs are updated.  Returns done ``[B]`` int32: 1 where there is
     room."""
-    layers, N, P, Hkv, d, dt, kp, vp = _pools(k_pages, v_pages)
+    layers, N, P, Hkv, d, dt, kp, vp, dev = _pools(k_pages, v_pages)
     B, M = table.shape
-    dev, i32 = k_pages.device, torch.int32
-    t, n, r, w = (_check_like(name, x, i32, shape, dev) for name, x, shape in (
-        ("table", table, (B, M)), ("lens", lens, (B,)), ("refs", refs, (N,)), ("rows", rows, (B,))))
-    L = lib()
+    i32 = torch.int32
+    args = (B, layers, Hkv, d, dt, kp, vp, N, P, _arg("table", table, i32, (B, M), dev), M,
+            _arg("lens", lens, i32, (B,), dev), _arg("refs", refs, i32, (N,), dev),
+            _arg("rows", rows, i32, (B,), dev))
+    L = _lib or lib()
     on = _On(dev, stream)
     try:
         if done is None:
             done = on.empty((B,), i32)
-        if workspace is None:
-            workspace = on.empty((max(L.cart_pages_workspace_size(B, M, N), 16),), torch.uint8)
-        rc = L.cart_pages_reserve(B, layers, Hkv, d, dt, kp, vp, N, P, t, M, n, r, w,
-                                  _check_like("done", done, i32, (B,), dev),
-                                  workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), on.handle)
+        ws, wp, wn = _scratch(on, workspace, L.cart_pages_workspace_size(B, M, N))
+        rc = L.cart_pages_reserve(*args, _arg("done", done, i32, (B,), dev), wp, wn, on.handle)
     finally:
         on.close()
     _check("cart_pages_reserve", rc)
@@ -584,19 +599,21 @@ def cart_pages_accept(k_pages, v_pages, table, lens, parents, node, *, new_lens=
     conversation's tree: its rows are moved to lens[b], lens[b] + 1, ... in
     every layer.  parents as in ``cart_attn_decode_tree`` (a tensor, or the
     number of nodes of chains).  Returns new_lens ``[B]`` int32."""
-    layers, N, P, Hkv, d, dt, kp, vp = _pools(k_pages, v_pages)
+    layers, N, P, Hkv, d, dt, kp, vp, dev = _pools(k_pages, v_pages)
     B, M = table.shape
-    dev, i32 = k_pages.device, torch.int32
-    T = parents if isinstance(parents, int) else parents.shape[-1]
-    t, n, x = (_check_like(name, y, i32, shape, dev) for name, y, shape in (
-        ("table", table, (B, M)), ("lens", lens, (B,)), ("node", node, (B,))))
-    up = None if isinstance(parents, int) else _check_like("parents", parents, i32, (B, T), dev)
+    i32 = torch.int32
+    chains = isinstance(parents, int)
+    T = parents if chains else parents.shape[-1]
+    args = (B, T, layers, Hkv, d, dt, kp, vp, N, P, _arg("table", table, i32, (B, M), dev), M,
+            _arg("lens", lens, i32, (B,), dev),
+            None if chains else _arg("parents", parents, i32, (B, T), dev),
+            _arg("node", node, i32, (B,), dev))
     on = _On(dev, stream)
     try:
         if new_lens is None:
             new_lens = on.empty((B,), i32)
-        rc = lib().cart_pages_accept(B, T, layers, Hkv, d, dt, kp, vp, N, P, t, M, n, up, x,
-                                     _check_like("new_lens", new_lens, i32, (B,), dev), on.handle)
+        rc = (_lib or lib()).cart_pages_accept(
+            *args, _arg("new_lens", new_lens, i32, (B,), dev), on.handle)
     finally:
         on.close()
     _check("cart_pages_accept", rc)
@@ -608,25 +625,21 @@ def cart_pages_compact(k_pages, v_pages, table, refs, *, moved=None, live=None, 
     """Moves the pool's live pages to its front, in every layer; table and
     refs are updated.  Returns ``(moved [pages], live [1])`` int32: each
     page's new number (-1: it was free) and the number of live pages."""
-    layers, N, P, Hkv, d, dt, kp, vp = _pools(k_pages, v_pages)
+    layers, N, P, Hkv, d, dt, kp, vp, dev = _pools(k_pages, v_pages)
     B, M = table.shape
-    dev, i32 = k_pages.device, torch.int32
-    t = _check_like("table", table, i32, (B, M), dev)
-    r = _check_like("refs", refs, i32, (N,), dev)
-    L = lib()
+    i32 = torch.int32
+    args = (B, layers, Hkv, d, dt, kp, vp, N, P, _arg("table", table, i32, (B, M), dev), M,
+            _arg("refs", refs, i32, (N,), dev))
+    L = _lib or lib()
     on = _On(dev, stream)
     try:
         if moved is None:
             moved = on.empty((N,), i32)
         if live is None:
             live = on.empty((1,), i32)
-        if workspace is None:
-            workspace = on.empty((max(L.cart_pages_workspace_size(B, M, N), 16),), torch.uint8)
-        rc = L.cart_pages_compact(B, layers, Hkv, d, dt, kp, vp, N, P, t, M, r,
-                                  _check_like("moved", moved, i32, (N,), dev),
-                                  _check_like("live", live, i32, (1,), dev),
-                                  workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), on.handle)
+        ws, wp, wn = _scratch(on, workspace, L.cart_pages_workspace_size(B, M, N))
+        rc = L.cart_pages_compact(*args, _arg("moved", moved, i32, (N,), dev),
+                                  _arg("live", live, i32, (1,), dev), wp, wn, on.handle)
     finally:
         on.close()
     _check("cart_pages_compact", rc)

@@ -227,12 +227,16 @@ bool make_rows_map(CUtensorMap* m, const void* base, int blocks, int rows, int H
 }  // namespace
 
 int check_device() {
+  // (a device's capability does not change: asked once per device)
+  static std::atomic<uint64_t> good{0};
   int dev = 0, major = 0, minor = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return CART_ERR_CUDA;
+  if (dev >= 0 && dev < 64 && (good.load(std::memory_order_relaxed) >> dev & 1)) return CART_OK;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
     return CART_ERR_CUDA;
   if (major != 10 || minor != 3) return CART_ERR_DEVICE;
+  if (dev >= 0 && dev < 64) good.fetch_or(1ull << dev);
   return CART_OK;
 }
 

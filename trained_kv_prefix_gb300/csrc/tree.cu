@@ -25,7 +25,7 @@
 // last tiles; a row's ancestor set masks them.
 //
 // The tiles of all segments, one after the other, are cut into equal runs,
-// one per CTA (a segment counts one tile more for its start and end), so
+// one per CTA (a segment counts some tiles more for its start and end), so
 // every SM has the same work whatever the lengths are, which the host does
 // not know.  A segment that one CTA walks whole, and whose rows no other
 // segment holds, is written at once; else its piece leaves a normalised
@@ -37,6 +37,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.cuh"
 #include "paged.cuh"
@@ -45,9 +46,11 @@
 namespace cart {
 namespace {
 
-// A node's ancestors and itself (0: unused), and those of them in its window.
+// A node's ancestors and itself (0: unused), those of them in its window, and
+// whether a value of the node (in any kv head) is not finite.
 struct NodeSet {
   unsigned long long anc, vis;
+  unsigned bad, unused;
 };
 
 struct TreeArgs {
@@ -60,10 +63,16 @@ struct TreeArgs {
   __nv_bfloat16* qr;        // [B, nodes, Hq, d] rotated queries
   NodeSet* set;             // [B, nodes]
   uint32_t* status;
-  // ---- schedule
-  int R, pairs, stacked, n_ctas;
-  long long* start;         // [B + 1] first unit of each conversation, then the end
-  int* cart_lo;             // first cartridge tile of the stacked segments
+  // ---- schedule: query rows of one (conversation, kv head), rows of a
+  // segment against the stacked cartridge and against the conversation's own
+  // keys (128 or 256), segments of a (conversation, kv head)
+  int R, rt_c, rt_p, segs;
+  int stacked, joint;    // joint: one launch walks both kinds of segments
+  int n_ctas_c, n_ctas_p;  // CTAs of the launch that walks each kind
+  int which;             // of this launch: 1 cartridge segments, 2 own segments
+  // the CTAs whose pieces hold tiles of each segment (see segment_span): the
+  // stacked segments, then those of every (conversation, kv head)
+  int2* spans;
   // ---- partial outputs
   float *part_c, *part_p, *lse_c, *lse_p;
 };
@@ -93,18 +102,21 @@ __device__ __forceinline__ ConvTiles conv_tiles(const TreeArgs& a, int b) {
             : c.n_cart + (min(c.len + a.nodes, rows) + kTile - 1) / kTile - c.row_lo;
   return c;
 }
-// A segment of n tiles is n + 1 units of the schedule.
+// A segment of n tiles is n + kStartUnits units of the schedule: its start and
+// end cost about as much as that many tiles.
+constexpr int kStartUnits = 2;
 __device__ __forceinline__ long long conv_units(const TreeArgs& a, int n) {
-  return n > 0 ? static_cast<long long>(n + 1) * a.Hkv * a.pairs : 0;
+  return n > 0 ? static_cast<long long>(n + kStartUnits) * a.Hkv * a.segs : 0;
 }
 
 // The schedule as every thread of a block needs it: the first unit of the
 // thread's conversations b0 .. b1 - 1 and the units they have, the stacked
-// segments' first cartridge tile and units (units 0 .. cart_units - 1), and
-// the number of all units.
+// segments' first cartridge tile and units, and the units of all
+// conversations.  In a joint launch the conversations' units follow the
+// cart_units of the stacked segments.
 struct Starts {
   int b0, b1, cart_lo;
-  long long start, mine, cart_units, total;
+  long long start, mine, cart_units, own_units;
 };
 template <int kThreads>
 struct StartsSmem {
@@ -146,137 +158,227 @@ __device__ __forceinline__ Starts scan_starts(const TreeArgs& a, StartsSmem<kThr
   __syncthreads();
   r.cart_lo = s.lo;
   const int n_c = n_ct - r.cart_lo;
-  const int stacks = (a.B * a.R + 2 * kTile - 1) / (2 * kTile);
-  r.cart_units = a.stacked && n_c > 0 ? static_cast<long long>(n_c + 1) * stacks * a.Hkv : 0;
-  r.start = r.cart_units + before + x - r.mine;
-  r.total = r.cart_units + all;
+  const int stacks = (a.B * a.R + a.rt_c - 1) / a.rt_c;
+  r.cart_units = a.stacked && n_c > 0 ? static_cast<long long>(n_c + kStartUnits) * stacks * a.Hkv : 0;
+  r.start = (a.joint ? r.cart_units : 0) + before + x - r.mine;
+  r.own_units = all;
   return r;
 }
 
-// For the merge: the first unit of every conversation, the total, and the
-// stacked segments' first cartridge tile.
-__device__ __forceinline__ void write_starts(const TreeArgs& a) {
-  __shared__ StartsSmem<256> s;
-  const Starts r = scan_starts<256>(a, s);
-  long long x = r.start;
-  for (int b = r.b0; b < r.b1; ++b) {
-    a.start[b] = x;
-    x += conv_units(a, conv_tiles(a, b).n);
-  }
-  if (threadIdx.x == 0) {
-    a.start[a.B] = r.total;
-    *a.cart_lo = r.cart_lo;
-  }
-}
-
-// Tiles [t0, t0 + n) of a segment of `tiles` tiles (tiles + 1 units from unit
-// `first`) that lie in the run [lo, hi) of one CTA.
+// Tiles [t0, t0 + n) of a segment of `tiles` tiles, from unit `first` on, that
+// lie in the run [lo, hi) of one CTA (n <= 0: its start alone).
 struct Cut {
   int t0, n;
-  bool at_lo;  // the piece begins where the run does
 };
 __device__ __forceinline__ Cut cut_segment(long long first, int tiles, long long lo, long long hi) {
-  const long long u0 = max(lo - first, 0ll), u1 = min(hi - first, static_cast<long long>(tiles + 1));
+  const long long u0 = max(lo - first, 0ll);
+  const long long u1 = min(hi - first, static_cast<long long>(tiles + kStartUnits));
   Cut c;
-  c.t0 = static_cast<int>(max(u0, 1ll) - 1);
-  c.n = static_cast<int>(u1 - 1) - c.t0;
-  c.at_lo = lo >= first;
+  c.t0 = static_cast<int>(max(u0 - kStartUnits, 0ll));
+  c.n = static_cast<int>(u1 - kStartUnits) - c.t0;
   return c;
 }
 
-// ----------------------------------------------------------------- prep ----
-// Rotates one head row x (D values) into y: lane l holds pairs j and j + D/2
-// for j = l * D/64 .. + D/64 - 1.
-template <int D>
-__device__ __forceinline__ void rotate_row(const __nv_bfloat16* x, __nv_bfloat16* y,
-                                           const float2 (&cs)[D / 64], int lane) {
-  if constexpr (D == 128) {
-    const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(x) + lane);
-    const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(x) + 32 + lane);
-    const float2 fa = bf16x2_to_float2(a), fb = bf16x2_to_float2(b);
-    float2 ya, yb;
-    rope_pair(fa.x, fb.x, cs[0], ya.x, yb.x);
-    rope_pair(fa.y, fb.y, cs[1], ya.y, yb.y);
-    reinterpret_cast<uint32_t*>(y)[lane] = pack_bf16x2(ya.x, ya.y);
-    reinterpret_cast<uint32_t*>(y)[32 + lane] = pack_bf16x2(yb.x, yb.y);
-  } else {
-    float ya, yb;
-    rope_pair(__bfloat162float(x[lane]), __bfloat162float(x[32 + lane]), cs[0], ya, yb);
-    y[lane] = __float2bfloat16_rn(ya);
-    y[32 + lane] = __float2bfloat16_rn(yb);
+// CTAs of a launch with runs of `chunk` units that hold tiles of a segment:
+// twice the first of them, plus 1 if its piece does not begin with its run,
+// and their number.
+__device__ __forceinline__ int2 segment_span(long long first, int tiles, long long chunk) {
+  if (tiles <= 0) return make_int2(0, 0);
+  int lo = static_cast<int>(first / chunk);
+  const int hi = static_cast<int>((first + tiles + kStartUnits - 1) / chunk);
+  // (runs may hold the segment's start alone, without a tile)
+  while (cut_segment(first, tiles, lo * chunk, (lo + 1) * chunk).n <= 0) ++lo;
+  return make_int2(2 * lo + (lo * chunk < first), hi - lo + 1);
+}
+
+// Units per CTA of a launch.
+__device__ __forceinline__ long long run_units(const Starts& r, int which, int n_ctas) {
+  const long long total = ((which & 1) ? r.cart_units : 0) + ((which & 2) ? r.own_units : 0);
+  return (total + n_ctas - 1) / n_ctas;
+}
+
+// One block: the spans of all segments, for the merge.
+__device__ __forceinline__ void write_spans(const TreeArgs& a) {
+  __shared__ StartsSmem<256> s;
+  const Starts r = scan_starts<256>(a, s);
+  const long long chunk_p = run_units(r, a.joint ? 3 : 2, a.n_ctas_p);
+  const int stacks = a.stacked ? (a.B * a.R + a.rt_c - 1) / a.rt_c * a.Hkv : 0;
+  if (a.stacked) {
+    const long long chunk_c = a.joint ? chunk_p : run_units(r, 1, a.n_ctas_c);
+    const int n_c = (a.p + kTile - 1) / kTile - r.cart_lo;
+    for (int i = threadIdx.x; i < stacks; i += 256)
+      a.spans[i] = segment_span(static_cast<long long>(i) * (n_c + kStartUnits), n_c, chunk_c);
+  }
+  long long x = r.start;
+  for (int b = r.b0; b < r.b1; ++b) {
+    const int n = conv_tiles(a, b).n, per = a.Hkv * a.segs;
+    int2* to = a.spans + stacks + static_cast<long long>(b) * per;
+    for (int i = 0; i < per; ++i) {
+      to[i] = segment_span(x, n, chunk_p);
+      if (n > 0) x += n + kStartUnits;
+    }
   }
 }
 
+// ----------------------------------------------------------------- prep ----
+// Rows of a node: its query heads, new keys, new values.  D/16 lanes share a
+// row: lane l of them holds the 8 values from 8l on and those D/2 further, so
+// a warp has 512/D rows of 2 x 16 bytes per lane at a time.
 template <int D>
-__global__ void __launch_bounds__(256) tree_prep_kernel(const TreeArgs a, const Turns f) {
+struct PrepShape {
+  static constexpr int kLanes = D / 16;      // lanes per row
+  static constexpr int kRows = 32 / kLanes;  // rows per warp at a time
+  static constexpr int kBatch = 2;           // of them in flight
+};
+constexpr int kPrepNodes = 8;  // most nodes per block
+
+// Whether one of two packed bf16 values is not finite.
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ bool not_finite(uint4 v) {
+  return not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w);
+}
+
+// Rotates eight pairs: (x, y) element by element by the angles c[0..7].
+__device__ __forceinline__ void rotate8(uint4& x, uint4& y, const float2* c) {
+  uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 fa = bf16x2_to_float2(a[i]), fb = bf16x2_to_float2(b[i]);
+    float2 ya, yb;
+    rope_pair(fa.x, fb.x, c[2 * i], ya.x, yb.x);
+    rope_pair(fa.y, fb.y, c[2 * i + 1], ya.y, yb.y);
+    a[i] = pack_bf16x2(ya.x, ya.y);
+    b[i] = pack_bf16x2(yb.x, yb.y);
+  }
+  x = make_uint4(a[0], a[1], a[2], a[3]);
+  y = make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+// Block 0 writes the spans; block 1 + i the nodes t0 .. t0 + per - 1 of one
+// conversation.  Bound by latency for a few nodes (lengths, pages, parents
+// and the rows are loaded side by side) and by HBM for many.
+template <int D>
+__global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ TreeArgs a,
+                                                        const __grid_constant__ Turns f, int per) {
+  using S = PrepShape<D>;
+  constexpr int HALF = D / 2;
   pdl_release();
-  if (blockIdx.x == a.B * a.nodes) {
-    write_starts(a);
+  if (blockIdx.x == 0) {
+    write_spans(a);
     return;
   }
   __shared__ TreeSmem tree;
-  const int t = blockIdx.x % a.nodes, b = blockIdx.x / a.nodes;
+  __shared__ float2 cs[kPrepNodes][HALF];
+  __shared__ int page_s[kPrepNodes], bad_s[kPrepNodes];
+  const int blocks = (a.nodes + per - 1) / per;  // per conversation
+  const int b = (blockIdx.x - 1) / blocks, t0 = (blockIdx.x - 1) % blocks * per;
+  const int mine = min(per, a.nodes - t0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long bt0 = static_cast<long long>(b) * a.nodes + t0;
+  const int heads = a.Hq + 2 * a.Hkv, rows = mine * heads;
+  const int sub = lane / S::kLanes, e0 = lane % S::kLanes * 8;
+  auto row_in = [&](int i) {
+    const int h = i % heads;
+    const long long bt = bt0 + i / heads;
+    return (h < a.Hq           ? a.q + (bt * a.Hq + h) * D
+            : h < a.Hq + a.Hkv ? a.k_new + (bt * a.Hkv + h - a.Hq) * D
+                               : a.v_new + (bt * a.Hkv + h - a.Hq - a.Hkv) * D) + e0;
+  };
+  uint4 lo[S::kBatch], hi[S::kBatch];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < S::kBatch; ++k) {
+      const int i = i0 + k * 8 * S::kRows;
+      if (i >= rows) break;
+      const __nv_bfloat16* x = row_in(i);
+      lo[k] = __ldg(reinterpret_cast<const uint4*>(x));
+      hi[k] = __ldg(reinterpret_cast<const uint4*>(x + HALF));
+    }
+  };
+  load(warp * S::kRows + sub);  // before the tree is known
   const int len = held_rows(a.pt, b);
   const int node = threadIdx.x;
   const int page = len >= 0 && node < a.nodes ? page_of(a.pt, b, len + node) : -1;
   const bool lost = tree_ancestors(
       tree, a.parents ? a.parents + static_cast<long long>(b) * a.nodes : nullptr, a.nodes,
       page >= 0);
-  if (lost && len >= 0 && node == t) atomicOr(a.status, kDevErrNoPage);
-  const unsigned long long anc = tree.anc[t];
-  const long long bt = static_cast<long long>(b) * a.nodes + t;
-  if (threadIdx.x == 0) {
+  if (node >= t0 && node < t0 + mine) {
+    const unsigned long long anc = tree.anc[node];
+    if (lost && len >= 0) atomicOr(a.status, kDevErrNoPage);
     // nearer ancestors have higher numbers: a window keeps the top ones
     unsigned long long vis = anc;
     if (a.window > 0)
       for (int n = __popcll(vis); n > a.window; --n) vis &= vis - 1;
-    a.set[bt] = NodeSet{anc, vis};
+    a.set[bt0 + node - t0].anc = anc;
+    a.set[bt0 + node - t0].vis = vis;
+    page_s[node - t0] = page;
+    bad_s[node - t0] = 0;
   }
-  if (!anc) {
-    uint4* o = reinterpret_cast<uint4*>(a.o + bt * a.Hq * D);
-    for (int i = threadIdx.x; i < a.Hq * D / 8; i += blockDim.x) o[i] = make_uint4(0, 0, 0, 0);
-    return;
+  for (int i = threadIdx.x; i < mine * HALF; i += 256) {
+    const int n = i / HALF, j = i % HALF;
+    cs[n][j] = rope_cs_turns(f.t[j], a.p + len + __popcll(tree.anc[t0 + n]) - 1);
   }
-  const int pos = a.p + len + __popcll(anc) - 1;
-  float2 cs[D / 64];
+  __syncthreads();
+  for (int i0 = warp * S::kRows + sub; i0 - sub < rows; i0 += 8 * S::kRows * S::kBatch) {
+    if (i0 >= 8 * S::kRows) load(i0);
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) cs[i] = rope_cs_turns(f.t[lane * (D / 64) + i], pos);
-  const int my_page = page_of(a.pt, b, len + t);
-  const long long row =
-      ((static_cast<long long>(my_page) << a.pt.page_log2) +
-       ((len + t) & ((1 << a.pt.page_log2) - 1))) * a.Hkv * D;
-  for (int h = warp; h < a.Hq + 2 * a.Hkv; h += 8) {
-    if (h < a.Hq) {
-      rotate_row<D>(a.q + (bt * a.Hq + h) * D, a.qr + (bt * a.Hq + h) * D, cs, lane);
-    } else if (h < a.Hq + a.Hkv) {
-      const int g = h - a.Hq;
-      rotate_row<D>(a.k_new + (bt * a.Hkv + g) * D, a.k_pages + row + g * D, cs, lane);
-    } else {
-      const int g = h - a.Hq - a.Hkv;
-      const uint32_t* v = reinterpret_cast<const uint32_t*>(a.v_new + (bt * a.Hkv + g) * D);
-      uint32_t* y = reinterpret_cast<uint32_t*>(a.v_pages + row + g * D);
-      for (int i = lane; i < D / 2; i += 32) y[i] = __ldg(v + i);
+    for (int k = 0; k < S::kBatch; ++k) {
+      const int i = i0 + k * 8 * S::kRows;
+      if (i >= rows) break;
+      const int n = i / heads, h = i % heads;
+      const long long bt = bt0 + n;
+      const bool used = tree.anc[t0 + n] != 0;
+      const long long row =
+          ((static_cast<long long>(page_s[n]) << a.pt.page_log2) +
+           ((len + t0 + n) & ((1 << a.pt.page_log2) - 1))) * a.Hkv * D;
+      if (h < a.Hq + a.Hkv) rotate8(lo[k], hi[k], &cs[n][e0]);
+      __nv_bfloat16* to;
+      if (h < a.Hq) {
+        if (used) {
+          to = a.qr + (bt * a.Hq + h) * D;
+        } else {
+          to = a.o + (bt * a.Hq + h) * D;
+          lo[k] = hi[k] = make_uint4(0, 0, 0, 0);
+        }
+      } else {
+        if (!used) continue;
+        const int g = h < a.Hq + a.Hkv ? h - a.Hq : h - a.Hq - a.Hkv;
+        to = (h < a.Hq + a.Hkv ? a.k_pages : a.v_pages) + row + g * D;
+        if (h >= a.Hq + a.Hkv && (not_finite(lo[k]) || not_finite(hi[k]))) bad_s[n] = 1;
+      }
+      *reinterpret_cast<uint4*>(to + e0) = lo[k];
+      *reinterpret_cast<uint4*>(to + e0 + HALF) = hi[k];
     }
   }
+  __syncthreads();
+  if (threadIdx.x < mine) a.set[bt0 + threadIdx.x].bad = bad_s[threadIdx.x];
 }
 
 // --------------------------------------------------------------- attend ----
-constexpr int kTreeThreads = 320;
-constexpr int kTreeMaxCtas = 160;  // bound of the workspace; one CTA per SM
+constexpr int kTreeMaxCtas = 320;  // bound of the workspace: two CTAs per SM
 constexpr int kAbsentRing = 8;
+// Stacked rows up to this many tiles of 128 go through the one-tile kernel.
+constexpr int kTreeOneTileStacks = 8;
 
-template <int D>
+// NT query tiles of 128 rows per CTA, each with a warpgroup of its own; they
+// share the staged keys.  NT = 2 (one CTA per SM) loads keys once for 256
+// rows; NT = 1 (two CTAs per SM) is for segments of at most 128 rows, where
+// one CTA's start, end and softmax overlap the other's loads and products.
+template <int D, int NT>
 struct TreeLayout {
+  static constexpr int kThreads = NT * 128 + 64;
   static constexpr int kTileBytes = kTile * D * 2;  // one 128-row Q, K or V tile
-  static constexpr int kQ = 0;                      // Q_A, Q_B
-  static constexpr int kK = kQ + 2 * kTileBytes;    // K ring, 2 stages
-  static constexpr int kV = kK + 2 * kTileBytes;    // V ring, 2 stages
-  static constexpr int kStage = kV + 2 * kTileBytes;  // output staging, 4 KB per softmax warp
-  static constexpr int kSmall = kStage + 8 * 4096;  // TreeSmall
-  static constexpr int kBytes = kSmall + 3072;
+  static constexpr int kStages = NT == 1 && D == 128 ? 1 : 2;  // K and V rings
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + NT * kTileBytes;
+  static constexpr int kV = kK + kStages * kTileBytes;
+  static constexpr int kStage = kV + kStages * kTileBytes;  // 4 KB per softmax warp
+  static constexpr int kSmall = kStage + NT * 4 * 4096;     // TreeSmall
+  static constexpr int kBytes = kSmall + 1024;
+  static_assert(kBytes <= (NT == 1 ? 115712 : 232448), "shared memory of one CTA");
 };
-static_assert(TreeLayout<kMaxHeadDim>::kBytes <= 232448, "shared memory of one CTA");
 
 // One piece of a segment, as the producer publishes it in a two-slot ring
 // (n == 0: no more).
@@ -290,7 +392,6 @@ struct Piece {
   int cart_lo, row_lo, t0;
   int ring;        // K/V ring position of its first tile
   int slot;        // partial output, -1: the final output
-  int split;       // the two streams share one query tile and take tiles in turn
   unsigned bad[2]; // new rows whose value is not finite
 };
 
@@ -315,26 +416,22 @@ enum TreeBar {
   kTPFull1,
   kTODone0,      // the piece's last PV of stream x
   kTODone1,
-  kTPair0,       // warps w and w + 4 of a split piece (64 arrivals)
-  kTPair1,
-  kTPair2,
-  kTPair3,
   kTDrain,
   kTNumBars
 };
 
 // The shared memory next to the tiles.
+template <int kThreads>
 struct TreeSmall {
-  float2 stats[2][kTile];  // split pieces: (m, l) of each stream's rows
   uint64_t bars[kTNumBars];
-  StartsSmem<kTreeThreads> scan;
+  StartsSmem<kThreads> scan;
   long long begin_off;
   int begin_b, abort_flag;
   uint32_t tmem;
   Piece pieces[2];
   unsigned absent[kAbsentRing];
 };
-static_assert(sizeof(TreeSmall) <= 3072, "shared memory next to the tiles");
+static_assert(sizeof(TreeSmall<320>) <= 1024, "shared memory next to the tiles");
 
 __device__ __forceinline__ unsigned low_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
@@ -352,7 +449,7 @@ struct Walk {
 __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o) {
   while (w.x < w.hi) {
     if (w.x < w.cart_units) {
-      const int v = w.n_cart_all + 1;
+      const int v = w.n_cart_all + kStartUnits;
       const int seg = static_cast<int>(w.x / v);
       const long long first = static_cast<long long>(seg) * v;
       const Cut k = cut_segment(first, w.n_cart_all, w.x, w.hi);
@@ -361,8 +458,8 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o)
       o.own = 0;
       o.b = 0;
       o.g = seg % a.Hkv;
-      o.row0 = seg / a.Hkv * 2 * kTile;
-      o.rows = min(a.B * a.R - o.row0, 2 * kTile);
+      o.row0 = seg / a.Hkv * a.rt_c;
+      o.rows = min(a.B * a.R - o.row0, a.rt_c);
       o.len = 0;
       o.n_cart = w.n_cart_all;
       o.cart_lo = w.cart_lo;
@@ -378,7 +475,7 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o)
       } while (w.c.n == 0);
       w.off = 0;
     }
-    const int v = w.c.n + 1;
+    const int v = w.c.n + kStartUnits;
     const int seg = static_cast<int>(w.off / v), in = static_cast<int>(w.off % v);
     const Cut k = cut_segment(w.x - in, w.c.n, w.x, w.hi);
     const bool at_lo = w.x == w.lo;
@@ -386,117 +483,116 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o)
     w.x += step;
     w.off += step;
     if (k.n <= 0) continue;
-    const int pair = seg % a.pairs;
+    const int part = seg % a.segs;
     o.own = 1;
     o.b = w.b;
-    o.g = seg / a.pairs;
-    o.row0 = w.b * a.R + pair * 2 * kTile;
-    o.rows = min(a.R - pair * 2 * kTile, 2 * kTile);
+    o.g = seg / a.segs;
+    o.row0 = w.b * a.R + part * a.rt_p;
+    o.rows = min(a.R - part * a.rt_p, a.rt_p);
     o.len = w.c.len;
     o.n_cart = w.c.n_cart;
     o.cart_lo = w.c.first_cart;
     o.row_lo = w.c.row_lo;
     o.t0 = k.t0;
     o.n = k.n;
-    o.slot = a.stacked ? (w.b * a.Hkv + o.g) * a.pairs + pair + w.cta
+    o.slot = a.stacked ? (w.b * a.Hkv + o.g) * a.segs + part + w.cta
                        : (k.n == w.c.n ? -1 : 2 * w.cta + (at_lo ? 0 : 1));
     return true;
   }
   return false;
 }
 
-// Values of staged V rows that must not reach the products: rows that are
-// nobody's (outside the window of every node, behind the sequence, unused
-// nodes) become 0, and in rows of used nodes what is not finite becomes 0
-// and is noted in bad (a bit per node), to be added to the rows that see it.
-// Thread i of a stream takes row i.  Both streams may do so for one tile:
-// they write the same values, and a bit is set before its value is replaced.
-template <int D>
-__device__ __forceinline__ void clean_v_row(const TreeArgs& a, uint32_t sv, int row, int r0,
-                                            int lo_row, int len, int b, unsigned* bad) {
-  const int r = r0 + row;
-  if (r >= lo_row && r < len) return;
+// What a staged V row needs before the products read it.
+enum VRow { kVKeep, kVZero, kVScan };
+
+// Row r of conversation b's rows: one that is nobody's (outside the window of
+// every node, behind the sequence, an unused node's) becomes 0, since 0 times
+// what is not finite is not 0; one of a used node with a value that is not
+// finite has those set to 0 and its node noted in `bad`, for the rows that
+// see it.
+__device__ __forceinline__ VRow v_row_kind(const TreeArgs& a, int b, int r, int lo_row, int len) {
+  if (r >= lo_row && r < len) return kVKeep;
   const int node = r - len;
-  const bool used = node >= 0 && node < a.nodes &&
-                    __ldcg(&a.set[static_cast<long long>(b) * a.nodes + node].anc) != 0;
-  bool noted = false;
-#pragma unroll 1
-  for (int k = 0; k < D / 8; ++k) {
-    const uint32_t at = sv + (k >> 3) * 16384 + sw128_offset(row, k & 7);
-    if (!used) {
-      sts_u4(at, make_uint4(0, 0, 0, 0));
-      continue;
-    }
-    const uint4 v = lds_u4(at);
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool any = false;
+  if (node < 0 || node >= a.nodes) return kVZero;
+  const NodeSet* s = a.set + static_cast<long long>(b) * a.nodes + node;
+  const unsigned long long anc = __ldcg(&s->anc);
+  const unsigned flag = __ldcg(&s->bad);
+  return !anc ? kVZero : flag ? kVScan : kVKeep;
+}
+
+// Thread i of a stream takes row i.  Both streams may do so for one tile: they
+// write the same values, and a node is noted before its value is replaced.
+template <int D>
+__device__ __forceinline__ void clean_v_row(uint32_t sv, int row, VRow kind, int node,
+                                            unsigned* bad) {
+  if (kind == kVZero) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if ((w[i] & 0x7f80u) == 0x7f80u) {
-        w[i] &= 0xffff0000u;
-        any = true;
-      }
-      if ((w[i] & 0x7f800000u) == 0x7f800000u) {
-        w[i] &= 0xffffu;
-        any = true;
-      }
-    }
-    if (any) {
-      if (!noted) {
-        atomicOr(&bad[node >> 5], 1u << (node & 31));
-        __threadfence_block();
-        noted = true;
+    for (int k = 0; k < D / 8; ++k)
+      sts_u4(sv + (k >> 3) * 16384 + sw128_offset(row, k & 7), make_uint4(0, 0, 0, 0));
+  } else if (kind == kVScan) {
+    atomicOr(&bad[node >> 5], 1u << (node & 31));
+    __threadfence_block();
+#pragma unroll 1
+    for (int k = 0; k < D / 8; ++k) {
+      const uint32_t at = sv + (k >> 3) * 16384 + sw128_offset(row, k & 7);
+      const uint4 v = lds_u4(at);
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
       }
       sts_u4(at, make_uint4(w[0], w[1], w[2], w[3]));
     }
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kTreeThreads, 1)
+template <int D, int NT>
+__global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
     tree_attend_kernel(const __grid_constant__ CUtensorMap mQ,
                        const __grid_constant__ CUtensorMap mKc,
                        const __grid_constant__ CUtensorMap mVc,
                        const __grid_constant__ CUtensorMap mKp,
                        const __grid_constant__ CUtensorMap mVp,
                        const __grid_constant__ TreeArgs a) {
-  using L = TreeLayout<D>;
+  using L = TreeLayout<D, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
     if (threadIdx.x == 0) atomicOr(a.status, kDevErrSmemLayout);
     pdl_wait();
     return;
   }
-  TreeSmall& sh = *reinterpret_cast<TreeSmall*>(smem + L::kSmall);
+  using Small = TreeSmall<L::kThreads>;
+  Small& sh = *reinterpret_cast<Small*>(smem + L::kSmall);
   uint64_t* const bars = sh.bars;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
     for (int i = 0; i < kTNumBars; ++i)
-      mbar_init(&bars[i], i == kTPFull0 || i == kTPFull1           ? 128
-                          : i == kTPieceEmpty0 || i == kTPieceEmpty1 ? 9
-                          : i >= kTPair0 && i <= kTPair3             ? 64
+      mbar_init(&bars[i], i == kTPFull0 || i == kTPFull1             ? 128
+                          : i == kTPieceEmpty0 || i == kTPieceEmpty1 ? 1 + 4 * NT
                                                                      : 1);
     fence_mbar_init();
   }
   // ---- this CTA's run (the lengths are not the prep kernel's: it may still
   // be running)
-  const Starts st = scan_starts<kTreeThreads>(a, sh.scan);
-  const long long chunk = (st.total + gridDim.x - 1) / gridDim.x;
+  const Starts st = scan_starts<L::kThreads>(a, sh.scan);
+  const long long total = ((a.which & 1) ? st.cart_units : 0) + ((a.which & 2) ? st.own_units : 0);
+  const long long chunk = run_units(st, a.which, gridDim.x);
   Walk walk;
-  walk.lo = walk.x = min(chunk * blockIdx.x, st.total);
-  walk.hi = min(walk.lo + chunk, st.total);
-  walk.cart_units = st.cart_units;
+  walk.lo = walk.x = min(chunk * blockIdx.x, total);
+  walk.hi = min(walk.lo + chunk, total);
+  walk.cart_units = (a.which & 1) ? st.cart_units : 0;
   walk.cart_lo = st.cart_lo;
   walk.n_cart_all = (a.p + kTile - 1) / kTile - st.cart_lo;
   walk.cta = blockIdx.x;
   if (walk.lo >= walk.hi) {
     pdl_release();
-    pdl_wait();  // this grid's end implies the prep kernel's
+    pdl_wait();  // this grid's end implies the end of those before it
     return;
   }
   {
-    const long long at = max(walk.x, st.cart_units);
+    const long long at = max(walk.x, walk.cart_units);
     if (at >= st.start && at < st.start + st.mine) {
       long long x = st.start;
       int b = st.b0;
@@ -509,8 +605,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       sh.begin_off = at - x;
     }
   }
-  if (warp == 9) {
-    tmem_alloc(&sh.tmem, 512);
+  if (warp == 4 * NT + 1) {
+    tmem_alloc(&sh.tmem, NT * 256);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -519,8 +615,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   const uint32_t tmem = sh.tmem;
   const uint32_t abort_s = smem_u32(&sh.abort_flag);
   const int g_log2 = __ffs(a.Hq / a.Hkv) - 1;
+  constexpr int kS = L::kStages;
 
-  if (warp == 8) {
+  if (warp == 4 * NT) {
     // ------------------------------------------------------------ producer --
     // The whole warp walks the run; lane 0 issues the tiled copies of the
     // queries and the cartridge, lane i those of a tile's i-th page.
@@ -562,7 +659,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         break;
       }
       o.ring = ring;
-      o.split = o.rows <= kTile;
       o.bad[0] = o.bad[1] = 0;
       if (lane == 0) {
         sh.pieces[sl] = o;
@@ -571,7 +667,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       __syncwarp();
       const int row_end = min(o.len + a.nodes, table_rows);
       for (int t = 0; t < o.n && ok; ++t, ++ring) {
-        const int s = ring & 1;
+        const int s = ring % kS, before = ring / kS - 1;  // ring slot, its earlier phase
         const int ta = o.t0 + t;
         const bool cart = ta < o.n_cart;
         const int r0 = cart ? 0 : (o.row_lo + ta - o.n_cart) * kTile;
@@ -602,8 +698,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               tma_load_4d(dst + h * 16384 + lane * page_rows * 128, mp, bar, h * 64, o.g, 0, page);
           }
         };
-        if (ring >= 2) {
-          ok = wait(&bars[kTKEmpty0 + s], ((ring >> 1) - 1) & 1);
+        if (before >= 0) {
+          ok = wait(&bars[kTKEmpty0 + s], before & 1);
           if (!ok) break;
         }
         if (lane == 0) sh.absent[ring % kAbsentRing] = gone;
@@ -617,18 +713,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (!ok) break;
           }
           if (lane == 0) {
-            const int tiles = o.split ? 1 : 2;
-            mbar_arrive_expect_tx(&bars[kTQFull], tiles * L::kTileBytes);
-            for (int x = 0; x < tiles; ++x)
+            // boxes of 32 rows, those that hold rows of the segment
+            const int boxes = (o.rows + 31) / 32;
+            mbar_arrive_expect_tx(&bars[kTQFull], boxes * 32 * D * 2);
+            for (int x = 0; x < boxes; ++x)
 #pragma unroll
               for (int h = 0; h < D / 64; ++h)
-                tma_load_4d(smem + L::kQ + x * L::kTileBytes + h * 16384, &mQ, &bars[kTQFull],
-                            h * 64, 0, o.g, (o.row0 + x * kTile) >> g_log2);
+                tma_load_4d(smem + L::kQ + (x >> 2) * L::kTileBytes + h * 16384 + (x & 3) * 4096,
+                            &mQ, &bars[kTQFull], h * 64, 0, o.g, (o.row0 + x * 32) >> g_log2);
           }
           ++nq;
         }
-        if (ring >= 2) {
-          ok = wait(&bars[kTVEmpty0 + s], ((ring >> 1) - 1) & 1);
+        if (before >= 0) {
+          ok = wait(&bars[kTVEmpty0 + s], before & 1);
           if (!ok) break;
         }
         load(L::kV, &mVc, &mVp, &bars[kTVFull0 + s]);
@@ -641,13 +738,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (!ok && lane == 0) {
       // copies in flight get a bounded chance to land before the CTA ends
       if (nq > 0) mbar_wait(&bars[kTQFull], (nq - 1) & 1, 0u, nullptr, 0);
-      for (int t = max(k_issued - 2, 0); t < k_issued; ++t)
-        mbar_wait(&bars[kTKFull0 + (t & 1)], (t >> 1) & 1, 0u, nullptr, 0);
-      for (int t = max(v_issued - 2, 0); t < v_issued; ++t)
-        mbar_wait(&bars[kTVFull0 + (t & 1)], (t >> 1) & 1, 0u, nullptr, 0);
+      for (int t = max(k_issued - kS, 0); t < k_issued; ++t)
+        mbar_wait(&bars[kTKFull0 + t % kS], (t / kS) & 1, 0u, nullptr, 0);
+      for (int t = max(v_issued - kS, 0); t < v_issued; ++t)
+        mbar_wait(&bars[kTVFull0 + t % kS], (t / kS) & 1, 0u, nullptr, 0);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 4 * NT + 1) {
     // ----------------------------------------------------------------- MMA --
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_s, a.status, kDevErrTimeoutMma));
@@ -660,9 +757,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint64_t dK1 = desc_add(dK0, L::kTileBytes);
     const uint64_t dV0 = sdesc_sw128(smem_u32(smem + L::kV), 16384u, 1024u);
     const uint64_t dV1 = desc_add(dV0, L::kTileBytes);
-    // S of stream x = Q tile y times the keys of ring slot s
-    auto issue_qk = [&](int x, int y, int s) {
-      const uint64_t dq = y ? dQ1 : dQ0, dk = s ? dK1 : dK0;
+    // S of stream x from the keys of ring slot s
+    auto issue_qk = [&](int x, int s) {
+      const uint64_t dq = x ? dQ1 : dQ0, dk = s ? dK1 : dK0;
       const uint32_t ts = tmem + x * 128;
       umma_bf16_ss_w(ts, dq, dk, idS, 0u);
 #pragma unroll
@@ -674,86 +771,59 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     };
     auto issue_pv = [&](int x, int s, bool acc) {
       const uint64_t dv = s ? dV1 : dV0;
-      const uint32_t tp = tmem + x * 128, to = tmem + 256 + x * 128;
+      const uint32_t tp = tmem + x * 128, to = tmem + (NT + x) * 128;
       umma_bf16_ts_w(to, tp, dv, idPV, acc ? 1u : 0u);
 #pragma unroll
       for (int k = 1; k < kTile / 16; ++k)
         umma_bf16_ts_w(to, tp + k * 8, desc_add(dv, k * 2048), idPV, 1u);
     };
-    int nP0 = 0, nP1 = 0;
+    int nP[2] = {0, 0};
     bool ok = true;
     for (int it = 0; ok; ++it) {
       ok = wait(&bars[kTPieceFull0 + (it & 1)], (it >> 1) & 1);
       if (!ok) break;
       const Piece& sp = sh.pieces[it & 1];
-      const int n = vld(sp.n), split = vld(sp.split), ring = vld(sp.ring);
+      const int n = vld(sp.n), ring = vld(sp.ring);
+      const bool two = NT == 2 && vld(sp.rows) > kTile;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kTPieceEmpty0 + (it & 1)]);
       if (n == 0) break;
-      // S of the tiles that the streams begin with
-      ok = wait(&bars[kTQFull], it & 1) && wait(&bars[kTKFull0 + (ring & 1)], (ring >> 1) & 1);
+      // Per tile t: PV_0(t), S_0(t+1), PV_1(t), S_1(t+1).  Products run in
+      // issue order, so the commit that publishes S_x(t+1) also says that
+      // PV_x(t) has read its weights and written O_x.
+      ok = wait(&bars[kTQFull], it & 1) && wait(&bars[kTKFull0 + ring % kS], (ring / kS) & 1);
       if (!ok) break;
       tc_fence_after();
-      issue_qk(0, 0, ring & 1);
-      if (!split) issue_qk(1, 1, ring & 1);
-      umma_commit_w(&bars[kTKEmpty0 + (ring & 1)]);
-      if (split && n > 1) {
-        ok = wait(&bars[kTKFull0 + ((ring + 1) & 1)], ((ring + 1) >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        issue_qk(1, 0, (ring + 1) & 1);
-        umma_commit_w(&bars[kTKEmpty0 + ((ring + 1) & 1)]);
-      }
-      const int ahead = split ? 2 : 1;  // a stream's next tile
-      if (n <= ahead) umma_commit_w(&bars[kTQEmpty]);
+      issue_qk(0, ring % kS);
+      if (two) issue_qk(1, ring % kS);
+      umma_commit_w(&bars[kTKEmpty0 + ring % kS]);
+      if (n == 1) umma_commit_w(&bars[kTQEmpty]);
       for (int t = 0; t < n && ok; ++t) {
-        const int gt = ring + t, s = gt & 1, gn = gt + ahead;
-        const bool next = t + ahead < n;
-        ok = wait(&bars[kTVFull0 + s], (gt >> 1) & 1);
-        if (!ok) break;
-        if (!split) {
-          ok = wait(&bars[kTPFull0], nP0 & 1);
+        const int gt = ring + t, s = gt % kS, sn = (gt + 1) % kS;
+        const bool next = t + 1 < n;
+        ok = wait(&bars[kTVFull0 + s], (gt / kS) & 1);
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          if (x == 1 && !two) break;
+          ok = ok && wait(&bars[kTPFull0 + x], nP[x] & 1);
           if (!ok) break;
-          ++nP0;
+          ++nP[x];
           tc_fence_after();
-          issue_pv(0, s, t > 0);
-          if (!next) umma_commit_w(&bars[kTODone0]);
-          if (next) {
-            ok = wait(&bars[kTKFull0 + (gn & 1)], (gn >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_qk(0, 0, gn & 1);
-          }
-          ok = wait(&bars[kTPFull1], nP1 & 1);
-          if (!ok) break;
-          ++nP1;
-          tc_fence_after();
-          issue_pv(1, s, t > 0);
-          if (!next) umma_commit_w(&bars[kTODone1]);
-          if (next) issue_qk(1, 1, gn & 1);
-        } else {
-          const int x = t & 1;
-          ok = wait(&bars[kTPFull0 + x], (x ? nP1 : nP0) & 1);
-          if (!ok) break;
-          if (x)
-            ++nP1;
-          else
-            ++nP0;
-          tc_fence_after();
-          issue_pv(x, s, t >= 2);
+          issue_pv(x, s, t > 0);
           if (!next) umma_commit_w(&bars[kTODone0 + x]);
+          if (x == (two ? 1 : 0)) umma_commit_w(&bars[kTVEmpty0 + s]);
           if (next) {
-            umma_commit_w(&bars[kTVEmpty0 + s]);  // before the keys' wait: V of tile t + 2 may come
-            ok = wait(&bars[kTKFull0 + (gn & 1)], (gn >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_qk(x, 0, gn & 1);
+            if (x == 0) {
+              ok = wait(&bars[kTKFull0 + sn], ((gt + 1) / kS) & 1);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            issue_qk(x, sn);
           }
         }
-        if (!(split && next)) umma_commit_w(&bars[kTVEmpty0 + s]);
-        if (next) {
-          umma_commit_w(&bars[kTKEmpty0 + (gn & 1)]);
-          if (t + ahead == n - 1) umma_commit_w(&bars[kTQEmpty]);
+        if (ok && next) {
+          umma_commit_w(&bars[kTKEmpty0 + sn]);
+          if (t + 2 == n) umma_commit_w(&bars[kTQEmpty]);
         }
       }
     }
@@ -764,14 +834,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   } else {
     // ------------------------------------------------------------- softmax --
     pdl_wait();
-    const int x = warp >> 2;
+    const int x = warp >> 2;  // the stream
     const int row = threadIdx.x & 127;  // TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + x * 128 + lane_off;
-    const uint32_t tO0 = tmem + 256 + lane_off;  // O of stream 0; stream 1's 128 columns on
-    const uint32_t tO = tO0 + x * 128;
+    const uint32_t tO = tmem + (NT + x) * 128 + lane_off;
     uint8_t* const stg = smem + L::kStage + warp * 4096;
-    int nS = 0, nO0 = 0, nO1 = 0, n_pair = 0;
+    int nS = 0, nO = 0;  // S tiles and pieces of this stream
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t err) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_s, a.status, err));
@@ -782,12 +851,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       Piece& sp = sh.pieces[it & 1];
       const int n = vld(sp.n);
       if (n == 0) break;
-      const int split = vld(sp.split), own = vld(sp.own), len = vld(sp.len), b = vld(sp.b);
+      if (x * kTile >= vld(sp.rows)) {  // no rows for this stream
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kTPieceEmpty0 + (it & 1)]);
+        continue;
+      }
+      const int own = vld(sp.own), len = vld(sp.len), b = vld(sp.b);
       const int ring = vld(sp.ring), n_cart = vld(sp.n_cart), t0 = vld(sp.t0);
       const int cart_lo = vld(sp.cart_lo), row_lo = vld(sp.row_lo);
-      const int step = split ? 2 : 1;
       // this thread's query row
-      const int local = split ? row : x * kTile + row;
+      const int local = x * kTile + row;
       bool live = local < vld(sp.rows);
       const int grow = vld(sp.row0) + local;
       unsigned long long vis = 0;
@@ -803,19 +876,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const unsigned live_rows = __ballot_sync(0xffffffffu, live);
       const int lo_row = a.window > 0 ? len - a.window + 1 : 0;  // of the shallowest node
       float m = -INFINITY, l = 0.f;
-      for (int t = split ? x : 0; t < n && ok; t += step) {
+      for (int t = 0; t < n && ok; ++t) {
+        const int ta = t0 + t, gt = ring + t;
+        const bool cart = ta < n_cart;
+        const int k0 = cart ? (cart_lo + ta) * kTile : (row_lo + ta - n_cart) * kTile;
+        const bool clean = !cart && (k0 + kTile > len || k0 < lo_row);
+        VRow kind = kVKeep;
+        if (clean) kind = v_row_kind(a, b, k0 + row, lo_row, len);
         ok = wait(&bars[kTSFull0 + x], nS & 1, kDevErrTimeoutSoftmax);
         if (!ok) break;
         ++nS;
         tc_fence_after();
-        const int ta = t0 + t, gt = ring + t;
-        const bool cart = ta < n_cart;
-        const int k0 = cart ? (cart_lo + ta) * kTile : (row_lo + ta - n_cart) * kTile;
-        if (!cart && (k0 + kTile > len || k0 < lo_row)) {
-          ok = wait(&bars[kTVFull0 + (gt & 1)], (gt >> 1) & 1, kDevErrTimeoutSoftmax);
+        if (clean) {
+          ok = wait(&bars[kTVFull0 + gt % kS], (gt / kS) & 1, kDevErrTimeoutSoftmax);
           if (!ok) break;
-          clean_v_row<D>(a, smem_u32(smem + L::kV + (gt & 1) * L::kTileBytes), row, k0, lo_row,
-                         len, b, sp.bad);
+          clean_v_row<D>(smem_u32(smem + L::kV + gt % kS * L::kTileBytes), row, kind,
+                         k0 + row - len, sp.bad);
           fence_proxy_async_smem();
         }
         if (live_rows) {
@@ -877,7 +953,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (rmax > m + 8.f) {
             alpha = exp2_approx(m - rmax);
             m = rmax;
-            rescale = t >= step;
+            rescale = t > 0;
           }
           const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
           const float mr = m == -INFINITY ? 0.f : m;  // no key yet: weights 0
@@ -924,40 +1000,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue --
-      // The output is c0 * O_0 + c1 * O_1 of the streams (one of them alone
-      // unless the piece is split, where warps w and w + 4 hold the same rows
-      // and each writes half of the columns).
-      const bool two = split && n > 1;
-      float c0, c1 = 0.f, lse;
-      if (split) {
-        sh.stats[x][row] = make_float2(m, l);
-        mbar_arrive(&bars[kTPair0 + (warp & 3)]);
-        ok = wait(&bars[kTPair0 + (warp & 3)], n_pair & 1, kDevErrTimeoutEpilogue);
-        if (!ok) break;
-        ++n_pair;
-        const float2 s0 = sh.stats[0][row], s1 = sh.stats[1][row];
-        const float top = fmaxf(s0.x, s1.x), base = top == -INFINITY ? 0.f : top;
-        const float f0 = exp2_approx(s0.x - base), f1 = exp2_approx(s1.x - base);
-        const float sum = s0.y * f0 + s1.y * f1;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        c0 = f0 * inv;
-        c1 = f1 * inv;
-        lse = sum == 0.f ? -INFINITY : top + __log2f(sum);
-      } else {
-        c0 = l == 0.f ? 0.f : 1.f / l;
-        lse = l == 0.f ? -INFINITY : m + __log2f(l);
-      }
-      if (split || x == 0) {
-        ok = wait(&bars[kTODone0], nO0 & 1, kDevErrTimeoutEpilogue);
-        if (!ok) break;
-      }
-      if (two || (!split && x == 1)) {
-        ok = wait(&bars[kTODone1], nO1 & 1, kDevErrTimeoutEpilogue);
-        if (!ok) break;
-      }
-      ++nO0;
-      if (two || !split) ++nO1;
+      ok = wait(&bars[kTODone0 + x], nO & 1, kDevErrTimeoutEpilogue);
+      if (!ok) break;
+      ++nO;
       tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       const int slot = vld(sp.slot), g = vld(sp.g);
       // new rows that this one sees and whose value is not finite
       const unsigned long long bad =
@@ -965,28 +1012,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                      << 32 |
                  *reinterpret_cast<volatile unsigned*>(&sp.bad[0]));
       if (live_rows) {
-        const int blk_lo = split ? x * (D / 64) : 0, blk_hi = split ? blk_lo + D / 64 : D / 32;
-        const int rows_cap = own ? min(a.R, 2 * kTile) : min(a.B * a.R, 2 * kTile);
+        const int row_cap = 32 - __clz(live_rows);  // behind the warp's last live row
+        const int rows_cap = own ? min(a.R, a.rt_p) : min(a.B * a.R, a.rt_c);
         const long long part0 =
             slot < 0 ? 0 : static_cast<long long>(slot) * rows_cap + (local - lane);
         float* const part = own ? a.part_p : a.part_c;
+        // 32 columns at a time through the warp's slice, so that stores cover
+        // whole sectors: 16-byte granule k of staged row r sits at
+        // r*128 + (k ^ (r & 7))*16
+        uint8_t* const my = stg + lane * 128;
+        const bool f32 = slot >= 0;
+        const int gpr = f32 ? 8 : 4, gl = f32 ? 3 : 2;  // granules per row
+        const int first_row = lane >> gl, gran = lane & (gpr - 1);
 #pragma unroll 1
-        for (int blk = blk_lo; blk < blk_hi; ++blk) {
+        for (int blk = 0; blk < D / 32; ++blk) {
           uint32_t v[32];
-          tmem_ld32((split ? tO0 : tO) + blk * 32, v);
+          tmem_ld32(tO + blk * 32, v);
           tmem_ld_wait();
           tmem_reg_fence(v);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * c0);
-          if (two) {
-            uint32_t y[32];
-            tmem_ld32(tO0 + 128 + blk * 32, y);
-            tmem_ld_wait();
-            tmem_reg_fence(y);
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              v[c] = __float_as_uint(fmaf(__uint_as_float(y[c]), c1, __uint_as_float(v[c])));
-          }
+          for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * inv);
           for (unsigned long long left = own ? bad : 0ull; left; left &= left - 1) {
             const __nv_bfloat16* y =
                 a.v_new + ((static_cast<long long>(b) * a.nodes + __ffsll(left) - 1) * a.Hkv + g) * D +
@@ -997,10 +1042,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               if (!isfinite(f)) v[c] = __float_as_uint(__uint_as_float(v[c]) + f);
             }
           }
-          // through the warp's slice, so that stores cover whole sectors: 16-byte
-          // granule k of staged row r sits at r*128 + (k ^ (r & 7))*16
-          uint8_t* my = stg + lane * 128;
-          if (slot >= 0) {
+          if (f32) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               *reinterpret_cast<uint4*>(my + ((k ^ (lane & 7)) << 4)) =
@@ -1015,33 +1057,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                   pack_bf16x2(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
           }
           __syncwarp();
-          const int gpr = slot >= 0 ? 8 : 4;
-          for (int i = lane; i < 32 * gpr; i += 32) {
-            const int r = i / gpr, k = i % gpr;
+#pragma unroll 1
+          for (int r = first_row; r < row_cap; r += 32 >> gl) {
             if (!(live_rows >> r & 1)) continue;
-            const uint4 y = *reinterpret_cast<const uint4*>(stg + r * 128 + ((k ^ (r & 7)) << 4));
-            if (slot >= 0) {
-              *reinterpret_cast<uint4*>(part + (part0 + r) * D + blk * 32 + k * 4) = y;
+            const uint4 y = *reinterpret_cast<const uint4*>(stg + r * 128 + ((gran ^ (r & 7)) << 4));
+            if (f32) {
+              *reinterpret_cast<uint4*>(part + (part0 + r) * D + blk * 32 + gran * 4) = y;
             } else {
               const int gr = grow - lane + r;
               const long long off = (static_cast<long long>(gr >> g_log2) * a.Hq + (g << g_log2) +
                                      (gr & ((1 << g_log2) - 1))) * D;
-              *reinterpret_cast<uint4*>(a.o + off + blk * 32 + k * 8) = y;
+              *reinterpret_cast<uint4*>(a.o + off + blk * 32 + gran * 8) = y;
             }
           }
           __syncwarp();
         }
-        if (slot >= 0 && live && (!split || x == 0))
-          (own ? a.lse_p : a.lse_c)[part0 + lane] = lse;
-      }
-      if (split) {
-        // both warps have read O of both streams (the next piece's products
-        // wait for their weights) and the other's statistics
-        tc_fence_before();
-        mbar_arrive(&bars[kTPair0 + (warp & 3)]);
-        ok = wait(&bars[kTPair0 + (warp & 3)], n_pair & 1, kDevErrTimeoutEpilogue);
-        ++n_pair;
-        tc_fence_after();
+        if (slot >= 0 && live)
+          (own ? a.lse_p : a.lse_c)[part0 + lane] = l == 0.f ? -INFINITY : m + __log2f(l);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kTPieceEmpty0 + (it & 1)]);
@@ -1051,109 +1083,126 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 4 * NT + 1) tmem_dealloc(tmem, NT * 256);
 }
 
 // ---------------------------------------------------------------- merge ----
-// One warp per output row: the parts that the pieces of its segments left,
-// in the order of the CTAs (o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M)).
-// Rows that one piece wrote whole have none.
+// Joins the parts that the pieces of a row's segments left, in the order of
+// the CTAs: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).  Block
+// (conversation and kv head, 32 of its rows), four rows per warp, with several
+// warps on the parts of one group of rows where the block has fewer; rows that
+// one piece wrote whole have no parts.
 template <int D>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int E = D / 32;  // output columns per lane
+  using Vec = std::conditional_t<E == 4, float4, float2>;
+  __shared__ float s_num[8][4][D], s_den[8][4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv, G = a.Hq / a.Hkv;
+  const int base = blockIdx.y * 32;
+  const int groups = min(8, (a.R - base + 3) >> 2);
+  const int slices = groups > 4 ? 1 : groups > 2 ? 2 : groups > 1 ? 4 : 8;
+  const int slice = warp / groups, r0 = base + warp % groups * 4;
+  // lane: part lane & 7 (of eight at a time) of row r0 + lane / 8
+  const int mine = r0 + (lane >> 3), part = base / a.rt_p;
+  const int gr = b * a.R + mine;
+  const int id_c = gr / a.rt_c * a.Hkv + g, id_p = (b * a.Hkv + g) * a.segs + part;
+  const int stacks = a.stacked ? (a.B * a.R + a.rt_c - 1) / a.rt_c * a.Hkv : 0;
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int rows = a.B * a.nodes * a.Hq, G = a.Hq / a.Hkv;
-  const long long total = a.start[a.B];
-  const long long chunk = (total + a.n_ctas - 1) / a.n_ctas;
-  const int cart_lo = *a.cart_lo, n_c = (a.p + kTile - 1) / kTile - cart_lo;
-  for (int w = (blockIdx.x * 256 + threadIdx.x) >> 5; w < rows; w += gridDim.x * 8) {
-    // rows of one (conversation, kv head) follow one another
-    const int b = w / (a.nodes * a.Hq), g = w / a.R % a.Hkv, r = w % a.R;
-    const int bt = b * a.nodes + r / G;
-    if (!__ldcg(&a.set[bt].anc)) continue;
-    const ConvTiles c = conv_tiles(a, b);
-    const int pair = r / (2 * kTile);
-    // its segments: [0] stacked rows against the cartridge, [1] own rows
-    long long first[2];
-    int tiles[2], id[2];
-    const int gr = b * a.R + r;
-    id[0] = gr / (2 * kTile) * a.Hkv + g;
-    tiles[0] = a.stacked ? n_c : 0;
-    first[0] = static_cast<long long>(id[0]) * (n_c + 1);
-    id[1] = (b * a.Hkv + g) * a.pairs + pair;
-    tiles[1] = c.n;
-    first[1] = a.start[b] + static_cast<long long>(g * a.pairs + pair) * (c.n + 1);
-    int c_lo[2], n_part[2];
+  const bool row_ok = slice < slices && mine < a.R;
+  const int2 sp = __ldcg(a.spans + stacks + id_p);
+  int2 sc = make_int2(0, 0);
+  if (a.stacked && row_ok) sc = __ldcg(a.spans + id_c);
+  unsigned long long anc = 0;
+  if (row_ok) anc = __ldcg(&a.set[b * a.nodes + mine / G].anc);
+  if (sp.y == 0 || (!a.stacked && sp.y == 1)) return;  // idle, or written by its piece
+  const int n = anc ? sc.y + sp.y : 0;
+  // row of part i of the lane's row in part_c, or ~ of it in part_p
+  const int rows_c = min(a.B * a.R, a.rt_c), rows_p = min(a.R, a.rt_p);
+  auto locate = [&](int i) {
+    if (i < sc.y) return (id_c + (sc.x >> 1) + i) * rows_c + gr % a.rt_c;
+    i -= sc.y;
+    const int slot = a.stacked ? id_p + (sp.x >> 1) + i : i ? 2 * ((sp.x >> 1) + i) : sp.x;
+    return ~(slot * rows_p + mine % a.rt_p);
+  };
+  auto lse_of = [&](int at) { return __ldcg(at >= 0 ? a.lse_c + at : a.lse_p + ~at); };
+  const int n_max = __reduce_max_sync(0xffffffffu, n);
+  float top = -INFINITY, lse0 = -INFINITY;
+  if ((lane & 7) < n) top = lse0 = lse_of(locate(lane & 7));
+  for (int i = (lane & 7) + 8; i < n; i += 8) top = fmaxf(top, lse_of(locate(i)));
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      c_lo[s] = static_cast<int>(first[s] / chunk);
-      const int c_hi = static_cast<int>((first[s] + tiles[s]) / chunk);
-      // (a run may hold the segment's start alone, without a tile)
-      if (tiles[s] > 0 &&
-          cut_segment(first[s], tiles[s], c_lo[s] * chunk, (c_lo[s] + 1) * chunk).n <= 0)
-        ++c_lo[s];
-      n_part[s] = tiles[s] > 0 ? c_hi - c_lo[s] + 1 : 0;
-    }
-    if (!a.stacked && n_part[1] == 1) continue;  // written by the piece
-    const int n = n_part[0] + n_part[1];
-    const float *out = nullptr, *lse_at = nullptr;
-    auto locate = [&](int i) {
-      if (i < n_part[0]) {
-        const long long at = static_cast<long long>(id[0] + c_lo[0] + i) *
-                                 min(a.B * a.R, 2 * kTile) + gr % (2 * kTile);
-        out = a.part_c + at * D;
-        lse_at = a.lse_c + at;
-      } else {
-        const int cta = c_lo[1] + i - n_part[0];
-        const long long slot =
-            a.stacked ? id[1] + cta : 2 * cta + (cta * chunk >= first[1] ? 0 : 1);
-        const long long at = slot * min(a.R, 2 * kTile) + r % (2 * kTile);
-        out = a.part_p + at * D;
-        lse_at = a.lse_p + at;
+  for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (top == -INFINITY) top = 0.f;
+  float num[4][E], den = 0.f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int e = 0; e < E; ++e) num[r][e] = 0.f;
+  for (int i0 = slice * 8; i0 < n_max; i0 += slices * 8) {
+    const int i = i0 + (lane & 7);
+    const int at = i < n ? locate(i) : 0;
+    const float f = i < n ? exp2_approx((i0 ? lse_of(at) : lse0) - top) : 0.f;
+    den += f;
+#pragma unroll 1
+    for (int j0 = 0; j0 < min(8, n_max - i0); j0 += 2) {  // two parts of four rows in flight
+      Vec v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int from = (q & 3) * 8 + j0 + (q >> 2);
+        const int src = __shfl_sync(0xffffffffu, at, from);
+        const bool some = i0 + j0 + (q >> 2) < __shfl_sync(0xffffffffu, n, from);
+        const float* out = src >= 0 ? a.part_c + static_cast<long long>(src) * D
+                                    : a.part_p + static_cast<long long>(~src) * D;
+        v[q] = some ? __ldcg(reinterpret_cast<const Vec*>(out) + lane) : Vec{};
       }
-    };
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32) {
-      locate(i);
-      top = fmaxf(top, __ldcg(lse_at));
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (top == -INFINITY) top = 0.f;
-    float num[E], den = 0.f;
+      for (int q = 0; q < 8; ++q) {
+        const float w = __shfl_sync(0xffffffffu, f, (q & 3) * 8 + j0 + (q >> 2));
+        const float* y = reinterpret_cast<const float*>(&v[q]);
 #pragma unroll
-    for (int e = 0; e < E; ++e) num[e] = 0.f;
-    for (int i = 0; i < n; ++i) {
-      locate(i);
-      const float f = exp2_approx(__ldcg(lse_at) - top);
-      den += f;
-      if constexpr (E == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(out) + lane);
-        num[0] = fmaf(f, v.x, num[0]);
-        num[1] = fmaf(f, v.y, num[1]);
-        num[2] = fmaf(f, v.z, num[2]);
-        num[3] = fmaf(f, v.w, num[3]);
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(out) + lane);
-        num[0] = fmaf(f, v.x, num[0]);
-        num[1] = fmaf(f, v.y, num[1]);
+        for (int e = 0; e < E; ++e) num[q & 3][e] = fmaf(w, y[e], num[q & 3][e]);
       }
     }
-    const float inv = 1.f / den;
-    __nv_bfloat16* o = a.o + (static_cast<long long>(bt) * a.Hq + g * G + r % G) * D + lane * E;
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  if (slices > 1) {  // join the slices of a group of rows, in their order
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < E; ++e) s_num[warp][r][e * 32 + lane] = num[r][e];
+    if ((lane & 7) == 0) s_den[warp][lane >> 3] = den;
+    __syncthreads();
+    if (slice > 0) return;
+    for (int k = 1; k < slices; ++k) {
+      const int w = warp + k * groups;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < E; ++e) num[r][e] += s_num[w][r][e * 32 + lane];
+      den += s_den[w][lane >> 3];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float inv = 1.f / __shfl_sync(0xffffffffu, den, r * 8);
+    if (!__shfl_sync(0xffffffffu, n, r * 8)) continue;
+    const int t = (r0 + r) / G;
+    __nv_bfloat16* o =
+        a.o + ((static_cast<long long>(b) * a.nodes + t) * a.Hq + g * G + (r0 + r) % G) * D +
+        lane * E;
     if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(num[0] * inv, num[1] * inv),
-                                                pack_bf16x2(num[2] * inv, num[3] * inv));
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(num[r][0] * inv, num[r][1] * inv),
+                                                pack_bf16x2(num[r][2] * inv, num[r][3] * inv));
     else
-      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(num[0] * inv, num[1] * inv);
+      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(num[r][0] * inv, num[r][1] * inv);
   }
 }
 
 // ------------------------------------------------------------- workspace ----
 struct TreeWs {
-  size_t qr, set, start, cart_lo, part_c, part_p, lse_c, lse_p, total;
-  int R, pairs, stacked;
+  size_t qr, set, spans, part_c, part_p, lse_c, lse_p, total;
+  int R, rt_c, rt_p, segs, stacked, joint;
 };
 
 TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
@@ -1166,24 +1215,27 @@ TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
   };
   const size_t n = static_cast<size_t>(B) * nodes;
   w.R = nodes * (Hq / Hkv);
-  w.pairs = (w.R + 2 * kTile - 1) / (2 * kTile);
-  // Stacking reads the cartridge once for 256 rows of several conversations;
+  // Stacking reads the cartridge once for the rows of several conversations;
   // with 256 rows of one conversation nothing is left to stack, and joining
   // the two kinds of segments would only cost.
   w.stacked = p > 0 && B > 1 && w.R < 2 * kTile;
+  w.rt_p = w.R > kTile ? 2 * kTile : kTile;
+  w.rt_c = static_cast<long long>(B) * w.R > kTile * kTreeOneTileStacks ? 2 * kTile : w.rt_p;
+  w.segs = (w.R + w.rt_p - 1) / w.rt_p;
+  w.joint = w.rt_c == w.rt_p;
   w.qr = take(n * Hq * d * 2);
   w.set = take(n * sizeof(NodeSet));
-  w.start = take((static_cast<size_t>(B) + 1) * 8);
-  w.cart_lo = take(4);
   // partial outputs: a slot per segment and cut, or two per run
-  const size_t rows_p = std::min(w.R, 2 * kTile);
+  const size_t rows_p = std::min(w.R, w.rt_p);
+  const size_t ctas_p = w.rt_p > kTile ? kTreeMaxCtas / 2 : kTreeMaxCtas;
+  const size_t ctas_c = w.rt_c > kTile ? kTreeMaxCtas / 2 : kTreeMaxCtas;
   const size_t slots_p =
-      w.stacked ? static_cast<size_t>(B) * Hkv * w.pairs + kTreeMaxCtas : 2 * kTreeMaxCtas;
-  const size_t rows_c = w.stacked ? std::min<size_t>(static_cast<size_t>(B) * w.R, 2 * kTile) : 0;
-  const size_t slots_c =
-      w.stacked
-          ? (static_cast<size_t>(B) * w.R + 2 * kTile - 1) / (2 * kTile) * Hkv + kTreeMaxCtas
-          : 0;
+      w.stacked ? static_cast<size_t>(B) * Hkv * w.segs + ctas_p : 2 * ctas_p;
+  const size_t all = static_cast<size_t>(B) * w.R;
+  const size_t rows_c = w.stacked ? std::min<size_t>(all, w.rt_c) : 0;
+  const size_t stacks = w.stacked ? (all + w.rt_c - 1) / w.rt_c * Hkv : 0;
+  const size_t slots_c = w.stacked ? stacks + ctas_c : 0;
+  w.spans = take((stacks + static_cast<size_t>(B) * Hkv * w.segs) * 8);
   w.part_c = take(slots_c * rows_c * d * 4);
   w.part_p = take(slots_p * rows_p * d * 4);
   w.lse_c = take(slots_c * rows_c * 4);
@@ -1206,47 +1258,66 @@ int check_tree(int B, int nodes, int Hq, int Hkv, int d, int p, int page_rows, i
   return CART_OK;
 }
 
+struct TreeMaps {
+  CUtensorMap q, kc, vc, kp, vp;
+};
+
+template <int D, int NT>
+cudaError_t launch_attend(TreeArgs a, int which, const TreeMaps& m, int ctas, cudaStream_t st) {
+  using L = TreeLayout<D, NT>;
+  const cudaError_t e = set_smem_once<tree_attend_kernel<D, NT>>(L::kBytes);
+  if (e != cudaSuccess) return e;
+  a.which = which;
+  return launch_dependent(tree_attend_kernel<D, NT>, dim3(ctas), dim3(L::kThreads), L::kBytes, st,
+                          m.q, m.kc, m.vc, m.kp, m.vp, a);
+}
+
 template <int D>
-cudaError_t launch_tree(TreeArgs a, const RopeFreqs& f, cudaStream_t st) {
+cudaError_t launch_tree(TreeArgs a, const Turns& turns, cudaStream_t st) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorInvalidValue;
-  a.n_ctas = std::min(sms, kTreeMaxCtas);
+  const int one = std::min(sms, kTreeMaxCtas / 2), two = 2 * one;  // CTAs with NT = 2, 1
+  a.n_ctas_c = a.rt_c > kTile ? one : two;
+  a.n_ctas_p = a.rt_p > kTile ? one : two;
   // rotated queries [B*nodes, Hkv, G, d] as (d, G, Hkv, B*nodes): a
-  // (64, G, 1, 128/G) box is 128 rows of one kv head; pools as (d, Hkv,
+  // (64, G, 1, 32/G) box is 32 rows of one kv head; pools as (d, Hkv,
   // page_rows, n_pages), a box one page of one kv head
-  CUtensorMap mQ, mKc, mVc, mKp, mVp;
+  TreeMaps m;
   const int G = a.Hq / a.Hkv;
   const uint64_t d = D, e2 = 2, hkv = a.Hkv;
   const uint64_t qdims[4] = {d, static_cast<uint64_t>(G), hkv,
                              static_cast<uint64_t>(a.B) * a.nodes};
   const uint64_t qstr[3] = {d * e2, G * d * e2, hkv * G * d * e2};
-  const uint32_t qbox[4] = {64, static_cast<uint32_t>(G), 1, static_cast<uint32_t>(kTile / G)};
+  const uint32_t qbox[4] = {64, static_cast<uint32_t>(G), 1, static_cast<uint32_t>(32 / G)};
   const unsigned page_rows = 1u << a.pt.page_log2;
-  if (!make_bf16_map4(&mQ, a.qr, qdims, qstr, qbox) ||
-      !make_bf16_rows_map(&mKp, a.k_pages, a.pt.n_pages, page_rows, a.Hkv, D, page_rows) ||
-      !make_bf16_rows_map(&mVp, a.v_pages, a.pt.n_pages, page_rows, a.Hkv, D, page_rows))
+  if (!make_bf16_map4(&m.q, a.qr, qdims, qstr, qbox) ||
+      !make_bf16_rows_map(&m.kp, a.k_pages, a.pt.n_pages, page_rows, a.Hkv, D, page_rows) ||
+      !make_bf16_rows_map(&m.vp, a.v_pages, a.pt.n_pages, page_rows, a.Hkv, D, page_rows))
     return cudaErrorInvalidValue;
   if (a.p == 0) {  // no cartridge tile is read
-    mKc = mKp;
-    mVc = mVp;
-  } else if (!make_bf16_rows_map(&mKc, a.kc, 1, a.p, a.Hkv, D, kTile) ||
-             !make_bf16_rows_map(&mVc, a.vc, 1, a.p, a.Hkv, D, kTile)) {
+    m.kc = m.kp;
+    m.vc = m.vp;
+  } else if (!make_bf16_rows_map(&m.kc, a.kc, 1, a.p, a.Hkv, D, kTile) ||
+             !make_bf16_rows_map(&m.vc, a.vc, 1, a.p, a.Hkv, D, kTile)) {
     return cudaErrorInvalidValue;
   }
-  Turns turns;
-  for (int j = 0; j < kMaxHeadDim / 2; ++j) turns.t[j] = f.turns[j];
-  using L = TreeLayout<D>;
-  cudaError_t e = set_smem_once<tree_attend_kernel<D>>(L::kBytes);
+  // nodes per prep block: one for a few nodes (latency), more for many, whose
+  // blocks then share a conversation's lookups
+  const int per = std::min(kPrepNodes, (a.B * a.nodes + 4 * sms - 1) / (4 * sms));
+  const int prep_blocks = a.B * ((a.nodes + per - 1) / per);
+  tree_prep_kernel<D><<<prep_blocks + 1, 256, 0, st>>>(a, turns, per);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  tree_prep_kernel<D><<<a.B * a.nodes + 1, 256, 0, st>>>(a, turns);
-  e = cudaGetLastError();
+  if (a.stacked && !a.joint) {
+    e = launch_attend<D, 2>(a, 1, m, a.n_ctas_c, st);
+    if (e != cudaSuccess) return e;
+  }
+  const int which = a.stacked && a.joint ? 3 : 2;
+  e = a.rt_p > kTile ? launch_attend<D, 2>(a, which, m, a.n_ctas_p, st)
+                     : launch_attend<D, 1>(a, which, m, a.n_ctas_p, st);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(tree_attend_kernel<D>, dim3(a.n_ctas), dim3(kTreeThreads), L::kBytes, st,
-                       mQ, mKc, mVc, mKp, mVp, a);
-  if (e != cudaSuccess) return e;
-  const int blocks = (a.B * a.nodes * a.Hq + 7) / 8;
-  return launch_dependent(tree_merge_kernel<D>, dim3(std::min(blocks, 8 * sms)), dim3(256), 0, st,
-                          a);
+  return launch_dependent(tree_merge_kernel<D>, dim3(a.B * a.Hkv, (a.R + 31) / 32), dim3(256), 0,
+                          st, a);
 }
 
 }  // namespace
@@ -1304,20 +1375,31 @@ int cart_attn_decode_tree(int B, int nodes, int window, int Hq, int Hkv, int d, 
   a.qr = reinterpret_cast<__nv_bfloat16*>(ws + w.qr);
   a.set = reinterpret_cast<NodeSet*>(ws + w.set);
   a.R = w.R;
-  a.pairs = w.pairs;
+  a.rt_c = w.rt_c;
+  a.rt_p = w.rt_p;
+  a.segs = w.segs;
   a.stacked = w.stacked;
-  a.start = reinterpret_cast<long long*>(ws + w.start);
-  a.cart_lo = reinterpret_cast<int*>(ws + w.cart_lo);
+  a.joint = w.joint;
+  a.spans = reinterpret_cast<int2*>(ws + w.spans);
   a.part_c = reinterpret_cast<float*>(ws + w.part_c);
   a.part_p = reinterpret_cast<float*>(ws + w.part_p);
   a.lse_c = reinterpret_cast<float*>(ws + w.lse_c);
   a.lse_p = reinterpret_cast<float*>(ws + w.lse_p);
   a.status = device_status_ptr();
   if (!a.status) return CART_ERR_CUDA;
-  const RopeFreqs f = make_rope_freqs(d, rope_theta);
+  // the turns of the last (d, theta) of this host thread
+  static thread_local Turns turns;
+  static thread_local int turns_d = 0;
+  static thread_local double turns_theta = 0.0;
+  if (turns_d != d || turns_theta != rope_theta) {
+    const RopeFreqs f = make_rope_freqs(d, rope_theta);
+    for (int j = 0; j < kMaxHeadDim / 2; ++j) turns.t[j] = f.turns[j];
+    turns_d = d;
+    turns_theta = rope_theta;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   TraceScope tr("decode_tree", st);
-  const cudaError_t e = d == 128 ? launch_tree<128>(a, f, st) : launch_tree<64>(a, f, st);
+  const cudaError_t e = d == 128 ? launch_tree<128>(a, turns, st) : launch_tree<64>(a, turns, st);
   return e == cudaSuccess ? CART_OK : CART_ERR_CUDA;
 }
 
