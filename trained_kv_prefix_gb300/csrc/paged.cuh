@@ -32,9 +32,11 @@ struct PageTable {
 
 // Rows that conversation b holds: -1 for an idle slot, at most what its
 // table row can name.
-__device__ __forceinline__ int held_rows(const PageTable& t, int b) {
-  const int len = __ldg(t.lens + b);
+__device__ __forceinline__ int held_rows_of(const PageTable& t, int len) {
   return len < 0 ? -1 : min(len, t.max_pages << t.page_log2);
+}
+__device__ __forceinline__ int held_rows(const PageTable& t, int b) {
+  return held_rows_of(t, __ldg(t.lens + b));
 }
 
 // Page of row r of conversation b, or -1.

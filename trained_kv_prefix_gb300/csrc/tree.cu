@@ -73,6 +73,7 @@ struct TreeArgs {
   // the CTAs whose pieces hold tiles of each segment (see segment_span): the
   // stacked segments, then those of every (conversation, kv head)
   int2* spans;
+  int* cut;  // fused: the segment that leaves each CTA's run unfinished, or -1
   // ---- partial outputs
   float *part_c, *part_p, *lse_c, *lse_p;
 };
@@ -88,9 +89,9 @@ struct Turns {
 struct ConvTiles {
   int len, first_cart, n_cart, row_lo, n;
 };
-__device__ __forceinline__ ConvTiles conv_tiles(const TreeArgs& a, int b) {
+__device__ __forceinline__ ConvTiles conv_tiles_of(const TreeArgs& a, int len) {
   ConvTiles c;
-  c.len = held_rows(a.pt, b);
+  c.len = len;
   const int rows = a.pt.max_pages << a.pt.page_log2, n_ct = (a.p + kTile - 1) / kTile;
   // position of the first key that the shallowest node sees
   const int lo = a.window > 0 ? a.p + c.len - a.window + 1 : 0;
@@ -102,9 +103,12 @@ __device__ __forceinline__ ConvTiles conv_tiles(const TreeArgs& a, int b) {
             : c.n_cart + (min(c.len + a.nodes, rows) + kTile - 1) / kTile - c.row_lo;
   return c;
 }
+__device__ __forceinline__ ConvTiles conv_tiles(const TreeArgs& a, int b) {
+  return conv_tiles_of(a, held_rows(a.pt, b));
+}
 // A segment of n tiles is n + kStartUnits units of the schedule: its start and
 // end cost about as much as that many tiles.
-constexpr int kStartUnits = 2;
+constexpr int kStartUnits = 3;
 __device__ __forceinline__ long long conv_units(const TreeArgs& a, int n) {
   return n > 0 ? static_cast<long long>(n + kStartUnits) * a.Hkv * a.segs : 0;
 }
@@ -200,7 +204,8 @@ __device__ __forceinline__ long long run_units(const Starts& r, int which, int n
 // One block: the spans of all segments, for the merge.
 __device__ __forceinline__ void write_spans(const TreeArgs& a) {
   __shared__ StartsSmem<256> s;
-  const Starts r = scan_starts<256>(a, s);
+  for (int i = threadIdx.x; i < a.n_ctas_p; i += 256) a.cut[i] = -1;
+  const Starts r = scan_starts<256>(a, s);  // (with barriers: the list is cleared)
   const long long chunk_p = run_units(r, a.joint ? 3 : 2, a.n_ctas_p);
   const int stacks = a.stacked ? (a.B * a.R + a.rt_c - 1) / a.rt_c * a.Hkv : 0;
   if (a.stacked) {
@@ -214,7 +219,9 @@ __device__ __forceinline__ void write_spans(const TreeArgs& a) {
     const int n = conv_tiles(a, b).n, per = a.Hkv * a.segs;
     int2* to = a.spans + stacks + static_cast<long long>(b) * per;
     for (int i = 0; i < per; ++i) {
-      to[i] = segment_span(x, n, chunk_p);
+      const int2 span = segment_span(x, n, chunk_p);
+      to[i] = span;
+      if (span.y > 1) a.cut[span.x >> 1] = b * per + i;
       if (n > 0) x += n + kStartUnits;
     }
   }
@@ -240,15 +247,16 @@ __device__ __forceinline__ bool not_finite(uint4 v) {
   return not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w);
 }
 
-// Rotates eight pairs: (x, y) element by element by the angles c[0..7].
-__device__ __forceinline__ void rotate8(uint4& x, uint4& y, const float2* c) {
+// Rotates eight pairs: (x, y) element by element by the angles c[0], c[step],
+// c[2 * step], ...
+__device__ __forceinline__ void rotate8(uint4& x, uint4& y, const float2* c, int step) {
   uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 fa = bf16x2_to_float2(a[i]), fb = bf16x2_to_float2(b[i]);
     float2 ya, yb;
-    rope_pair(fa.x, fb.x, c[2 * i], ya.x, yb.x);
-    rope_pair(fa.y, fb.y, c[2 * i + 1], ya.y, yb.y);
+    rope_pair(fa.x, fb.x, c[2 * i * step], ya.x, yb.x);
+    rope_pair(fa.y, fb.y, c[(2 * i + 1) * step], ya.y, yb.y);
     a[i] = pack_bf16x2(ya.x, ya.y);
     b[i] = pack_bf16x2(yb.x, yb.y);
   }
@@ -318,7 +326,9 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
   }
   for (int i = threadIdx.x; i < mine * HALF; i += 256) {
     const int n = i / HALF, j = i % HALF;
-    cs[n][j] = rope_cs_turns(f.t[j], a.p + len + __popcll(tree.anc[t0 + n]) - 1);
+    // (the i-th angles of a row's lanes side by side: no bank conflicts)
+    cs[n][j % 8 * S::kLanes + j / 8] =
+        rope_cs_turns(f.t[j], a.p + len + __popcll(tree.anc[t0 + n]) - 1);
   }
   __syncthreads();
   for (int i0 = warp * S::kRows + sub; i0 - sub < rows; i0 += 8 * S::kRows * S::kBatch) {
@@ -333,7 +343,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       const long long row =
           ((static_cast<long long>(page_s[n]) << a.pt.page_log2) +
            ((len + t0 + n) & ((1 << a.pt.page_log2) - 1))) * a.Hkv * D;
-      if (h < a.Hq + a.Hkv) rotate8(lo[k], hi[k], &cs[n][e0]);
+      if (h < a.Hq + a.Hkv) rotate8(lo[k], hi[k], &cs[n][lane % S::kLanes], S::kLanes);
       __nv_bfloat16* to;
       if (h < a.Hq) {
         if (used) {
@@ -426,7 +436,7 @@ struct TreeSmall {
   uint64_t bars[kTNumBars];
   StartsSmem<kThreads> scan;
   long long begin_off;
-  int begin_b, abort_flag;
+  int begin_b, begin_len, abort_flag;
   uint32_t tmem;
   Piece pieces[2];
   unsigned absent[kAbsentRing];
@@ -442,8 +452,12 @@ struct Walk {
   long long x, lo, hi, cart_units;
   int cta, cart_lo, n_cart_all, b;
   long long off;  // units of conversation b that lie before x
+  int len_next;   // lens[b + 1], loaded ahead
   ConvTiles c;
 };
+__device__ __forceinline__ void load_next_len(const TreeArgs& a, Walk& w) {
+  if (w.b + 1 < a.B) w.len_next = __ldg(a.pt.lens + w.b + 1);
+}
 
 // The next piece that has tiles; false at the run's end.
 __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o) {
@@ -471,7 +485,9 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o)
     }
     if (w.off >= conv_units(a, w.c.n)) {  // the next conversation that has work
       do {
-        w.c = conv_tiles(a, ++w.b);
+        ++w.b;
+        w.c = conv_tiles_of(a, held_rows_of(a.pt, w.len_next));
+        load_next_len(a, w);
       } while (w.c.n == 0);
       w.off = 0;
     }
@@ -566,6 +582,13 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
   Small& sh = *reinterpret_cast<Small*>(smem + L::kSmall);
   uint64_t* const bars = sh.bars;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&mQ);
+    tma_prefetch_desc(&mKc);
+    tma_prefetch_desc(&mVc);
+    tma_prefetch_desc(&mKp);
+    tma_prefetch_desc(&mVp);
+  }
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
     for (int i = 0; i < kTNumBars; ++i)
@@ -597,8 +620,12 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
       long long x = st.start;
       int b = st.b0;
       for (;; ++b) {
-        const long long u = conv_units(a, conv_tiles(a, b).n);
-        if (at < x + u) break;
+        const ConvTiles c = conv_tiles(a, b);
+        const long long u = conv_units(a, c.n);
+        if (at < x + u) {
+          sh.begin_len = c.len;
+          break;
+        }
         x += u;
       }
       sh.begin_b = b;
@@ -621,13 +648,6 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
     // ------------------------------------------------------------ producer --
     // The whole warp walks the run; lane 0 issues the tiled copies of the
     // queries and the cartridge, lane i those of a tile's i-th page.
-    if (lane == 0) {
-      tma_prefetch_desc(&mQ);
-      tma_prefetch_desc(&mKc);
-      tma_prefetch_desc(&mVc);
-      tma_prefetch_desc(&mKp);
-      tma_prefetch_desc(&mVp);
-    }
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_s, a.status, kDevErrTimeoutTma));
     };
@@ -641,9 +661,25 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
     };
     walk.b = sh.begin_b;
     walk.off = sh.begin_off;
-    if (walk.hi > walk.cart_units) walk.c = conv_tiles(a, walk.b);
-    Piece o;
+    if (walk.hi > walk.cart_units) {
+      walk.c = conv_tiles_of(a, sh.begin_len);
+      load_next_len(a, walk);
+    }
+    // Table entry of the page that this lane copies of tile t of piece q (-1
+    // where it copies none), looked up a tile ahead.  (Bringing the pages of
+    // later tiles into L2 as well made it slower: 337 -> 367 us one tile ahead
+    // and 560 us three ahead for 64 histories of 8k rows, which stream at 96 %
+    // of the copy bandwidth without.)
+    auto look_up = [&](const Piece& q, int t) {
+      const int ta = q.t0 + t;
+      const int k = ((q.row_lo + ta - q.n_cart) * kTile >> a.pt.page_log2) + lane;
+      return ta >= q.n_cart && lane < tile_pages && k < a.pt.max_pages
+                 ? __ldg(a.pt.table + static_cast<long long>(q.b) * a.pt.max_pages + k)
+                 : -1;
+    };
+    Piece o{}, o_next{};
     bool more = next_piece(a, walk, o), ok = true;
+    int entry = more ? look_up(o, 0) : -1;
     int ring = 0, nq = 0, k_issued = 0, v_issued = 0;
     for (int it = 0; ok; ++it) {
       const int sl = it & 1;
@@ -674,10 +710,10 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
         // pages of the tile: -1 behind the last row, n_pages (a box outside
         // the pool, which reads as 0) for one that is not there
         int page = -1;
-        if (!cart && lane < tile_pages && r0 + lane * page_rows < row_end) {
-          page = page_of(a.pt, o.b, r0 + lane * page_rows);
-          if (page < 0) page = a.pt.n_pages;
-        }
+        if (!cart && lane < tile_pages && r0 + lane * page_rows < row_end)
+          page = static_cast<unsigned>(entry) < static_cast<unsigned>(a.pt.n_pages)
+                     ? entry
+                     : a.pt.n_pages;
         const unsigned gone = __ballot_sync(0xffffffffu, page == a.pt.n_pages);
         const uint32_t bytes =
             cart ? L::kTileBytes
@@ -724,6 +760,13 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
           }
           ++nq;
         }
+        // what comes next, while V's slot is waited for
+        if (t + 1 < o.n) {
+          entry = look_up(o, t + 1);
+        } else {
+          more = next_piece(a, walk, o_next);
+          if (more) entry = look_up(o_next, 0);
+        }
         if (before >= 0) {
           ok = wait(&bars[kTVEmpty0 + s], before & 1);
           if (!ok) break;
@@ -731,7 +774,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
         load(L::kV, &mVc, &mVp, &bars[kTVFull0 + s]);
         v_issued = ring + 1;
       }
-      if (ok) more = next_piece(a, walk, o);
+      o = o_next;
     }
     after_prep();
     pdl_release();
@@ -1012,65 +1055,87 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
                      << 32 |
                  *reinterpret_cast<volatile unsigned*>(&sp.bad[0]));
       if (live_rows) {
-        const int row_cap = 32 - __clz(live_rows);  // behind the warp's last live row
         const int rows_cap = own ? min(a.R, a.rt_p) : min(a.B * a.R, a.rt_c);
         const long long part0 =
             slot < 0 ? 0 : static_cast<long long>(slot) * rows_cap + (local - lane);
         float* const part = own ? a.part_p : a.part_c;
-        // 32 columns at a time through the warp's slice, so that stores cover
-        // whole sectors: 16-byte granule k of staged row r sits at
-        // r*128 + (k ^ (r & 7))*16
-        uint8_t* const my = stg + lane * 128;
+        // Through the warp's slice, so that stores cover whole sectors: 32 rows of
+        // 128 bytes (32 f32 or 64 bf16 columns), 16-byte granule k of row r at
+        // r*128 + (k ^ (r & 7))*16.  Lane l stores granule l % 8 of rows
+        // l / 8 + 4*i.  (A loop: unrolled, the epilogue does not stay in the
+        // instruction cache next to the tile loop and took 3 us a piece.)
         const bool f32 = slot >= 0;
-        const int gpr = f32 ? 8 : 4, gl = f32 ? 3 : 2;  // granules per row
-        const int first_row = lane >> gl, gran = lane & (gpr - 1);
+        uint8_t* const my = stg + lane * 128;
+        const int r1 = lane >> 3, k1 = lane & 7;
+        const uint8_t* const from0 = stg + r1 * 128 + ((k1 ^ r1) << 4);
+        const uint8_t* const from1 = stg + (r1 + 4) * 128 + ((k1 ^ (r1 + 4)) << 4);
+        float* const part_to = part + (part0 + r1) * D + k1 * 4;
+        __nv_bfloat16* const o_to =
+            a.o + (static_cast<long long>((grow - lane) >> g_log2) * a.Hq + (g << g_log2)) * D + k1 * 8;
+        const unsigned mine = live_rows >> r1;
+        auto put = [&](int k, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+          *reinterpret_cast<uint4*>(my + ((k ^ (lane & 7)) << 4)) = make_uint4(x, y, z, w);
+        };
 #pragma unroll 1
-        for (int blk = 0; blk < D / 32; ++blk) {
-          uint32_t v[32];
-          tmem_ld32(tO + blk * 32, v);
-          tmem_ld_wait();
-          tmem_reg_fence(v);
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t v[64];
+          {
+            uint32_t(&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(v);
+            uint32_t(&v1)[32] = *reinterpret_cast<uint32_t(*)[32]>(v + 32);
+            tmem_ld32(tO + h * 64, v0);
+            tmem_ld32(tO + h * 64 + 32, v1);
+            tmem_ld_wait();
+            tmem_reg_fence(v0);
+            tmem_reg_fence(v1);
+          }
 #pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * inv);
+          for (int c = 0; c < 64; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * inv);
           for (unsigned long long left = own ? bad : 0ull; left; left &= left - 1) {
             const __nv_bfloat16* y =
                 a.v_new + ((static_cast<long long>(b) * a.nodes + __ffsll(left) - 1) * a.Hkv + g) * D +
-                blk * 32;
+                h * 64;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
+            for (int c = 0; c < 64; ++c) {
               const float f = __bfloat162float(y[c]);
               if (!isfinite(f)) v[c] = __float_as_uint(__uint_as_float(v[c]) + f);
             }
           }
           if (f32) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(my + ((k ^ (lane & 7)) << 4)) =
-                  make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            for (int q = 0; q < 2; ++q) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                put(k, v[32 * q + 4 * k], v[32 * q + 4 * k + 1], v[32 * q + 4 * k + 2],
+                    v[32 * q + 4 * k + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4 y =
+                    *reinterpret_cast<const uint4*>((i & 1 ? from1 : from0) + (i >> 1) * 1024);
+                if (mine >> (4 * i) & 1)
+                  *reinterpret_cast<uint4*>(part_to + i * 4 * D + h * 64 + q * 32) = y;
+              }
+              __syncwarp();
+            }
           } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(my + ((k ^ (lane & 7)) << 4)) = make_uint4(
-                  pack_bf16x2(__uint_as_float(v[8 * k]), __uint_as_float(v[8 * k + 1])),
+            for (int k = 0; k < 8; ++k)
+              put(k, pack_bf16x2(__uint_as_float(v[8 * k]), __uint_as_float(v[8 * k + 1])),
                   pack_bf16x2(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
                   pack_bf16x2(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
                   pack_bf16x2(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7])));
-          }
-          __syncwarp();
-#pragma unroll 1
-          for (int r = first_row; r < row_cap; r += 32 >> gl) {
-            if (!(live_rows >> r & 1)) continue;
-            const uint4 y = *reinterpret_cast<const uint4*>(stg + r * 128 + ((gran ^ (r & 7)) << 4));
-            if (f32) {
-              *reinterpret_cast<uint4*>(part + (part0 + r) * D + blk * 32 + gran * 4) = y;
-            } else {
-              const int gr = grow - lane + r;
-              const long long off = (static_cast<long long>(gr >> g_log2) * a.Hq + (g << g_log2) +
-                                     (gr & ((1 << g_log2) - 1))) * D;
-              *reinterpret_cast<uint4*>(a.o + off + blk * 32 + gran * 8) = y;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 y =
+                  *reinterpret_cast<const uint4*>((i & 1 ? from1 : from0) + (i >> 1) * 1024);
+              const int r = r1 + 4 * i;
+              if (mine >> (4 * i) & 1)
+                *reinterpret_cast<uint4*>(
+                    o_to + ((r >> g_log2) * a.Hq + (r & ((1 << g_log2) - 1))) * D + h * 64) = y;
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
         if (slot >= 0 && live)
           (own ? a.lse_p : a.lse_c)[part0 + lane] = l == 0.f ? -INFINITY : m + __log2f(l);
@@ -1088,34 +1153,37 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
 
 // ---------------------------------------------------------------- merge ----
 // Joins the parts that the pieces of a row's segments left, in the order of
-// the CTAs: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).  Block
-// (conversation and kv head, 32 of its rows), four rows per warp, with several
-// warps on the parts of one group of rows where the block has fewer; rows that
-// one piece wrote whole have no parts.
+// the CTAs: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).  Block (segment,
+// 32 of its rows), four rows per warp, with several warps on the parts of one
+// group of rows where the block has fewer.  Stacked: every segment of own
+// rows; fused: those that a run left unfinished, at most one per run.
 template <int D>
 __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int E = D / 32;  // output columns per lane
   using Vec = std::conditional_t<E == 4, float4, float2>;
   __shared__ float s_num[8][4][D], s_den[8][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv, G = a.Hq / a.Hkv;
-  const int base = blockIdx.y * 32;
+  pdl_wait();
+  const int id_p = a.stacked ? blockIdx.x : __ldcg(a.cut + blockIdx.x);
+  if (id_p < 0) return;
+  const int b = id_p / (a.Hkv * a.segs), g = id_p / a.segs % a.Hkv, G = a.Hq / a.Hkv;
+  const int base = id_p % a.segs * a.rt_p + blockIdx.y * 32;
+  if (base >= a.R) return;
   const int groups = min(8, (a.R - base + 3) >> 2);
   const int slices = groups > 4 ? 1 : groups > 2 ? 2 : groups > 1 ? 4 : 8;
   const int slice = warp / groups, r0 = base + warp % groups * 4;
   // lane: part lane & 7 (of eight at a time) of row r0 + lane / 8
-  const int mine = r0 + (lane >> 3), part = base / a.rt_p;
+  const int mine = r0 + (lane >> 3);
   const int gr = b * a.R + mine;
-  const int id_c = gr / a.rt_c * a.Hkv + g, id_p = (b * a.Hkv + g) * a.segs + part;
+  const int id_c = gr / a.rt_c * a.Hkv + g;
   const int stacks = a.stacked ? (a.B * a.R + a.rt_c - 1) / a.rt_c * a.Hkv : 0;
-  pdl_wait();
   const bool row_ok = slice < slices && mine < a.R;
   const int2 sp = __ldcg(a.spans + stacks + id_p);
   int2 sc = make_int2(0, 0);
   if (a.stacked && row_ok) sc = __ldcg(a.spans + id_c);
   unsigned long long anc = 0;
   if (row_ok) anc = __ldcg(&a.set[b * a.nodes + mine / G].anc);
-  if (sp.y == 0 || (!a.stacked && sp.y == 1)) return;  // idle, or written by its piece
+  if (sp.y == 0) return;  // idle
   const int n = anc ? sc.y + sp.y : 0;
   // row of part i of the lane's row in part_c, or ~ of it in part_p
   const int rows_c = min(a.B * a.R, a.rt_c), rows_p = min(a.R, a.rt_p);
@@ -1201,7 +1269,7 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
 
 // ------------------------------------------------------------- workspace ----
 struct TreeWs {
-  size_t qr, set, spans, part_c, part_p, lse_c, lse_p, total;
+  size_t qr, set, spans, cut, part_c, part_p, lse_c, lse_p, total;
   int R, rt_c, rt_p, segs, stacked, joint;
 };
 
@@ -1236,6 +1304,7 @@ TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
   const size_t stacks = w.stacked ? (all + w.rt_c - 1) / w.rt_c * Hkv : 0;
   const size_t slots_c = w.stacked ? stacks + ctas_c : 0;
   w.spans = take((stacks + static_cast<size_t>(B) * Hkv * w.segs) * 8);
+  w.cut = take(kTreeMaxCtas * 4);
   w.part_c = take(slots_c * rows_c * d * 4);
   w.part_p = take(slots_p * rows_p * d * 4);
   w.lse_c = take(slots_c * rows_c * 4);
@@ -1316,8 +1385,10 @@ cudaError_t launch_tree(TreeArgs a, const Turns& turns, cudaStream_t st) {
   e = a.rt_p > kTile ? launch_attend<D, 2>(a, which, m, a.n_ctas_p, st)
                      : launch_attend<D, 1>(a, which, m, a.n_ctas_p, st);
   if (e != cudaSuccess) return e;
-  return launch_dependent(tree_merge_kernel<D>, dim3(a.B * a.Hkv, (a.R + 31) / 32), dim3(256), 0,
-                          st, a);
+  return launch_dependent(tree_merge_kernel<D>,
+                          dim3(a.stacked ? a.B * a.Hkv * a.segs : a.n_ctas_p,
+                               (std::min(a.R, a.rt_p) + 31) / 32),
+                          dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -1381,6 +1452,7 @@ int cart_attn_decode_tree(int B, int nodes, int window, int Hq, int Hkv, int d, 
   a.stacked = w.stacked;
   a.joint = w.joint;
   a.spans = reinterpret_cast<int2*>(ws + w.spans);
+  a.cut = reinterpret_cast<int*>(ws + w.cut);
   a.part_c = reinterpret_cast<float*>(ws + w.part_c);
   a.part_p = reinterpret_cast<float*>(ws + w.part_p);
   a.lse_c = reinterpret_cast<float*>(ws + w.lse_c);
