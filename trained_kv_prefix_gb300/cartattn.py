@@ -526,7 +526,7 @@ def cart_attn_decode_tree(q, k_new, v_new, kc, vc, k_pages, v_pages, table, lens
     on = _On(dev, stream)
     try:
         if o is None:
-            o = on.empty(q.shape, bf)
+            o = torch.empty_like(q) if on.stream is None else on.empty(q.shape, bf)
         ws, wp, wn = _scratch(on, workspace, L.cart_attn_decode_tree_workspace_size(
             B, T, Hq, Hkv, d, p, P, M))
         rc = L.cart_attn_decode_tree(
@@ -584,9 +584,14 @@ def cart_pages_reserve(k_pages, v_pages, table, lens, refs, rows, *, done=None, 
     L = _lib or lib()
     on = _On(dev, stream)
     try:
-        if done is None:
-            done = on.empty((B,), i32)
-        ws, wp, wn = _scratch(on, workspace, L.cart_pages_workspace_size(B, M, N))
+        if done is None and workspace is None:  # one allocation for both
+            need = L.cart_pages_workspace_size(B, M, N)
+            ws = on.empty((need // 4 + B,), i32)
+            wp, wn, done = ws.data_ptr(), need, ws[need // 4:]
+        else:
+            if done is None:
+                done = on.empty((B,), i32)
+            ws, wp, wn = _scratch(on, workspace, L.cart_pages_workspace_size(B, M, N))
         rc = L.cart_pages_reserve(*args, _arg("done", done, i32, (B,), dev), wp, wn, on.handle)
     finally:
         on.close()
@@ -633,11 +638,14 @@ def cart_pages_compact(k_pages, v_pages, table, refs, *, moved=None, live=None, 
     L = _lib or lib()
     on = _On(dev, stream)
     try:
-        if moved is None:
-            moved = on.empty((N,), i32)
-        if live is None:
-            live = on.empty((1,), i32)
-        ws, wp, wn = _scratch(on, workspace, L.cart_pages_workspace_size(B, M, N))
+        if moved is None and live is None and workspace is None:  # one allocation for all
+            need = L.cart_pages_workspace_size(B, M, N)
+            ws = on.empty((need // 4 + N + 1,), i32)
+            wp, wn, moved, live = ws.data_ptr(), need, ws[need // 4:-1], ws[-1:]
+        else:
+            moved = on.empty((N,), i32) if moved is None else moved
+            live = on.empty((1,), i32) if live is None else live
+            ws, wp, wn = _scratch(on, workspace, L.cart_pages_workspace_size(B, M, N))
         rc = L.cart_pages_compact(*args, _arg("moved", moved, i32, (N,), dev),
                                   _arg("live", live, i32, (1,), dev), wp, wn, on.handle)
     finally:

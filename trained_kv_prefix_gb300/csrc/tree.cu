@@ -7,20 +7,20 @@
 //           node's queries rotated into the workspace, its rotated key and
 //           value written to its page row, its output set to 0 if unused.
 //           One more block writes the start of every conversation's work.
-//   attend  persistent, one CTA per SM: tcgen05 products over 128-key tiles.
+//   attend  persistent, one or two CTAs per SM: tcgen05 products over 128-key
+//           tiles.
 //   merge   joins the parts of rows whose keys more than one CTA walked.
 //
 // Work.  The query rows of conversation b and kv head g are r = t*G + hh (t
 // the node, hh the head of the group): R = nodes*G rows that see the same
-// cached keys.  A segment is up to 256 of them (two 128-row tiles) with the
-// key tiles they walk:
-//   fused    (R >= 256, or B == 1, or p == 0) cartridge tiles, then the
+// cached keys.  A segment is up to 128 of them, or 256 (two query tiles that
+// share the staged keys) where R is above 128, with the key tiles they walk:
+//   fused    (R near 256 or above, or B == 1, or p == 0) cartridge tiles, then the
 //            conversation's own rows, cached and new: one segment per
-//            (conversation, kv head, 256 rows).
-//   stacked  (else) the rows of all conversations, stacked 256 at a time,
-//            against the cartridge, so that it is read once for many of
-//            them; and one segment per (conversation, kv head) against its
-//            own rows.
+//            (conversation, kv head, 128 or 256 rows).
+//   stacked  (else) the rows of all conversations, stacked, against the
+//            cartridge, so that its tiles meet full query tiles; and one
+//            segment per (conversation, kv head) against its own rows.
 // New rows lie behind the cached ones in the same pages, so they share the
 // last tiles; a row's ancestor set masks them.
 //
@@ -63,13 +63,10 @@ struct TreeArgs {
   __nv_bfloat16* qr;        // [B, nodes, Hq, d] rotated queries
   NodeSet* set;             // [B, nodes]
   uint32_t* status;
-  // ---- schedule: query rows of one (conversation, kv head), rows of a
-  // segment against the stacked cartridge and against the conversation's own
-  // keys (128 or 256), segments of a (conversation, kv head)
-  int R, rt_c, rt_p, segs;
-  int stacked, joint;    // joint: one launch walks both kinds of segments
-  int n_ctas_c, n_ctas_p;  // CTAs of the launch that walks each kind
-  int which;             // of this launch: 1 cartridge segments, 2 own segments
+  // ---- schedule: query rows of one (conversation, kv head), most rows of a
+  // segment (128 or 256), segments of a (conversation, kv head)
+  int R, rt, segs;
+  int stacked, n_ctas;
   // the CTAs whose pieces hold tiles of each segment (see segment_span): the
   // stacked segments, then those of every (conversation, kv head)
   int2* spans;
@@ -115,12 +112,11 @@ __device__ __forceinline__ long long conv_units(const TreeArgs& a, int n) {
 
 // The schedule as every thread of a block needs it: the first unit of the
 // thread's conversations b0 .. b1 - 1 and the units they have, the stacked
-// segments' first cartridge tile and units, and the units of all
-// conversations.  In a joint launch the conversations' units follow the
-// cart_units of the stacked segments.
+// segments' first cartridge tile and units, which come first, and the number
+// of all units.
 struct Starts {
   int b0, b1, cart_lo;
-  long long start, mine, cart_units, own_units;
+  long long start, mine, cart_units, total;
 };
 template <int kThreads>
 struct StartsSmem {
@@ -162,10 +158,10 @@ __device__ __forceinline__ Starts scan_starts(const TreeArgs& a, StartsSmem<kThr
   __syncthreads();
   r.cart_lo = s.lo;
   const int n_c = n_ct - r.cart_lo;
-  const int stacks = (a.B * a.R + a.rt_c - 1) / a.rt_c;
+  const int stacks = (a.B * a.R + a.rt - 1) / a.rt;
   r.cart_units = a.stacked && n_c > 0 ? static_cast<long long>(n_c + kStartUnits) * stacks * a.Hkv : 0;
-  r.start = (a.joint ? r.cart_units : 0) + before + x - r.mine;
-  r.own_units = all;
+  r.start = r.cart_units + before + x - r.mine;
+  r.total = r.cart_units + all;
   return r;
 }
 
@@ -183,7 +179,7 @@ __device__ __forceinline__ Cut cut_segment(long long first, int tiles, long long
   return c;
 }
 
-// CTAs of a launch with runs of `chunk` units that hold tiles of a segment:
+// CTAs, with runs of `chunk` units, that hold tiles of a segment:
 // twice the first of them, plus 1 if its piece does not begin with its run,
 // and their number.
 __device__ __forceinline__ int2 segment_span(long long first, int tiles, long long chunk) {
@@ -195,31 +191,24 @@ __device__ __forceinline__ int2 segment_span(long long first, int tiles, long lo
   return make_int2(2 * lo + (lo * chunk < first), hi - lo + 1);
 }
 
-// Units per CTA of a launch.
-__device__ __forceinline__ long long run_units(const Starts& r, int which, int n_ctas) {
-  const long long total = ((which & 1) ? r.cart_units : 0) + ((which & 2) ? r.own_units : 0);
-  return (total + n_ctas - 1) / n_ctas;
-}
-
 // One block: the spans of all segments, for the merge.
 __device__ __forceinline__ void write_spans(const TreeArgs& a) {
   __shared__ StartsSmem<256> s;
-  for (int i = threadIdx.x; i < a.n_ctas_p; i += 256) a.cut[i] = -1;
+  for (int i = threadIdx.x; i < a.n_ctas; i += 256) a.cut[i] = -1;
   const Starts r = scan_starts<256>(a, s);  // (with barriers: the list is cleared)
-  const long long chunk_p = run_units(r, a.joint ? 3 : 2, a.n_ctas_p);
-  const int stacks = a.stacked ? (a.B * a.R + a.rt_c - 1) / a.rt_c * a.Hkv : 0;
+  const long long chunk = (r.total + a.n_ctas - 1) / a.n_ctas;
+  const int stacks = a.stacked ? (a.B * a.R + a.rt - 1) / a.rt * a.Hkv : 0;
   if (a.stacked) {
-    const long long chunk_c = a.joint ? chunk_p : run_units(r, 1, a.n_ctas_c);
     const int n_c = (a.p + kTile - 1) / kTile - r.cart_lo;
     for (int i = threadIdx.x; i < stacks; i += 256)
-      a.spans[i] = segment_span(static_cast<long long>(i) * (n_c + kStartUnits), n_c, chunk_c);
+      a.spans[i] = segment_span(static_cast<long long>(i) * (n_c + kStartUnits), n_c, chunk);
   }
   long long x = r.start;
   for (int b = r.b0; b < r.b1; ++b) {
     const int n = conv_tiles(a, b).n, per = a.Hkv * a.segs;
     int2* to = a.spans + stacks + static_cast<long long>(b) * per;
     for (int i = 0; i < per; ++i) {
-      const int2 span = segment_span(x, n, chunk_p);
+      const int2 span = segment_span(x, n, chunk);
       to[i] = span;
       if (span.y > 1) a.cut[span.x >> 1] = b * per + i;
       if (n > 0) x += n + kStartUnits;
@@ -369,8 +358,6 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
 // --------------------------------------------------------------- attend ----
 constexpr int kTreeMaxCtas = 320;  // bound of the workspace: two CTAs per SM
 constexpr int kAbsentRing = 8;
-// Stacked rows up to this many tiles of 128 go through the one-tile kernel.
-constexpr int kTreeOneTileStacks = 8;
 
 // NT query tiles of 128 rows per CTA, each with a warpgroup of its own; they
 // share the staged keys.  NT = 2 (one CTA per SM) loads keys once for 256
@@ -472,8 +459,8 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o)
       o.own = 0;
       o.b = 0;
       o.g = seg % a.Hkv;
-      o.row0 = seg / a.Hkv * a.rt_c;
-      o.rows = min(a.B * a.R - o.row0, a.rt_c);
+      o.row0 = seg / a.Hkv * a.rt;
+      o.rows = min(a.B * a.R - o.row0, a.rt);
       o.len = 0;
       o.n_cart = w.n_cart_all;
       o.cart_lo = w.cart_lo;
@@ -503,8 +490,8 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o)
     o.own = 1;
     o.b = w.b;
     o.g = seg / a.segs;
-    o.row0 = w.b * a.R + part * a.rt_p;
-    o.rows = min(a.R - part * a.rt_p, a.rt_p);
+    o.row0 = w.b * a.R + part * a.rt;
+    o.rows = min(a.R - part * a.rt, a.rt);
     o.len = w.c.len;
     o.n_cart = w.c.n_cart;
     o.cart_lo = w.c.first_cart;
@@ -600,12 +587,11 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
   // ---- this CTA's run (the lengths are not the prep kernel's: it may still
   // be running)
   const Starts st = scan_starts<L::kThreads>(a, sh.scan);
-  const long long total = ((a.which & 1) ? st.cart_units : 0) + ((a.which & 2) ? st.own_units : 0);
-  const long long chunk = run_units(st, a.which, gridDim.x);
+  const long long chunk = (st.total + a.n_ctas - 1) / a.n_ctas;
   Walk walk;
-  walk.lo = walk.x = min(chunk * blockIdx.x, total);
-  walk.hi = min(walk.lo + chunk, total);
-  walk.cart_units = (a.which & 1) ? st.cart_units : 0;
+  walk.lo = walk.x = min(chunk * blockIdx.x, st.total);
+  walk.hi = min(walk.lo + chunk, st.total);
+  walk.cart_units = st.cart_units;
   walk.cart_lo = st.cart_lo;
   walk.n_cart_all = (a.p + kTile - 1) / kTile - st.cart_lo;
   walk.cta = blockIdx.x;
@@ -1055,7 +1041,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
                      << 32 |
                  *reinterpret_cast<volatile unsigned*>(&sp.bad[0]));
       if (live_rows) {
-        const int rows_cap = own ? min(a.R, a.rt_p) : min(a.B * a.R, a.rt_c);
+        const int rows_cap = own ? min(a.R, a.rt) : min(a.B * a.R, a.rt);
         const long long part0 =
             slot < 0 ? 0 : static_cast<long long>(slot) * rows_cap + (local - lane);
         float* const part = own ? a.part_p : a.part_c;
@@ -1167,7 +1153,7 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   const int id_p = a.stacked ? blockIdx.x : __ldcg(a.cut + blockIdx.x);
   if (id_p < 0) return;
   const int b = id_p / (a.Hkv * a.segs), g = id_p / a.segs % a.Hkv, G = a.Hq / a.Hkv;
-  const int base = id_p % a.segs * a.rt_p + blockIdx.y * 32;
+  const int base = id_p % a.segs * a.rt + blockIdx.y * 32;
   if (base >= a.R) return;
   const int groups = min(8, (a.R - base + 3) >> 2);
   const int slices = groups > 4 ? 1 : groups > 2 ? 2 : groups > 1 ? 4 : 8;
@@ -1175,8 +1161,8 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   // lane: part lane & 7 (of eight at a time) of row r0 + lane / 8
   const int mine = r0 + (lane >> 3);
   const int gr = b * a.R + mine;
-  const int id_c = gr / a.rt_c * a.Hkv + g;
-  const int stacks = a.stacked ? (a.B * a.R + a.rt_c - 1) / a.rt_c * a.Hkv : 0;
+  const int id_c = gr / a.rt * a.Hkv + g;
+  const int stacks = a.stacked ? (a.B * a.R + a.rt - 1) / a.rt * a.Hkv : 0;
   const bool row_ok = slice < slices && mine < a.R;
   const int2 sp = __ldcg(a.spans + stacks + id_p);
   int2 sc = make_int2(0, 0);
@@ -1186,12 +1172,12 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   if (sp.y == 0) return;  // idle
   const int n = anc ? sc.y + sp.y : 0;
   // row of part i of the lane's row in part_c, or ~ of it in part_p
-  const int rows_c = min(a.B * a.R, a.rt_c), rows_p = min(a.R, a.rt_p);
+  const int rows_c = min(a.B * a.R, a.rt), rows_p = min(a.R, a.rt);
   auto locate = [&](int i) {
-    if (i < sc.y) return (id_c + (sc.x >> 1) + i) * rows_c + gr % a.rt_c;
+    if (i < sc.y) return (id_c + (sc.x >> 1) + i) * rows_c + gr % a.rt;
     i -= sc.y;
     const int slot = a.stacked ? id_p + (sp.x >> 1) + i : i ? 2 * ((sp.x >> 1) + i) : sp.x;
-    return ~(slot * rows_p + mine % a.rt_p);
+    return ~(slot * rows_p + mine % a.rt);
   };
   auto lse_of = [&](int at) { return __ldcg(at >= 0 ? a.lse_c + at : a.lse_p + ~at); };
   const int n_max = __reduce_max_sync(0xffffffffu, n);
@@ -1270,7 +1256,7 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
 // ------------------------------------------------------------- workspace ----
 struct TreeWs {
   size_t qr, set, spans, cut, part_c, part_p, lse_c, lse_p, total;
-  int R, rt_c, rt_p, segs, stacked, joint;
+  int R, rt, segs, stacked;
 };
 
 TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
@@ -1283,26 +1269,30 @@ TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
   };
   const size_t n = static_cast<size_t>(B) * nodes;
   w.R = nodes * (Hq / Hkv);
-  // Stacking reads the cartridge once for the rows of several conversations;
-  // with 256 rows of one conversation nothing is left to stack, and joining
-  // the two kinds of segments would only cost.
-  w.stacked = p > 0 && B > 1 && w.R < 2 * kTile;
-  w.rt_p = w.R > kTile ? 2 * kTile : kTile;
-  w.rt_c = static_cast<long long>(B) * w.R > kTile * kTreeOneTileStacks ? 2 * kTile : w.rt_p;
-  w.segs = (w.R + w.rt_p - 1) / w.rt_p;
-  w.joint = w.rt_c == w.rt_p;
+  // Stacking fills the query tiles that walk the cartridge with rows of
+  // several conversations, but its segments have to be joined with those of
+  // the own rows; near 256 rows there is little left to fill.  64
+  // conversations behind 4096 rows, stacked against fused: R = 132 208 us
+  // against 234, R = 160 226 against 238, R = 192 257 against 247, R = 224 296
+  // against 252.
+  w.stacked = p > 0 && B > 1 && 4 * w.R < 3 * 2 * kTile;
+  // Up to 128 rows: one query tile per CTA and two CTAs per SM, so that one
+  // covers the other's starts and ends, although the cartridge is then staged
+  // twice as often (24 nodes, G = 4, 8192 rows: 210 us against 219 with two
+  // tiles per CTA).  Above: two tiles that share the keys (64 nodes: 252
+  // against 270 us; 25 nodes, G = 8, 49k rows: 135 against 164).
+  w.rt = w.R > kTile ? 2 * kTile : kTile;
+  w.segs = (w.R + w.rt - 1) / w.rt;
   w.qr = take(n * Hq * d * 2);
   w.set = take(n * sizeof(NodeSet));
   // partial outputs: a slot per segment and cut, or two per run
-  const size_t rows_p = std::min(w.R, w.rt_p);
-  const size_t ctas_p = w.rt_p > kTile ? kTreeMaxCtas / 2 : kTreeMaxCtas;
-  const size_t ctas_c = w.rt_c > kTile ? kTreeMaxCtas / 2 : kTreeMaxCtas;
-  const size_t slots_p =
-      w.stacked ? static_cast<size_t>(B) * Hkv * w.segs + ctas_p : 2 * ctas_p;
+  const size_t ctas = w.rt > kTile ? kTreeMaxCtas / 2 : kTreeMaxCtas;
+  const size_t rows_p = std::min(w.R, w.rt);
+  const size_t slots_p = w.stacked ? static_cast<size_t>(B) * Hkv * w.segs + ctas : 2 * ctas;
   const size_t all = static_cast<size_t>(B) * w.R;
-  const size_t rows_c = w.stacked ? std::min<size_t>(all, w.rt_c) : 0;
-  const size_t stacks = w.stacked ? (all + w.rt_c - 1) / w.rt_c * Hkv : 0;
-  const size_t slots_c = w.stacked ? stacks + ctas_c : 0;
+  const size_t rows_c = w.stacked ? std::min<size_t>(all, w.rt) : 0;
+  const size_t stacks = w.stacked ? (all + w.rt - 1) / w.rt * Hkv : 0;
+  const size_t slots_c = w.stacked ? stacks + ctas : 0;
   w.spans = take((stacks + static_cast<size_t>(B) * Hkv * w.segs) * 8);
   w.cut = take(kTreeMaxCtas * 4);
   w.part_c = take(slots_c * rows_c * d * 4);
@@ -1332,12 +1322,11 @@ struct TreeMaps {
 };
 
 template <int D, int NT>
-cudaError_t launch_attend(TreeArgs a, int which, const TreeMaps& m, int ctas, cudaStream_t st) {
+cudaError_t launch_attend(const TreeArgs& a, const TreeMaps& m, cudaStream_t st) {
   using L = TreeLayout<D, NT>;
   const cudaError_t e = set_smem_once<tree_attend_kernel<D, NT>>(L::kBytes);
   if (e != cudaSuccess) return e;
-  a.which = which;
-  return launch_dependent(tree_attend_kernel<D, NT>, dim3(ctas), dim3(L::kThreads), L::kBytes, st,
+  return launch_dependent(tree_attend_kernel<D, NT>, dim3(a.n_ctas), dim3(L::kThreads), L::kBytes, st,
                           m.q, m.kc, m.vc, m.kp, m.vp, a);
 }
 
@@ -1345,9 +1334,7 @@ template <int D>
 cudaError_t launch_tree(TreeArgs a, const Turns& turns, cudaStream_t st) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorInvalidValue;
-  const int one = std::min(sms, kTreeMaxCtas / 2), two = 2 * one;  // CTAs with NT = 2, 1
-  a.n_ctas_c = a.rt_c > kTile ? one : two;
-  a.n_ctas_p = a.rt_p > kTile ? one : two;
+  a.n_ctas = std::min(sms, kTreeMaxCtas / 2) * (a.rt > kTile ? 1 : 2);
   // rotated queries [B*nodes, Hkv, G, d] as (d, G, Hkv, B*nodes): a
   // (64, G, 1, 32/G) box is 32 rows of one kv head; pools as (d, Hkv,
   // page_rows, n_pages), a box one page of one kv head
@@ -1377,17 +1364,11 @@ cudaError_t launch_tree(TreeArgs a, const Turns& turns, cudaStream_t st) {
   tree_prep_kernel<D><<<prep_blocks + 1, 256, 0, st>>>(a, turns, per);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (a.stacked && !a.joint) {
-    e = launch_attend<D, 2>(a, 1, m, a.n_ctas_c, st);
-    if (e != cudaSuccess) return e;
-  }
-  const int which = a.stacked && a.joint ? 3 : 2;
-  e = a.rt_p > kTile ? launch_attend<D, 2>(a, which, m, a.n_ctas_p, st)
-                     : launch_attend<D, 1>(a, which, m, a.n_ctas_p, st);
+  e = a.rt > kTile ? launch_attend<D, 2>(a, m, st) : launch_attend<D, 1>(a, m, st);
   if (e != cudaSuccess) return e;
   return launch_dependent(tree_merge_kernel<D>,
-                          dim3(a.stacked ? a.B * a.Hkv * a.segs : a.n_ctas_p,
-                               (std::min(a.R, a.rt_p) + 31) / 32),
+                          dim3(a.stacked ? a.B * a.Hkv * a.segs : a.n_ctas,
+                               (std::min(a.R, a.rt) + 31) / 32),
                           dim3(256), 0, st, a);
 }
 
@@ -1446,11 +1427,9 @@ int cart_attn_decode_tree(int B, int nodes, int window, int Hq, int Hkv, int d, 
   a.qr = reinterpret_cast<__nv_bfloat16*>(ws + w.qr);
   a.set = reinterpret_cast<NodeSet*>(ws + w.set);
   a.R = w.R;
-  a.rt_c = w.rt_c;
-  a.rt_p = w.rt_p;
+  a.rt = w.rt;
   a.segs = w.segs;
   a.stacked = w.stacked;
-  a.joint = w.joint;
   a.spans = reinterpret_cast<int2*>(ws + w.spans);
   a.cut = reinterpret_cast<int*>(ws + w.cut);
   a.part_c = reinterpret_cast<float*>(ws + w.part_c);
