@@ -257,7 +257,7 @@ __device__ __forceinline__ void rotate8(uint4& x, uint4& y, const float2* c, int
 // conversation.  Bound by latency for a few nodes (lengths, pages, parents
 // and the rows are loaded side by side) and by HBM for many.
 template <int D>
-__global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ TreeArgs a,
+__global__ void __launch_bounds__(256, 4) tree_prep_kernel(const __grid_constant__ TreeArgs a,
                                                         const __grid_constant__ Turns f, int per) {
   using S = PrepShape<D>;
   constexpr int HALF = D / 2;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
                                : a.v_new + (bt * a.Hkv + h - a.Hq - a.Hkv) * D) + e0;
   };
   uint4 lo[S::kBatch], hi[S::kBatch];
-  auto load = [&](int i0) {
+  auto load = [&](int i0, uint4 (&lo)[S::kBatch], uint4 (&hi)[S::kBatch]) {
 #pragma unroll
     for (int k = 0; k < S::kBatch; ++k) {
       const int i = i0 + k * 8 * S::kRows;
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
       hi[k] = __ldg(reinterpret_cast<const uint4*>(x + HALF));
     }
   };
-  load(warp * S::kRows + sub);  // before the tree is known
+  load(warp * S::kRows + sub, lo, hi);  // before the tree is known
   const int len = held_rows(a.pt, b);
   const int node = threadIdx.x;
   const int page = len >= 0 && node < a.nodes ? page_of(a.pt, b, len + node) : -1;
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const __grid_constant__ 
   }
   __syncthreads();
   for (int i0 = warp * S::kRows + sub; i0 - sub < rows; i0 += 8 * S::kRows * S::kBatch) {
-    if (i0 >= 8 * S::kRows) load(i0);
+    if (i0 >= 8 * S::kRows) load(i0, lo, hi);
 #pragma unroll
     for (int k = 0; k < S::kBatch; ++k) {
       const int i = i0 + k * 8 * S::kRows;
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
   walk.cta = blockIdx.x;
   if (walk.lo >= walk.hi) {
     pdl_release();
-    pdl_wait();  // this grid's end implies the end of those before it
+    pdl_wait();  // this grid's end implies the prep kernel's
     return;
   }
   {
@@ -885,9 +885,8 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
         if (lane == 0) mbar_arrive(&bars[kTPieceEmpty0 + (it & 1)]);
         continue;
       }
-      const int own = vld(sp.own), len = vld(sp.len), b = vld(sp.b);
-      const int ring = vld(sp.ring), n_cart = vld(sp.n_cart), t0 = vld(sp.t0);
-      const int cart_lo = vld(sp.cart_lo), row_lo = vld(sp.row_lo);
+      // (the piece's fields are read where they are used, so that none takes a
+      // register across the tile loop)
       // this thread's query row
       const int local = x * kTile + row;
       bool live = local < vld(sp.rows);
@@ -900,27 +899,37 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
         vis = __ldcg(&a.set[bt].vis);
         live = anc != 0;
         if (a.window > 0)
-          first = a.p + (own ? len : held_rows(a.pt, bt / a.nodes)) + __popcll(anc) - a.window;
+          first = a.p + (vld(sp.own) ? vld(sp.len) : held_rows(a.pt, bt / a.nodes)) +
+                  __popcll(anc) - a.window;
       }
       const unsigned live_rows = __ballot_sync(0xffffffffu, live);
-      const int lo_row = a.window > 0 ? len - a.window + 1 : 0;  // of the shallowest node
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < n && ok; ++t) {
-        const int ta = t0 + t, gt = ring + t;
-        const bool cart = ta < n_cart;
-        const int k0 = cart ? (cart_lo + ta) * kTile : (row_lo + ta - n_cart) * kTile;
-        const bool clean = !cart && (k0 + kTile > len || k0 < lo_row);
+        // the tile's first key (a cartridge row or an own row), the keys before
+        // `end` and from `from` on, and pages that are not there
+        const int ta = vld(sp.t0) + t - vld(sp.n_cart);
+        const bool cart = ta < 0;
+        const int k0 = cart ? (vld(sp.cart_lo) + vld(sp.t0) + t) * kTile
+                            : (vld(sp.row_lo) + ta) * kTile;
+        const int end = (cart ? a.p : vld(sp.len)) - k0;
+        const int from = first - (cart ? k0 : a.p + k0);
+        // (from the shallowest node's first row on)
+        const bool clean =
+            !cart && (end < kTile || (a.window > 0 && k0 < vld(sp.len) - a.window + 1));
         VRow kind = kVKeep;
-        if (clean) kind = v_row_kind(a, b, k0 + row, lo_row, len);
+        if (clean)
+          kind = v_row_kind(a, vld(sp.b), k0 + row,
+                            a.window > 0 ? vld(sp.len) - a.window + 1 : 0, vld(sp.len));
         ok = wait(&bars[kTSFull0 + x], nS & 1, kDevErrTimeoutSoftmax);
         if (!ok) break;
         ++nS;
         tc_fence_after();
         if (clean) {
+          const int gt = vld(sp.ring) + t;
           ok = wait(&bars[kTVFull0 + gt % kS], (gt / kS) & 1, kDevErrTimeoutSoftmax);
           if (!ok) break;
-          clean_v_row<D>(smem_u32(smem + L::kV + gt % kS * L::kTileBytes), row, kind,
-                         k0 + row - len, sp.bad);
+          clean_v_row<D>(smem_u32(smem + L::kV + gt % kS * L::kTileBytes), row, kind, row - end,
+                         sp.bad);
           fence_proxy_async_smem();
         }
         if (live_rows) {
@@ -934,12 +943,10 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
           tmem_reg_fence(r[1]);
           tmem_reg_fence(r[2]);
           tmem_reg_fence(r[3]);
-          // keys of the tile before `end` and from `from` on, on pages that
-          // are there, and new rows by the node's set
-          const int end = (cart ? a.p : len) - k0;
-          const int from = first - (cart ? k0 : a.p + k0);
           const unsigned gone =
-              cart ? 0u : *reinterpret_cast<volatile unsigned*>(&sh.absent[gt % kAbsentRing]);
+              cart ? 0u
+                   : *reinterpret_cast<volatile unsigned*>(
+                         &sh.absent[(vld(sp.ring) + t) % kAbsentRing]);
           if (__any_sync(0xffffffffu, end < kTile || from > 0 || gone)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -1034,7 +1041,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
       ++nO;
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int slot = vld(sp.slot), g = vld(sp.g);
+      const int slot = vld(sp.slot), g = vld(sp.g), own = vld(sp.own), b = vld(sp.b);
       // new rows that this one sees and whose value is not finite
       const unsigned long long bad =
           vis & (static_cast<unsigned long long>(*reinterpret_cast<volatile unsigned*>(&sp.bad[1]))
@@ -1149,7 +1156,8 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   using Vec = std::conditional_t<E == 4, float4, float2>;
   __shared__ float s_num[8][4][D], s_den[8][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
+  // (the lists and sets are the prep kernel's, which had ended before any CTA
+  // of the attend kernel let this one start)
   const int id_p = a.stacked ? blockIdx.x : __ldcg(a.cut + blockIdx.x);
   if (id_p < 0) return;
   const int b = id_p / (a.Hkv * a.segs), g = id_p / a.segs % a.Hkv, G = a.Hq / a.Hkv;
@@ -1170,6 +1178,7 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   unsigned long long anc = 0;
   if (row_ok) anc = __ldcg(&a.set[b * a.nodes + mine / G].anc);
   if (sp.y == 0) return;  // idle
+  pdl_wait();
   const int n = anc ? sc.y + sp.y : 0;
   // row of part i of the lane's row in part_c, or ~ of it in part_p
   const int rows_c = min(a.B * a.R, a.rt), rows_p = min(a.R, a.rt);
