@@ -46,7 +46,7 @@ def make_tree(seed, B, nodes, Hq, Hkv, d, p, lens, P, kind="random", spare_pages
     lens = np.asarray(lens, np.int32)
     assert lens.shape == (B,)
     M = max(1, -(-(int(lens.max(initial=0)) + nodes) // P)) + 1
-    need = [max(0, -(-(max(int(n), 0) + nodes) // P)) for n in lens]
+    need = [-(-(max(int(n), 0) + nodes) // P) for n in lens]
     N = sum(need) + spare_pages
     ids, table, at = rng.permutation(N), np.full((B, M), -1, np.int32), 0
     for b in range(B):
@@ -226,6 +226,14 @@ def test_tree_visible_infinities_reach_the_nodes_that_see_them():
     want[0, [1, 2], :, 5] = float("inf")
     want[0, [4, 5], :, 7] = float("nan")
     torch.testing.assert_close(o, want, rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("p,nodes", [(70, 1), (0, 2), (130, 3)])
+def test_tree_many_conversations(p, nodes):
+    """More conversations than the schedule's blocks have threads."""
+    B = 530 if nodes == 1 else 300
+    lens = np.random.default_rng(B).integers(-1, 60, B)
+    check_tree(*make_tree(24 + nodes, B, nodes, 2, 1, 64, p, lens, 16, "random"))
 
 
 def test_tree_large_logits():

@@ -179,13 +179,19 @@ __device__ __forceinline__ Cut cut_segment(long long first, int tiles, long long
   return c;
 }
 
+// x / y for x >= 0, y > 0; the 64-bit division takes several times as long as
+// the 32-bit one that nearly every schedule gets by with.
+__device__ __forceinline__ long long div_units(long long x, long long y) {
+  return ((x | y) >> 31) == 0 ? static_cast<unsigned>(x) / static_cast<unsigned>(y) : x / y;
+}
+
 // CTAs, with runs of `chunk` units, that hold tiles of a segment:
 // twice the first of them, plus 1 if its piece does not begin with its run,
 // and their number.
 __device__ __forceinline__ int2 segment_span(long long first, int tiles, long long chunk) {
   if (tiles <= 0) return make_int2(0, 0);
-  int lo = static_cast<int>(first / chunk);
-  const int hi = static_cast<int>((first + tiles + kStartUnits - 1) / chunk);
+  int lo = static_cast<int>(div_units(first, chunk));
+  const int hi = static_cast<int>(div_units(first + tiles + kStartUnits - 1, chunk));
   // (runs may hold the segment's start alone, without a tile)
   while (cut_segment(first, tiles, lo * chunk, (lo + 1) * chunk).n <= 0) ++lo;
   return make_int2(2 * lo + (lo * chunk < first), hi - lo + 1);
@@ -196,23 +202,40 @@ __device__ __forceinline__ void write_spans(const TreeArgs& a) {
   __shared__ StartsSmem<256> s;
   for (int i = threadIdx.x; i < a.n_ctas; i += 256) a.cut[i] = -1;
   const Starts r = scan_starts<256>(a, s);  // (with barriers: the list is cleared)
-  const long long chunk = (r.total + a.n_ctas - 1) / a.n_ctas;
+  const long long chunk = div_units(r.total + a.n_ctas - 1, a.n_ctas);
   const int stacks = a.stacked ? (a.B * a.R + a.rt - 1) / a.rt * a.Hkv : 0;
   if (a.stacked) {
     const int n_c = (a.p + kTile - 1) / kTile - r.cart_lo;
     for (int i = threadIdx.x; i < stacks; i += 256)
       a.spans[i] = segment_span(static_cast<long long>(i) * (n_c + kStartUnits), n_c, chunk);
   }
+  // own segments, by threads over all of them (their conversations' starts
+  // through shared memory, 256 conversations at a time)
+  __shared__ long long start[256];
+  __shared__ int tiles[256];
+  const int per = a.Hkv * a.segs;
+  const int rounds = (a.B + 255) / 256;  // conversations per thread of the scan
   long long x = r.start;
-  for (int b = r.b0; b < r.b1; ++b) {
-    const int n = conv_tiles(a, b).n, per = a.Hkv * a.segs;
-    int2* to = a.spans + stacks + static_cast<long long>(b) * per;
-    for (int i = 0; i < per; ++i) {
-      const int2 span = segment_span(x, n, chunk);
-      to[i] = span;
-      if (span.y > 1) a.cut[span.x >> 1] = b * per + i;
-      if (n > 0) x += n + kStartUnits;
+  for (int k = 0; k < rounds; ++k) {
+    const int b = r.b0 + k;
+    if (b < r.b1) {
+      tiles[threadIdx.x] = conv_tiles(a, b).n;
+      start[threadIdx.x] = x;
+      x += conv_units(a, tiles[threadIdx.x]);
+    } else {
+      tiles[threadIdx.x] = -1;  // no conversation
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 256 * per; i += 256) {
+      const int t = i / per, n = tiles[t];
+      if (n < 0) continue;
+      const int seg = i % per, id = (t * rounds + k) * per + seg;
+      const int2 span =
+          segment_span(start[t] + static_cast<long long>(seg) * (n + kStartUnits), n, chunk);
+      a.spans[stacks + id] = span;
+      if (span.y > 1) a.cut[span.x >> 1] = id;
+    }
+    __syncthreads();
   }
 }
 
@@ -451,7 +474,7 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o)
   while (w.x < w.hi) {
     if (w.x < w.cart_units) {
       const int v = w.n_cart_all + kStartUnits;
-      const int seg = static_cast<int>(w.x / v);
+      const int seg = static_cast<int>(div_units(w.x, v));
       const long long first = static_cast<long long>(seg) * v;
       const Cut k = cut_segment(first, w.n_cart_all, w.x, w.hi);
       w.x = min(first + v, w.hi);
@@ -479,7 +502,8 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o)
       w.off = 0;
     }
     const int v = w.c.n + kStartUnits;
-    const int seg = static_cast<int>(w.off / v), in = static_cast<int>(w.off % v);
+    const int seg = static_cast<int>(div_units(w.off, v));
+    const int in = static_cast<int>(w.off - static_cast<long long>(seg) * v);
     const Cut k = cut_segment(w.x - in, w.c.n, w.x, w.hi);
     const bool at_lo = w.x == w.lo;
     const long long step = min(static_cast<long long>(v - in), w.hi - w.x);
@@ -587,7 +611,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
   // ---- this CTA's run (the lengths are not the prep kernel's: it may still
   // be running)
   const Starts st = scan_starts<L::kThreads>(a, sh.scan);
-  const long long chunk = (st.total + a.n_ctas - 1) / a.n_ctas;
+  const long long chunk = div_units(st.total + a.n_ctas - 1, a.n_ctas);
   Walk walk;
   walk.lo = walk.x = min(chunk * blockIdx.x, st.total);
   walk.hi = min(walk.lo + chunk, st.total);
