@@ -9,6 +9,7 @@ implementation to fall back to.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -493,6 +494,7 @@ def _pools(k_pages, v_pages):
             _arg("k_pages", k_pages, dt, shape, dev), _arg("v_pages", v_pages, dt, shape, dev), dev)
 
 
+@functools.lru_cache(maxsize=1024)  # (a function of the sizes alone; the call costs 2 us)
 def decode_tree_workspace_size(B, nodes, Hq, Hkv, d, p, page_rows, max_pages) -> int:
     return int(lib().cart_attn_decode_tree_workspace_size(B, nodes, Hq, Hkv, d, p, page_rows,
                                                           max_pages))
@@ -522,22 +524,25 @@ def cart_attn_decode_tree(q, k_new, v_new, kc, vc, k_pages, v_pages, table, lens
             _arg("table", table, i32, (B, M), dev), M,
             _arg("lens", lens, i32, (B,), dev),
             None if parents is None else _arg("parents", parents, i32, (B, T), dev))
-    L = _lib or lib()
     on = _On(dev, stream)
     try:
         if o is None:
             o = torch.empty_like(q) if on.stream is None else on.empty(q.shape, bf)
-        ws, wp, wn = _scratch(on, workspace, L.cart_attn_decode_tree_workspace_size(
-            B, T, Hq, Hkv, d, p, P, M))
-        rc = L.cart_attn_decode_tree(
-            B, T, window, Hq, Hkv, d, p, d ** -0.5 if scale is None else scale, theta, *args,
-            _arg("o", o, bf, q.shape, dev), wp, wn, on.handle)
+            op = o.data_ptr()
+        else:
+            op = _arg("o", o, bf, q.shape, dev)
+        ws, wp, wn = _scratch(on, workspace,
+                              decode_tree_workspace_size(B, T, Hq, Hkv, d, p, P, M))
+        rc = (_lib or lib()).cart_attn_decode_tree(
+            B, T, window, Hq, Hkv, d, p, d ** -0.5 if scale is None else scale, theta, *args, op,
+            wp, wn, on.handle)
     finally:
         on.close()
     _check("cart_attn_decode_tree", rc)
     return o
 
 
+@functools.lru_cache(maxsize=1024)
 def pages_workspace_size(B, max_pages, n_pages) -> int:
     return int(lib().cart_pages_workspace_size(B, max_pages, n_pages))
 
@@ -581,18 +586,13 @@ def cart_pages_reserve(k_pages, v_pages, table, lens, refs, rows, *, done=None, 
     args = (B, layers, Hkv, d, dt, kp, vp, N, P, _arg("table", table, i32, (B, M), dev), M,
             _arg("lens", lens, i32, (B,), dev), _arg("refs", refs, i32, (N,), dev),
             _arg("rows", rows, i32, (B,), dev))
-    L = _lib or lib()
     on = _On(dev, stream)
     try:
-        if done is None and workspace is None:  # one allocation for both
-            need = L.cart_pages_workspace_size(B, M, N)
-            ws = on.empty((need // 4 + B,), i32)
-            wp, wn, done = ws.data_ptr(), need, ws[need // 4:]
-        else:
-            if done is None:
-                done = on.empty((B,), i32)
-            ws, wp, wn = _scratch(on, workspace, L.cart_pages_workspace_size(B, M, N))
-        rc = L.cart_pages_reserve(*args, _arg("done", done, i32, (B,), dev), wp, wn, on.handle)
+        if done is None:
+            done = on.empty((B,), i32)
+        ws, wp, wn = _scratch(on, workspace, pages_workspace_size(B, M, N))
+        rc = (_lib or lib()).cart_pages_reserve(*args, _arg("done", done, i32, (B,), dev), wp, wn,
+                                                on.handle)
     finally:
         on.close()
     _check("cart_pages_reserve", rc)
@@ -635,19 +635,16 @@ def cart_pages_compact(k_pages, v_pages, table, refs, *, moved=None, live=None, 
     i32 = torch.int32
     args = (B, layers, Hkv, d, dt, kp, vp, N, P, _arg("table", table, i32, (B, M), dev), M,
             _arg("refs", refs, i32, (N,), dev))
-    L = _lib or lib()
     on = _On(dev, stream)
     try:
-        if moved is None and live is None and workspace is None:  # one allocation for all
-            need = L.cart_pages_workspace_size(B, M, N)
-            ws = on.empty((need // 4 + N + 1,), i32)
-            wp, wn, moved, live = ws.data_ptr(), need, ws[need // 4:-1], ws[-1:]
-        else:
-            moved = on.empty((N,), i32) if moved is None else moved
-            live = on.empty((1,), i32) if live is None else live
-            ws, wp, wn = _scratch(on, workspace, L.cart_pages_workspace_size(B, M, N))
-        rc = L.cart_pages_compact(*args, _arg("moved", moved, i32, (N,), dev),
-                                  _arg("live", live, i32, (1,), dev), wp, wn, on.handle)
+        if moved is None:
+            moved = on.empty((N,), i32)
+        if live is None:
+            live = on.empty((1,), i32)
+        ws, wp, wn = _scratch(on, workspace, pages_workspace_size(B, M, N))
+        rc = (_lib or lib()).cart_pages_compact(*args, _arg("moved", moved, i32, (N,), dev),
+                                                _arg("live", live, i32, (1,), dev), wp, wn,
+                                                on.handle)
     finally:
         on.close()
     _check("cart_pages_compact", rc)
