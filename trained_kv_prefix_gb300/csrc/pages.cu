@@ -28,7 +28,7 @@ constexpr int kMaxForks = 8192;
 
 // Workspace of reserve and compact (int32 words): the head, then the lists.
 struct PagesWs {
-  size_t count, base, ids, slots, copies, total;  // byte offsets
+  size_t count, base, ids, slots, copies, starts, total;  // byte offsets
 };
 enum { kHeadSeg = 0, kHeadCopies = 16, kHeadFirst = 17, kHeadInts = 64 };
 
@@ -45,6 +45,7 @@ PagesWs pages_ws(int B, int n_pages) {
   w.ids = take(static_cast<size_t>(n_pages) * 4);
   w.slots = take(static_cast<size_t>(n_pages) * 4);
   w.copies = take(static_cast<size_t>(std::max(B, n_pages)) * 16);
+  w.starts = take((static_cast<size_t>(B) + 1) * 8);
   w.total = off;
   return w;
 }
@@ -129,6 +130,14 @@ __global__ void __launch_bounds__(256) fork_kernel(int B, int* table, int max_pa
   }
 }
 
+// Copies go by chunks of 16 KB: 256 threads with four 16-byte loads each.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyLoads = 4;
+constexpr int kChunk = kCopyThreads * kCopyLoads * 16;
+__host__ __device__ __forceinline__ int chunks_of(int rows, int row_bytes) {
+  return static_cast<int>((static_cast<long long>(rows) * row_bytes + kChunk - 1) / kChunk);
+}
+
 // -------------------------------------------------------------- reserve ----
 struct ReserveArgs {
   int B, max_pages, n_pages, page_log2;
@@ -136,6 +145,8 @@ struct ReserveArgs {
   const int* rows;
   int *head, *count, *base, *free;
   int4* copies;  // [B]: (from page, to page, rows); rows 0: none
+  long long* starts;  // [B + 1]: chunks of one layer and pool before each copy
+  int row_bytes;
 };
 
 // Conversation b's request: whether it asks, its first page to be written
@@ -182,7 +193,7 @@ __global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads
   for (int b = gw; b < a.B; b += kMetaWarps) {
     const Request q = request(a, b);
     int* row = a.table + static_cast<long long>(b) * a.max_pages;
-    int n = 0;
+    int n = 0, part_rows = 0;
     for (int k0 = q.first; k0 < q.end; k0 += 32) {
       const int k = k0 + lane;
       bool need = false;
@@ -191,10 +202,14 @@ __global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads
         const bool held = is_page(page, a.n_pages);
         need = !held || __ldcg(a.refs + page) > 1;
         if (need) row[k] = held ? mark_shared(page) : -1;
+        if (need && held && k == q.first) part_rows = q.len & ((1 << a.page_log2) - 1);
       }
       n += __popc(__ballot_sync(0xffffffffu, need));
     }
-    if (lane == 0) a.count[b] = n;
+    if (lane == 0) {  // (page q.first is lane 0's)
+      a.count[b] = n;
+      a.copies[b].z = part_rows;
+    }
   }
   const int part = (a.n_pages + kMetaCtas - 1) / kMetaCtas;
   const int lo = rank * part, hi = min(lo + part, a.n_pages);
@@ -203,8 +218,8 @@ __global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads
   block_scan(mine, sums, &n_part);
   if (threadIdx.x == 0) a.head[kHeadSeg + rank] = n_part;
   cluster_sync();
-  // ---- free pages in order (every CTA its part), and the running need
-  // over conversations (CTA 0)
+  // ---- free pages in order (every CTA its part), and over conversations the
+  // running need and the chunks to copy (CTA 0)
   int before = 0, n_free = 0;
   for (int r = 0; r < kMetaCtas; ++r) {
     const int n = __ldcg(a.head + kHeadSeg + r);
@@ -220,14 +235,24 @@ __global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads
     before += n;
   }
   if (rank == 0) {
-    long long run = 0;  // saturates above any pool
+    long long run = 0, chunks = 0;  // run saturates above any pool
     for (int b0 = 0; b0 < a.B; b0 += kMetaThreads) {
       const int b = b0 + threadIdx.x;
+      const int need = b < a.B ? __ldcg(a.count + b) : 0;
+      const int rows = b < a.B ? __ldcg(&a.copies[b].z) : 0;
       int n;
-      const int at = block_scan(b < a.B ? __ldcg(a.count + b) : 0, sums, &n);
-      if (b < a.B) a.base[b] = static_cast<int>(min(run + at, 0x40000000ll));
+      const int base = static_cast<int>(min(run + block_scan(need, sums, &n), 0x40000000ll));
       run += n;
+      // (a conversation that finds too few pages copies nothing)
+      const int c = base + need <= n_free ? chunks_of(rows, a.row_bytes) : 0;
+      const int at = block_scan(c, sums, &n);
+      if (b < a.B) {
+        a.base[b] = base;
+        a.starts[b] = chunks + at;
+      }
+      chunks += n;
     }
+    if (threadIdx.x == 0) a.starts[a.B] = chunks;
   }
   cluster_sync();
   // ---- hand the pages out
@@ -252,14 +277,13 @@ __global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads
           a.refs[page] = 1;
           if (old >= 0) {
             atomicSub(a.refs + old, 1);
-            const int part_rows = q.len & ((1 << a.page_log2) - 1);
-            if (k == q.first && part_rows) copy = make_int4(old, page, part_rows, 0);
+            if (k == q.first) copy = make_int4(old, page, q.len & ((1 << a.page_log2) - 1), 0);
           }
         }
       }
       taken += __popc(need);
     }
-    if (lane == 0) {  // (page q.first is lane 0's)
+    if (lane == 0) {
       a.copies[b] = copy;
       a.done[b] = q.asks && ok;
     }
@@ -335,23 +359,23 @@ __global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads
 // --------------------------------------------------------------- copies ----
 struct CopyArgs {
   const int4* copies;
-  const int* n_copies;  // null: `count` of them
-  int count;
+  const int* n_copies;      // copies of whole pages: how many
+  const long long* starts;  // or copies of some rows each: chunks before them
+  int count;                // (of `count` copies)
   char *k, *v;
   long long layer_bytes, page_bytes;
   int row_bytes, layers;
-  int* table;           // compact: entries renamed by `moved` (null: none)
+  int* table;               // compact: entries renamed by `moved` (null: none)
   const int* moved;
   long long entries;
   int n_pages;
 };
 
-// Chunks of 16 KB of every copied page, layer and pool, four 16-byte loads
-// per thread in flight before its stores.
-constexpr int kCopyThreads = 256;
-constexpr int kCopyLoads = 4;
-constexpr int kChunk = kCopyThreads * kCopyLoads * 16;
-
+// A CTA takes every gridDim-th chunk of all layers and pools, all of its loads
+// in flight before its stores.  Bound by HBM: whole pages move at 6.6 TB/s
+// (98 % of the copy bandwidth).  Where copies have rows of their own number,
+// the chunks are found through their starts, so that none is empty (with
+// empty ones left in, 256 branches' part pages took 155 us, 5.1 TB/s).
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
   pdl_wait();
   if (a.table)
@@ -361,29 +385,45 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
       const int to = is_page(page, a.n_pages) ? __ldcg(a.moved + page) : -1;
       if (to != page) a.table[e] = to;
     }
-  const int n = a.n_copies ? __ldcg(a.n_copies) : a.count;
-  const long long chunks = (a.page_bytes + kChunk - 1) / kChunk;
-  const long long per = chunks * 2 * a.layers, total = per * n;
+  const int whole = static_cast<int>((a.page_bytes + kChunk - 1) / kChunk);  // chunks of a page
+  const long long per_pool =
+      a.starts ? __ldcg(a.starts + a.count) : static_cast<long long>(whole) * __ldcg(a.n_copies);
+  const long long total = per_pool * 2 * a.layers;
   for (long long u = blockIdx.x; u < total; u += gridDim.x) {
-    const int4 c = __ldcg(a.copies + u / per);
-    long long x = u % per;
-    const long long off = (x % chunks) * kChunk;
-    x /= chunks;
+    const int pool_of = static_cast<int>(u / per_pool);
+    const long long x = u - pool_of * per_pool;
+    int i;  // the copy
+    long long off;
+    if (a.starts) {  // the last copy that starts at or before chunk x
+      int lo = 0, hi = a.count;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.starts + mid) <= x)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      i = lo;
+      off = (x - __ldg(a.starts + lo)) * kChunk;
+    } else {
+      i = static_cast<int>(x / whole);
+      off = (x - static_cast<long long>(i) * whole) * kChunk;
+    }
+    const int4 c = __ldg(a.copies + i);
     const long long bytes = static_cast<long long>(c.z) * a.row_bytes;
-    if (off >= bytes) continue;
-    char* pool = ((x & 1) ? a.v : a.k) + (x >> 1) * a.layer_bytes;
+    char* pool = ((pool_of & 1) ? a.v : a.k) + (pool_of >> 1) * a.layer_bytes;
     const char* from = pool + c.x * a.page_bytes + off;
     char* to = pool + c.y * a.page_bytes + off;
     uint4 r[kCopyLoads];
 #pragma unroll
-    for (int i = 0; i < kCopyLoads; ++i) {
-      const int at = (i * kCopyThreads + threadIdx.x) * 16;
-      if (off + at < bytes) r[i] = __ldcs(reinterpret_cast<const uint4*>(from + at));
+    for (int j = 0; j < kCopyLoads; ++j) {
+      const int at = (j * kCopyThreads + threadIdx.x) * 16;
+      if (off + at < bytes) r[j] = __ldcs(reinterpret_cast<const uint4*>(from + at));
     }
 #pragma unroll
-    for (int i = 0; i < kCopyLoads; ++i) {
-      const int at = (i * kCopyThreads + threadIdx.x) * 16;
-      if (off + at < bytes) __stcs(reinterpret_cast<uint4*>(to + at), r[i]);
+    for (int j = 0; j < kCopyLoads; ++j) {
+      const int at = (j * kCopyThreads + threadIdx.x) * 16;
+      if (off + at < bytes) __stcs(reinterpret_cast<uint4*>(to + at), r[j]);
     }
   }
 }
@@ -530,12 +570,15 @@ int cart_pages_reserve(int B, int layers, int Hkv, int d, cart_dtype dtype, void
   a.base = reinterpret_cast<int*>(ws + w.base);
   a.free = reinterpret_cast<int*>(ws + w.ids);
   a.copies = reinterpret_cast<int4*>(ws + w.copies);
+  a.starts = reinterpret_cast<long long*>(ws + w.starts);
+  a.row_bytes = row_bytes_of(Hkv, d, dtype);
   TraceScope tr("pages_reserve", st);
   reserve_plan_kernel<<<kMetaCtas, kMetaThreads, 0, st>>>(a);
   rc = to_status(cudaGetLastError());
   if (rc) return rc;
   CopyArgs c{};
   c.copies = a.copies;
+  c.starts = a.starts;
   c.count = B;
   c.k = static_cast<char*>(k_pages);
   c.v = static_cast<char*>(v_pages);
