@@ -363,7 +363,9 @@ CART_API int cart_attn_decode_noalloc(int B, int Hq, int Hkv, int d, int p, floa
  * that no other conversation uses (cart_pages_reserve sees to it).
  * Hq / Hkv must be 1, 2, 4 or 8, d 64 or 128, B * nodes <= 65535.
  * Workspace: cart_attn_decode_tree_workspace_size(); its contents need no
- * initial value and nothing in it outlives the call.                      */
+ * initial value and nothing in it outlives the call.  Calls that may overlap
+ * (on other streams, or captured into graphs that are replayed at once) need
+ * workspaces of their own; so for the page operators below.               */
 #define CART_MAX_TREE_NODES 64
 CART_API size_t cart_attn_decode_tree_workspace_size(int B, int nodes, int Hq, int Hkv, int d,
                                                      int p, int page_rows, int max_pages);

@@ -228,6 +228,25 @@ def test_tree_visible_infinities_reach_the_nodes_that_see_them():
     torch.testing.assert_close(o, want, rtol=0, atol=0, equal_nan=True)
 
 
+@pytest.mark.parametrize("fill", [0, 255, 127])
+@pytest.mark.parametrize("B,nodes,p", [(3, 5, 200), (1, 5, 200), (2, 64, 200), (3, 5, 0)])
+def test_tree_workspace_needs_no_initial_value(B, nodes, p, fill):
+    """Any bytes in the workspace, for stacked and fused segments; then every
+    conversation idle over what that call left there, and over any bytes."""
+    t, table, lens, parents = make_tree(25, B, nodes, 8, 2, 64, p, (300, 5, 90)[:B], 16, "random")
+    want, _ = run_tree(t, table, lens, parents)
+    n = ca.decode_tree_workspace_size(B, nodes, 8, 2, 64, p, 16, table.shape[1])
+    ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+    o, _ = run_tree(t, table, lens, parents, workspace=ws)
+    assert torch.equal(o, want)
+    idle = np.full(B, -1, np.int32)
+    for again in range(2):
+        o, g = run_tree(t, table, idle, parents, workspace=ws)
+        assert not o.any() and torch.equal(g["k_pages"].cpu(), t["k_pages"])
+        ws.fill_(fill)
+    assert ca.device_status(clear=True) == 0
+
+
 @pytest.mark.parametrize("p,nodes", [(70, 1), (0, 2), (130, 3)])
 def test_tree_many_conversations(p, nodes):
     """More conversations than the schedule's blocks have threads."""

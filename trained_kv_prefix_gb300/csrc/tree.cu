@@ -3,10 +3,10 @@
 // (cart_attn_decode_tree).
 //
 // Three kernels, chained by programmatic dependent launch:
-//   prep    one block per (conversation, node): the tree's ancestor sets, the
-//           node's queries rotated into the workspace, its rotated key and
-//           value written to its page row, its output set to 0 if unused.
-//           One more block writes the start of every conversation's work.
+//   prep    up to eight nodes of a conversation per block: the tree's ancestor
+//           sets, the nodes' queries rotated into the workspace, their rotated
+//           keys and values written to their page rows, the output of unused
+//           ones set to 0.  One more block writes which CTAs walk which segment.
 //   attend  persistent, one or two CTAs per SM: tcgen05 products over 128-key
 //           tiles.
 //   merge   joins the parts of rows whose keys more than one CTA walked.
@@ -50,7 +50,7 @@ namespace {
 // whether a value of the node (in any kv head) is not finite.
 struct NodeSet {
   unsigned long long anc, vis;
-  unsigned bad, unused;
+  unsigned bad, pad;
 };
 
 struct TreeArgs {
@@ -620,8 +620,9 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
   walk.n_cart_all = (a.p + kTile - 1) / kTile - st.cart_lo;
   walk.cta = blockIdx.x;
   if (walk.lo >= walk.hi) {
+    // (the merge reads what the prep kernel wrote before it waits for this grid)
+    pdl_wait();
     pdl_release();
-    pdl_wait();  // this grid's end implies the prep kernel's
     return;
   }
   {
@@ -1180,13 +1181,16 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   using Vec = std::conditional_t<E == 4, float4, float2>;
   __shared__ float s_num[8][4][D], s_den[8][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // (the lists and sets are the prep kernel's, which had ended before any CTA
-  // of the attend kernel let this one start)
+  // The lists and sets are the prep kernel's, which had ended before any CTA of
+  // the attend kernel let this one start, so they are read before the wait.
+  // Every block waits, so that this grid's end implies the attend kernel's.
   const int id_p = a.stacked ? blockIdx.x : __ldcg(a.cut + blockIdx.x);
-  if (id_p < 0) return;
+  const int base = id_p < 0 ? a.R : id_p % a.segs * a.rt + blockIdx.y * 32;
+  if (base >= a.R) {
+    pdl_wait();
+    return;
+  }
   const int b = id_p / (a.Hkv * a.segs), g = id_p / a.segs % a.Hkv, G = a.Hq / a.Hkv;
-  const int base = id_p % a.segs * a.rt + blockIdx.y * 32;
-  if (base >= a.R) return;
   const int groups = min(8, (a.R - base + 3) >> 2);
   const int slices = groups > 4 ? 1 : groups > 2 ? 2 : groups > 1 ? 4 : 8;
   const int slice = warp / groups, r0 = base + warp % groups * 4;
@@ -1201,8 +1205,8 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   if (a.stacked && row_ok) sc = __ldcg(a.spans + id_c);
   unsigned long long anc = 0;
   if (row_ok) anc = __ldcg(&a.set[b * a.nodes + mine / G].anc);
-  if (sp.y == 0) return;  // idle
   pdl_wait();
+  if (sp.y == 0) return;  // idle
   const int n = anc ? sc.y + sp.y : 0;
   // row of part i of the lane's row in part_c, or ~ of it in part_p
   const int rows_c = min(a.B * a.R, a.rt), rows_p = min(a.R, a.rt);
