@@ -329,9 +329,10 @@ CART_API int cart_attn_decode_noalloc(int B, int Hq, int Hkv, int d, int p, floa
  *   lens   [B] int32: rows that the conversation holds; < 0 an idle slot.
  *   refs   [n_pages] int32: how many table entries name the page (a caller
  *          may add its own holds); <= 0 is free.
- * All tables are DEVICE memory, 4-byte aligned, max_pages * page_rows +
- * p < 2^24, and a call reads and updates them on the stream: a step of reserve, tree
- * attention, accept and fork never waits for the host and can be captured.
+ * All tables are DEVICE memory, 4-byte aligned, max_pages * page_rows < 2^24
+ * (with p and CART_MAX_TREE_NODES added, for the tree attention), and a call
+ * reads and updates them on the stream: a step of reserve, tree attention,
+ * accept and fork never waits for the host and can be captured.
  * Two calls that touch one table or pool must be ordered by the caller.   */
 
 /* ------------------------------------------------------------------------
@@ -424,7 +425,8 @@ CART_API int cart_pages_reserve(int B, int layers, int Hkv, int d, cart_dtype dt
  *          accepted with it.  -1, or an unused node: nothing is.
  *   new_lens [B] int32 (output, not lens itself): lens[b] + accepted nodes
  * Row lens[b] + (i-th node of the path) goes to row lens[b] + i.  The rows
- * behind new_lens[b] are left as they are.                                */
+ * behind new_lens[b] are left as they are, and a row whose new place has no
+ * page is dropped.                                                        */
 CART_API int cart_pages_accept(int B, int nodes, int layers, int Hkv, int d, cart_dtype dtype,
                                void* k_pages, void* v_pages, int n_pages, int page_rows,
                                const int* table, int max_pages, const int* lens,

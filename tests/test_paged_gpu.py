@@ -255,6 +255,37 @@ def test_tree_many_conversations(p, nodes):
     check_tree(*make_tree(24 + nodes, B, nodes, 2, 1, 64, p, lens, 16, "random"))
 
 
+def test_tree_windows_that_cut_nothing():
+    """Up to the largest window, bit for bit as without one."""
+    t, table, lens, parents = make_tree(26, 3, 40, 8, 2, 64, 150, (90, 0, 301), 16, "random")
+    want, _ = run_tree(t, table, lens, parents)
+    for window in (600, 2 ** 24 - 1, 2 ** 24, 2 ** 31 - 1):
+        o, _ = run_tree(t, table, lens, parents, window=window)
+        assert torch.equal(o, want), window
+    assert ca.device_status(clear=True) == 0
+
+
+def test_tree_largest_batch():
+    """The most conversations a call takes, a few of them checked."""
+    B = 65535
+    lens = np.random.default_rng(27).integers(-1, 15, B)
+    t, table, lens, _ = make_tree(27, B, 1, 2, 1, 64, 3, lens, 16, "chain")
+    o, _ = run_tree(t, table, lens, None)
+    assert ca.device_status(clear=True) == 0
+    some = np.r_[0, 1, 255, 256, 257, 32767, 65533, 65534, np.arange(5, B, 997)]
+    a = {k: synth.f64(v) for k, v in t.items() if k in ("kc", "vc")}
+    pages = table[some][:, :1]
+    a |= {k: synth.f64(t[k][some]) for k in ("q", "k_new", "v_new")}
+    a |= {k: synth.f64(t[k][pages[:, 0]]) for k in ("k_pages", "v_pages")}
+    own = np.arange(len(some), dtype=np.int32)[:, None]
+    o_ref, bound, _ = ref.tree(**a, table=own, lens=lens[some], parents=None, window=0)
+    assert (np.abs(synth.f64(o[torch.from_numpy(some).cuda()]) - o_ref) <= bound).all()
+
+
+def test_tree_most_heads():
+    check_tree(*make_tree(28, 1, 64, 1024, 128, 64, 130, (140,), 16, "wide"))
+
+
 def test_tree_large_logits():
     """Logits of hundreds: the weights are all on a few keys."""
     t, table, lens, parents = make_tree(23, 2, 9, 4, 2, 64, 200, (90, 300), 32, "random")

@@ -523,8 +523,9 @@ int cart_pages_fork(int B, int* table, int max_pages, int* lens, int* refs, int 
   int rc = check_tables(B, max_pages, n_pages, page_rows);
   if (rc) return rc;
   if (forks < 1 || forks > kMaxForks) return CART_ERR_GEOMETRY;
-  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(refs, 4) || !aligned_to(src, 4) || !aligned_to(dst, 4) ||
-      (rows && !aligned_to(rows, 4)) || !aligned_to(done, 4))
+  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(refs, 4) ||
+      !aligned_to(src, 4) || !aligned_to(dst, 4) || (rows && !aligned_to(rows, 4)) ||
+      !aligned_to(done, 4))
     return CART_ERR_POINTER;
   rc = check_device();
   if (rc) return rc;
@@ -547,7 +548,8 @@ int cart_pages_reserve(int B, int layers, int Hkv, int d, cart_dtype dtype, void
   int rc = check_tables(B, max_pages, n_pages, page_rows);
   if (!rc) rc = check_pool(layers, Hkv, d, dtype, k_pages, v_pages);
   if (rc) return rc;
-  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(refs, 4) || !aligned_to(rows, 4) || !aligned_to(done, 4))
+  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(refs, 4) ||
+      !aligned_to(rows, 4) || !aligned_to(done, 4))
     return CART_ERR_POINTER;
   const PagesWs w = pages_ws(B, n_pages);
   if (!aligned_to(workspace, 16) || workspace_bytes < w.total) return CART_ERR_WORKSPACE;
@@ -597,8 +599,8 @@ int cart_pages_accept(int B, int nodes, int layers, int Hkv, int d, cart_dtype d
   if (!rc) rc = check_pool(layers, Hkv, d, dtype, k_pages, v_pages);
   if (rc) return rc;
   if (nodes < 1 || nodes > kMaxNodes) return CART_ERR_GEOMETRY;
-  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || (parents && !aligned_to(parents, 4)) || !aligned_to(node, 4) ||
-      !aligned_to(new_lens, 4) || new_lens == lens)
+  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || (parents && !aligned_to(parents, 4)) ||
+      !aligned_to(node, 4) || !aligned_to(new_lens, 4) || new_lens == lens)
     return CART_ERR_POINTER;
   rc = check_device();
   if (rc) return rc;
@@ -628,7 +630,9 @@ int cart_pages_compact(int B, int layers, int Hkv, int d, cart_dtype dtype, void
   int rc = check_tables(B, max_pages, n_pages, page_rows);
   if (!rc) rc = check_pool(layers, Hkv, d, dtype, k_pages, v_pages);
   if (rc) return rc;
-  if (!aligned_to(table, 4) || !aligned_to(refs, 4) || !aligned_to(moved, 4) || !aligned_to(live, 4)) return CART_ERR_POINTER;
+  if (!aligned_to(table, 4) || !aligned_to(refs, 4) || !aligned_to(moved, 4) ||
+      !aligned_to(live, 4))
+    return CART_ERR_POINTER;
   const PagesWs w = pages_ws(B, n_pages);
   if (!aligned_to(workspace, 16) || workspace_bytes < w.total) return CART_ERR_WORKSPACE;
   rc = check_device();

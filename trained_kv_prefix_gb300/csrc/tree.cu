@@ -1437,7 +1437,8 @@ int cart_attn_decode_tree(int B, int nodes, int window, int Hq, int Hkv, int d, 
   for (const void* ptr : ptrs)
     if (!aligned_to(ptr, 16)) return CART_ERR_POINTER;
   if (p > 0 && (!aligned_to(kc, 16) || !aligned_to(vc, 16))) return CART_ERR_POINTER;
-  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || (parents && !aligned_to(parents, 4))) return CART_ERR_POINTER;
+  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || (parents && !aligned_to(parents, 4)))
+    return CART_ERR_POINTER;
   const TreeWs w = tree_ws(B, nodes, Hq, Hkv, d, p);
   if (!aligned_to(workspace, 16) || workspace_bytes < w.total) return CART_ERR_WORKSPACE;
   rc = check_device();
@@ -1450,7 +1451,9 @@ int cart_attn_decode_tree(int B, int nodes, int window, int Hq, int Hkv, int d, 
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.p = p;
-  a.window = window;
+  // positions lie below 2^24: a window from there on cuts nothing, and
+  // differences with it might leave 32 bits
+  a.window = window < (1 << 24) ? window : 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k_new = static_cast<const __nv_bfloat16*>(k_new);
