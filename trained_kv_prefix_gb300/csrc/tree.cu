@@ -70,9 +70,13 @@ struct TreeArgs {
   // the CTAs whose pieces hold tiles of each segment (see segment_span): the
   // stacked segments, then those of every (conversation, kv head)
   int2* spans;
-  int* cut;  // fused: the segment that leaves each CTA's run unfinished, or -1
-  // ---- partial outputs
-  float *part_c, *part_p, *lse_c, *lse_p;
+  int* cut;  // the own segment that each CTA's run leaves unfinished, or -1
+  // ---- partial outputs: rows of the stacked pieces, from row own0 on those of
+  // the own ones
+  float *part, *lse;
+  int own0;
+  // ---- merge: blocks by cut (else by own segment), rows of a block
+  int by_cut, merge_rows;
 };
 
 struct Turns {
@@ -159,7 +163,8 @@ __device__ __forceinline__ Starts scan_starts(const TreeArgs& a, StartsSmem<kThr
   r.cart_lo = s.lo;
   const int n_c = n_ct - r.cart_lo;
   const int stacks = (a.B * a.R + a.rt - 1) / a.rt;
-  r.cart_units = a.stacked && n_c > 0 ? static_cast<long long>(n_c + kStartUnits) * stacks * a.Hkv : 0;
+  r.cart_units =
+      a.stacked && n_c > 0 ? static_cast<long long>(n_c + kStartUnits) * stacks * a.Hkv : 0;
   r.start = r.cart_units + before + x - r.mine;
   r.total = r.cart_units + all;
   return r;
@@ -1074,9 +1079,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
                  *reinterpret_cast<volatile unsigned*>(&sp.bad[0]));
       if (live_rows) {
         const int rows_cap = own ? min(a.R, a.rt) : min(a.B * a.R, a.rt);
-        const long long part0 =
-            slot < 0 ? 0 : static_cast<long long>(slot) * rows_cap + (local - lane);
-        float* const part = own ? a.part_p : a.part_c;
+        const int part0 = slot < 0 ? 0 : (own ? a.own0 : 0) + slot * rows_cap + (local - lane);
         // Through the warp's slice, so that stores cover whole sectors: 32 rows of
         // 128 bytes (32 f32 or 64 bf16 columns), 16-byte granule k of row r at
         // r*128 + (k ^ (r & 7))*16.  Lane l stores granule l % 8 of rows
@@ -1087,9 +1090,10 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
         const int r1 = lane >> 3, k1 = lane & 7;
         const uint8_t* const from0 = stg + r1 * 128 + ((k1 ^ r1) << 4);
         const uint8_t* const from1 = stg + (r1 + 4) * 128 + ((k1 ^ (r1 + 4)) << 4);
-        float* const part_to = part + (part0 + r1) * D + k1 * 4;
+        float* const part_to = a.part + static_cast<long long>(part0 + r1) * D + k1 * 4;
         __nv_bfloat16* const o_to =
-            a.o + (static_cast<long long>((grow - lane) >> g_log2) * a.Hq + (g << g_log2)) * D + k1 * 8;
+            a.o + (static_cast<long long>((grow - lane) >> g_log2) * a.Hq + (g << g_log2)) * D +
+            k1 * 8;
         const unsigned mine = live_rows >> r1;
         auto put = [&](int k, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
           *reinterpret_cast<uint4*>(my + ((k ^ (lane & 7)) << 4)) = make_uint4(x, y, z, w);
@@ -1110,8 +1114,8 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
           for (int c = 0; c < 64; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * inv);
           for (unsigned long long left = own ? bad : 0ull; left; left &= left - 1) {
             const __nv_bfloat16* y =
-                a.v_new + ((static_cast<long long>(b) * a.nodes + __ffsll(left) - 1) * a.Hkv + g) * D +
-                h * 64;
+                a.v_new + h * 64 +
+                ((static_cast<long long>(b) * a.nodes + __ffsll(left) - 1) * a.Hkv + g) * D;
 #pragma unroll
             for (int c = 0; c < 64; ++c) {
               const float f = __bfloat162float(y[c]);
@@ -1156,7 +1160,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
           }
         }
         if (slot >= 0 && live)
-          (own ? a.lse_p : a.lse_c)[part0 + lane] = l == 0.f ? -INFINITY : m + __log2f(l);
+          a.lse[part0 + lane] = l == 0.f ? -INFINITY : m + __log2f(l);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kTPieceEmpty0 + (it & 1)]);
@@ -1170,13 +1174,15 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
 }
 
 // ---------------------------------------------------------------- merge ----
-// Joins the parts that the pieces of a row's segments left, in the order of
-// the CTAs: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).  Block (segment,
-// 32 of its rows), four rows per warp, with several warps on the parts of one
-// group of rows where the block has fewer.  Stacked: every segment of own
-// rows; fused: those that a run left unfinished, at most one per run.
+// Joins the parts that the pieces of a row's segments left, in an order that
+// the schedule alone decides: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).
+// Block (own segment, merge_rows of its rows), four rows per warp; where that
+// leaves warps over, `slices` warps share four rows, each taking every
+// slices-th pair of parts.  Bound by the latency of L2 (spans, then the first
+// parts and log-sum-exps side by side, then two more parts of four rows at a
+// time) and, for many rows, by its bandwidth.
 template <int D>
-__global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(256, 3) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int E = D / 32;  // output columns per lane
   using Vec = std::conditional_t<E == 4, float4, float2>;
   __shared__ float s_num[8][4][D], s_den[8][4];
@@ -1184,43 +1190,57 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   // The lists and sets are the prep kernel's, which had ended before any CTA of
   // the attend kernel let this one start, so they are read before the wait.
   // Every block waits, so that this grid's end implies the attend kernel's.
-  const int id_p = a.stacked ? blockIdx.x : __ldcg(a.cut + blockIdx.x);
-  const int base = id_p < 0 ? a.R : id_p % a.segs * a.rt + blockIdx.y * 32;
-  if (base >= a.R) {
+  const int id = a.by_cut ? __ldcg(a.cut + blockIdx.x) : blockIdx.x;
+  const int base = id < 0 ? a.R : id % a.segs * a.rt + blockIdx.y * a.merge_rows;
+  const int rows = min(a.merge_rows, a.R - base);
+  if (rows <= 0) {
     pdl_wait();
     return;
   }
-  const int b = id_p / (a.Hkv * a.segs), g = id_p / a.segs % a.Hkv, G = a.Hq / a.Hkv;
-  const int groups = min(8, (a.R - base + 3) >> 2);
+  const int b = id / (a.Hkv * a.segs), g = id / a.segs % a.Hkv, G = a.Hq / a.Hkv;
+  const int groups = (rows + 3) >> 2;
   const int slices = groups > 4 ? 1 : groups > 2 ? 2 : groups > 1 ? 4 : 8;
   const int slice = warp / groups, r0 = base + warp % groups * 4;
-  // lane: part lane & 7 (of eight at a time) of row r0 + lane / 8
+  // lane: its row is r0 + lane / 8
   const int mine = r0 + (lane >> 3);
   const int gr = b * a.R + mine;
   const int id_c = gr / a.rt * a.Hkv + g;
   const int stacks = a.stacked ? (a.B * a.R + a.rt - 1) / a.rt * a.Hkv : 0;
-  const bool row_ok = slice < slices && mine < a.R;
-  const int2 sp = __ldcg(a.spans + stacks + id_p);
+  const bool row_ok = slice < slices && mine < base + rows;
+  const int2 sp = __ldcg(a.spans + stacks + id);
   int2 sc = make_int2(0, 0);
   if (a.stacked && row_ok) sc = __ldcg(a.spans + id_c);
   unsigned long long anc = 0;
   if (row_ok) anc = __ldcg(&a.set[b * a.nodes + mine / G].anc);
   pdl_wait();
-  if (sp.y == 0) return;  // idle
+  if (sp.y <= (a.stacked ? 0 : 1)) return;  // idle, or written by its one CTA
   const int n = anc ? sc.y + sp.y : 0;
-  // row of part i of the lane's row in part_c, or ~ of it in part_p
+  // row of part i of the lane's row
   const int rows_c = min(a.B * a.R, a.rt), rows_p = min(a.R, a.rt);
   auto locate = [&](int i) {
     if (i < sc.y) return (id_c + (sc.x >> 1) + i) * rows_c + gr % a.rt;
     i -= sc.y;
-    const int slot = a.stacked ? id_p + (sp.x >> 1) + i : i ? 2 * ((sp.x >> 1) + i) : sp.x;
-    return ~(slot * rows_p + mine % a.rt);
+    const int slot = a.stacked ? id + (sp.x >> 1) + i : i ? 2 * ((sp.x >> 1) + i) : sp.x;
+    return a.own0 + slot * rows_p + mine % a.rt;
   };
-  auto lse_of = [&](int at) { return __ldcg(at >= 0 ? a.lse_c + at : a.lse_p + ~at); };
+  // part that is the slice's u-th
+  auto part = [&](int u) { return 2 * (slice + (u >> 1) * slices) + (u & 1); };
+  // parts u0 + j and u0 + j + 1 of four rows, whose places lanes 8 r + j hold
+  Vec v[8];
+  auto load = [&](int at, int j) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int from = __shfl_sync(0xffffffffu, at, (q & 3) * 8 + j + (q >> 2));
+      const float* out = a.part + static_cast<long long>(from) * D;
+      v[q] = from >= 0 ? __ldcg(reinterpret_cast<const Vec*>(out) + lane) : Vec{};
+    }
+  };
   const int n_max = __reduce_max_sync(0xffffffffu, n);
-  float top = -INFINITY, lse0 = -INFINITY;
-  if ((lane & 7) < n) top = lse0 = lse_of(locate(lane & 7));
-  for (int i = (lane & 7) + 8; i < n; i += 8) top = fmaxf(top, lse_of(locate(i)));
+  int i = part(lane & 7), at = i < n ? locate(i) : -1;
+  load(at, 0);  // (on their way together with the log-sum-exps)
+  float lse = at >= 0 ? __ldcg(a.lse + at) : -INFINITY, top = lse;
+  if (slices > 1 || n > 8)
+    for (int k = lane & 7; k < n; k += 8) top = fmaxf(top, __ldcg(a.lse + locate(k)));
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (top == -INFINITY) top = 0.f;
@@ -1229,31 +1249,27 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   for (int r = 0; r < 4; ++r)
 #pragma unroll
     for (int e = 0; e < E; ++e) num[r][e] = 0.f;
-  for (int i0 = slice * 8; i0 < n_max; i0 += slices * 8) {
-    const int i = i0 + (lane & 7);
-    const int at = i < n ? locate(i) : 0;
-    const float f = i < n ? exp2_approx((i0 ? lse_of(at) : lse0) - top) : 0.f;
+  for (int u0 = 0;;) {
+    const float f = exp2_approx(lse - top);  // (0 where there is no part)
     den += f;
-#pragma unroll 1
-    for (int j0 = 0; j0 < min(8, n_max - i0); j0 += 2) {  // two parts of four rows in flight
-      Vec v[8];
+    for (int j = 0;;) {
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const int from = (q & 3) * 8 + j0 + (q >> 2);
-        const int src = __shfl_sync(0xffffffffu, at, from);
-        const bool some = i0 + j0 + (q >> 2) < __shfl_sync(0xffffffffu, n, from);
-        const float* out = src >= 0 ? a.part_c + static_cast<long long>(src) * D
-                                    : a.part_p + static_cast<long long>(~src) * D;
-        v[q] = some ? __ldcg(reinterpret_cast<const Vec*>(out) + lane) : Vec{};
-      }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float w = __shfl_sync(0xffffffffu, f, (q & 3) * 8 + j0 + (q >> 2));
+        const float w = __shfl_sync(0xffffffffu, f, (q & 3) * 8 + j + (q >> 2));
         const float* y = reinterpret_cast<const float*>(&v[q]);
 #pragma unroll
         for (int e = 0; e < E; ++e) num[q & 3][e] = fmaf(w, y[e], num[q & 3][e]);
       }
+      j += 2;
+      if (j == 8 || part(u0 + j) >= n_max) break;
+      load(at, j);
     }
+    u0 += 8;
+    if (part(u0) >= n_max) break;
+    i = part(u0 + (lane & 7));
+    at = i < n ? locate(i) : -1;
+    load(at, 0);
+    lse = at >= 0 ? __ldcg(a.lse + at) : -INFINITY;
   }
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
@@ -1292,8 +1308,8 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
 
 // ------------------------------------------------------------- workspace ----
 struct TreeWs {
-  size_t qr, set, spans, cut, part_c, part_p, lse_c, lse_p, total;
-  int R, rt, segs, stacked;
+  size_t qr, set, spans, cut, part, lse, total;
+  int R, rt, segs, stacked, own0;
 };
 
 TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
@@ -1332,10 +1348,9 @@ TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
   const size_t slots_c = w.stacked ? stacks + ctas : 0;
   w.spans = take((stacks + static_cast<size_t>(B) * Hkv * w.segs) * 8);
   w.cut = take(kTreeMaxCtas * 4);
-  w.part_c = take(slots_c * rows_c * d * 4);
-  w.part_p = take(slots_p * rows_p * d * 4);
-  w.lse_c = take(slots_c * rows_c * 4);
-  w.lse_p = take(slots_p * rows_p * 4);
+  w.own0 = static_cast<int>(slots_c * rows_c);
+  w.part = take((w.own0 + slots_p * rows_p) * d * 4);
+  w.lse = take((w.own0 + slots_p * rows_p) * 4);
   w.total = off;
   return w;
 }
@@ -1363,8 +1378,8 @@ cudaError_t launch_attend(const TreeArgs& a, const TreeMaps& m, cudaStream_t st)
   using L = TreeLayout<D, NT>;
   const cudaError_t e = set_smem_once<tree_attend_kernel<D, NT>>(L::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_dependent(tree_attend_kernel<D, NT>, dim3(a.n_ctas), dim3(L::kThreads), L::kBytes, st,
-                          m.q, m.kc, m.vc, m.kp, m.vp, a);
+  return launch_dependent(tree_attend_kernel<D, NT>, dim3(a.n_ctas), dim3(L::kThreads), L::kBytes,
+                          st, m.q, m.kc, m.vc, m.kp, m.vp, a);
 }
 
 template <int D>
@@ -1372,6 +1387,15 @@ cudaError_t launch_tree(TreeArgs a, const Turns& turns, cudaStream_t st) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorInvalidValue;
   a.n_ctas = std::min(sms, kTreeMaxCtas / 2) * (a.rt > kTile ? 1 : 2);
+  // The merge goes by own segments, or by the CTAs' cuts where those are fewer.
+  // Runs per segment, about the parts of a row, set a block's rows: 32 (a warp
+  // for every four) where they are few, less where warps can share them.  In
+  // us, with 32, 16, 8 and 4 rows: 2.4 runs per segment 77, 80, 87, 104; 4.8
+  // 126, 126, 128, 134; 9.5 34, 31, 33, 36; 19 55, 50, 48, 51; 38 35, 29, 25, 24.
+  const int own = a.B * a.Hkv * a.segs;
+  const int runs = a.n_ctas / (a.stacked ? (a.B * a.R + a.rt - 1) / a.rt * a.Hkv : own);
+  a.by_cut = !a.stacked && own > a.n_ctas;
+  a.merge_rows = runs < 4 ? 32 : runs < 12 ? 16 : runs < 24 ? 8 : 4;
   // rotated queries [B*nodes, Hkv, G, d] as (d, G, Hkv, B*nodes): a
   // (64, G, 1, 32/G) box is 32 rows of one kv head; pools as (d, Hkv,
   // page_rows, n_pages), a box one page of one kv head
@@ -1404,8 +1428,8 @@ cudaError_t launch_tree(TreeArgs a, const Turns& turns, cudaStream_t st) {
   e = a.rt > kTile ? launch_attend<D, 2>(a, m, st) : launch_attend<D, 1>(a, m, st);
   if (e != cudaSuccess) return e;
   return launch_dependent(tree_merge_kernel<D>,
-                          dim3(a.stacked ? a.B * a.Hkv * a.segs : a.n_ctas,
-                               (std::min(a.R, a.rt) + 31) / 32),
+                          dim3(a.by_cut ? a.n_ctas : own,
+                               (std::min(a.R, a.rt) + a.merge_rows - 1) / a.merge_rows),
                           dim3(256), 0, st, a);
 }
 
@@ -1472,10 +1496,9 @@ int cart_attn_decode_tree(int B, int nodes, int window, int Hq, int Hkv, int d, 
   a.stacked = w.stacked;
   a.spans = reinterpret_cast<int2*>(ws + w.spans);
   a.cut = reinterpret_cast<int*>(ws + w.cut);
-  a.part_c = reinterpret_cast<float*>(ws + w.part_c);
-  a.part_p = reinterpret_cast<float*>(ws + w.part_p);
-  a.lse_c = reinterpret_cast<float*>(ws + w.lse_c);
-  a.lse_p = reinterpret_cast<float*>(ws + w.lse_p);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.lse = reinterpret_cast<float*>(ws + w.lse);
+  a.own0 = w.own0;
   a.status = device_status_ptr();
   if (!a.status) return CART_ERR_CUDA;
   // the turns of the last (d, theta) of this host thread
