@@ -96,7 +96,8 @@ __device__ __forceinline__ bool is_page(int page, int n_pages) {
 // ---------------------------------------------------------------- fork ----
 // One block per fork.  A conversation that is a destination is nobody's
 // source and no other fork's destination (checked over the lists), so the
-// block alone touches its table row, and no source row changes.
+// block alone touches its table row, and no source row changes.  Bound by
+// latency: 700 forks of up to 512 pages take 8.4 us.
 __global__ void __launch_bounds__(256) fork_kernel(int B, int* table, int max_pages, int* lens,
                                                    int* refs, int n_pages, int page_log2,
                                                    const int* __restrict__ src,
@@ -169,6 +170,9 @@ __device__ __forceinline__ Request request(const ReserveArgs& a, int b) {
 // its page is shared.
 __device__ __forceinline__ int mark_shared(int page) { return -2 - page; }
 
+// Bound by the latency of its four phases, each a chain of a few loads behind
+// a cluster barrier; one launch of eight CTAs, since a launch per phase would
+// cost 3 us of host time each.  13 us alone for 256 branches over 1600 pages.
 __global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads)
     reserve_plan_kernel(const ReserveArgs a) {
   pdl_release();
@@ -301,7 +305,7 @@ struct CompactArgs {
 
 // With lp(i) the live pages below i and n = lp(n_pages): the free page i < n
 // is the (i - lp(i))-th hole, and the live page j >= n the (lp(j) - lp(n))-th
-// to move.
+// to move.  Bound by latency: 9 us alone for 1200 pages.
 __global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads)
     compact_plan_kernel(const CompactArgs a) {
   pdl_release();
@@ -372,10 +376,11 @@ struct CopyArgs {
 };
 
 // A CTA takes every gridDim-th chunk of all layers and pools, all of its loads
-// in flight before its stores.  Bound by HBM: whole pages move at 6.6 TB/s
-// (98 % of the copy bandwidth).  Where copies have rows of their own number,
-// the chunks are found through their starts, so that none is empty (with
-// empty ones left in, 256 branches' part pages took 155 us, 5.1 TB/s).
+// in flight before its stores.  Bound by HBM: compacting 16 layers moves 2.38
+// GB of whole pages in 354 us, 6.7 TB/s, as fast as a plain copy.  Where copies
+// have rows of their own number, the chunks are found through their starts, so
+// that none is empty: 256 branches' part pages, 0.79 GB, take 122 us, 6.5 TB/s
+// (with empty chunks left in 155 us).
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs a) {
   pdl_wait();
   if (a.table)
@@ -447,7 +452,8 @@ struct AcceptArgs {
 // Block (layer and pool, conversation).  Thread i owns 16-byte columns of the
 // rows and moves them along the path in order: node i of the path is never
 // before slot i, so a slot is written only after the node that lay there has
-// been read.
+// been read.  Bound by the latency of eight rows at a time: paths in trees of
+// 64 nodes, 64 conversations, 32 layers take 11 us, 4.5 TB/s.
 __global__ void __launch_bounds__(128) accept_kernel(const AcceptArgs a) {
   __shared__ TreeSmem tree;
   __shared__ long long from[kMaxNodes], to[kMaxNodes];
