@@ -406,7 +406,9 @@ CART_API int cart_pages_fork(int B, int* table, int max_pages, int* lens, int* r
  * order), and in the place of one that is shared (refs > 1) a free one is
  * taken, with the rows of b that it holds (below lens[b]) copied in every
  * layer.  When the pool runs out, the conversation that finds too few free
- * pages and all later ones that need any keep what they have, done 0.
+ * pages and all later ones that need any keep what they have, done 0; their
+ * next rows may lie in a shared page, so they must not append in that step
+ * (parents -2 for all their nodes, or lens < 0).
  * Pages that lose their last holder to such a copy are free from the next
  * call on.
  *   k_pages, v_pages: dtype CART_BF16 or CART_F32, row = Hkv * d elements

@@ -634,6 +634,30 @@ def test_served_together():
     assert int(s.refs.abs().sum()) == 0 and int(s.table.max()) == -1
 
 
+def test_no_room_sits_the_step_out():
+    """A pool that runs out: the conversation without room takes no part, and
+    the page that it shares stays as it is."""
+    rng = np.random.default_rng(43)
+    k = _bf16(rng, (1, 3, 16, 1, 64)).cuda()
+    v = _bf16(rng, (1, 3, 16, 1, 64)).cuda()
+    table, lens, refs = _i32([[0, -1], [0, -1], [1, -1]]), _i32([5, 5, 16]), _i32([2, 1, 0])
+    k0, v0 = k.clone(), v.clone()
+    done = ca.cart_pages_reserve(k, v, table, lens, refs, lens + 2)
+    assert done.tolist() == [1, 0, 0]       # one free page: the first's copy
+    assert table.tolist() == [[2, -1], [0, -1], [1, -1]] and refs.tolist() == [1, 1, 1]
+    parents = torch.where(done[:, None] == 1, _i32([[-1, 0]] * 3), -2)
+    q = _bf16(rng, (3, 2, 2, 64)).cuda()
+    new = _bf16(rng, (3, 2, 1, 64)).cuda()
+    c = _bf16(rng, (4, 1, 64)).cuda()
+    o = ca.cart_attn_decode_tree(q, new, new, c, c, k[0], v[0], table, lens, parents)
+    assert ca.device_status(clear=True) == 0
+    assert o[0].any() and not o[1:].any()
+    assert torch.equal(k[:, :2], k0[:, :2]) and torch.equal(v[:, :2], v0[:, :2])
+    assert torch.equal(k[0, 2, :5], k0[0, 0, :5]) and torch.equal(v[0, 2, 5:7], new[0])
+    after = ca.cart_pages_accept(k, v, table, lens, parents, _i32([1, 1, 1]))
+    assert after.tolist() == [7, 5, 16]
+
+
 def test_captured_step_replays():
     """A step of reserve, tree attention and accept captured into a graph
     gives the same results as eager calls, replay after replay."""

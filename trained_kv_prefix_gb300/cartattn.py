@@ -579,7 +579,8 @@ def cart_pages_reserve(k_pages, v_pages, table, lens, refs, rows, *, done=None, 
     int32 on the device, < 0: left as it is, 0: everything is given back.
     Pools ``[layers, pages, page_rows, Hkv, d]`` (bf16 or f32); table, lens
     and refs are updated.  Returns done ``[B]`` int32: 1 where there is
-    room."""
+    room; a conversation without it must not append (its next row may lie in
+    a shared page): -2 for its ``parents``."""
     layers, N, P, Hkv, d, dt, kp, vp, dev = _pools(k_pages, v_pages)
     B, M = table.shape
     i32 = torch.int32
