@@ -164,6 +164,24 @@ MapCache& map_cache() {
   return c;
 }
 
+// Tensor map with 128-byte swizzle, dims innermost first, strides in bytes.
+bool encode_map(CUtensorMap* m, CUtensorMapDataType dtype, int rank, const void* base,
+                const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dd[5], ss[4];
+  cuuint32_t bb[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    dd[i] = dims[i];
+    bb[i] = box[i];
+    es[i] = 1;
+  }
+  for (int i = 0; i + 1 < rank; ++i) ss[i] = strides[i];
+  return fn(m, dtype, rank, const_cast<void*>(base), dd, ss, bb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_cached(CUtensorMap* m, CUtensorMapDataType dtype, int rank, const void* base,
                    const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
   MapKey k{};
@@ -184,20 +202,7 @@ bool encode_cached(CUtensorMap* m, CUtensorMapDataType dtype, int rank, const vo
         return true;
       }
   }
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dd[5], ss[4];
-  cuuint32_t bb[5], es[5];
-  for (int i = 0; i < rank; ++i) {
-    dd[i] = dims[i];
-    bb[i] = box[i];
-    es[i] = 1;
-  }
-  for (int i = 0; i + 1 < rank; ++i) ss[i] = strides[i];
-  if (fn(m, dtype, rank, const_cast<void*>(base), dd, ss, bb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
+  if (!encode_map(m, dtype, rank, base, dims, strides, box)) return false;
   std::lock_guard<std::mutex> lk(c.mu);
   c.key[c.next] = k;
   c.map[c.next] = *m;
@@ -248,6 +253,11 @@ bool make_bf16_rows_map(CUtensorMap* m, const void* base, int blocks, int rows, 
 bool make_bf16_map4(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],
                     const uint64_t (&strides)[3], const uint32_t (&box)[4]) {
   return encode_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box);
+}
+
+bool encode_bf16_map4(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],
+                      const uint64_t (&strides)[3], const uint32_t (&box)[4]) {
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box);
 }
 
 bool make_f32_map4(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],

@@ -158,7 +158,11 @@ __device__ __forceinline__ long long lse_index(const int* cu, int total, int n, 
 // first, strides in bytes for dims 1..3 (api.cu).
 bool make_bf16_map4(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],
                     const uint64_t (&strides)[3], const uint32_t (&box)[4]);
-// The same for f32 data (api.cu).
+// The same, encoded at every call: for a caller that meets more addresses than
+// the cache holds (every layer has pools of its own) (api.cu).
+bool encode_bf16_map4(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],
+                      const uint64_t (&strides)[3], const uint32_t (&box)[4]);
+// The same as make_bf16_map4 for f32 data (api.cu).
 bool make_f32_map4(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],
                    const uint64_t (&strides)[3], const uint32_t (&box)[4]);
 

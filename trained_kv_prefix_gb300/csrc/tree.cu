@@ -1427,16 +1427,22 @@ cudaError_t launch_tree(TreeArgs a, const Turns& turns, cudaStream_t st) {
                              static_cast<uint64_t>(a.B) * a.nodes};
   const uint64_t qstr[3] = {d * e2, G * d * e2, hkv * G * d * e2};
   const uint32_t qbox[4] = {64, static_cast<uint32_t>(G), 1, static_cast<uint32_t>(32 / G)};
-  const unsigned page_rows = 1u << a.pt.page_log2;
-  if (!make_bf16_map4(&m.q, a.qr, qdims, qstr, qbox) ||
-      !make_bf16_rows_map(&m.kp, a.k_pages, a.pt.n_pages, page_rows, a.Hkv, D, page_rows) ||
-      !make_bf16_rows_map(&m.vp, a.v_pages, a.pt.n_pages, page_rows, a.Hkv, D, page_rows))
+  auto rows_map = [&](CUtensorMap* map, const void* base, uint64_t blocks, uint64_t rows,
+                      uint32_t box_rows) {
+    const uint64_t dims[4] = {d, hkv, rows, blocks};
+    const uint64_t strides[3] = {d * e2, hkv * d * e2, rows * hkv * d * e2};
+    const uint32_t box[4] = {64, 1, box_rows, 1};
+    return encode_bf16_map4(map, base, dims, strides, box);
+  };
+  const uint32_t page_rows = 1u << a.pt.page_log2;
+  if (!encode_bf16_map4(&m.q, a.qr, qdims, qstr, qbox) ||
+      !rows_map(&m.kp, a.k_pages, a.pt.n_pages, page_rows, page_rows) ||
+      !rows_map(&m.vp, a.v_pages, a.pt.n_pages, page_rows, page_rows))
     return cudaErrorInvalidValue;
   if (a.p == 0) {  // no cartridge tile is read
     m.kc = m.kp;
     m.vc = m.vp;
-  } else if (!make_bf16_rows_map(&m.kc, a.kc, 1, a.p, a.Hkv, D, kTile) ||
-             !make_bf16_rows_map(&m.vc, a.vc, 1, a.p, a.Hkv, D, kTile)) {
+  } else if (!rows_map(&m.kc, a.kc, 1, a.p, kTile) || !rows_map(&m.vc, a.vc, 1, a.p, kTile)) {
     return cudaErrorInvalidValue;
   }
   // nodes per prep block: one for a few nodes (latency), more for many, whose
