@@ -344,6 +344,69 @@ def test_tree_pool_beyond_32_bits():
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("B,window", [(1, 0), (2, 0), (2, 9_000_001)])
+def test_tree_longest_rows(B, window):
+    """The most rows a conversation can have; its table names eight pages over
+    and over, so the plain form weighs each key by how often it is there."""
+    M, P, p, nodes, d, N = 131071, 128, 20, 3, 64, 10
+    rng = np.random.default_rng(33)
+    table = np.full((B, M), -1, np.int32)
+    table[0] = np.arange(M) % 8
+    table[0, -1] = 8
+    lens = np.array([M * P - 5, 77][:B], np.int32)
+    if B > 1:
+        table[1, 0] = 9
+    t = dict(q=_bf16(rng, (B, nodes, 4, d)), k_new=_bf16(rng, (B, nodes, 1, d)),
+             v_new=_bf16(rng, (B, nodes, 1, d)), kc=_bf16(rng, (p, 1, d)),
+             vc=_bf16(rng, (p, 1, d)), k_pages=_bf16(rng, (N, P, 1, d)),
+             v_pages=_bf16(rng, (N, P, 1, d)))
+    parents = np.tile(np.array([-1, 0, 0], np.int32), (B, 1))
+    o, g = run_tree(t, table, lens, parents, window=window)
+    assert ca.device_status(clear=True) == 0
+    a = {k: synth.f64(v) for k, v in t.items()}
+    L, G = int(lens[0]), 4
+    first_new = [ref.rope(a["k_new"][0, n], p + L + (n > 0)) for n in range(nodes)]
+    for n in range(nodes):
+        pos = p + L + (n > 0)
+        first = pos - window + 1 if window else 0
+        r0 = max(first - p, 0)                      # the first row it sees
+        times = np.zeros((9, P))
+        pages, rows = np.unique(np.arange(r0 // P + 1, M - 1) % 8, return_counts=True)
+        times[pages] += rows[:, None]
+        times[(r0 // P) % 8, r0 % P:] += 1
+        times[8, :P - 5] = 1
+        seen = [0, n] if n else [0]
+        k = np.concatenate([a["k_pages"][:9, :, 0].reshape(-1, d),
+                            a["kc"][first:, 0] if first < p else np.zeros((0, d))] +
+                           [first_new[x] for x in seen])
+        v = np.concatenate([a["v_pages"][:9, :, 0].reshape(-1, d),
+                            a["vc"][first:, 0] if first < p else np.zeros((0, d))] +
+                           [a["v_new"][0, x] for x in seen])
+        c = np.concatenate([times.ravel(), np.ones(len(k) - times.size)])
+        for h in range(G):
+            x = ref.rope(a["q"][0, n, h], pos)
+            s = d ** -0.5 * (k @ x)
+            w = c * np.exp(s - s.max())
+            w /= w.sum()
+            # as ref.tree: each of the rotated query and key, the weights and
+            # the output rounded once; 2e-4 for f32 sums of 2^24 rows in 2^17
+            # tiles (2^-24 of the sum at each of at most 2^9 steps of a run,
+            # 2^7 terms each, and of the runs' merge)
+            e = d ** -0.5 * (np.abs(k) @ np.abs(x)) * (2 * ref.HALF_BF16 + 1e-5)
+            rel = np.expm1(2 * e.max()) + ref.HALF_BF16 + 2e-4
+            bound = rel * (w @ np.abs(v)) + ref.HALF_BF16 * np.abs(w @ v) + 1e-6
+            off = np.abs(synth.f64(o[0, n, h]) - w @ v)
+            assert (off <= bound).all(), (n, h, float((off - bound).max()))
+    if B > 1:                                       # its neighbour is not disturbed
+        one = {k: v if k in ("kc", "vc", "k_pages", "v_pages") else v[1:] for k, v in t.items()}
+        alone, _ = run_tree(one, table[1:], lens[1:], parents[1:], window=window)
+        o_ref, bound, _ = ref.tree(**{k: synth.f64(v) for k, v in one.items()},
+                                   table=table[1:, :2], lens=lens[1:], parents=parents[1:],
+                                   window=window)
+        assert (np.abs(synth.f64(o[1:]) - o_ref) <= bound).all()
+        assert (np.abs(synth.f64(alone) - o_ref) <= bound).all()
+
+
 # ------------------------------------------------------------ page operators
 def make_tables(rng, B, M, P, N, share=0.4):
     """Random tables: conversations that hold rows of their own and of others,
