@@ -980,12 +980,13 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
           fence_proxy_async_smem();
         }
         if (live_rows) {
+          // (one load: four of 32 columns, with the maximum taken after them, need
+          // more registers than there are, and the calls 4 to 9 % more time)
           uint32_t r[4][32];
-          tmem_ld32(tS, r[0]);
-          tmem_ld32(tS + 32, r[1]);
-          tmem_ld32(tS + 64, r[2]);
-          tmem_ld32(tS + 96, r[3]);
+          float most;
+          tmem_ld128_max(tS, r[0], r[1], r[2], r[3], most);
           tmem_ld_wait();
+          tmem_max_fence(most);
           tmem_reg_fence(r[0]);
           tmem_reg_fence(r[1]);
           tmem_reg_fence(r[2]);
@@ -995,6 +996,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
                    : *reinterpret_cast<volatile unsigned*>(
                          &sh.absent[(vld(sp.ring) + t) % kAbsentRing]);
           if (__any_sync(0xffffffffu, end < kTile || from > 0 || gone)) {
+            most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               unsigned w = low_bits(end - 32 * i) & ~low_bits(from - 32 * i);
@@ -1016,19 +1018,15 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
 #pragma unroll
               for (int c = 0; c < 32; ++c)
                 if (!(w >> c & 1u)) r[i][c] = __float_as_uint(-INFINITY);
+              float v = fmax3(__uint_as_float(r[i][0]), __uint_as_float(r[i][1]),
+                              __uint_as_float(r[i][2]));
+#pragma unroll
+              for (int c = 3; c < 31; c += 2)
+                v = fmax3(v, __uint_as_float(r[i][c]), __uint_as_float(r[i][c + 1]));
+              most = fmax3(most, v, __uint_as_float(r[i][31]));
             }
           }
-          float mx[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float v = fmax3(__uint_as_float(r[q][0]), __uint_as_float(r[q][1]),
-                            __uint_as_float(r[q][2]));
-#pragma unroll
-            for (int c = 3; c < 31; c += 2)
-              v = fmax3(v, __uint_as_float(r[q][c]), __uint_as_float(r[q][c + 1]));
-            mx[q] = fmaxf(v, __uint_as_float(r[q][31]));
-          }
-          const float rmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+          const float rmax = most * a.scale_log2;
           // the running maximum is kept until a row's grows by more than 8
           // (weights stay below 2^8), so O is rarely rescaled
           float alpha = 1.f;
@@ -1041,8 +1039,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
           const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
           const float mr = m == -INFINITY ? 0.f : m;  // no key yet: weights 0
           const float2 nm2 = make_float2(-mr, -mr);
-          float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                          make_float2(0.f, 0.f)};
+          float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t pk[16];
@@ -1050,13 +1047,13 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
             for (int c = 0; c < 16; ++c) {
               const float2 e = __ffma2_rn(u2f2(r[q][2 * c], r[q][2 * c + 1]), sc2, nm2);
               const float2 w = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-              rs[c & 3] = __fadd2_rn(rs[c & 3], w);
+              rs[c & 1] = __fadd2_rn(rs[c & 1], w);
               pk[c] = pack_bf16x2(w.x, w.y);
             }
             tmem_st16(tS + 16 * q, pk);
           }
-          const float2 rs01 = __fadd2_rn(rs[0], rs[1]), rs23 = __fadd2_rn(rs[2], rs[3]);
-          l = l * alpha + ((rs01.x + rs01.y) + (rs23.x + rs23.y));
+          const float2 rs01 = __fadd2_rn(rs[0], rs[1]);
+          l = l * alpha + (rs01.x + rs01.y);
           if (__any_sync(0xffffffffu, rescale)) {
             // (the stream's last PV has completed: the commit that published
             // this S follows it)
