@@ -117,6 +117,18 @@ TREES = [
     ("window_wide_rows", 2, 64, 8, 1, 64, 500, (130, 700), 16, "random", 333),
     ("long_rows", 2, 6, 4, 1, 64, 30, (5003, 2048), 128, "random", 0),
     ("long_cartridge", 1, 4, 4, 2, 64, 4500, (40,), 64, "random", 0),
+    # cartridges long enough that the rows of all conversations walk them together
+    ("stacked_tokens", 5, 1, 8, 2, 128, 700, (0, 1, 200, 64, 333), 64, "chain", 0),
+    ("stacked_g1", 7, 9, 2, 2, 64, 640, (0, 15, 16, 17, 300, 1, 128), 16, "random", 0),
+    ("stacked_g2", 4, 16, 4, 2, 128, 1100, (255, 256, 0, 31), 64, "wide", 0),
+    ("stacked_g8", 9, 20, 8, 1, 64, 2700, (0, 5, 128, 310, 64, 77, 1, 90, 12), 32, "random", 0),
+    ("stacked_two_tiles", 8, 36, 4, 1, 64, 2500, (3, 0, 127, 130, 40, 9, 250, 64), 16, "wide", 0),
+    ("stacked_ragged", 6, 13, 8, 2, 128, 1200, (0, 3, 129, 250, 64, 31), 16, "ragged", 0),
+    ("stacked_many", 40, 3, 4, 2, 64, 520, tuple(range(0, 200, 5)), 16, "random", 0),
+    ("stacked_window_in_rows", 5, 6, 8, 2, 64, 700, (0, 255, 599, 90, 101), 64, "random", 100),
+    ("stacked_window_in_cartridge", 5, 9, 4, 2, 64, 900, (0, 17, 200, 300, 5), 32, "random", 350),
+    ("stacked_window_wide", 8, 36, 4, 1, 64, 2500, (3, 0, 700, 130, 40, 9, 250, 64), 64, "random",
+     333),
 ]
 
 
@@ -133,11 +145,12 @@ def test_tree_chains_without_parents_equal_given_chains():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("p", [200, 900])
 @pytest.mark.parametrize("nodes,G", [(1, 4), (4, 4), (3, 2), (8, 1)])
-def test_tree_chain_agrees_with_span_verify(nodes, G):
+def test_tree_chain_agrees_with_span_verify(nodes, G, p):
     """A chain over pages is the span verify over a dense cache."""
     rng = np.random.default_rng(5)
-    B, Hkv, d, p, P, rows = 4, 2, 128, 200, 32, 320
+    B, Hkv, d, P, rows = 4, 2, 128, 32, 320
     lens = np.array([0, 31, 150, rows - nodes], np.int32)
     x = {k: _bf16(rng, s).cuda() for k, s in dict(
         q=(B, nodes, G * Hkv, d), k_new=(B, nodes, Hkv, d), v_new=(B, nodes, Hkv, d),
@@ -159,10 +172,11 @@ def test_tree_chain_agrees_with_span_verify(nodes, G):
         2 * ref.HALF_BF16 * 2 * float(x["k_new"].abs().max())
 
 
-def test_tree_idle_and_pageless_conversations():
+@pytest.mark.parametrize("p", [50, 900])
+def test_tree_idle_and_pageless_conversations(p):
     """Idle slots, missing pages among the cached rows (not seen) and under
     new nodes (unused, reported)."""
-    t, table, lens, parents = make_tree(11, 4, 7, 8, 2, 64, 50, (40, 0, 33, 60), 16, "random",
+    t, table, lens, parents = make_tree(11, 4, 7, 8, 2, 64, p, (40, 0, 33, 60), 16, "random",
                                         hole=True)
     lens = lens.copy()
     lens[1] = -1
@@ -178,11 +192,12 @@ def test_tree_lens_beyond_the_table():
 
 
 @pytest.mark.parametrize("window", [0, 40])
-@pytest.mark.parametrize("nodes,Hq,Hkv,d", [(6, 4, 2, 64), (64, 8, 1, 128), (13, 8, 1, 128)])
-def test_tree_masked_places_may_hold_anything(nodes, Hq, Hkv, d, window):
+@pytest.mark.parametrize("nodes,Hq,Hkv,d,p", [(6, 4, 2, 64, 30), (64, 8, 1, 128, 30),
+                                               (13, 8, 1, 128, 30), (6, 4, 2, 64, 900)])
+def test_tree_masked_places_may_hold_anything(nodes, Hq, Hkv, d, p, window):
     """NaN and infinities in rows behind the sequence, in pages of nobody, in
     rows left behind by the window, and in other branches."""
-    t, table, lens, parents = make_tree(21, 3, nodes, Hq, Hkv, d, 30, (0, 77, 130), 16, "star")
+    t, table, lens, parents = make_tree(21, 3, nodes, Hq, Hkv, d, p, (0, 77, 130), 16, "star")
     parents[1] = random_tree(np.random.default_rng(1), nodes, "ragged")
     clean = check_tree(t, table, lens, parents, window=window)
     bad = [float("nan"), float("inf"), -float("inf"), 3e38]
@@ -212,10 +227,11 @@ def test_tree_masked_places_may_hold_anything(nodes, Hq, Hkv, d, window):
     ca.device_status(clear=True)
 
 
-def test_tree_visible_infinities_reach_the_nodes_that_see_them():
+@pytest.mark.parametrize("B,p", [(1, 30), (4, 900)])
+def test_tree_visible_infinities_reach_the_nodes_that_see_them(B, p):
     """A value of an ancestor that is infinite or NaN reaches its descendants
     in that element alone."""
-    t, table, lens, parents = make_tree(22, 1, 6, 2, 1, 64, 30, (50,), 16, "chain")
+    t, table, lens, parents = make_tree(22, B, 6, 2, 1, 64, p, (50,) * B, 16, "chain")
     parents[0] = [-1, 0, 1, -1, 3, 4]
     clean, _ = run_tree(t, table, lens, parents)
     t["v_new"] = t["v_new"].clone()
@@ -229,7 +245,7 @@ def test_tree_visible_infinities_reach_the_nodes_that_see_them():
 
 
 @pytest.mark.parametrize("fill", [0, 255, 127])
-@pytest.mark.parametrize("B,nodes,p", [(3, 5, 200), (1, 5, 200), (2, 64, 200), (3, 5, 0)])
+@pytest.mark.parametrize("B,nodes,p", [(3, 5, 200), (1, 5, 200), (2, 64, 200), (3, 5, 0), (3, 5, 900)])
 def test_tree_workspace_needs_no_initial_value(B, nodes, p, fill):
     """Any bytes in the workspace, for stacked and fused segments; then every
     conversation idle over what that call left there, and over any bytes."""
@@ -247,7 +263,7 @@ def test_tree_workspace_needs_no_initial_value(B, nodes, p, fill):
     assert ca.device_status(clear=True) == 0
 
 
-@pytest.mark.parametrize("p,nodes", [(70, 1), (0, 2), (130, 3)])
+@pytest.mark.parametrize("p,nodes", [(70, 1), (0, 2), (130, 3), (700, 2)])
 def test_tree_many_conversations(p, nodes):
     """More conversations than the schedule's blocks have threads."""
     B = 530 if nodes == 1 else 300
@@ -255,21 +271,23 @@ def test_tree_many_conversations(p, nodes):
     check_tree(*make_tree(24 + nodes, B, nodes, 2, 1, 64, p, lens, 16, "random"))
 
 
-def test_tree_windows_that_cut_nothing():
+@pytest.mark.parametrize("p", [150, 2900])
+def test_tree_windows_that_cut_nothing(p):
     """Up to the largest window, bit for bit as without one."""
-    t, table, lens, parents = make_tree(26, 3, 40, 8, 2, 64, 150, (90, 0, 301), 16, "random")
+    t, table, lens, parents = make_tree(26, 3, 40, 8, 2, 64, p, (90, 0, 301), 16, "random")
     want, _ = run_tree(t, table, lens, parents)
-    for window in (600, 2 ** 24 - 1, 2 ** 24, 2 ** 31 - 1):
+    for window in (p + 600, 2 ** 24 - 1, 2 ** 24, 2 ** 31 - 1):
         o, _ = run_tree(t, table, lens, parents, window=window)
         assert torch.equal(o, want), window
     assert ca.device_status(clear=True) == 0
 
 
-def test_tree_largest_batch():
+@pytest.mark.parametrize("p", [3, 600])
+def test_tree_largest_batch(p):
     """The most conversations a call takes, a few of them checked."""
     B = 65535
     lens = np.random.default_rng(27).integers(-1, 15, B)
-    t, table, lens, _ = make_tree(27, B, 1, 2, 1, 64, 3, lens, 16, "chain")
+    t, table, lens, _ = make_tree(27, B, 1, 2, 1, 64, p, lens, 16, "chain")
     o, _ = run_tree(t, table, lens, None)
     assert ca.device_status(clear=True) == 0
     some = np.r_[0, 1, 255, 256, 257, 32767, 65533, 65534, np.arange(5, B, 997)]
@@ -286,9 +304,10 @@ def test_tree_most_heads():
     check_tree(*make_tree(28, 1, 64, 1024, 128, 64, 130, (140,), 16, "wide"))
 
 
-def test_tree_large_logits():
+@pytest.mark.parametrize("p", [200, 900])
+def test_tree_large_logits(p):
     """Logits of hundreds: the weights are all on a few keys."""
-    t, table, lens, parents = make_tree(23, 2, 9, 4, 2, 64, 200, (90, 300), 32, "random")
+    t, table, lens, parents = make_tree(23, 2, 9, 4, 2, 64, p, (90, 300), 32, "random")
     t["q"] = (t["q"].float() * 64).to(torch.bfloat16)
     o, g = run_tree(t, table, lens, parents)
     assert torch.isfinite(o).all()
@@ -785,8 +804,9 @@ def test_calls_on_another_stream():
     assert torch.equal(o, want)
 
 
-def test_tree_repeats_bit_for_bit():
-    t, table, lens, parents = make_tree(53, 9, 24, 16, 2, 128, 700,
+@pytest.mark.parametrize("nodes", [24, 4])
+def test_tree_repeats_bit_for_bit(nodes):
+    t, table, lens, parents = make_tree(53, 9, nodes, 16, 2, 128, 700,
                                         (3, 400, 0, 170, 1000, 5, 90, 333, 64), 32, "random")
     a, _ = run_tree(t, table, lens, parents)
     for _ in range(3):
@@ -794,9 +814,10 @@ def test_tree_repeats_bit_for_bit():
         assert torch.equal(a, b)
 
 
-def test_tree_calls_do_not_share_scratch():
+@pytest.mark.parametrize("p", [500, 1500])
+def test_tree_calls_do_not_share_scratch(p):
     """Two calls in flight on two streams, each with a workspace of its own."""
-    cases = [make_tree(60 + i, 6, 12, 8, 2, 128, 500, (900, 2, 77, 300, 0, 640), 64, "random")
+    cases = [make_tree(60 + i, 6, 12, 8, 2, 128, p, (900, 2, 77, 300, 0, 640), 64, "random")
              for i in range(2)]
     want = [run_tree(*c)[0] for c in cases]
     gs = [{k: v.cuda() for k, v in c[0].items()} for c in cases]

@@ -15,12 +15,12 @@
 // the node, hh the head of the group): R = nodes*G rows that see the same
 // cached keys.  A segment is up to 128 of them, or 256 (two query tiles that
 // share the staged keys) where R is above 128, with the key tiles they walk:
-//   fused    (R near 256 or above, or B == 1, or p == 0) cartridge tiles, then the
-//            conversation's own rows, cached and new: one segment per
-//            (conversation, kv head, 128 or 256 rows).
-//   stacked  (else) the rows of all conversations, stacked, against the
-//            cartridge, so that its tiles meet full query tiles; and one
-//            segment per (conversation, kv head) against its own rows.
+//   fused    cartridge tiles, then the conversation's own rows, cached and new:
+//            one segment per (conversation, kv head, 128 or 256 rows).
+//   stacked  (where that saves enough cartridge tiles, see tree_ws) the rows of
+//            all conversations, stacked, against the cartridge, so that its
+//            tiles meet full query tiles; and one segment per (conversation,
+//            kv head) against its own rows.
 // New rows lie behind the cached ones in the same pages, so they share the
 // last tiles; a row's ancestor set masks them.
 //
@@ -910,7 +910,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
   } else {
     // ------------------------------------------------------------- softmax --
     pdl_wait();
-    const int x = warp >> 2;  // the stream
+    const int x = NT == 1 ? 0 : warp >> 2;  // the stream
     const int row = threadIdx.x & 127;  // TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + x * 128 + lane_off;
@@ -1057,7 +1057,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
           if (__any_sync(0xffffffffu, rescale)) {
             // (the stream's last PV has completed: the commit that published
             // this S follows it)
-#pragma unroll
+#pragma unroll 1
             for (int blk = 0; blk < D / 32; ++blk) {
               uint32_t v[32];
               tmem_ld32(tO + blk * 32, v);
@@ -1340,13 +1340,6 @@ TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
   };
   const size_t n = static_cast<size_t>(B) * nodes;
   w.R = nodes * (Hq / Hkv);
-  // Stacking fills the query tiles that walk the cartridge with rows of
-  // several conversations, but its segments have to be joined with those of
-  // the own rows; near 256 rows there is little left to fill.  64
-  // conversations behind 4096 rows, stacked against fused: R = 132 208 us
-  // against 234, R = 160 226 against 238, R = 192 257 against 247, R = 224 296
-  // against 252.
-  w.stacked = p > 0 && B > 1 && 4 * w.R < 3 * 2 * kTile;
   // Up to 128 rows: one query tile per CTA and two CTAs per SM, so that one
   // covers the other's starts and ends, although the cartridge is then staged
   // twice as often (24 nodes, G = 4, 8192 rows: 210 us against 219 with two
@@ -1354,6 +1347,17 @@ TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
   // against 270 us; 25 nodes, G = 8, 49k rows: 135 against 164).
   w.rt = w.R > kTile ? 2 * kTile : kTile;
   w.segs = (w.R + w.rt - 1) / w.rt;
+  // Stacking fills the query tiles that walk the cartridge with rows of
+  // several conversations, which saves cartridge tiles; but then a conversation
+  // has a segment more, and all rows have to be joined: about as much as 3 +
+  // R/40 tiles of it.  Stacked against fused in us, 64 conversations, G = 4:
+  // p = 1024, R = 4 47, 60; R = 64 72, 68; R = 96 88, 74; R = 160 132, 107;
+  // p = 4096, R = 4 49, 118; R = 64 99, 125; R = 96 132, 133; R = 160 188, 204;
+  // R = 192 216, 212.  Over p = 128 to 4096, 2 to 64 conversations and R = 4 to
+  // 192 the rule loses 0.6 % against the better of the two, at most 13 %.
+  const long long row_tiles = (static_cast<long long>(B) * w.R + w.rt - 1) / w.rt;
+  const long long cart_tiles = (p + kTile - 1) / kTile;
+  w.stacked = B > 1 && w.segs == 1 && 40 * cart_tiles * (B - row_tiles) > (120ll + w.R) * B;
   w.qr = take(n * Hq * d * 2);
   w.set = take(n * sizeof(NodeSet));
   // partial outputs: a slot per segment and cut, or two per run
