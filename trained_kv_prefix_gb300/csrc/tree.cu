@@ -589,12 +589,12 @@ __device__ __forceinline__ void clean_v_row(uint32_t sv, int row, VRow kind, int
 // what the tensor core multiplies.
 //
 // Bound by the tensor pipe where queries are many: 64 conversations with 64
-// nodes behind 4096 rows, 215 us alone, pipe active for 65 % of the time, 1475
+// nodes behind 4096 rows, 198 us alone, pipe active for 71 % of the time, 1600
 // TFLOP/s with the masked products (the rest is the exchange of S and P
 // between a stream's products and its softmax, and pieces' starts and ends);
-// four conversations with 25 nodes, G = 8, over 49k rows 115 us, 590 MB, 5.1
-// TB/s, pipe active for 64 %.  Single tokens, 64 conversations: 46 us, 172 MB,
-// 3.7 TB/s; there the loads of a CTA's next tile wait for the products of the
+// four conversations with 25 nodes, G = 8, over 49k rows 114 us, 589 MB, 5.2
+// TB/s, pipe active for 68 %.  Single tokens, 64 conversations: 42 us, 170 MB,
+// 4.0 TB/s; there the loads of a CTA's next tile wait for the products of the
 // one before, with 64 KB of keys and values per CTA.
 template <int D, int NT>
 __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
@@ -1342,9 +1342,10 @@ TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
   w.R = nodes * (Hq / Hkv);
   // Up to 128 rows: one query tile per CTA and two CTAs per SM, so that one
   // covers the other's starts and ends, although the cartridge is then staged
-  // twice as often (24 nodes, G = 4, 8192 rows: 210 us against 219 with two
-  // tiles per CTA).  Above: two tiles that share the keys (64 nodes: 252
-  // against 270 us; 25 nodes, G = 8, 49k rows: 135 against 164).
+  // twice as often (in us, one against two tiles per CTA, 64 conversations, G =
+  // 4: 24 nodes behind 4096 rows 134, 136, behind 8192 rows 195, 188; 32 nodes
+  // 138, 161).  Above: two tiles that share the keys (40 nodes 242, 193; 64
+  // nodes 254, 224; 25 nodes, G = 8, 49k rows 152, 118).
   w.rt = w.R > kTile ? 2 * kTile : kTile;
   w.segs = (w.R + w.rt - 1) / w.rt;
   // Stacking fills the query tiles that walk the cartridge with rows of
