@@ -428,8 +428,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 class _On:
     """Where a call on a paged cache runs: on ``device``, made current while
-    it is not, and on ``stream`` or the device's current one.  What the call
-    allocates is kept for the stream that uses it."""
+    it is not, and on ``stream`` or the device's current one."""
 
     __slots__ = ("device", "guard", "stream", "handle")
 
@@ -439,6 +438,8 @@ class _On:
         index = device.index
         if device.type != "cuda":
             raise ValueError(f"tensors must be on a GPU, not on {device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream must be one of {device}, not of {stream.device}")
         if index != torch.cuda.current_device():
             self.guard = torch.cuda.device(device)
             self.guard.__enter__()
@@ -448,9 +449,15 @@ class _On:
             self.stream, self.handle = stream, stream.cuda_stream
 
     def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.stream is not None:
-            t.record_stream(self.stream)
+        """Memory of the stream that the call's kernels run on: the current
+        stream's could be a block that it has freed and is still working on.
+        It is kept for the current stream too, which reads what the call
+        returns."""
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
     def close(self):
