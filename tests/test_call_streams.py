@@ -130,6 +130,41 @@ PAGED = {
 }
 
 
+def leaves():
+    return new(5, 2, 64, dtype=F32), new(5, 2, 64, dtype=F32)
+
+
+def seqs():
+    return new(3, 4, 8, 64), new(3, 4, 2, 64), new(3, 4, 2, 64)
+
+
+def packed():
+    return new(12, 8, 64), new(12, 2, 64), new(12, 2, 64)
+
+
+DENSE = {
+    "fwd": lambda **kw: ca.cart_attn_fwd(*seqs(), *leaves(), **kw),
+    "bwd": lambda **kw: ca.cart_attn_bwd(*seqs(), *leaves(), seqs()[0], new(3, 8, 4, dtype=F32),
+                                         seqs()[0], accumulate=True, **kw),
+    "bwd_parts": lambda **kw: ca.cart_attn_bwd(*seqs(), *leaves(), seqs()[0],
+                                               new(3, 8, 4, dtype=F32), seqs()[0],
+                                               frozen_rows=[2], **kw),
+    "bwd_reuse": lambda **kw: ca.cart_attn_bwd(*seqs(), *leaves(), seqs()[0],
+                                               new(3, 8, 4, dtype=F32), seqs()[0],
+                                               fwd_workspace=new(99, dtype=torch.uint8), **kw),
+    "fwd_packed": lambda **kw: ca.cart_attn_fwd_packed(*packed(), *leaves(), ints(4), 4, **kw),
+    "bwd_packed": lambda **kw: ca.cart_attn_bwd_packed(*packed(), *leaves(), packed()[0],
+                                                       new(8, 12, dtype=F32), packed()[0], ints(4),
+                                                       4, accumulate=True, **kw),
+    "decode": lambda **kw: ca.cart_attn_decode(new(3, 8, 64), new(3, 2, 64), new(3, 2, 64),
+                                               new(5, 2, 64), new(5, 2, 64), new(3, 9, 2, 64),
+                                               new(3, 9, 2, 64), ints(3), **kw),
+    "decode_span": lambda **kw: ca.cart_attn_decode_span(*seqs(), new(5, 2, 64), new(5, 2, 64),
+                                                         new(3, 9, 2, 64), new(3, 9, 2, 64),
+                                                         ints(3), **kw),
+}
+
+
 def check(fake, call):
     """All that the call makes is memory of the stream that its kernels run on;
     what it returns is kept for the caller's current stream too, which reads
@@ -150,6 +185,11 @@ def check(fake, call):
 @pytest.mark.parametrize("name", PAGED)
 def test_paged_calls_allocate_on_their_stream(fake, name):
     check(fake, PAGED[name])
+
+
+@pytest.mark.parametrize("name", DENSE)
+def test_dense_calls_allocate_on_their_stream(fake, name):
+    check(fake, DENSE[name])
 
 
 @pytest.mark.parametrize("name", PAGED)

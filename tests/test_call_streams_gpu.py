@@ -1,5 +1,5 @@
-"""The paged calls on a stream that the caller names, while the current stream
-still has work to do on memory that it has freed."""
+"""Calls on a stream that the caller names, while the current stream still has
+work to do on memory that it has freed."""
 import numpy as np
 import pytest
 import torch
@@ -7,6 +7,7 @@ import torch
 from tests import paged_reference as ref
 from tests.test_paged_gpu import _i32, _pool, make_tables, make_tree, run_tree
 from trained_kv_prefix_gb300 import cartattn as ca
+from trained_kv_prefix_gb300 import synth
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +106,39 @@ def test_fork_beside_a_busy_stream(busy):
     torch.cuda.synchronize()
     for got, w in zip((tb, ln, rf, done), want):
         np.testing.assert_array_equal(got.cpu().numpy(), w)
+
+
+def test_training_step_beside_a_busy_stream(busy):
+    """Forward and backward that add to gradients of their own: the same bits
+    as on the current stream."""
+    s = synth.TrainShape("side", B=2, n=150, Hq=4, Hkv=2, d=64, p=40, dtype="bf16", seed=74)
+    g = {k: v.cuda() for k, v in synth.train_inputs(s).items()}
+    args = [g[k] for k in ("q", "k", "v", "kc", "vc")]
+
+    def step(**kw):
+        o, lse = ca.cart_attn_fwd(*args, **kw)
+        return (o, lse) + ca.cart_attn_bwd(*args, o, lse, g["do"], accumulate=True, **kw)
+
+    want = step()
+    side = torch.cuda.Stream()
+    geom = ca.geom(2, 150, 4, 2, 64, 40)
+    busy(ca.fwd_workspace_size(geom, 0, 1), ca.bwd_workspace_size(geom, 0, 1),
+         *(t.numel() * t.element_size() for t in want))
+    got = step(stream=side)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert ca.device_status(clear=True) == 0
+
+
+def test_decode_step_beside_a_busy_stream(busy):
+    s = synth.DecodeShape("side", B=3, Hq=4, Hkv=2, d=128, p=400, max_private=90, seed=75,
+                          fixed_len=(0, 7, 90))
+    g = {k: v.cuda() for k, v in synth.decode_inputs(s).items()}
+    args = [g[k] for k in ("q", "k_new", "v_new", "kc", "vc", "k_cache", "v_cache", "lens")]
+    want = ca.cart_attn_decode(*args)
+    side = torch.cuda.Stream()
+    busy(ca.decode_workspace_size(3, 4, 2, 128, 400, g["k_cache"].shape[1]), want.numel() * 2)
+    got = ca.cart_attn_decode(*args, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

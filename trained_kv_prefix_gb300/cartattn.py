@@ -174,10 +174,24 @@ def geom(B, n, Hq, Hkv, d, p, frozen_prefix=1, scale=None, theta=1.0e6, window=0
     return _Geom(B, n, Hq, Hkv, d, p, frozen_prefix, float(scale), float(theta), int(window))
 
 
-def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
+def _make(stream, make, *args, **kwargs):
+    """``make(*args, **kwargs)``, a tensor that a call on ``stream`` (None: the
+    current one) works on: allocated, and filled, on that stream, since the
+    current stream's memory could be a block that it has freed and is still
+    working on; and kept for the current stream too, which reads what the call
+    returns."""
+    if stream is None:
+        return make(*args, **kwargs)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kwargs)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor], stream) -> torch.Tensor:
     if workspace is not None and workspace.numel() * workspace.element_size() >= nbytes:
         return workspace
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    return _make(stream, torch.empty, max(nbytes, 16), dtype=torch.uint8, device=device)
 
 
 # ------------------------------------------------------------------ calls ----
@@ -213,10 +227,10 @@ def cart_attn_fwd(q, k, v, kc, vc, *, frozen_prefix=1, scale=None, theta=1.0e6, 
     g = geom(B, n, Hq, Hkv, d, p, min(frozen_prefix, p), scale, theta, window)
     dt, cd = _dt(q), _dt(kc)
     if o is None:
-        o = torch.empty_like(q)
+        o = _make(stream, torch.empty_like, q)
     if lse is None:
-        lse = torch.empty((B, Hq, n), dtype=torch.float32, device=q.device)
-    ws = _workspace(fwd_workspace_size(g, dt, cd), q.device, workspace)
+        lse = _make(stream, torch.empty, (B, Hq, n), dtype=torch.float32, device=q.device)
+    ws = _workspace(fwd_workspace_size(g, dt, cd), q.device, workspace, stream)
     rc = lib().cart_attn_fwd(ctypes.byref(g), dt, cd, _ptr(q), _ptr(k), _ptr(v), _ptr(kc),
                              _ptr(vc), _ptr(o), _ptr(lse), _ptr(ws), ws.numel(),
                              _stream(stream, q.device))
@@ -240,20 +254,20 @@ def cart_attn_bwd(q, k, v, kc, vc, o, lse, dout, *, frozen_prefix=1, scale=None,
     p = kc.shape[0]
     g = geom(B, n, Hq, Hkv, d, p, frozen_prefix, scale, theta, window)
     dt, cd = _dt(q), _dt(kc)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _make(stream, torch.empty_like, q) if dq is None else dq
+    dk = _make(stream, torch.empty_like, k) if dk is None else dk
+    dv = _make(stream, torch.empty_like, v) if dv is None else dv
     if dkc is None:
-        dkc = (torch.zeros if accumulate else torch.empty)((max(p, 1), Hkv, d),
-                                                           dtype=torch.float32, device=q.device)
+        dkc = _make(stream, torch.zeros if accumulate else torch.empty, (max(p, 1), Hkv, d),
+                    dtype=torch.float32, device=q.device)
     if dvc is None:
-        dvc = (torch.zeros if accumulate else torch.empty)((max(p, 1), Hkv, d),
-                                                           dtype=torch.float32, device=q.device)
+        dvc = _make(stream, torch.zeros if accumulate else torch.empty, (max(p, 1), Hkv, d),
+                    dtype=torch.float32, device=q.device)
     if fwd_workspace is not None:
         if frozen_rows is not None:
             raise ValueError("fwd_workspace does not combine with frozen_rows")
         ws = _workspace(int(lib().cart_attn_bwd_reuse_workspace_size(ctypes.byref(g), dt, cd)),
-                        q.device, workspace)
+                        q.device, workspace, stream)
         rc = lib().cart_attn_bwd_reuse(ctypes.byref(g), dt, cd, _ptr(q), _ptr(k), _ptr(v),
                                        _ptr(kc), _ptr(vc), _ptr(o), _ptr(lse), _ptr(dout),
                                        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dkc), _ptr(dvc),
@@ -262,7 +276,7 @@ def cart_attn_bwd(q, k, v, kc, vc, o, lse, dout, *, frozen_prefix=1, scale=None,
                                        _stream(stream, q.device))
         _check("cart_attn_bwd_reuse", rc)
         return dq, dk, dv, dkc[:p], dvc[:p]
-    ws = _workspace(bwd_workspace_size(g, dt, cd), q.device, workspace)
+    ws = _workspace(bwd_workspace_size(g, dt, cd), q.device, workspace, stream)
     if frozen_rows is None:
         rc = lib().cart_attn_bwd(ctypes.byref(g), dt, cd, _ptr(q), _ptr(k), _ptr(v), _ptr(kc),
                                  _ptr(vc), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
@@ -315,10 +329,10 @@ def cart_attn_fwd_packed(q, k, v, kc, vc, cu_seqlens, max_seqlen, *, frozen_pref
     g = geom(S, n, Hq, Hkv, d, p, min(frozen_prefix, p), scale, theta, window)
     dt, cd = _dt(q), _dt(kc)
     if o is None:
-        o = torch.empty_like(q)
+        o = _make(stream, torch.empty_like, q)
     if lse is None:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-    ws = _workspace(fwd_packed_workspace_size(g, T, dt, cd), q.device, workspace)
+        lse = _make(stream, torch.empty, (Hq, T), dtype=torch.float32, device=q.device)
+    ws = _workspace(fwd_packed_workspace_size(g, T, dt, cd), q.device, workspace, stream)
     rc = lib().cart_attn_fwd_packed(ctypes.byref(g), T, _ptr(cu_seqlens), dt, cd, _ptr(q),
                                     _ptr(k), _ptr(v), _ptr(kc), _ptr(vc), _ptr(o), _ptr(lse),
                                     _ptr(ws), ws.numel(), _stream(stream, q.device))
@@ -339,16 +353,16 @@ def cart_attn_bwd_packed(q, k, v, kc, vc, o, lse, dout, cu_seqlens, max_seqlen, 
     p = kc.shape[0]
     g = geom(S, n, Hq, Hkv, d, p, frozen_prefix, scale, theta, window)
     dt, cd = _dt(q), _dt(kc)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _make(stream, torch.empty_like, q) if dq is None else dq
+    dk = _make(stream, torch.empty_like, k) if dk is None else dk
+    dv = _make(stream, torch.empty_like, v) if dv is None else dv
     if dkc is None:
-        dkc = (torch.zeros if accumulate else torch.empty)((max(p, 1), Hkv, d),
-                                                           dtype=torch.float32, device=q.device)
+        dkc = _make(stream, torch.zeros if accumulate else torch.empty, (max(p, 1), Hkv, d),
+                    dtype=torch.float32, device=q.device)
     if dvc is None:
-        dvc = (torch.zeros if accumulate else torch.empty)((max(p, 1), Hkv, d),
-                                                           dtype=torch.float32, device=q.device)
-    ws = _workspace(bwd_packed_workspace_size(g, T, dt, cd), q.device, workspace)
+        dvc = _make(stream, torch.zeros if accumulate else torch.empty, (max(p, 1), Hkv, d),
+                    dtype=torch.float32, device=q.device)
+    ws = _workspace(bwd_packed_workspace_size(g, T, dt, cd), q.device, workspace, stream)
     rows = list(frozen_rows)
     arr = (ctypes.c_int * max(len(rows), 1))(*rows)
     rc = lib().cart_attn_bwd_packed(ctypes.byref(g), T, _ptr(cu_seqlens), dt, cd, _ptr(q),
@@ -379,8 +393,8 @@ def cart_attn_decode(q, k_new, v_new, kc, vc, k_cache, v_cache, lens, *, scale=N
     if lens.dtype != torch.int32:
         raise TypeError("lens must be int32")
     if o is None:
-        o = torch.empty_like(q)
-    ws = _workspace(decode_workspace_size(B, Hq, Hkv, d, p, rows), q.device, workspace)
+        o = _make(stream, torch.empty_like, q)
+    ws = _workspace(decode_workspace_size(B, Hq, Hkv, d, p, rows), q.device, workspace, stream)
     rc = lib().cart_attn_decode(B, Hq, Hkv, d, p, float(scale), float(theta), _ptr(q),
                                 _ptr(k_new), _ptr(v_new), _ptr(kc), _ptr(vc), _ptr(k_cache),
                                 _ptr(v_cache), rows, _ptr(lens), _ptr(o), _ptr(ws), ws.numel(),
@@ -409,8 +423,9 @@ def cart_attn_decode_span(q, k_new, v_new, kc, vc, k_cache, v_cache, lens, *, sc
     if lens.dtype != torch.int32:
         raise TypeError("lens must be int32")
     if o is None:
-        o = torch.empty_like(q)
-    ws = _workspace(decode_span_workspace_size(B, span, Hq, Hkv, d, p, rows), q.device, workspace)
+        o = _make(stream, torch.empty_like, q)
+    ws = _workspace(decode_span_workspace_size(B, span, Hq, Hkv, d, p, rows), q.device, workspace,
+                    stream)
     rc = lib().cart_attn_decode_span(B, span, int(window), Hq, Hkv, d, p, float(scale),
                                      float(theta), _ptr(q),
                                      _ptr(k_new), _ptr(v_new), _ptr(kc), _ptr(vc),
