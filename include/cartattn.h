@@ -353,8 +353,9 @@ CART_API int cart_attn_decode_noalloc(int B, int Hq, int Hkv, int d, int p, floa
  * and its value are written to private row lens[b] + t, and it attends to
  * the cartridge, private rows 0 .. lens[b] - 1 (at positions p + row), its
  * ancestors and itself; with window > 0, to those of them at its last
- * `window` positions (as in cart_geom).  Other nodes' values, whatever they
- * hold, do not reach it.
+ * `window` positions (as in cart_geom).  Keys and values that it does not
+ * attend to, other nodes' and cached rows' that its window has left behind,
+ * do not reach it, whatever they hold (but for the cartridge's, above).
  * A node is unused when its row has no page, or its parent is neither -1
  * nor an earlier used node (-2 by convention pads a ragged tree): its o is
  * 0, its row is not written, and no node attends to it.  An unused node

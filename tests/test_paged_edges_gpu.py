@@ -1,0 +1,101 @@
+"""Edges of the paged operators on the GPU, against the plain 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+from tests import paged_reference as ref
+from tests.test_paged_gpu import check_tree, make_tree, run_tree
+from trained_kv_prefix_gb300 import cartattn as ca
+from trained_kv_prefix_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+
+BAD = (float("inf"), -float("inf"), float("nan"))
+
+WINDOWS = [
+    # id, B, nodes, Hq, Hkv, d, p, lens, P, kind, window
+    ("chain", 1, 2, 4, 2, 64, 30, (77,), 16, "chain", 40),
+    ("window_in_tree", 2, 8, 4, 2, 128, 30, (77, 3), 16, "chain", 5),
+    ("across_tiles", 2, 40, 2, 2, 64, 50, (240, 390), 32, "chain", 128),
+    ("two_query_tiles", 2, 64, 8, 1, 128, 64, (190, 400), 64, "random", 100),
+    ("most_nodes", 1, 64, 2, 2, 64, 0, (500,), 16, "chain", 400),
+    ("from_the_cartridge", 3, 30, 4, 2, 64, 64, (60, 20, 75), 16, "chain", 70),
+    ("stacked", 6, 9, 8, 2, 128, 1200, (100, 300, 129, 250, 64, 31), 16, "chain", 60),
+    ("cut_among_ctas", 1, 12, 8, 2, 128, 30, (9003,), 128, "chain", 8800),
+    ("tree", 2, 33, 4, 1, 64, 40, (100, 300), 32, "wide", 90),
+]
+
+
+@pytest.mark.parametrize("case", WINDOWS, ids=[c[0] for c in WINDOWS])
+@pytest.mark.parametrize("with_key", [False, True])
+def test_values_that_a_deeper_node_has_left_behind(case, with_key):
+    """Cached rows in the window of the shallowest node and out of a deeper
+    one's that are not finite: they reach the nodes that see them, in the
+    elements that are not finite, and no other."""
+    _, B, nodes, Hq, Hkv, d, p, lens, P, kind, window = case
+    t, table, lens, parents = make_tree(81, B, nodes, Hq, Hkv, d, p, lens, P, kind)
+    t["v_pages"], t["k_pages"] = t["v_pages"].clone(), t["k_pages"].clone()
+    n = 0
+    for b in range(B):
+        for r in range(max(lens[b] - window, 0), min(lens[b] - window + nodes + 2, lens[b])):
+            page, row = table[b, r // P], r % P
+            t["v_pages"][page, row, r % Hkv, 5 * r % d] = BAD[r % 3]
+            n += 1
+        if with_key:
+            r = lens[b] - window + 1
+            if 0 <= r < lens[b]:
+                t["k_pages"][table[b, r // P], r % P, 0, 3] = float("nan")
+    assert n > 1
+    o, g = run_tree(t, table, lens, parents, window=window)
+    assert ca.device_status(clear=True) == 0
+    a = {k: synth.f64(v) for k, v in t.items()}
+    with np.errstate(invalid="ignore"):
+        o_ref, bound, _ = ref.tree(**a, table=table, lens=lens, parents=parents, window=window)
+    got, finite = synth.f64(o), np.isfinite(o_ref)
+    assert finite.any() and not finite.all()
+    np.testing.assert_array_equal(got[~finite], o_ref[~finite])
+    assert (np.abs(got[finite] - o_ref[finite]) <= bound[finite]).all()
+    # the cached rows stay as they are
+    for b in range(B):
+        for r in range(lens[b]):
+            at = table[b, r // P], r % P
+            np.testing.assert_array_equal(synth.f64(g["v_pages"][at]), a["v_pages"][at])
+
+
+def test_window_of_single_tokens_equals_their_chain():
+    """A chain with a window is the single-token steps in order, whatever the
+    rows that each step has left behind hold."""
+    window, nodes = 40, 6
+    t, table, lens, parents = make_tree(82, 2, nodes, 4, 2, 64, 30, (77, 160), 16, "chain")
+    t["v_pages"] = t["v_pages"].clone()
+    for b in range(2):
+        for i in range(nodes):
+            r = lens[b] - window + 1 + i
+            t["v_pages"][table[b, r // 16], r % 16, 0, i] = BAD[i % 3]
+    o, _ = run_tree(t, table, lens, parents, window=window)
+    a = {k: synth.f64(v) for k, v in t.items()}
+    with np.errstate(invalid="ignore"):
+        _, bound, _ = ref.tree(**a, table=table, lens=lens, parents=parents, window=window)
+    g = {k: v.cuda() for k, v in t.items()}
+    tb = torch.tensor(table, dtype=torch.int32, device="cuda")
+    for i in range(nodes):
+        ln = torch.tensor(lens + i, dtype=torch.int32, device="cuda")
+        one = ca.cart_attn_decode_tree(*(g[k][:, i:i + 1].contiguous() for k in
+                                         ("q", "k_new", "v_new")), g["kc"], g["vc"], g["k_pages"],
+                                       g["v_pages"], tb, ln, window=window)
+        x, y = synth.f64(one[:, 0]), synth.f64(o[:, i])
+        same = np.isfinite(x)
+        np.testing.assert_array_equal(np.isfinite(y), same)
+        np.testing.assert_array_equal(x[~same], y[~same])
+        # each within its bound of one value
+        assert (np.abs(x[same] - y[same]) <= 2 * bound[:, i][same]).all()
+    assert ca.device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("window", [1, 5, 39, 40, 90])
+def test_windows_of_idle_empty_and_full_conversations(window):
+    t, table, lens, parents = make_tree(83, 4, 40, 4, 2, 64, 30, (50, 0, 8, 60), 16, "random")
+    lens[0] = -1
+    check_tree(t, table, lens, parents, window=window)
+    lens[3] = table.shape[1] * 16           # no node of it fits
+    check_tree(t, table, lens, parents, window=window, status=128)

@@ -46,11 +46,16 @@
 namespace cart {
 namespace {
 
+// What a staged V row needs before the products read it; else it has a value
+// that is not finite (in any kv head), and this is its bit of Piece::bad.
+constexpr int kVKeep = -1, kVZero = -2;
+
 // A node's ancestors and itself (0: unused), those of them in its window, and
-// whether a value of the node (in any kv head) is not finite.
+// what its V row needs; with a window also what cached row first_row() + i
+// needs, where the node is the i-th.
 struct NodeSet {
   unsigned long long anc, vis;
-  unsigned bad, pad;
+  int row, cached;
 };
 
 struct TreeArgs {
@@ -83,6 +88,11 @@ struct Turns {
   float2 t[kMaxHeadDim / 2];
 };
 
+// First row in the window of a conversation's shallowest node (below 0: in the
+// cartridge).  The node with D ancestors sees from D rows further on, so all
+// nodes see the rows from nodes - 1 further on.
+__device__ __forceinline__ int first_row(const TreeArgs& a, int len) { return len - a.window + 1; }
+
 // ------------------------------------------------------------- schedule ----
 // Key tiles of conversation b's own segments (n == 0: it has no used node):
 // cartridge tiles cart_lo .. n_ct - 1 (fused only), then tiles of 128 own rows
@@ -95,7 +105,7 @@ __device__ __forceinline__ ConvTiles conv_tiles_of(const TreeArgs& a, int len) {
   c.len = len;
   const int rows = a.pt.max_pages << a.pt.page_log2, n_ct = (a.p + kTile - 1) / kTile;
   // position of the first key that the shallowest node sees
-  const int lo = a.window > 0 ? a.p + c.len - a.window + 1 : 0;
+  const int lo = a.window > 0 ? a.p + first_row(a, c.len) : 0;
   c.first_cart = lo > 0 ? min(lo / kTile, n_ct) : 0;
   c.n_cart = a.stacked ? 0 : n_ct - c.first_cart;
   c.row_lo = lo > a.p ? (lo - a.p) / kTile : 0;
@@ -255,6 +265,8 @@ struct PrepShape {
   static constexpr int kBatch = 2;           // of them in flight
 };
 constexpr int kPrepNodes = 8;  // most nodes per block
+// blocks per conversation of note_cached_rows
+__host__ __device__ __forceinline__ int cached_blocks(int nodes) { return (nodes - 1 + 7) / 8; }
 
 // Whether one of two packed bf16 values is not finite.
 __device__ __forceinline__ bool not_finite(uint32_t w) {
@@ -281,13 +293,35 @@ __device__ __forceinline__ void rotate8(uint4& x, uint4& y, const float2* c, int
   y = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// Block 0 writes the spans; block 1 + i the nodes t0 .. t0 + per - 1 of one
+// Eight of the nodes - 1 cached rows of a conversation that some nodes see and
+// others do not, a warp per row: whether a value of it is not finite.
+template <int D>
+__device__ __forceinline__ void note_cached_rows(const TreeArgs& a, int block) {
+  const int blocks = cached_blocks(a.nodes), b = block / blocks;
+  const int i = block % blocks * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (i >= a.nodes - 1) return;
+  const int len = held_rows(a.pt, b), r = first_row(a, len) + i;
+  const int page = r < len ? page_of(a.pt, b, r) : -1;
+  bool bad = false;
+  if (page >= 0) {
+    const uint4* v = reinterpret_cast<const uint4*>(
+        a.v_pages + ((static_cast<long long>(page) << a.pt.page_log2) +
+                     (r & ((1 << a.pt.page_log2) - 1))) * a.Hkv * D);
+#pragma unroll 4
+    for (int e = lane; e < a.Hkv * D / 8; e += 32) bad |= not_finite(__ldcg(v + e));
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0) a.set[b * a.nodes + i].cached = bad ? kMaxNodes + i : kVKeep;
+}
+
+// Block 0 writes the spans; with a window, the next ones look through cached
+// rows; each of the others prepares the nodes t0 .. t0 + per - 1 of one
 // conversation.  Bound by latency for a few nodes (lengths, pages, parents
 // and the rows are loaded side by side): 7 us alone for 64 conversations with
 // one node; by the rows' traffic for many: 64 nodes, G = 4, 101 MB in and out,
 // 22.6 us, 4.5 TB/s.  (More rows in flight, other launch bounds or other nodes
 // per block move a call by 2 % either way.)
-template <int D>
+template <int D, bool kWindow>
 __global__ void __launch_bounds__(256, 4) tree_prep_kernel(const __grid_constant__ TreeArgs a,
                                                         const __grid_constant__ Turns f, int per) {
   using S = PrepShape<D>;
@@ -301,7 +335,16 @@ __global__ void __launch_bounds__(256, 4) tree_prep_kernel(const __grid_constant
   __shared__ float2 cs[kPrepNodes][HALF];
   __shared__ int page_s[kPrepNodes], bad_s[kPrepNodes];
   const int blocks = (a.nodes + per - 1) / per;  // per conversation
-  const int b = (blockIdx.x - 1) / blocks, t0 = (blockIdx.x - 1) % blocks * per;
+  int block = blockIdx.x - 1;
+  if (kWindow) {
+    const int cached = a.B * cached_blocks(a.nodes);
+    if (block < cached) {
+      note_cached_rows<D>(a, block);
+      return;
+    }
+    block -= cached;
+  }
+  const int b = block / blocks, t0 = block % blocks * per;
   const int mine = min(per, a.nodes - t0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long bt0 = static_cast<long long>(b) * a.nodes + t0;
@@ -337,7 +380,7 @@ __global__ void __launch_bounds__(256, 4) tree_prep_kernel(const __grid_constant
     if (lost && len >= 0) atomicOr(a.status, kDevErrNoPage);
     // nearer ancestors have higher numbers: a window keeps the top ones
     unsigned long long vis = anc;
-    if (a.window > 0)
+    if (kWindow)
       for (int n = __popcll(vis); n > a.window; --n) vis &= vis - 1;
     a.set[bt0 + node - t0].anc = anc;
     a.set[bt0 + node - t0].vis = vis;
@@ -383,7 +426,10 @@ __global__ void __launch_bounds__(256, 4) tree_prep_kernel(const __grid_constant
     }
   }
   __syncthreads();
-  if (threadIdx.x < mine) a.set[bt0 + threadIdx.x].bad = bad_s[threadIdx.x];
+  if (threadIdx.x < mine) {
+    const int t = t0 + threadIdx.x;
+    a.set[bt0 + threadIdx.x].row = !tree.anc[t] ? kVZero : bad_s[threadIdx.x] ? t : kVKeep;
+  }
 }
 
 // --------------------------------------------------------------- attend ----
@@ -420,7 +466,9 @@ struct Piece {
   int cart_lo, row_lo, t0;
   int ring;        // K/V ring position of its first tile
   int slot;        // partial output, -1: the final output
-  unsigned bad[2]; // new rows whose value is not finite
+  // values that are not finite: of new rows (by node), and of the cached rows
+  // that some nodes' windows hold and others' do not (see v_row_kind)
+  unsigned bad[4];
 };
 
 enum TreeBar {
@@ -537,36 +585,32 @@ __device__ __forceinline__ bool next_piece(const TreeArgs& a, Walk& w, Piece& o)
   return false;
 }
 
-// What a staged V row needs before the products read it.
-enum VRow { kVKeep, kVZero, kVScan };
-
 // Row r of conversation b's rows: one that is nobody's (outside the window of
 // every node, behind the sequence, an unused node's) becomes 0, since 0 times
-// what is not finite is not 0; one of a used node with a value that is not
-// finite has those set to 0 and its node noted in `bad`, for the rows that
-// see it.
-__device__ __forceinline__ VRow v_row_kind(const TreeArgs& a, int b, int r, int lo_row, int len) {
-  if (r >= lo_row && r < len) return kVKeep;
-  const int node = r - len;
-  if (node < 0 || node >= a.nodes) return kVZero;
-  const NodeSet* s = a.set + static_cast<long long>(b) * a.nodes + node;
-  const unsigned long long anc = __ldcg(&s->anc);
-  const unsigned flag = __ldcg(&s->bad);
-  return !anc ? kVZero : flag ? kVScan : kVKeep;
+// what is not finite is not 0; one that only some nodes see (a used node's, or
+// one of the nodes - 1 cached rows from first_row() on, which the windows of
+// deeper nodes leave behind) and that has values that are not finite has them
+// set to 0 and its bit set in `bad`, for the query rows that see it.
+__device__ __forceinline__ int v_row_kind(const TreeArgs& a, int b, int r, int len) {
+  const bool cached = r < len;
+  if (cached && a.window == 0) return kVKeep;
+  const int i = r - (cached ? first_row(a, len) : len);
+  if (i < 0) return kVZero;
+  if (i >= (cached ? a.nodes - 1 : a.nodes)) return cached ? kVKeep : kVZero;
+  const NodeSet* s = a.set + b * a.nodes + i;
+  return __ldcg(cached ? &s->cached : &s->row);
 }
 
 // Thread i of a stream takes row i.  Both streams may do so for one tile: they
-// write the same values, and a node is noted before its value is replaced.
+// write the same values, and a row's bit is set before a value of it is
+// replaced.
 template <int D>
-__device__ __forceinline__ void clean_v_row(uint32_t sv, int row, VRow kind, int node,
-                                            unsigned* bad) {
+__device__ __forceinline__ void clean_v_row(uint32_t sv, int row, int kind, unsigned* bad) {
   if (kind == kVZero) {
 #pragma unroll
     for (int k = 0; k < D / 8; ++k)
       sts_u4(sv + (k >> 3) * 16384 + sw128_offset(row, k & 7), make_uint4(0, 0, 0, 0));
-  } else if (kind == kVScan) {
-    atomicOr(&bad[node >> 5], 1u << (node & 31));
-    __threadfence_block();
+  } else if (kind >= 0) {
 #pragma unroll 1
     for (int k = 0; k < D / 8; ++k) {
       const uint32_t at = sv + (k >> 3) * 16384 + sw128_offset(row, k & 7);
@@ -577,7 +621,11 @@ __device__ __forceinline__ void clean_v_row(uint32_t sv, int row, VRow kind, int
         if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
         if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
       }
-      sts_u4(at, make_uint4(w[0], w[1], w[2], w[3]));
+      if ((w[0] ^ v.x) | (w[1] ^ v.y) | (w[2] ^ v.z) | (w[3] ^ v.w)) {
+        atomicOr(&bad[kind >> 5], 1u << (kind & 31));
+        __threadfence_block();
+        sts_u4(at, make_uint4(w[0], w[1], w[2], w[3]));
+      }
     }
   }
 }
@@ -728,7 +776,7 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
         break;
       }
       o.ring = ring;
-      o.bad[0] = o.bad[1] = 0;
+      o.bad[0] = o.bad[1] = o.bad[2] = o.bad[3] = 0;
       if (lane == 0) {
         sh.pieces[sl] = o;
         mbar_arrive(&bars[kTPieceFull0 + sl]);
@@ -960,23 +1008,21 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
                             : (vld(sp.row_lo) + ta) * kTile;
         const int end = (cart ? a.p : vld(sp.len)) - k0;
         const int from = first - (cart ? k0 : a.p + k0);
-        // (from the shallowest node's first row on)
+        // (it holds rows that not every node sees)
         const bool clean =
-            !cart && (end < kTile || (a.window > 0 && k0 < vld(sp.len) - a.window + 1));
-        VRow kind = kVKeep;
-        if (clean)
-          kind = v_row_kind(a, vld(sp.b), k0 + row,
-                            a.window > 0 ? vld(sp.len) - a.window + 1 : 0, vld(sp.len));
+            !cart &&
+            (end < kTile || (a.window > 0 && k0 < first_row(a, vld(sp.len)) + a.nodes - 1));
+        int kind = kVKeep;
+        if (clean) kind = v_row_kind(a, vld(sp.b), k0 + row, vld(sp.len));
         ok = wait(&bars[kTSFull0 + x], nS & 1, kDevErrTimeoutSoftmax);
         if (!ok) break;
         ++nS;
         tc_fence_after();
-        if (clean) {
+        if (__any_sync(0xffffffffu, kind != kVKeep)) {
           const int gt = vld(sp.ring) + t;
           ok = wait(&bars[kTVFull0 + gt % kS], (gt / kS) & 1, kDevErrTimeoutSoftmax);
           if (!ok) break;
-          clean_v_row<D>(smem_u32(smem + L::kV + gt % kS * L::kTileBytes), row, kind, row - end,
-                         sp.bad);
+          clean_v_row<D>(smem_u32(smem + L::kV + gt % kS * L::kTileBytes), row, kind, sp.bad);
           fence_proxy_async_smem();
         }
         if (live_rows) {
@@ -1086,11 +1132,17 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int slot = vld(sp.slot), g = vld(sp.g), own = vld(sp.own), b = vld(sp.b);
-      // new rows that this one sees and whose value is not finite
-      const unsigned long long bad =
-          vis & (static_cast<unsigned long long>(*reinterpret_cast<volatile unsigned*>(&sp.bad[1]))
-                     << 32 |
-                 *reinterpret_cast<volatile unsigned*>(&sp.bad[0]));
+      // rows that this one sees and whose value is not finite: new ones, and
+      // cached ones from the first that its own window holds
+      auto noted = [&](int i) {
+        return static_cast<unsigned long long>(*reinterpret_cast<volatile unsigned*>(&sp.bad[i + 1]))
+                   << 32 |
+               *reinterpret_cast<volatile unsigned*>(&sp.bad[i]);
+      };
+      const unsigned long long bad = vis & noted(0);
+      unsigned long long bad_cached = 0;
+      if (live && own && a.window > 0)
+        bad_cached = noted(2) & ~0ull << (first - a.p - first_row(a, vld(sp.len)));
       if (live_rows) {
         const int rows_cap = own ? min(a.R, a.rt) : min(a.B * a.R, a.rt);
         const int part0 = slot < 0 ? 0 : (own ? a.own0 : 0) + slot * rows_cap + (local - lane);
@@ -1126,10 +1178,21 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
           }
 #pragma unroll
           for (int c = 0; c < 64; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * inv);
-          for (unsigned long long left = own ? bad : 0ull; left; left &= left - 1) {
-            const __nv_bfloat16* y =
-                a.v_new + h * 64 +
-                ((static_cast<long long>(b) * a.nodes + __ffsll(left) - 1) * a.Hkv + g) * D;
+          unsigned long long left = own ? bad : 0ull, left_cached = bad_cached;
+          while (left | left_cached) {
+            const __nv_bfloat16* y;
+            if (left) {
+              y = a.v_new + (static_cast<long long>(b) * a.nodes + __ffsll(left) - 1) * a.Hkv * D;
+              left &= left - 1;
+            } else {
+              const int r = first_row(a, vld(sp.len)) + __ffsll(left_cached) - 1;
+              const int page = page_of(a.pt, b, r);
+              left_cached &= left_cached - 1;
+              if (page < 0) continue;  // (cannot be: its rows were loaded as 0)
+              y = a.v_pages + ((static_cast<long long>(page) << a.pt.page_log2) +
+                               (r & ((1 << a.pt.page_log2) - 1))) * a.Hkv * D;
+            }
+            y += g * D + h * 64;
 #pragma unroll
             for (int c = 0; c < 64; ++c) {
               const float f = __bfloat162float(y[c]);
@@ -1451,7 +1514,11 @@ cudaError_t launch_tree(TreeArgs a, const Turns& turns, cudaStream_t st) {
   // blocks then share a conversation's lookups
   const int per = std::min(kPrepNodes, (a.B * a.nodes + 4 * sms - 1) / (4 * sms));
   const int prep_blocks = a.B * ((a.nodes + per - 1) / per);
-  tree_prep_kernel<D><<<prep_blocks + 1, 256, 0, st>>>(a, turns, per);
+  if (a.window > 0)
+    tree_prep_kernel<D, true>
+        <<<1 + prep_blocks + a.B * cached_blocks(a.nodes), 256, 0, st>>>(a, turns, per);
+  else
+    tree_prep_kernel<D, false><<<1 + prep_blocks, 256, 0, st>>>(a, turns, per);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = a.rt > kTile ? launch_attend<D, 2>(a, m, st) : launch_attend<D, 1>(a, m, st);
