@@ -356,6 +356,7 @@ CART_API int cart_attn_decode_noalloc(int B, int Hq, int Hkv, int d, int p, floa
  * `window` positions (as in cart_geom).  Keys and values that it does not
  * attend to, other nodes' and cached rows' that its window has left behind,
  * do not reach it, whatever they hold (but for the cartridge's, above).
+ * A query whose every logit is -inf has o = 0.
  * A node is unused when its row has no page, or its parent is neither -1
  * nor an earlier used node (-2 by convention pads a ragged tree): its o is
  * 0, its row is not written, and no node attends to it.  An unused node

@@ -99,3 +99,22 @@ def test_windows_of_idle_empty_and_full_conversations(window):
     check_tree(t, table, lens, parents, window=window)
     lens[3] = table.shape[1] * 16           # no node of it fits
     check_tree(t, table, lens, parents, window=window, status=128)
+
+
+@pytest.mark.parametrize("B,nodes,p,lens", [(1, 3, 900, (40,)), (1, 2, 0, (5,)), (3, 5, 30, (0, 9, 200)),
+                                            (6, 4, 1100, (0, 9, 200, 40, 3, 1)),
+                                            (2, 40, 300, (4000, 17))])
+def test_logits_of_minus_infinity(B, nodes, p, lens):
+    """Rows whose every logit is -inf are 0, whether one CTA walked their keys
+    or several did.  One dimension of the slowest angle holds the queries and,
+    negated, the keys: 2^100 * -2^100 is -inf in f32, and so is the product of
+    what the rotation moves to the dimension's other half."""
+    d = 64
+    t, table, lens, parents = make_tree(84, B, nodes, 4, 2, d, p, lens, 16, "random")
+    for name in ("q", "k_new", "kc", "k_pages"):
+        x = torch.zeros_like(t[name])
+        x[..., d // 2 - 1] = 2.0 ** 100 if name == "q" else -2.0 ** 100
+        t[name] = x
+    o, _ = run_tree(t, table, lens, parents)
+    assert ca.device_status(clear=True) == 0
+    assert not torch.isnan(o).any() and not o.any()

@@ -1373,7 +1373,8 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const __grid_constan
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    const float inv = 1.f / __shfl_sync(0xffffffffu, den, r * 8);
+    const float sum = __shfl_sync(0xffffffffu, den, r * 8);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (all logits -inf: 0, as in attend)
     if (!__shfl_sync(0xffffffffu, n, r * 8)) continue;
     const int t = (r0 + r) / G;
     __nv_bfloat16* o =
