@@ -402,15 +402,19 @@ CART_API int cart_pages_fork(int B, int* table, int max_pages, int* lens, int* r
  *          the conversation is left as it is.  0 gives all its pages back.
  *   done   [B] int32 (output): 1 where rows[b] rows have room
  * lens[b] becomes min(max(lens[b], 0), rows[b]).  Pages behind the last of
- * rows[b] rows are given back first, of all conversations.  Then the rows
- * lens[b] .. rows[b] - 1 come to lie in pages that b alone holds: missing
- * ones are taken from the pool (lowest free page first, conversations in
- * order), and in the place of one that is shared (refs > 1) a free one is
+ * rows[b] rows are given back first, of all conversations.  Then the pages
+ * from that of row lens[b] to that of row rows[b] - 1 come to be b's alone:
+ * missing ones are taken from the pool (lowest free page first, conversations
+ * in order), and in the place of one that is shared (refs > 1) a free one is
  * taken, with the rows of b that it holds (below lens[b]) copied in every
  * layer.  When the pool runs out, the conversation that finds too few free
  * pages and all later ones that need any keep what they have, done 0; their
  * next rows may lie in a shared page, so they must not append in that step
  * (parents -2 for all their nodes, or lens < 0).
+ * Where rows[b] <= lens[b] nothing is to be appended and done is 1.  The page
+ * in which rows[b] rows end, if they do not fill it, becomes b's alone even
+ * so if a free page is left when it is b's turn.  (A caller that only lowers
+ * lens[b] keeps that page shared; a later call gives back those behind.)
  * Pages that lose their last holder to such a copy are free from the next
  * call on.
  *   k_pages, v_pages: dtype CART_BF16 or CART_F32, row = Hkv * d elements

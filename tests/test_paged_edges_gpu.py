@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import paged_reference as ref
-from tests.test_paged_gpu import check_tree, make_tree, run_tree
+from tests.test_paged_gpu import _i32, _pool, check_tree, make_tree, run_tree
 from trained_kv_prefix_gb300 import cartattn as ca
 from trained_kv_prefix_gb300 import synth
 
@@ -118,3 +118,42 @@ def test_logits_of_minus_infinity(B, nodes, p, lens):
     o, _ = run_tree(t, table, lens, parents)
     assert ca.device_status(clear=True) == 0
     assert not torch.isnan(o).any() and not o.any()
+
+
+NOTHING_TO_APPEND = [
+    # id, table, lens, refs, rows -> table, lens, refs, done, copies (from, to, rows); 16 rows a page
+    # two that share their part page ask for what they hold: each gets its own
+    ("free", [[0, -1], [0, -1]], [5, 5], [2, 0, 0], [5, 5],
+     [[1, -1], [2, -1]], [5, 5], [0, 1, 1], [1, 1], [(0, 1, 5), (0, 2, 5)]),
+    # without a free page they keep it, and have their rows
+    ("full", [[0, -1], [0, 1]], [5, 20], [2, 1], [5, 20],
+     [[0, -1], [0, 1]], [5, 20], [2, 1], [1, 1], []),
+    # a rewind into the part page that both share; nothing is given back
+    ("rewind_full", [[0, -1], [0, -1], [1, -1]], [9, 9, 16], [2, 1], [3, -1, 16],
+     [[0, -1], [0, -1], [1, -1]], [3, 9, 16], [2, 1], [1, 0, 1], []),
+    # a rewind that gives back a page of its own takes that one
+    ("rewind", [[0, 1], [0, -1]], [20, 9], [2, 1], [3, -1],
+     [[1, -1], [0, -1]], [3, 9], [1, 1], [1, 0], [(0, 1, 3)]),
+    # rows that end with a page need no other
+    ("whole_pages", [[0, 1], [0, 1]], [32, 20], [2, 2], [32, 16],
+     [[0, 1], [0, -1]], [32, 16], [2, 1], [1, 1], []),
+    # one that has nothing to append does not keep back the answer of one that has
+    ("both", [[0, -1], [0, -1], [1, -1]], [5, 5, 16], [2, 1], [5, 6, 17],
+     [[0, -1], [0, -1], [1, -1]], [5, 5, 16], [2, 1], [1, 0, 0], []),
+]
+
+
+@pytest.mark.parametrize("case", NOTHING_TO_APPEND, ids=[c[0] for c in NOTHING_TO_APPEND])
+def test_reserve_with_nothing_to_append(case):
+    _, table, lens, refs, rows, wt, wl, wr, wd, copies = case
+    k, v = (_pool((2, len(refs), 16, 1, 64), torch.bfloat16, s) for s in (1, 2))
+    tb, ln, rf = _i32(table), _i32(lens), _i32(refs)
+    before = k.clone(), v.clone()
+    done = ca.cart_pages_reserve(k, v, tb, ln, rf, _i32(rows))
+    assert done.tolist() == wd and ln.tolist() == wl
+    assert tb.tolist() == wt and rf.tolist() == wr
+    for now, old in zip((k, v), before):
+        want = old.clone()
+        for a, z, n in copies:
+            want[:, z, :n] = old[:, a, :n]
+        assert torch.equal(now, want)

@@ -596,9 +596,10 @@ def cart_pages_fork(table, lens, refs, src, dst, rows=None, *, page_rows, done=N
 def cart_pages_reserve(k_pages, v_pages, table, lens, refs, rows, *, done=None, workspace=None,
                        stream=None):
     """Room for rows[b] rows in all of every conversation: pages behind them
-    are given back, and rows lens[b] .. rows[b] - 1 come to lie in pages that
-    b alone holds (a shared one is copied in every layer).  rows ``[B]``
-    int32 on the device, < 0: left as it is, 0: everything is given back.
+    are given back, and those of rows lens[b] .. rows[b] - 1 come to be b's
+    alone (a shared one is copied in every layer).  rows ``[B]`` int32 on the device, < 0: left as it is, 0:
+    everything is given back, at most lens[b]: nothing is to be appended (see
+    the header).
     Pools ``[layers, pages, page_rows, Hkv, d]`` (bf16 or f32); table, lens
     and refs are updated.  Returns done ``[B]`` int32: 1 where there is
     room; a conversation without it must not append (its next row may lie in

@@ -150,10 +150,10 @@ struct ReserveArgs {
   int row_bytes;
 };
 
-// Conversation b's request: whether it asks, its first page to be written
-// and the end of its pages.
+// Conversation b's request: whether it asks, whether it is to append, the page
+// of its next row and the end of its pages.
 struct Request {
-  bool asks;
+  bool asks, appends;
   int first, end, len;
 };
 __device__ __forceinline__ Request request(const ReserveArgs& a, int b) {
@@ -161,6 +161,7 @@ __device__ __forceinline__ Request request(const ReserveArgs& a, int b) {
   Request r;
   r.asks = n >= 0 && n <= (a.max_pages << a.page_log2);
   r.len = min(max(__ldcg(a.lens + b), 0), n);
+  r.appends = r.len < n;
   r.first = r.asks ? r.len >> a.page_log2 : 0;
   r.end = r.asks ? (n + (1 << a.page_log2) - 1) >> a.page_log2 : 0;
   return r;
@@ -289,7 +290,7 @@ __global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads
     }
     if (lane == 0) {
       a.copies[b] = copy;
-      a.done[b] = q.asks && ok;
+      a.done[b] = q.asks && (ok || !q.appends);
     }
   }
 }
