@@ -325,7 +325,8 @@ CART_API int cart_attn_decode_noalloc(int B, int Hq, int Hkv, int d, int p, floa
  *          r % page_rows of page table[b][r / page_rows].  An entry outside
  *          0 .. n_pages - 1 (-1 by convention) is no page: its rows are not
  *          there, which is never an error (pages that a sliding window has
- *          left behind may be taken out).
+ *          left behind may be taken out, but for the one that row lens[b]
+ *          lies in, if it holds rows below: see cart_pages_reserve).
  *   lens   [B] int32: rows that the conversation holds; < 0 an idle slot.
  *   refs   [n_pages] int32: how many table entries name the page (a caller
  *          may add its own holds); <= 0 is free.
@@ -415,6 +416,10 @@ CART_API int cart_pages_fork(int B, int* table, int max_pages, int* lens, int* r
  * in which rows[b] rows end, if they do not fill it, becomes b's alone even
  * so if a free page is left when it is b's turn.  (A caller that only lowers
  * lens[b] keeps that page shared; a later call gives back those behind.)
+ * A missing page is taken as it is.  Where it is the page of row lens[b] and
+ * has rows below that, those are there again, with what the page last held,
+ * another conversation's rows perhaps: the caller writes them, or does not
+ * take that page out.
  * Pages that lose their last holder to such a copy are free from the next
  * call on.
  *   k_pages, v_pages: dtype CART_BF16 or CART_F32, row = Hkv * d elements

@@ -157,3 +157,14 @@ def test_reserve_with_nothing_to_append(case):
         for a, z, n in copies:
             want[:, z, :n] = old[:, a, :n]
         assert torch.equal(now, want)
+
+
+def test_reserve_takes_a_missing_page_as_it_is():
+    """The page of row lens is missing: a free one is taken, nothing is copied,
+    and its rows below lens are seen again, with what the page holds."""
+    k, v = (_pool((1, 3, 16, 1, 64), torch.bfloat16, s) for s in (1, 2))
+    before = k.clone(), v.clone()
+    tb, ln, rf = _i32([[0, -1]]), _i32([21]), _i32([1, 0, 0])
+    done = ca.cart_pages_reserve(k, v, tb, ln, rf, _i32([22]))
+    assert done.tolist() == [1] and tb.tolist() == [[0, 1]] and rf.tolist() == [1, 1, 0]
+    assert torch.equal(k, before[0]) and torch.equal(v, before[1])

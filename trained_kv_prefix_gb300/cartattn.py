@@ -597,7 +597,8 @@ def cart_pages_reserve(k_pages, v_pages, table, lens, refs, rows, *, done=None, 
                        stream=None):
     """Room for rows[b] rows in all of every conversation: pages behind them
     are given back, and those of rows lens[b] .. rows[b] - 1 come to be b's
-    alone (a shared one is copied in every layer).  rows ``[B]`` int32 on the device, < 0: left as it is, 0:
+    alone (a shared one is copied in every layer; one that is missing is taken
+    as it is).  rows ``[B]`` int32 on the device, < 0: left as it is, 0:
     everything is given back, at most lens[b]: nothing is to be appended (see
     the header).
     Pools ``[layers, pages, page_rows, Hkv, d]`` (bf16 or f32); table, lens
