@@ -494,6 +494,14 @@ def _arg(name, t, dtype, shape, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _fits(**sizes):
+    """Refuses a number that the library's 32 bits would take for another
+    (those that fit are its own to refuse)."""
+    for name, n in sizes.items():
+        if not -1 << 31 <= n < 1 << 31:
+            raise ValueError(f"{name}: {n} does not fit 32 bits")
+
+
 def _scratch(on, workspace, need):
     """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
     if workspace is None:
@@ -537,6 +545,8 @@ def cart_attn_decode_tree(q, k_new, v_new, kc, vc, k_pages, v_pages, table, lens
     Hkv, p = k_new.shape[2], kc.shape[0]
     N, P = k_pages.shape[0], k_pages.shape[1]
     M, dev, bf, i32 = table.shape[-1], q.device, torch.bfloat16, torch.int32
+    if (B | M | N | window) >> 31:
+        _fits(conversations=B, max_pages=M, pages=N, window=window)
     new = (B, T, Hkv, d)
     args = (_arg("q", q, bf, q.shape, dev),
             _arg("k_new", k_new, bf, new, dev), _arg("v_new", v_new, bf, new, dev),
@@ -577,6 +587,8 @@ def cart_pages_fork(table, lens, refs, src, dst, rows=None, *, page_rows, done=N
     for a fork that was left out (dst also named by another fork)."""
     B, M = table.shape
     F, N = src.shape[0], refs.shape[0]
+    if (B | M | F | N | page_rows) >> 31:
+        _fits(conversations=B, max_pages=M, forks=F, pages=N, page_rows=page_rows)
     dev, i32 = table.device, torch.int32
     args = (B, _arg("table", table, i32, (B, M), dev), M, _arg("lens", lens, i32, (B,), dev),
             _arg("refs", refs, i32, (N,), dev), N, page_rows, _arg("src", src, i32, (F,), dev),
@@ -607,6 +619,8 @@ def cart_pages_reserve(k_pages, v_pages, table, lens, refs, rows, *, done=None, 
     a shared page): -2 for its ``parents``."""
     layers, N, P, Hkv, d, dt, kp, vp, dev = _pools(k_pages, v_pages)
     B, M = table.shape
+    if (B | M | N) >> 31:
+        _fits(conversations=B, max_pages=M, pages=N)
     i32 = torch.int32
     args = (B, layers, Hkv, d, dt, kp, vp, N, P, _arg("table", table, i32, (B, M), dev), M,
             _arg("lens", lens, i32, (B,), dev), _arg("refs", refs, i32, (N,), dev),
@@ -634,6 +648,8 @@ def cart_pages_accept(k_pages, v_pages, table, lens, parents, node, *, new_lens=
     i32 = torch.int32
     chains = isinstance(parents, int)
     T = parents if chains else parents.shape[-1]
+    if (B | M | N | T) >> 31:
+        _fits(conversations=B, max_pages=M, pages=N, nodes=T)
     args = (B, T, layers, Hkv, d, dt, kp, vp, N, P, _arg("table", table, i32, (B, M), dev), M,
             _arg("lens", lens, i32, (B,), dev),
             None if chains else _arg("parents", parents, i32, (B, T), dev),
@@ -657,6 +673,8 @@ def cart_pages_compact(k_pages, v_pages, table, refs, *, moved=None, live=None, 
     page's new number (-1: it was free) and the number of live pages."""
     layers, N, P, Hkv, d, dt, kp, vp, dev = _pools(k_pages, v_pages)
     B, M = table.shape
+    if (B | M | N) >> 31:
+        _fits(conversations=B, max_pages=M, pages=N)
     i32 = torch.int32
     args = (B, layers, Hkv, d, dt, kp, vp, N, P, _arg("table", table, i32, (B, M), dev), M,
             _arg("refs", refs, i32, (N,), dev))
