@@ -360,7 +360,9 @@ CART_API int cart_attn_decode_noalloc(int B, int Hq, int Hkv, int d, int p, floa
  * A query whose every logit is -inf has o = 0.
  * A node is unused when its row has no page, or its parent is neither -1
  * nor an earlier used node (-2 by convention pads a ragged tree): its o is
- * 0, its row is not written, and no node attends to it.  An unused node
+ * 0, its row is not written, and no node attends to it.  (A conversation
+ * that has no used node costs as much as one that has; an idle one, below,
+ * costs nothing.)  An unused node
  * that has a valid parent but no page sets device status bit 7.  All nodes
  * of an idle conversation are unused.  lens[b] above max_pages * page_rows
  * counts as that.  The rows lens[b] .. lens[b] + nodes - 1 must lie in pages
@@ -411,7 +413,8 @@ CART_API int cart_pages_fork(int B, int* table, int max_pages, int* lens, int* r
  * layer.  When the pool runs out, the conversation that finds too few free
  * pages and all later ones that need any keep what they have, done 0; their
  * next rows may lie in a shared page, so they must not append in that step
- * (parents -2 for all their nodes, or lens < 0).
+ * (lens < 0 for them in its other calls, which then do no work for them, and
+ * their real lens kept apart; or parents -2 for all their nodes).
  * Where rows[b] <= lens[b] nothing is to be appended and done is 1.  The page
  * in which rows[b] rows end, if they do not fill it, becomes b's alone even
  * so if a free page is left when it is b's turn.  (A caller that only lowers

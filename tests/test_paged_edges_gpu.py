@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import paged_reference as ref
-from tests.test_paged_gpu import _i32, _pool, check_tree, make_tree, run_tree
+from tests.test_paged_gpu import _bf16, _i32, _pool, check_tree, make_tree, run_tree
 from trained_kv_prefix_gb300 import cartattn as ca
 from trained_kv_prefix_gb300 import synth
 
@@ -157,6 +157,45 @@ def test_reserve_with_nothing_to_append(case):
         for a, z, n in copies:
             want[:, z, :n] = old[:, a, :n]
         assert torch.equal(now, want)
+
+
+def test_a_step_sat_out():
+    """A conversation without room is idle for a step, keeps its rows, and goes
+    on once there is room."""
+    rng = np.random.default_rng(85)
+    t, _, _, _ = make_tree(85, 3, 2, 2, 1, 64, 4, (0, 0, 0), 16, "chain")
+    k, v = (_bf16(rng, (1, 3, 16, 1, 64)).cuda() for _ in range(2))
+    table, lens, refs = _i32([[0, -1], [0, -1], [1, -1]]), _i32([5, 5, 16]), _i32([2, 1, 0])
+    parents = _i32([[-1, 0]] * 3)
+    g = {n: x.cuda() for n, x in t.items()}
+
+    def step(rows):
+        nonlocal lens
+        done = ca.cart_pages_reserve(k, v, table, lens, refs, rows)
+        now = torch.where((done == 1) & (rows > lens), lens, -1)
+        before = k.clone(), v.clone()
+        o = ca.cart_attn_decode_tree(g["q"], g["k_new"], g["v_new"], g["kc"], g["vc"], k[0], v[0],
+                                     table, now, parents)
+        a = {n: synth.f64(x) for n, x in t.items() if n not in ("k_pages", "v_pages")}
+        o_ref, bound, wrote = ref.tree(**a, k_pages=synth.f64(before[0][0]),
+                                       v_pages=synth.f64(before[1][0]),
+                                       table=table.cpu().numpy(), lens=now.cpu().numpy(),
+                                       parents=parents.cpu().numpy())
+        assert (np.abs(synth.f64(o) - o_ref) <= bound).all()
+        left = torch.ones(3, 16, dtype=torch.bool)
+        for page, row in wrote:
+            left[page, row] = False
+        assert torch.equal(k[0].cpu()[left], before[0][0].cpu()[left])
+        new = ca.cart_pages_accept(k, v, table, now, parents, _i32([1, 1, 1]))
+        lens = torch.where(now < 0, lens, new)
+        return done.tolist()
+
+    assert step(lens + 2) == [1, 0, 0] and lens.tolist() == [7, 5, 16]
+    assert table.tolist() == [[2, -1], [0, -1], [1, -1]] and refs.tolist() == [1, 1, 1]
+    # the second's page is its own now; the first leaves, and the third takes its page
+    assert step(_i32([0, 7, 18])) == [1, 1, 1] and lens.tolist() == [0, 7, 18]
+    assert table.tolist() == [[-1, -1], [0, -1], [1, 2]]
+    assert ca.device_status(clear=True) == 0
 
 
 def test_reserve_takes_a_missing_page_as_it_is():

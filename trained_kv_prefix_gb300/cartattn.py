@@ -616,7 +616,8 @@ def cart_pages_reserve(k_pages, v_pages, table, lens, refs, rows, *, done=None, 
     Pools ``[layers, pages, page_rows, Hkv, d]`` (bf16 or f32); table, lens
     and refs are updated.  Returns done ``[B]`` int32: 1 where there is
     room; a conversation without it must not append (its next row may lie in
-    a shared page): -2 for its ``parents``."""
+    a shared page): ``lens`` -1 for it in the step's other calls, its real
+    one kept apart."""
     layers, N, P, Hkv, d, dt, kp, vp, dev = _pools(k_pages, v_pages)
     B, M = table.shape
     if (B | M | N) >> 31:

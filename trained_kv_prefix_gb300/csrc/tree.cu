@@ -94,8 +94,9 @@ struct Turns {
 __device__ __forceinline__ int first_row(const TreeArgs& a, int len) { return len - a.window + 1; }
 
 // ------------------------------------------------------------- schedule ----
-// Key tiles of conversation b's own segments (n == 0: it has no used node):
-// cartridge tiles cart_lo .. n_ct - 1 (fused only), then tiles of 128 own rows
+// Key tiles of conversation b's own segments (n == 0: it is idle, or its table
+// has no place for a new row; which nodes are used is not known here, so one
+// whose every node is unused has its tiles all the same): cartridge tiles cart_lo .. n_ct - 1 (fused only), then tiles of 128 own rows
 // from row_lo on.  first_cart: the first cartridge tile any of its nodes sees.
 struct ConvTiles {
   int len, first_cart, n_cart, row_lo, n;
