@@ -142,3 +142,38 @@ def test_decode_step_beside_a_busy_stream(busy):
     got = ca.cart_attn_decode(*args, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_captured_on_a_forked_stream():
+    """A capture that hands the calls to a stream of its own: what they allocate
+    lives as long as the graph."""
+    t, table, lens, parents = make_tree(76, 4, 9, 8, 2, 128, 700, (3, 400, 0, 170), 64, "random")
+    want, _ = run_tree(t, table, lens, parents)
+    g = {k: v.cuda() for k, v in t.items()}
+    tb, ln, up = _i32(table), _i32(lens), _i32(parents)
+    refs = _i32(np.bincount(table[table >= 0], minlength=g["k_pages"].shape[0]))
+    rows = ln + 9
+    side = torch.cuda.Stream()
+
+    def step(**kw):
+        done = ca.cart_pages_reserve(g["k_pages"][None], g["v_pages"][None], tb, ln, refs, rows, **kw)
+        return done, ca.cart_attn_decode_tree(g["q"], g["k_new"], g["v_new"], g["kc"], g["vc"],
+                                              g["k_pages"], g["v_pages"], tb, ln, up, **kw)
+
+    step(stream=side)                         # lazy set-up before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        now = torch.cuda.current_stream()
+        side.wait_stream(now)
+        done, o = step(stream=side)
+        now.wait_stream(side)
+    for _ in range(3):
+        o.fill_(float("nan"))
+        done.fill_(7)
+        graph.replay()
+        junk = torch.full((1 << 24,), float("nan"), device="cuda")
+        del junk
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and done.tolist() == [1] * 4
+    assert ca.device_status(clear=True) == 0

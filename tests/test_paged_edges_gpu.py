@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import paged_reference as ref
-from tests.test_paged_gpu import _bf16, _i32, _pool, check_tree, make_tree, run_tree
+from tests.test_paged_gpu import _bf16, _i32, _pool, check_tree, make_tables, make_tree, run_tree
 from trained_kv_prefix_gb300 import cartattn as ca
 from trained_kv_prefix_gb300 import synth
 
@@ -207,3 +207,40 @@ def test_reserve_takes_a_missing_page_as_it_is():
     done = ca.cart_pages_reserve(k, v, tb, ln, rf, _i32([22]))
     assert done.tolist() == [1] and tb.tolist() == [[0, 1]] and rf.tolist() == [1, 1, 0]
     assert torch.equal(k, before[0]) and torch.equal(v, before[1])
+
+
+def test_largest_tables_and_lists():
+    """65535 conversations: 8192 forks at once, then room for all of them."""
+    B, M, P, F, N = 65535, 2, 16, 8192, 90000
+    rng = np.random.default_rng(86)
+    table, lens, refs = make_tables(rng, B, M, P, N, share=0.6)
+    src, dst = np.split(rng.permutation(B)[:2 * F].astype(np.int32), 2)
+    src[5], dst[9], dst[11] = -1, B, dst[12]
+    bad = {5, 9, 11, 12}
+    tb, ln, rf = _i32(table), _i32(lens), _i32(refs)
+    done = ca.cart_pages_fork(tb, ln, rf, _i32(src), _i32(dst), page_rows=P)
+    good = np.array([f not in bad for f in range(F)])
+    np.testing.assert_array_equal(done.cpu().numpy(), good.astype(np.int32))
+    # no destination is a source: all rows move at once
+    a, z = src[good], dst[good]
+    n = np.maximum(lens[a], 0)
+    new = np.where(np.arange(M) * P < n[:, None], table[a], -1)
+    for pages, by in ((table[z], -1), (new, 1)):
+        np.add.at(refs, pages[pages >= 0], by)
+    table[z], lens[z] = new, n
+    for got, w in ((tb, table), (ln, lens), (rf, refs)):
+        np.testing.assert_array_equal(got.cpu().numpy(), w)
+    rows = np.where(lens < 0, -1, np.minimum(lens + 3, M * P)).astype(np.int32)
+    k, v = (_pool((1, N, P, 1, 8), torch.bfloat16, s) for s in (1, 2))
+    k0 = k.clone()
+    done = ca.cart_pages_reserve(k, v, tb, ln, rf, _i32(rows))
+    wt, wl, wr, wd, copies = ref.reserve(table, lens, refs, rows, P)
+    wd = np.where((rows >= 0) & (rows == lens), 1, wd)      # nothing to append
+    assert 0 < wd.sum() < B and len(copies) > 1000
+    for got, w in zip((tb, ln, rf, done), (wt, wl, wr, wd)):
+        np.testing.assert_array_equal(got.cpu().numpy(), w)
+    want = k0.clone()
+    fr, to, n = (torch.tensor(x, device="cuda") for x in np.array(copies).T)
+    part = (torch.arange(P, device="cuda") < n[:, None])[None, :, :, None, None]
+    want[:, to] = torch.where(part, k0[:, fr], k0[:, to])
+    assert torch.equal(k, want)
