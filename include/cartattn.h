@@ -387,7 +387,8 @@ CART_API int cart_attn_decode_tree(int B, int nodes, int window, int Hq, int Hkv
  * cart_pages_fork -- conversation dst[f] becomes the first rows[f] rows of
  * conversation src[f], sharing its pages (no row is copied).
  *   src, dst, rows [forks] int32 (device); rows may be NULL: all rows.
- *          rows[f] above lens[src[f]] counts as that, below 0 as 0.
+ *          rows[f] above lens[src[f]] counts as that, below 0 as 0 (of an
+ *          idle src dst gets no rows: its lens becomes 0).
  *   done   [forks] int32 (output): 1, or 0 for a fork that was left out: src
  *          or dst outside 0 .. B - 1, dst[f] also named by another fork of
  *          the call as its dst, or by any as its src.

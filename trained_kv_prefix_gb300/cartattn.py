@@ -534,10 +534,10 @@ def cart_attn_decode_tree(q, k_new, v_new, kc, vc, k_pages, v_pages, table, lens
                           scale=None, theta=1.0e6, window=0, o=None, workspace=None, stream=None):
     """One step over a tree of drafted tokens per conversation, its private
     rows in pages.  q ``[B, nodes, Hq, d]``, k_new/v_new ``[B, nodes, Hkv,
-    d]`` (bf16, not rotated), kc/vc ``[p, Hkv, d]`` bf16 shared cartridge,
-    k_pages/v_pages ``[pages, page_rows, Hkv, d]`` bf16 pools (the rows
-    lens[b] + t of the used nodes t are written), table ``[B, max_pages]``
-    and lens ``[B]`` int32.  parents ``[B, nodes]`` int32: the node that each
+    d]`` (bf16, not rotated), kc/vc ``[p, Hkv, d]`` bf16 shared cartridge
+    (``[0, Hkv, d]``: none), k_pages/v_pages ``[pages, page_rows, Hkv, d]``
+    bf16 pools (the rows lens[b] + t of the used nodes t are written), table
+    ``[B, max_pages]`` and lens ``[B]`` int32.  parents ``[B, nodes]`` int32: the node that each
     node follows, an earlier one, -1 for the cached rows, -2 for an unused
     node; None: chains.  Returns o ``[B, nodes, Hq, d]`` bf16, 0 for unused
     nodes.  ``window`` as in ``cart_attn_decode_span``."""

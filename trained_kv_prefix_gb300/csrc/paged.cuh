@@ -51,7 +51,6 @@ __device__ __forceinline__ int page_of(const PageTable& t, int b, int r) {
 struct TreeSmem {
   unsigned long long anc[kMaxNodes];
   int jump[kMaxNodes];
-  int page;  // the caller's
 };
 
 // Ancestor sets of one tree, by the whole block (at least 64 threads): on

@@ -1260,9 +1260,9 @@ __global__ void __launch_bounds__(TreeLayout<D, NT>::kThreads, 3 - NT)
 // parts and log-sum-exps side by side, then two more parts of four rows at a
 // time) and, for many rows, by its bandwidth: alone 12 us for 64 conversations
 // with one node, 10 us for 25 nodes over four long histories, 16 us for 64
-// conversations with 64 nodes.  (80 registers, three blocks per SM: with four
-// per SM registers spill, and calls took up to 10 us more, that of 64
-// single tokens 1 us less.)
+// conversations with 64 nodes.  (80 registers, three blocks per SM: 16 bytes
+// spill at d = 128; with four per SM more do, and calls took up to 10 us more,
+// that of 64 single tokens 1 us less.)
 template <int D>
 __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int E = D / 32;  // output columns per lane
@@ -1420,7 +1420,8 @@ TreeWs tree_ws(int B, int nodes, int Hq, int Hkv, int d, int p) {
   // p = 1024, R = 4 47, 60; R = 64 72, 68; R = 96 88, 74; R = 160 132, 107;
   // p = 4096, R = 4 49, 118; R = 64 99, 125; R = 96 132, 133; R = 160 188, 204;
   // R = 192 216, 212.  Over p = 128 to 4096, 2 to 64 conversations and R = 4 to
-  // 192 the rule loses 0.6 % against the better of the two, at most 13 %.
+  // 192 the rule loses 0.6 % against the better of the two, at most 13 %.  (All
+  // at G = 4 and d = 128; elsewhere it is taken as it is.)
   const long long row_tiles = (static_cast<long long>(B) * w.R + w.rt - 1) / w.rt;
   const long long cart_tiles = (p + kTile - 1) / kTile;
   w.stacked = B > 1 && w.segs == 1 && 40 * cart_tiles * (B - row_tiles) > (120ll + w.R) * B;
@@ -1479,7 +1480,8 @@ cudaError_t launch_tree(TreeArgs a, const Turns& turns, cudaStream_t st) {
   // Runs per segment, about the parts of a row, set a block's rows: 32 (a warp
   // for every four) where they are few, less where warps can share them.  In
   // us, with 32, 16, 8 and 4 rows: 2.4 runs per segment 77, 80, 87, 104; 4.8
-  // 126, 126, 128, 134; 9.5 34, 31, 33, 36; 19 55, 50, 48, 51; 38 35, 29, 25, 24.
+  // 126, 126, 128, 134; 9.5 34, 31, 33, 36; 19 55, 50, 48, 51; 38 35, 29, 25, 24
+  // (G = 4, d = 128).
   const int own = a.B * a.Hkv * a.segs;
   const int runs = a.n_ctas / (a.stacked ? (a.B * a.R + a.rt - 1) / a.rt * a.Hkv : own);
   a.by_cut = !a.stacked && own > a.n_ctas;
