@@ -167,13 +167,13 @@ DENSE = {
 
 def check(fake, call):
     """All that the call makes is memory of the stream that its kernels run on;
-    what it returns is kept for the caller's current stream too, which reads
-    it later."""
+    what it returns, and that alone, is kept for the caller's current stream
+    too, which reads it later."""
     side = Stream(9)
     out = call(stream=side)
     out = out if isinstance(out, tuple) else (out,)
     assert fake.made and all(t.home is side for t in fake.made)
-    assert all(fake.default in t.kept_for for t in fake.made if t in out)
+    assert all(t.kept_for == ({fake.default} if t in out else set()) for t in fake.made)
     assert fake.now is fake.default
     # on the current stream, named or not, memory is that stream's
     for kw in ({}, {"stream": fake.default}):

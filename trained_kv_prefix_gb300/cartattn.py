@@ -174,24 +174,26 @@ def geom(B, n, Hq, Hkv, d, p, frozen_prefix=1, scale=None, theta=1.0e6, window=0
     return _Geom(B, n, Hq, Hkv, d, p, frozen_prefix, float(scale), float(theta), int(window))
 
 
-def _make(stream, make, *args, **kwargs):
+def _make(stream, make, *args, returned=True, **kwargs):
     """``make(*args, **kwargs)``, a tensor that a call on ``stream`` (None: the
     current one) works on: allocated, and filled, on that stream, since the
     current stream's memory could be a block that it has freed and is still
-    working on; and kept for the current stream too, which reads what the call
-    returns."""
+    working on; and one that the call returns is kept for the current stream
+    too, which reads it."""
     if stream is None:
         return make(*args, **kwargs)
     with torch.cuda.stream(stream):
         t = make(*args, **kwargs)
-    t.record_stream(torch.cuda.current_stream(t.device))
+    if returned:
+        t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 
 def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor], stream) -> torch.Tensor:
     if workspace is not None and workspace.numel() * workspace.element_size() >= nbytes:
         return workspace
-    return _make(stream, torch.empty, max(nbytes, 16), dtype=torch.uint8, device=device)
+    return _make(stream, torch.empty, max(nbytes, 16), dtype=torch.uint8, device=device,
+                 returned=False)
 
 
 # ------------------------------------------------------------------ calls ----
@@ -463,17 +465,12 @@ class _On:
         if stream is not None and stream.cuda_stream != self.handle:
             self.stream, self.handle = stream, stream.cuda_stream
 
-    def empty(self, shape, dtype):
-        """Memory of the stream that the call's kernels run on: the current
-        stream's could be a block that it has freed and is still working on.
-        It is kept for the current stream too, which reads what the call
-        returns."""
+    def empty(self, shape, dtype, returned=True):
+        """Memory of the stream that the call's kernels run on (see _make)."""
         if self.stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-        t.record_stream(torch.cuda.current_stream(self.device))
-        return t
+        return _make(self.stream, torch.empty, shape, dtype=dtype, device=self.device,
+                     returned=returned)
 
     def close(self):
         if self.guard is not None:
@@ -506,7 +503,7 @@ def _scratch(on, workspace, need):
     """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
     if workspace is None:
         need = max(need, 16)
-        workspace = on.empty((need,), torch.uint8)
+        workspace = on.empty((need,), torch.uint8, returned=False)
         return workspace, workspace.data_ptr(), need
     if workspace.device != on.device or not workspace.is_contiguous():
         raise ValueError(f"the workspace must be contiguous and on {on.device}")
