@@ -462,6 +462,142 @@ CART_API int cart_pages_compact(int B, int layers, int Hkv, int d, cart_dtype dt
                                 int max_pages, int* refs, int* moved, int* live, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A paged cache held to a budget of rows.  The calls below go with the paged
+ * private caches above (tables, pools and their rules are the same): a prompt's
+ * rows are appended, the attention weight that each row gets is added up, rows
+ * of little weight are evicted, and decoding goes on.  Evicting moves rows
+ * together, so that a row's place no longer tells its token's position:
+ *   place     cartridge row j has place j, private row r place p + r.  What a
+ *             query sees goes by places: a query at place x the places up to x,
+ *             with window > 0 those above x - window, and always those below
+ *             `sinks` (>= 0; cartridge rows, and private ones where it is
+ *             above p)
+ *   position  of the rotation: pos [B] int32 (device), or NULL for positions
+ *             equal to places, which they are until rows are evicted.  Values
+ *             outside 0 .. 2^24 - 1 are clamped into it.
+ *   weights   [B, Hkv, weight_rows] f32, one layer's: weights[b][g][r] belongs
+ *             to private row r of conversation b in kv head g; weight_rows >=
+ *             max_pages * page_rows.  Kept by conversation and row, not by
+ *             page: fork, reserve and compact leave them as they are (a caller
+ *             that forks copies its weights along).
+ * Hq / Hkv is 1 to 8 here, any of them, and d 64 or 128.
+ * Workspaces as above: no initial value, nothing outlives the call, calls that
+ * may overlap need workspaces of their own.                                */
+
+/* ------------------------------------------------------------------------
+ * cart_pages_append -- a run of tokens per conversation goes to its next rows,
+ * in one layer: what a prompt's attention leaves to decoding.
+ *   cu_seqlens NULL: k, v [B, n, Hkv, d] bf16, n tokens each; total = B * n
+ *          [B + 1] int32 (device): k, v [total, Hkv, d], conversation b's tokens
+ *          are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (as in the packed calls;
+ *          n is not read).  A token in no conversation's run is left out and
+ *          sets device status bit 6.
+ *   k      NOT rotated
+ *   pos    position of the conversation's first token here (NULL: p + lens[b])
+ * Token i of conversation b goes to row lens[b] + i: its key rotated at its
+ * position, rounded to bf16, and its value.  The rows must lie in pages that no
+ * other conversation uses (cart_pages_reserve sees to it).  A row that has no
+ * page is dropped and sets device status bit 7; an idle conversation (lens < 0)
+ * has nothing written.  lens is not changed (every layer has its call).      */
+CART_API int cart_pages_append(int B, int n, int total, const int* cu_seqlens, int Hkv, int d,
+                               int p, double rope_theta, const void* k, const void* v,
+                               void* k_pages, void* v_pages, int n_pages, int page_rows,
+                               const int* table, int max_pages, const int* lens, const int* pos,
+                               void* stream);
+
+/* ------------------------------------------------------------------------
+ * cart_attn_weights -- the attention weight that each key gets from the last
+ * `queries` tokens of each conversation, whose rows are cached already.
+ *   q      [B, queries, Hq, d] bf16, NOT rotated: query i of conversation b has
+ *          place p + lens[b] - queries + i (end-aligned); those that would lie
+ *          before its first row are not there, and what q and lse hold for them
+ *          is not read
+ *   lse    [B, Hq, queries] f32: their natural-log log-sum-exps, as
+ *          cart_attn_fwd returns them
+ *   pos    position of query 0 (NULL: its place)
+ *   kc     [p, Hkv, d] bf16 (NULL when p == 0)
+ *   weights, and cart [B, Hkv, p] f32 for the cartridge's rows (NULL when
+ *          p == 0): the sum over the queries that see the key and over the
+ *          heads of its group of exp(scale * q . k - lse).
+ *          accumulate == 0: rows 0 .. lens[b] - 1 and all of cart are set; 1:
+ *          it is added, but for the rows of the queries themselves (from
+ *          lens[b] - queries on), which are set.  Rows that have no page count
+ *          as seen by no query.  Rows from lens[b] on are left as they are.
+ * The rotated queries enter the products as two bf16 terms (2^-16 of their
+ * value), the sums are f32.  A key that a query does not see gets nothing from
+ * it, whatever either holds.
+ * Workspace: cart_attn_weights_workspace_size().                          */
+CART_API size_t cart_attn_weights_workspace_size(int B, int queries, int Hq, int Hkv, int d, int p,
+                                                 int page_rows, int max_pages);
+CART_API int cart_attn_weights(int B, int queries, int window, int sinks, int Hq, int Hkv, int d,
+                               int p, float scale, double rope_theta, const void* q,
+                               const float* lse, const void* kc, const void* k_pages, int n_pages,
+                               int page_rows, const int* table, int max_pages, const int* lens,
+                               const int* pos, int accumulate, float* weights, int weight_rows,
+                               float* cart, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* ------------------------------------------------------------------------
+ * cart_pages_evict -- conversations that hold more than keep[b] rows come down
+ * to keep[b], in every layer and kv head by its own weights.
+ *   keep   [B] int32 (device): < 0, or at least lens[b]: left as it is
+ *   first, recent  the rows below `first` stay, and the last `recent` ones as
+ *          far as there is room beside those; the room that is left goes to the
+ *          rows between that have most weight, ties to the lower row, NaN
+ *          counting as most
+ *   weights [layers, B, Hkv, weight_rows] f32, or NULL: the last rows stay
+ *   done   [B] int32 (output): 1, or 0 where the conversation holds more than
+ *          keep[b] rows and was left as it is: a page of its rows is not there,
+ *          or there were too few free pages
+ * The rows that stay keep their order: the i-th of them becomes row i, and its
+ * weight weights[..][i]; rows and weights behind are left as they were.  Pages
+ * that rows would be moved into and that are shared (refs > 1) are not written:
+ * a free one takes the place of each (lowest first, conversations in order; one
+ * that finds too few, and all later ones that need any, are left).  Pages
+ * behind the last of keep[b] rows are given back.  What is given back, or loses
+ * its last holder, is free from the next call on.  lens[b] becomes keep[b].
+ *   k_pages, v_pages: all layers, CART_BF16 or CART_F32; a head's row, d
+ *          values, must be a multiple of 16 bytes
+ * Workspace: cart_pages_evict_workspace_size().                           */
+CART_API size_t cart_pages_evict_workspace_size(int B, int max_pages, int n_pages);
+CART_API int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtype, void* k_pages,
+                              void* v_pages, int n_pages, int page_rows, int* table, int max_pages,
+                              int* lens, int* refs, float* weights, int weight_rows,
+                              const int* keep, int first, int recent, int* done, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * cart_attn_decode_paged -- one new token per conversation, as
+ * cart_attn_decode_tree with one node, with positions apart from rows, a window
+ * with sinks, and the weights that the token gives.
+ *   q [B, Hq, d], k_new, v_new [B, Hkv, d], o [B, Hq, d] bf16; kc, vc
+ *          [p, Hkv, d] bf16 (NULL when p == 0)
+ *   pos    position of the new token (NULL: p + lens[b])
+ *   weights NULL: not kept.  Else to those of rows below lens[b] is added what
+ *          the token's heads give the row, and that of row lens[b] is set.
+ * The token's rotated key (rounded to bf16) and its value are written to row
+ * lens[b], which must lie in a page of its own; it attends to what it sees of
+ * the cartridge and rows 0 .. lens[b] (rows without a page are not there; keys
+ * and values that it does not see do not reach it, whatever they hold).  A
+ * query whose every logit is -inf has o = 0 and gives no weight.  A key that is
+ * not finite makes the logits of those that see it NaN or infinite.
+ * An idle conversation (lens < 0) has o = 0 and nothing written, and so has one
+ * whose row lens[b] has no page, which sets device status bit 7.
+ * The rotated queries enter the products with private rows as two bf16 terms.
+ * Workspace: cart_attn_decode_paged_workspace_size(), `weights` 1 where they are
+ * kept.                                                                    */
+CART_API size_t cart_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int d, int p,
+                                                      int page_rows, int max_pages, int weights);
+CART_API int cart_attn_decode_paged(int B, int window, int sinks, int Hq, int Hkv, int d, int p,
+                                    float scale, double rope_theta, const void* q,
+                                    const void* k_new, const void* v_new, const void* kc,
+                                    const void* vc, void* k_pages, void* v_pages, int n_pages,
+                                    int page_rows, const int* table, int max_pages,
+                                    const int* lens, const int* pos, float* weights,
+                                    int weight_rows, void* o, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a cart_status value (static string). */
 CART_API const char* cart_status_string(int status);
 

@@ -105,6 +105,20 @@ def lib():
                                             vp]
             L.cart_pages_compact.argtypes = [i, i, i, i, i, vp, vp, i, i, vp, i, vp, vp, vp, vp,
                                              sz, vp]
+            L.cart_pages_append.argtypes = [i, i, i, vp, i, i, i, d, vp, vp, vp, vp, i, i, vp, i, vp,
+                                            vp, vp]
+            L.cart_attn_weights_workspace_size.argtypes = [i] * 8
+            L.cart_attn_weights_workspace_size.restype = sz
+            L.cart_attn_weights.argtypes = [i, i, i, i, i, i, i, i, f, d, vp, vp, vp, vp, i, i, vp, i,
+                                            vp, vp, i, vp, i, vp, vp, sz, vp]
+            L.cart_pages_evict_workspace_size.argtypes = [i, i, i]
+            L.cart_pages_evict_workspace_size.restype = sz
+            L.cart_pages_evict.argtypes = [i, i, i, i, i, vp, vp, i, i, vp, i, vp, vp, vp, i, vp, i, i,
+                                           vp, vp, sz, vp]
+            L.cart_attn_decode_paged_workspace_size.argtypes = [i] * 8
+            L.cart_attn_decode_paged_workspace_size.restype = sz
+            L.cart_attn_decode_paged.argtypes = [i, i, i, i, i, i, i, f, d, vp, vp, vp, vp, vp, vp, vp,
+                                                 i, i, vp, i, vp, vp, vp, i, vp, vp, sz, vp]
             L.cart_status_string.argtypes = [i]
             L.cart_status_string.restype = ctypes.c_char_p
             L.cart_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i]
@@ -118,7 +132,8 @@ def lib():
                          "cart_attn_fwd_packed", "cart_attn_bwd_packed",
                          "cart_attn_decode", "cart_attn_decode_span", "cart_device_status",
                          "cart_attn_decode_tree", "cart_pages_fork", "cart_pages_reserve",
-                         "cart_pages_accept", "cart_pages_compact",
+                         "cart_pages_accept", "cart_pages_compact", "cart_pages_append",
+                         "cart_attn_weights", "cart_pages_evict", "cart_attn_decode_paged",
                          "cart_trace_enable",
                          "cart_trace_count", "cart_trace_get"):
                 getattr(L, name).restype = ctypes.c_int
@@ -137,7 +152,9 @@ EXPORTS = ("cart_write_to_cache", "cart_attn_fwd_workspace_size", "cart_attn_fwd
            "cart_attn_bwd_packed_workspace_size", "cart_attn_bwd_packed", "cart_release",
            "cart_attn_decode_tree_workspace_size", "cart_attn_decode_tree", "cart_pages_fork",
            "cart_pages_workspace_size", "cart_pages_reserve", "cart_pages_accept",
-           "cart_pages_compact")
+           "cart_pages_compact", "cart_pages_append", "cart_attn_weights_workspace_size",
+           "cart_attn_weights", "cart_pages_evict_workspace_size", "cart_pages_evict",
+           "cart_attn_decode_paged_workspace_size", "cart_attn_decode_paged")
 
 
 def _check(fn: str, rc: int):
@@ -690,6 +707,183 @@ def cart_pages_compact(k_pages, v_pages, table, refs, *, moved=None, live=None, 
         on.close()
     _check("cart_pages_compact", rc)
     return moved, live
+
+
+# ------------------------------- a paged cache held to a budget of rows ----
+def cart_pages_append(k, v, k_pages, v_pages, table, lens, *, p, pos=None, cu_seqlens=None,
+                      theta=1.0e6, stream=None):
+    """Tokens go to each conversation's next rows, in one layer: their keys,
+    rotated at p + lens[b] + i (or pos[b] + i), and values.  k/v ``[B, n, Hkv,
+    d]`` bf16 (not rotated), or ``[T, Hkv, d]`` with cu_seqlens ``[B + 1]``
+    int32; pools ``[pages, page_rows, Hkv, d]`` bf16, table ``[B, max_pages]``,
+    lens and pos ``[B]`` int32; p the cartridge's rows.  The rows' pages must be
+    the conversation's alone.  Returns ``(k_pages, v_pages)``."""
+    B, M = table.shape
+    N, P = k_pages.shape[0], k_pages.shape[1]
+    dev, bf, i32 = table.device, torch.bfloat16, torch.int32
+    Hkv, d = k.shape[-2:]
+    if cu_seqlens is None:
+        n, new = k.shape[1], (B, k.shape[1], Hkv, d)
+        total = B * n
+    else:
+        n, total, new = 0, k.shape[0], (k.shape[0], Hkv, d)
+    if (B | M | N | n | total | p) >> 31:
+        _fits(conversations=B, max_pages=M, pages=N, tokens=n, all_tokens=total, p=p)
+    args = (B, n, total,
+            None if cu_seqlens is None else _arg("cu_seqlens", cu_seqlens, i32, (B + 1,), dev),
+            Hkv, d, p, theta, _arg("k", k, bf, new, dev), _arg("v", v, bf, new, dev),
+            _arg("k_pages", k_pages, bf, (N, P, Hkv, d), dev),
+            _arg("v_pages", v_pages, bf, (N, P, Hkv, d), dev), N, P,
+            _arg("table", table, i32, (B, M), dev), M, _arg("lens", lens, i32, (B,), dev),
+            None if pos is None else _arg("pos", pos, i32, (B,), dev))
+    on = _On(dev, stream)
+    try:
+        rc = (_lib or lib()).cart_pages_append(*args, on.handle)
+    finally:
+        on.close()
+    _check("cart_pages_append", rc)
+    return k_pages, v_pages
+
+
+@functools.lru_cache(maxsize=1024)
+def weights_workspace_size(B, queries, Hq, Hkv, d, p, page_rows, max_pages) -> int:
+    return int(lib().cart_attn_weights_workspace_size(B, queries, Hq, Hkv, d, p, page_rows,
+                                                      max_pages))
+
+
+def cart_attn_weights(q, lse, kc, k_pages, table, lens, weights, cart=None, *, pos=None,
+                      accumulate=False, scale=None, theta=1.0e6, window=0, sinks=0, workspace=None,
+                      stream=None):
+    """The attention weight that each key gets from each conversation's last
+    tokens, whose rows are cached: q ``[B, queries, Hq, d]`` bf16 (not rotated,
+    the last one at the conversation's last row), lse ``[B, Hq, queries]`` f32
+    as ``cart_attn_fwd`` returns it, kc ``[p, Hkv, d]`` bf16, k_pages ``[pages,
+    page_rows, Hkv, d]`` bf16.  weights ``[B, Hkv, rows]`` f32 (rows >=
+    max_pages * page_rows) gets the private rows', cart ``[B, Hkv, p]`` f32
+    (None: a new one) the cartridge's.  ``accumulate``: added to what they hold
+    (a new cart's 0), the queries' own rows set.  pos ``[B]`` int32: position of
+    query 0; window and sinks by places (see the header).  Returns ``(weights,
+    cart)``."""
+    B, T, Hq, d = q.shape
+    p, Hkv = kc.shape[0], kc.shape[1]
+    N, P = k_pages.shape[0], k_pages.shape[1]
+    M, dev, bf, i32, f32 = table.shape[-1], q.device, torch.bfloat16, torch.int32, torch.float32
+    W = weights.shape[-1]
+    if (B | T | M | N | W | window | sinks) >> 31:
+        _fits(conversations=B, queries=T, max_pages=M, pages=N, weight_rows=W, window=window,
+              sinks=sinks)
+    args = (_arg("q", q, bf, q.shape, dev), _arg("lse", lse, f32, (B, Hq, T), dev),
+            _arg("kc", kc, bf, (p, Hkv, d), dev), _arg("k_pages", k_pages, bf, (N, P, Hkv, d), dev),
+            N, P, _arg("table", table, i32, (B, M), dev), M, _arg("lens", lens, i32, (B,), dev),
+            None if pos is None else _arg("pos", pos, i32, (B,), dev), 1 if accumulate else 0,
+            _arg("weights", weights, f32, (B, Hkv, W), dev), W)
+    on = _On(dev, stream)
+    try:
+        if cart is None:
+            cart = _make(on.stream, torch.zeros if accumulate else torch.empty, (B, Hkv, p),
+                         dtype=f32, device=dev)
+        cp = _arg("cart", cart, f32, (B, Hkv, p), dev)
+        ws, wp, wn = _scratch(on, workspace, weights_workspace_size(B, T, Hq, Hkv, d, p, P, M))
+        rc = (_lib or lib()).cart_attn_weights(
+            B, T, window, sinks, Hq, Hkv, d, p, d ** -0.5 if scale is None else scale, theta, *args,
+            cp, wp, wn, on.handle)
+    finally:
+        on.close()
+    _check("cart_attn_weights", rc)
+    return weights, cart
+
+
+@functools.lru_cache(maxsize=1024)
+def evict_workspace_size(B, max_pages, n_pages) -> int:
+    return int(lib().cart_pages_evict_workspace_size(B, max_pages, n_pages))
+
+
+def cart_pages_evict(k_pages, v_pages, table, lens, refs, weights, keep, *, first=0, recent=0,
+                     done=None, workspace=None, stream=None):
+    """Conversations that hold more than keep[b] (``[B]`` int32; < 0: left as
+    it is) rows come down to that many, in every layer and kv head: the rows
+    below ``first``, the last ``recent`` ones and those of most weight stay, in
+    their order.  weights ``[layers, B, Hkv, rows]`` f32 are moved along (None:
+    the last rows stay).  Pools ``[layers, pages, page_rows, Hkv, d]`` (bf16 or
+    f32); table, lens and refs are updated, shared pages replaced and pages
+    behind given back.  Returns done ``[B]`` int32: 0 where more than keep[b]
+    rows are held still (a page is not there, or too few are free)."""
+    layers, N, P, Hkv, d, dt, kp, vp, dev = _pools(k_pages, v_pages)
+    B, M = table.shape
+    W = 0 if weights is None else weights.shape[-1]
+    if (B | M | N | W | first | recent) >> 31:
+        _fits(conversations=B, max_pages=M, pages=N, weight_rows=W, first=first, recent=recent)
+    i32 = torch.int32
+    # one layer's pool goes with one layer's weights
+    held = (layers, B, Hkv, W) if k_pages.dim() == 5 else (B, Hkv, W)
+    args = (B, layers, Hkv, d, dt, kp, vp, N, P, _arg("table", table, i32, (B, M), dev), M,
+            _arg("lens", lens, i32, (B,), dev), _arg("refs", refs, i32, (N,), dev),
+            None if weights is None else _arg("weights", weights, torch.float32, held, dev), W,
+            _arg("keep", keep, i32, (B,), dev), first, recent)
+    on = _On(dev, stream)
+    try:
+        if done is None:
+            done = on.empty((B,), i32)
+        ws, wp, wn = _scratch(on, workspace, evict_workspace_size(B, M, N))
+        rc = (_lib or lib()).cart_pages_evict(*args, _arg("done", done, i32, (B,), dev), wp, wn,
+                                              on.handle)
+    finally:
+        on.close()
+    _check("cart_pages_evict", rc)
+    return done
+
+
+@functools.lru_cache(maxsize=1024)
+def decode_paged_workspace_size(B, Hq, Hkv, d, p, page_rows, max_pages, weights) -> int:
+    return int(lib().cart_attn_decode_paged_workspace_size(B, Hq, Hkv, d, p, page_rows, max_pages,
+                                                           1 if weights else 0))
+
+
+def cart_attn_decode_paged(q, k_new, v_new, kc, vc, k_pages, v_pages, table, lens, *, pos=None,
+                           weights=None, scale=None, theta=1.0e6, window=0, sinks=0, o=None,
+                           workspace=None, stream=None):
+    """One decode step over paged rows.  q ``[B, Hq, d]``, k_new/v_new ``[B,
+    Hkv, d]`` (bf16, not rotated), kc/vc ``[p, Hkv, d]`` bf16 shared cartridge,
+    k_pages/v_pages ``[pages, page_rows, Hkv, d]`` bf16 pools (row lens[b] is
+    written), table ``[B, max_pages]`` and lens ``[B]`` int32.  pos ``[B]``
+    int32: the token's position (None: p + lens[b]; rows that were evicted leave
+    it ahead of that).  ``weights`` ``[B, Hkv, rows]`` f32 (rows >= max_pages *
+    page_rows) gets what the token gives each row added, and row lens[b] set.
+    window and sinks by places (see the header).  Returns o ``[B, Hq, d]``
+    bf16, 0 for idle conversations."""
+    B, Hq, d = q.shape
+    Hkv, p = k_new.shape[1], kc.shape[0]
+    N, P = k_pages.shape[0], k_pages.shape[1]
+    M, dev, bf, i32 = table.shape[-1], q.device, torch.bfloat16, torch.int32
+    W = 0 if weights is None else weights.shape[-1]
+    if (B | M | N | W | window | sinks) >> 31:
+        _fits(conversations=B, max_pages=M, pages=N, weight_rows=W, window=window, sinks=sinks)
+    new = (B, Hkv, d)
+    args = (_arg("q", q, bf, q.shape, dev),
+            _arg("k_new", k_new, bf, new, dev), _arg("v_new", v_new, bf, new, dev),
+            _arg("kc", kc, bf, (p, Hkv, d), dev), _arg("vc", vc, bf, (p, Hkv, d), dev),
+            _arg("k_pages", k_pages, bf, (N, P, Hkv, d), dev),
+            _arg("v_pages", v_pages, bf, (N, P, Hkv, d), dev), N, P,
+            _arg("table", table, i32, (B, M), dev), M, _arg("lens", lens, i32, (B,), dev),
+            None if pos is None else _arg("pos", pos, i32, (B,), dev),
+            None if weights is None else _arg("weights", weights, torch.float32, (B, Hkv, W), dev),
+            W)
+    on = _On(dev, stream)
+    try:
+        if o is None:
+            o = torch.empty_like(q) if on.stream is None else on.empty(q.shape, bf)
+            op = o.data_ptr()
+        else:
+            op = _arg("o", o, bf, q.shape, dev)
+        ws, wp, wn = _scratch(on, workspace, decode_paged_workspace_size(
+            B, Hq, Hkv, d, p, P, M, weights is not None))
+        rc = (_lib or lib()).cart_attn_decode_paged(
+            B, window, sinks, Hq, Hkv, d, p, d ** -0.5 if scale is None else scale, theta, *args, op,
+            wp, wn, on.handle)
+    finally:
+        on.close()
+    _check("cart_attn_decode_paged", rc)
+    return o
 
 
 def release() -> None:

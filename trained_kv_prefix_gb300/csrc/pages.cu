@@ -21,9 +21,6 @@
 namespace cart {
 namespace {
 
-constexpr int kMetaCtas = 8;        // CTAs of a planning cluster
-constexpr int kMetaThreads = 1024;  // threads of each
-constexpr int kMetaWarps = kMetaCtas * kMetaThreads / 32;
 constexpr int kMaxForks = 8192;
 
 // Workspace of reserve and compact (int32 words): the head, then the lists.
@@ -48,49 +45,6 @@ PagesWs pages_ws(int B, int n_pages) {
   w.starts = take((static_cast<size_t>(B) + 1) * 8);
   w.total = off;
   return w;
-}
-
-// Every thread of the cluster arrives (its writes released to the cluster)
-// and waits for the others.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ int cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return static_cast<int>(r);
-}
-
-// Exclusive prefix sum of v over the block's 1024 threads; *total the sum.
-// Every thread calls it; sums: 33 words of shared memory.
-__device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();  // sums may still be read from an earlier call
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int w = sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    sums[lane] = w;
-  }
-  __syncthreads();
-  *total = sums[31];
-  return x - v + (warp ? sums[warp - 1] : 0);
-}
-
-__device__ __forceinline__ bool is_page(int page, int n_pages) {
-  return static_cast<unsigned>(page) < static_cast<unsigned>(n_pages);
 }
 
 // ---------------------------------------------------------------- fork ----
@@ -494,24 +448,6 @@ __global__ void __launch_bounds__(128) accept_kernel(const AcceptArgs a) {
 }
 
 // ----------------------------------------------------------- arguments ----
-int check_tables(int B, int max_pages, int n_pages, int page_rows) {
-  if (B < 1 || B > 65535 || max_pages < 1 || n_pages < 1 || n_pages > (1 << 30) ||
-      page_log2_of(page_rows) < 0)
-    return CART_ERR_GEOMETRY;
-  if (static_cast<long long>(max_pages) * page_rows >= (1ll << 24)) return CART_ERR_GEOMETRY;
-  return CART_OK;
-}
-
-int check_pool(int layers, int Hkv, int d, cart_dtype dtype, const void* k, const void* v) {
-  if (layers < 1 || layers > 32767 || Hkv < 1 || d < 1 || Hkv > 65535 || d > 65535)
-    return CART_ERR_GEOMETRY;
-  if (dtype != CART_BF16 && dtype != CART_F32) return CART_ERR_DTYPE;
-  const long long row = static_cast<long long>(Hkv) * d * (dtype == CART_BF16 ? 2 : 4);
-  if (row % 16 != 0 || row > (1 << 24)) return CART_ERR_GEOMETRY;
-  if (!aligned_to(k, 16) || !aligned_to(v, 16)) return CART_ERR_POINTER;
-  return CART_OK;
-}
-
 int row_bytes_of(int Hkv, int d, cart_dtype dtype) {
   return Hkv * d * (dtype == CART_BF16 ? 2 : 4);
 }

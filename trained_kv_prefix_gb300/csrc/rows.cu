@@ -1,0 +1,564 @@
+// rows.cu -- operators on the rows of paged private caches (cartattn.h, "A
+// paged cache held to a budget of rows"): append a prompt's rows, evict rows of
+// little weight.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "internal.cuh"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace cart {
+namespace {
+
+struct Turns {
+  float2 t[kMaxHeadDim / 2];
+};
+
+// --------------------------------------------------------------- append ----
+struct AppendArgs {
+  PageTable pt;
+  int B, n, total, Hkv, d, p;
+  const int* cu;   // packed: [B + 1]; null: sequences of n tokens
+  const int* pos;  // null: p + lens
+  const __nv_bfloat16 *k, *v;
+  __nv_bfloat16 *k_pages, *v_pages;
+  uint32_t* status;
+};
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendTokens = 4;  // tokens per block
+
+// Segment of token t: the last b with cu[b] <= t (0 if none).
+__device__ __forceinline__ int segment_of(const int* cu, int B, int t) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Four tokens of the token axis per block: their page rows and angles first,
+// then 16-byte pieces, a key's with those d/2 further on.
+__global__ void __launch_bounds__(kAppendThreads)
+    append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Turns f) {
+  __shared__ float2 cs[kAppendTokens][kMaxHeadDim / 2];
+  __shared__ long long at_s[kAppendTokens];  // row of the pool, -1: dropped
+  __shared__ int pos_s[kAppendTokens];
+  const int tid = threadIdx.x, half = a.d / 2;
+  const int t0 = blockIdx.x * kAppendTokens, nt = min(kAppendTokens, a.total - t0);
+  if (tid < nt) {
+    const int t = t0 + tid;
+    int b, i;
+    bool ok = true;
+    if (a.cu) {
+      b = segment_of(a.cu, a.B, t);
+      i = t - __ldg(a.cu + b);
+      ok = i >= 0 && t < __ldg(a.cu + b + 1);
+      if (!ok) atomicOr(a.status, kDevErrSegments);
+    } else {
+      b = t / a.n;
+      i = t % a.n;
+    }
+    const int len = ok ? __ldg(a.pt.lens + b) : -1;
+    // (below 2^25: both are below 2^24 where the row can have a page)
+    const long long r = static_cast<long long>(len) + i;
+    const int page = len >= 0 && r < (a.pt.max_pages << a.pt.page_log2)
+                         ? page_of(a.pt, b, static_cast<int>(r))
+                         : -1;
+    if (len >= 0 && page < 0) atomicOr(a.status, kDevErrNoPage);
+    at_s[tid] = page < 0 ? -1
+                         : (static_cast<long long>(page) << a.pt.page_log2) +
+                               (r & ((1 << a.pt.page_log2) - 1));
+    const long long first = a.pos ? __ldg(a.pos + b) : static_cast<long long>(a.p) + len;
+    pos_s[tid] = static_cast<int>(min(max(first + i, 0ll), (1ll << 24) - 1));
+  }
+  __syncthreads();
+  for (int e = tid; e < nt * half; e += kAppendThreads) {
+    const int t = e / half, j = e % half;
+    cs[t][j] = rope_cs_turns(f.t[j], pos_s[t]);
+  }
+  __syncthreads();
+  const int row = a.Hkv * a.d;  // elements of a row
+  // keys: pairs of 8 values
+  const int per_head = half / 8, per_tok = a.Hkv * per_head;
+  for (int e = tid; e < nt * per_tok; e += kAppendThreads) {
+    const int t = e / per_tok, c = e % per_tok, h = c / per_head, j0 = c % per_head * 8;
+    if (at_s[t] < 0) continue;
+    const __nv_bfloat16* x = a.k + static_cast<long long>(t0 + t) * row + h * a.d + j0;
+    const uint4 lo = __ldg(reinterpret_cast<const uint4*>(x));
+    const uint4 hi = __ldg(reinterpret_cast<const uint4*>(x + half));
+    const uint32_t pl[4] = {lo.x, lo.y, lo.z, lo.w}, ph[4] = {hi.x, hi.y, hi.z, hi.w};
+    uint32_t yl[4], yh[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 fl = bf16x2_to_float2(pl[k]), fh = bf16x2_to_float2(ph[k]);
+      float2 u, w;
+      rope_pair(fl.x, fh.x, cs[t][j0 + 2 * k], u.x, w.x);
+      rope_pair(fl.y, fh.y, cs[t][j0 + 2 * k + 1], u.y, w.y);
+      yl[k] = pack_bf16x2(u.x, u.y);
+      yh[k] = pack_bf16x2(w.x, w.y);
+    }
+    __nv_bfloat16* y = a.k_pages + at_s[t] * row + h * a.d + j0;
+    *reinterpret_cast<uint4*>(y) = make_uint4(yl[0], yl[1], yl[2], yl[3]);
+    *reinterpret_cast<uint4*>(y + half) = make_uint4(yh[0], yh[1], yh[2], yh[3]);
+  }
+  const int v_tok = row / 8;
+  for (int e = tid; e < nt * v_tok; e += kAppendThreads) {
+    const int t = e / v_tok, c = e % v_tok * 8;
+    if (at_s[t] < 0) continue;
+    *reinterpret_cast<uint4*>(a.v_pages + at_s[t] * row + c) =
+        __ldg(reinterpret_cast<const uint4*>(a.v + static_cast<long long>(t0 + t) * row + c));
+  }
+}
+
+// ---------------------------------------------------------------- evict ----
+// Conversations that hold more than keep[b] rows give up all but that many, in
+// every layer and kv head on their own: the rows below `first`, the last
+// `recent` ones, and of those between the ones of most weight, ties to the
+// lower row.  Three launches: a plan (pages that are needed, and given back),
+// the moves, and the new tables and lengths.
+struct EvictArgs {
+  PageTable pt;  // (as it was before the call, until the last launch)
+  int B, layers, Hkv, first, recent, weight_rows;
+  int *table, *lens, *refs, *done;
+  const int* keep;
+  float* weights;  // [layers, B, Hkv, weight_rows], or null
+  // workspace: free pages per CTA of the plan; shared pages that a conversation
+  // needs replaced (kIdle: nothing to evict, kTorn: a page of its rows is not
+  // there); such pages before it; whether it is evicted; free pages; the new
+  // pages of its rows [B, max_pages]
+  int *head, *need, *base, *go, *free, *to;
+  char *k, *v;
+  long long layer_bytes, page_bytes;
+  int row_bytes, piece;  // bytes of a row and of one head's part of it
+};
+enum { kIdle = -2, kTorn = -1, kSwap = -2 };  // kSwap: an entry of `to` for a shared page
+
+struct EvictWs {
+  size_t need, base, go, free, to, total;
+};
+EvictWs evict_ws(int B, int max_pages, int n_pages) {
+  EvictWs w{};
+  size_t off = 256;  // (the head)
+  auto take = [&](size_t ints) {
+    const size_t o = off;
+    off += (ints * 4 + 255) & ~static_cast<size_t>(255);
+    return o;
+  };
+  w.need = take(B);
+  w.base = take(B);
+  w.go = take(B);
+  w.free = take(n_pages);
+  w.to = take(static_cast<size_t>(B) * max_pages);
+  w.total = off;
+  return w;
+}
+
+// What conversation b is to come down to: rows held and kept (len <= keep: it
+// is left as it is), the first row that may change.
+struct Budget {
+  int len, keep, first;
+};
+__device__ __forceinline__ Budget budget_of(const EvictArgs& a, int b) {
+  Budget q;
+  q.len = held_rows(a.pt, b);
+  q.keep = __ldg(a.keep + b);
+  if (q.keep < 0 || q.len <= q.keep) q.keep = q.len;
+  q.first = min(a.first, q.keep);
+  return q;
+}
+__device__ __forceinline__ int pages_for(const EvictArgs& a, int rows) {
+  return (rows + (1 << a.pt.page_log2) - 1) >> a.pt.page_log2;
+}
+
+// Bound by latency, as the plan of cart_pages_reserve, whose shape it has.
+__global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads)
+    evict_plan_kernel(const __grid_constant__ EvictArgs a) {
+  pdl_release();
+  __shared__ int sums[33];
+  const int rank = cluster_rank(), lane = threadIdx.x & 31;
+  const int gw = rank * (kMetaThreads / 32) + (threadIdx.x >> 5);
+  // ---- pages of the rows that stay and change, shared with others
+  for (int b = gw; b < a.B; b += kMetaWarps) {
+    const Budget q = budget_of(a, b);
+    int n = kIdle;
+    if (q.len > q.keep) {
+      const int* row = a.pt.table + static_cast<long long>(b) * a.pt.max_pages;
+      int* to = a.to + static_cast<long long>(b) * a.pt.max_pages;
+      const int held = pages_for(a, q.len), end = pages_for(a, q.keep);
+      const int from = q.first < q.keep ? q.first >> a.pt.page_log2 : end;  // (see kSwap)
+      bool torn = false;
+      n = 0;
+      for (int k0 = 0; k0 < held; k0 += 32) {
+        const int k = k0 + lane;
+        const int page = k < held ? __ldg(row + k) : 0;
+        const bool there = is_page(page, a.pt.n_pages);
+        torn |= k < held && !there;
+        const bool swap = there && k >= from && k < end && __ldcg(a.refs + page) > 1;
+        if (k < end) to[k] = swap ? kSwap : page;
+        n += __popc(__ballot_sync(0xffffffffu, swap));
+      }
+      if (__any_sync(0xffffffffu, torn)) n = kTorn;
+    }
+    if (lane == 0) a.need[b] = n;
+  }
+  const int part = (a.pt.n_pages + kMetaCtas - 1) / kMetaCtas;
+  const int lo = rank * part, hi = min(lo + part, a.pt.n_pages);
+  int mine = 0, n_part = 0;
+  for (int i = lo + threadIdx.x; i < hi; i += kMetaThreads) mine += __ldcg(a.refs + i) <= 0;
+  block_scan(mine, sums, &n_part);
+  if (threadIdx.x == 0) a.head[rank] = n_part;
+  cluster_sync();
+  // ---- free pages in order (every CTA its part), and over conversations the
+  // running need (CTA 0)
+  int before = 0, n_free = 0;
+  for (int r = 0; r < kMetaCtas; ++r) {
+    const int n = __ldcg(a.head + r);
+    before += r < rank ? n : 0;
+    n_free += n;
+  }
+  for (int i0 = lo; i0 < hi; i0 += kMetaThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool is_free = i < hi && __ldcg(a.refs + i) <= 0;
+    int n;
+    const int at = block_scan(is_free, sums, &n);
+    if (is_free) a.free[before + at] = i;
+    before += n;
+  }
+  if (rank == 0) {
+    long long run = 0;  // saturates above any pool
+    for (int b0 = 0; b0 < a.B; b0 += kMetaThreads) {
+      const int b = b0 + threadIdx.x;
+      int n;
+      const int at = block_scan(b < a.B ? max(__ldcg(a.need + b), 0) : 0, sums, &n);
+      if (b < a.B) a.base[b] = static_cast<int>(min(run + at, 0x40000000ll));
+      run += n;
+    }
+  }
+  cluster_sync();
+  // ---- the new pages; counts of those left and given back
+  for (int b = gw; b < a.B; b += kMetaWarps) {
+    const Budget q = budget_of(a, b);
+    const int n = __ldcg(a.need + b), base = __ldcg(a.base + b);
+    const bool go = n >= 0 && (n == 0 || base + n <= n_free);
+    if (lane == 0) {
+      a.go[b] = go;
+      a.done[b] = go || n == kIdle;
+    }
+    if (!go) continue;
+    const int* row = a.pt.table + static_cast<long long>(b) * a.pt.max_pages;
+    int* to = a.to + static_cast<long long>(b) * a.pt.max_pages;
+    const int end = pages_for(a, q.keep);
+    int taken = 0;
+    for (int k0 = 0; k0 < a.pt.max_pages; k0 += 32) {
+      const int k = k0 + lane;
+      const int page = k < a.pt.max_pages ? __ldg(row + k) : -1;
+      const bool there = is_page(page, a.pt.n_pages), swap = k < end && __ldcg(to + k) == kSwap;
+      const unsigned m = __ballot_sync(0xffffffffu, swap);
+      if (swap) {
+        const int now = __ldcg(a.free + base + taken + __popc(m & ((1u << lane) - 1)));
+        a.refs[now] = 1;
+        to[k] = now;
+      }
+      if (there && (swap || k >= end)) atomicSub(a.refs + page, 1);
+      taken += __popc(m);
+    }
+  }
+}
+
+// Weights as unsigned numbers of the same order: -0 as 0, NaN above all.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveLoads = 4;      // 16-byte pieces of K, and of V, per thread in flight
+constexpr int kMoveKeys = 4096;    // weights of the rows between held in shared memory
+
+// Inclusive prefix sum of v over the block, and the sum.  Every thread calls it.
+__device__ __forceinline__ uint2 move_scan(uint32_t v, uint32_t* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // sums may still be read from an earlier call
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kMoveThreads / 32; ++w) {
+    before += w < warp ? sums[w] : 0;
+    all += sums[w];
+  }
+  return make_uint2(before + x, all);
+}
+
+// Block (layer, conversation, kv head): the weight of the last row that stays
+// by a search over its 32 bits, eight at a time from the top (a histogram of
+// the rows that agree so far), then the rows in order, 256 at a time.  Row i of
+// those that stay is never before place i, so a run of rows may be written
+// once all of it has been read, whatever is read later.
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_move_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ uint32_t keys[kMoveKeys];
+  __shared__ uint32_t hist[256], sums[kMoveThreads / 32], pick[2];
+  __shared__ long long src[kMoveThreads], dst[kMoveThreads];
+  __shared__ float held_w[kMoveThreads];
+  pdl_wait();
+  pdl_release();
+  const int g = blockIdx.x % a.Hkv, lb = blockIdx.x / a.Hkv;
+  const int b = lb % a.B, layer = lb / a.B, tid = threadIdx.x;
+  if (!__ldcg(a.go + b)) return;
+  const Budget q = budget_of(a, b);
+  float* w = a.weights ? a.weights + (static_cast<long long>(lb) * a.Hkv + g) * a.weight_rows
+                       : nullptr;
+  const int last = w ? min(a.recent, q.keep - q.first) : q.keep - q.first;
+  const int m0 = q.first, m1 = q.len - last;        // the rows between
+  const int stay = q.keep - q.first - last;         // and how many of them stay
+  uint32_t cut = 0xffffffffu, ties = 0;  // rows of a higher key stay, and so many of this key
+  bool any = false;
+  if (stay > 0) {
+    any = true;
+    const bool cached = m1 - m0 <= kMoveKeys;
+    uint32_t left = stay, prefix = 0;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      hist[tid] = 0;
+      __syncthreads();
+      const uint32_t above = shift == 24 ? 0 : 0xffffffffu << (shift + 8);
+      for (int i = m0 + tid; i < m1; i += kMoveThreads) {
+        uint32_t key;
+        if (shift == 24 || !cached) {
+          key = weight_key(w[i]);
+          if (cached) keys[i - m0] = key;
+        } else {
+          key = keys[i - m0];
+        }
+        if ((key & above) == prefix) atomicAdd(hist + (key >> shift & 255), 1);
+      }
+      __syncthreads();
+      const uint32_t mine = hist[255 - tid];
+      const uint32_t upto = move_scan(mine, sums).x;
+      if (upto >= left && upto - mine < left) {
+        pick[0] = 255 - tid;
+        pick[1] = left - (upto - mine);
+      }
+      __syncthreads();
+      prefix |= pick[0] << shift;
+      left = pick[1];
+    }
+    cut = prefix;
+    ties = left;
+  }
+  const int* from_row = a.pt.table + static_cast<long long>(b) * a.pt.max_pages;
+  const int* to_row = a.to + static_cast<long long>(b) * a.pt.max_pages;
+  const int mask = (1 << a.pt.page_log2) - 1;
+  char* const kp = a.k + layer * a.layer_bytes + static_cast<long long>(g) * a.piece;
+  char* const vp = a.v + layer * a.layer_bytes + static_cast<long long>(g) * a.piece;
+  const int per = a.piece / 16;
+  // rows that stay so far, and of them those of key `cut` (all of that key)
+  uint32_t above = 0, equal = 0;
+  // (the pages of the rows before are as they were)
+  const int begin = q.first & ~mask;
+  above = begin;
+  for (int r0 = begin; r0 < q.len; r0 += kMoveThreads) {
+    const int r = r0 + tid;
+    bool more = false, same = false;
+    float x = 0.f;
+    if (r < q.len) {
+      if (w) x = w[r];
+      if (r < m0 || r >= m1) {
+        more = true;
+      } else if (any) {
+        const uint32_t key = weight_key(x);
+        more = key > cut;
+        same = key == cut;
+      }
+    }
+    // both counts in one scan: at most 256 of each
+    const uint2 s = move_scan(static_cast<uint32_t>(more) | static_cast<uint32_t>(same) << 16, sums);
+    const uint32_t more_to = above + (s.x & 0xffff), same_to = equal + (s.x >> 16);
+    const bool stays = more || (same && same_to <= ties);
+    const int base = static_cast<int>(above + min(equal, ties));
+    above += s.y & 0xffff;
+    equal += s.y >> 16;
+    const int n = static_cast<int>(above + min(equal, ties)) - base;
+    if (stays) {
+      const int z = static_cast<int>(more_to + min(same_to, ties)) - 1;  // its place
+      const int page = __ldg(from_row + (r >> a.pt.page_log2));
+      const int now = __ldcg(to_row + (z >> a.pt.page_log2));
+      const bool moves = z != r || now != page;
+      src[z - base] = page * a.page_bytes + static_cast<long long>(r & mask) * a.row_bytes;
+      dst[z - base] =
+          moves ? now * a.page_bytes + static_cast<long long>(z & mask) * a.row_bytes : -1;
+      held_w[z - base] = x;
+    }
+    __syncthreads();
+    if (w && tid < n) w[base + tid] = held_w[tid];
+    for (int t0 = 0; t0 < n * per; t0 += kMoveThreads * kMoveLoads) {
+      uint4 rk[kMoveLoads], rv[kMoveLoads];
+      long long to[kMoveLoads];
+#pragma unroll
+      for (int u = 0; u < kMoveLoads; ++u) {
+        const int t = t0 + u * kMoveThreads + tid;
+        to[u] = -1;
+        if (t < n * per) {
+          const int i = t / per, c = (t - i * per) * 16;
+          if (dst[i] >= 0) {
+            to[u] = dst[i] + c;
+            rk[u] = __ldcg(reinterpret_cast<const uint4*>(kp + src[i] + c));
+            rv[u] = __ldcg(reinterpret_cast<const uint4*>(vp + src[i] + c));
+          }
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMoveLoads; ++u)
+        if (to[u] >= 0) {
+          *reinterpret_cast<uint4*>(kp + to[u]) = rk[u];
+          *reinterpret_cast<uint4*>(vp + to[u]) = rv[u];
+        }
+    }
+    __syncthreads();  // the lists are free again
+  }
+}
+
+// The new tables and lengths, a warp per conversation.
+__global__ void __launch_bounds__(256) evict_tables_kernel(const __grid_constant__ EvictArgs a) {
+  pdl_wait();
+  const int b = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (b >= a.B || !__ldcg(a.go + b)) return;
+  const int keep = __ldg(a.keep + b), end = pages_for(a, keep);
+  int* row = a.table + static_cast<long long>(b) * a.pt.max_pages;
+  const int* to = a.to + static_cast<long long>(b) * a.pt.max_pages;
+  for (int k = lane; k < a.pt.max_pages; k += 32) row[k] = k < end ? __ldcg(to + k) : -1;
+  if (lane == 0) a.lens[b] = keep;
+}
+
+}  // namespace
+}  // namespace cart
+
+using namespace cart;
+
+extern "C" {
+
+int cart_pages_append(int B, int n, int total, const int* cu_seqlens, int Hkv, int d, int p,
+                      double rope_theta, const void* k, const void* v, void* k_pages,
+                      void* v_pages, int n_pages, int page_rows, const int* table, int max_pages,
+                      const int* lens, const int* pos, void* stream) {
+  int rc = check_tables(B, max_pages, n_pages, page_rows);
+  if (!rc) rc = check_pool(1, Hkv, d, CART_BF16, k_pages, v_pages);
+  if (rc) return rc;
+  if (d != 64 && d != 128) return CART_ERR_GEOMETRY;
+  if (p < 0 || static_cast<long long>(p) + static_cast<long long>(max_pages) * page_rows >=
+                   (1ll << 24))
+    return CART_ERR_GEOMETRY;
+  if (!(rope_theta > 0.0) || !std::isfinite(rope_theta)) return CART_ERR_GEOMETRY;
+  if (total < 1 || (!cu_seqlens && (n < 1 || static_cast<long long>(B) * n != total)))
+    return CART_ERR_GEOMETRY;
+  if (!aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(table, 4) || !aligned_to(lens, 4) ||
+      (cu_seqlens && !aligned_to(cu_seqlens, 4)) || (pos && !aligned_to(pos, 4)))
+    return CART_ERR_POINTER;
+  rc = check_device();
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  AppendArgs a{};
+  a.pt = PageTable{table, lens, max_pages, n_pages, page_log2_of(page_rows)};
+  a.B = B;
+  a.n = n;
+  a.total = total;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.p = p;
+  a.cu = cu_seqlens;
+  a.pos = pos;
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.k_pages = static_cast<__nv_bfloat16*>(k_pages);
+  a.v_pages = static_cast<__nv_bfloat16*>(v_pages);
+  a.status = device_status_ptr();
+  const RopeFreqs f = make_rope_freqs(d, rope_theta);
+  Turns turns{};
+  for (int j = 0; j < d / 2; ++j) turns.t[j] = f.turns[j];
+  TraceScope tr("pages_append", st);
+  append_kernel<<<(total + kAppendTokens - 1) / kAppendTokens, kAppendThreads, 0, st>>>(a, turns);
+  return cudaGetLastError() == cudaSuccess ? CART_OK : CART_ERR_CUDA;
+}
+
+size_t cart_pages_evict_workspace_size(int B, int max_pages, int n_pages) {
+  if (check_tables(B, max_pages, n_pages, 16)) return 0;
+  return evict_ws(B, max_pages, n_pages).total;
+}
+
+int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtype, void* k_pages,
+                     void* v_pages, int n_pages, int page_rows, int* table, int max_pages,
+                     int* lens, int* refs, float* weights, int weight_rows, const int* keep,
+                     int first, int recent, int* done, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  int rc = check_tables(B, max_pages, n_pages, page_rows);
+  if (!rc) rc = check_pool(layers, Hkv, d, dtype, k_pages, v_pages);
+  if (rc) return rc;
+  const int piece = d * (dtype == CART_BF16 ? 2 : 4);
+  if (piece % 16 != 0 || first < 0 || recent < 0) return CART_ERR_GEOMETRY;
+  if (weights && weight_rows < max_pages * page_rows) return CART_ERR_GEOMETRY;
+  const long long blocks = static_cast<long long>(layers) * B;
+  if (blocks > 0x7fffffff / Hkv) return CART_ERR_GEOMETRY;
+  if (!aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(refs, 4) ||
+      !aligned_to(keep, 4) || !aligned_to(done, 4) || (weights && !aligned_to(weights, 16)))
+    return CART_ERR_POINTER;
+  const EvictWs w = evict_ws(B, max_pages, n_pages);
+  if (!aligned_to(workspace, 16) || workspace_bytes < w.total) return CART_ERR_WORKSPACE;
+  rc = check_device();
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  EvictArgs a{};
+  a.pt = PageTable{table, lens, max_pages, n_pages, page_log2_of(page_rows)};
+  a.B = B;
+  a.layers = layers;
+  a.Hkv = Hkv;
+  a.first = first;
+  a.recent = recent;
+  a.weight_rows = weight_rows;
+  a.table = table;
+  a.lens = lens;
+  a.refs = refs;
+  a.done = done;
+  a.keep = keep;
+  a.weights = weights;
+  a.head = reinterpret_cast<int*>(ws);
+  a.need = reinterpret_cast<int*>(ws + w.need);
+  a.base = reinterpret_cast<int*>(ws + w.base);
+  a.go = reinterpret_cast<int*>(ws + w.go);
+  a.free = reinterpret_cast<int*>(ws + w.free);
+  a.to = reinterpret_cast<int*>(ws + w.to);
+  a.k = static_cast<char*>(k_pages);
+  a.v = static_cast<char*>(v_pages);
+  a.piece = piece;
+  a.row_bytes = Hkv * piece;
+  a.page_bytes = static_cast<long long>(a.row_bytes) * page_rows;
+  a.layer_bytes = a.page_bytes * n_pages;
+  TraceScope tr("pages_evict", st);
+  evict_plan_kernel<<<kMetaCtas, kMetaThreads, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = launch_dependent(evict_move_kernel, dim3(static_cast<unsigned>(blocks * Hkv)),
+                         dim3(kMoveThreads), 0, st, a);
+  if (e == cudaSuccess)
+    e = launch_dependent(evict_tables_kernel, dim3((B + 7) / 8), dim3(256), 0, st, a);
+  return e == cudaSuccess ? CART_OK : CART_ERR_CUDA;
+}
+
+}  // extern "C"
