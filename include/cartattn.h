@@ -579,7 +579,8 @@ CART_API int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtyp
  * The token's rotated key (rounded to bf16) and its value are written to row
  * lens[b], which must lie in a page of its own; it attends to what it sees of
  * the cartridge and rows 0 .. lens[b] (rows without a page are not there; keys
- * and values that it does not see do not reach it, whatever they hold).  A
+ * and values that it does not see do not reach it, whatever they hold, but for
+ * a cartridge value that is not finite and that some conversation sees).  A
  * query whose every logit is -inf has o = 0 and gives no weight.  A key that is
  * not finite makes the logits of those that see it NaN or infinite.
  * An idle conversation (lens < 0) has o = 0 and nothing written, and so has one
