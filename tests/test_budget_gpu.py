@@ -401,6 +401,7 @@ STEPS = [
     ("long_d128", 1, 32, 8, 128, 513, (3001,), 64, 0, 0, True),
     # more tiles and rows than CTAs: several a CTA, in pieces of several segments
     ("runs_of_tiles", 3, 8, 8, 64, 2700, (40, 7, 0), 16, 0, 0, False),
+    ("runs_across", 3, 8, 8, 128, 2700, (40, 7, 0), 16, 0, 0, False),
     ("runs_of_both", 34, 32, 8, 128, 1500, tuple(range(0, 680, 20)), 64, 0, 0, False),
     ("runs_wide", 20, 35, 5, 64, 2900, tuple(range(9, 609, 30)), 32, 0, 0, True),
     ("runs_window", 20, 32, 8, 64, 1500, tuple(range(0, 2000, 100)), 32, 700, 70, False),

@@ -107,6 +107,8 @@ enum CartBar {
   kCPFull0 = kCSFull0 + 2,    // its weights are (128 arrivals); by buffer, since those
                               // of the next tile may come before these are waited for
   kCPvDone = kCPFull0 + 2,    // O has them, and V has been read
+  kCODone,                    // O has those of the piece's last tile (waits for this one
+                              // may come two tiles after the last for the one before)
   kCDrain,
   kCBars
 };
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(kCartThreads, 2)
   const int total = a.Hkv * a.row_tiles * a.key_tiles;
   const int lo = min(blockIdx.x * a.cart_chunk, total), hi = min(lo + a.cart_chunk, total);
   const int R = a.B * a.G;
-  int step = 0;  // tiles walked, in every role
+  int step = 0, pieces = 0;  // tiles walked, and pieces that had any, in every role
   bool ok = true;
   for (int u = lo; u < hi;) {
     const int seg = u / a.key_tiles, t0 = u - seg * a.key_tiles;
@@ -297,6 +299,7 @@ __global__ void __launch_bounds__(kCartThreads, 2)
           umma_bf16_ts_w(tO, tS + (s & 1) * kCartKeys + k * 8, desc_add(dV, k * 2048), idPV,
                          t > 0 || k > 0 ? 1u : 0u);
         umma_commit_w(&bars[kCPvDone]);
+        if (t == n - 1) umma_commit_w(&bars[kCODone]);
       }
     } else {
       // ----------------------------------------------------------- softmax --
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(kCartThreads, 2)
       // ---- the piece's part: column blocks of four by row
       const int part = blockIdx.x - seg * a.key_tiles / a.cart_chunk;
       const long long slot = static_cast<long long>(seg) * a.cart_parts + part;
-      if (ok && n > 0) ok = wait(&bars[kCPvDone], (step + n - 1) & 1, kDevErrTimeoutEpilogue);
+      if (ok && n > 0) ok = wait(&bars[kCODone], pieces & 1, kDevErrTimeoutEpilogue);
       if (ok) {
         tc_fence_after();
         const bool any = l > 0.f || l != l;
@@ -434,6 +437,7 @@ __global__ void __launch_bounds__(kCartThreads, 2)
       }
     }
     step += n;
+    pieces += n > 0;
     u += t1 - t0;
     // every role is done with the piece's Q, barriers and O; one that gave up
     // ends them all
