@@ -8,14 +8,14 @@
 //           as tcgen05 products: 128 rows and 64 keys at a time, Q resident as
 //           two bf16 terms, S and O in TMEM.  All (kv head, row tile, key tile)
 //           triples are cut into equal runs, one per CTA.
-//   rows    the private rows, bound by HBM: each row's heads (up to four of them)
-//           by one bulk copy into a padded slot, three stages of up to 16 KB of
-//           keys and of values per CTA, a warp per head and 16 rows: m16n8k16
-//           products with the query's terms in the rows of A that a group of
-//           heads leaves free, and V^T as A of the second product, whose B has
-//           the layout that the first one leaves.  The producer warp writes the
-//           new token's rotated key and value to its row and to the stage.  All
-//           conversations' rows, one after the other, are cut into equal runs.
+//   rows    the private rows, bound by HBM: 16 rows of up to four heads by one
+//           box each for keys and values and 64 dims, three stages of up to 16 KB
+//           of both per CTA, a warp per head and 16 rows: m16n8k16 products with
+//           the query's terms in the rows of A that a group of heads leaves free,
+//           and V^T as A of the second product, whose B has the layout that the
+//           first one leaves.  The producer warp writes the new token's rotated
+//           key and value to its row before it loads that.  All conversations'
+//           rows, one after the other, are cut into equal runs.
 //   finish  joins a (conversation, kv head)'s parts by their log-sum-exps, and
 //           adds exp2(logit - log-sum-exp) of the group's heads to each row.
 #include <cuda_bf16.h>
@@ -50,12 +50,12 @@ struct StepArgs {
   int row_tiles, key_tiles, cart_chunk, cart_parts;
   float *cart_o, *cart_lse;  // [Hkv * row_tiles, cart_parts, d / 4, 128] float4; [.., 128]
   // ---- rows: heads of a unit (of which a conversation has `units`), 16-row
-  // groups that its warps take side by side, rows of a stage, CTAs
-  int heads, units, subs, stage_rows, row_ctas;
+  // groups that its warps take side by side, and of a stage, CTAs
+  int heads, units, subs, stage_groups, row_ctas;
   long long* starts;         // [B + 1]: chunks of a unit before each conversation's
-  float *row_o, *row_lse;    // [slots, groups * subs, heads, G, d], [.., G]
+  float *row_o, *row_lse;    // [slots, subs, heads, G, d], [.., G]
   int cap;                   // most private rows
-  float* logits;             // [B, Hkv, G, cap], log2 domain, by the order of rows seen
+  float* logits;             // [B, Hkv, G, cap], log2 domain, by the order of groups seen
 };
 
 struct Turns {
@@ -63,12 +63,13 @@ struct Turns {
 };
 
 // The step of conversation b: the row of its new token (-1: idle, or the row
-// has no page), that row's page, its rotary position; the rows it sees: those
-// below `low` and from `high` to `row`, n in all.
+// has no page), that row's page; the rows it sees: those below `low` and from
+// `high` to `row`, in n groups of 16: those below g_low and from g_high on.
 struct StepOf {
-  int row, page, low, high, n;
+  int row, page, low, high, g_low, g_high, n;
   bool lost;  // not idle, but without a page
-  __device__ __forceinline__ int seen(int v) const { return v < low ? v : v - low + high; }
+  __device__ __forceinline__ int group(int i) const { return i < g_low ? i : i - g_low + g_high; }
+  __device__ __forceinline__ bool sees(int r) const { return r <= row && (r < low || r >= high); }
 };
 __device__ __forceinline__ StepOf step_of(const StepArgs& a, int b) {
   StepOf s;
@@ -78,7 +79,9 @@ __device__ __forceinline__ StepOf step_of(const StepArgs& a, int b) {
   s.row = s.page < 0 ? -1 : len;
   s.high = a.window > 0 ? max(s.row - a.window + 1, 0) : 0;
   s.low = min(max(a.sinks - a.p, 0), s.high);
-  s.n = s.row < 0 ? 0 : s.low + s.row + 1 - s.high;
+  s.g_high = s.high >> 4;
+  s.g_low = min((s.low + 15) >> 4, s.g_high);
+  s.n = s.row < 0 ? 0 : s.g_low + (s.row >> 4) + 1 - s.g_high;
   return s;
 }
 __device__ __forceinline__ int position_of(const StepArgs& a, int b, int row) {
@@ -117,8 +120,9 @@ struct CartMaps {
   CUtensorMap k, v;
 };
 
+// (144 registers, and 112 of the rows' kernel: both fit each quarter of an SM)
 template <int D>
-__global__ void __launch_bounds__(kCartThreads, 2)
+__global__ void __maxnreg__(144)
     step_cart_kernel(const __grid_constant__ CartMaps maps, const __grid_constant__ StepArgs a,
                      const __grid_constant__ Turns f) {
   using L = CartSmem<D>;
@@ -457,28 +461,30 @@ __global__ void __launch_bounds__(kCartThreads, 2)
 }
 
 // ----------------------------------------------------------------- rows ----
-constexpr int kRowGroups = 2;     // of four warps, which take a piece's chunks in turn
-constexpr int kRowThreads = 128 * kRowGroups + 32;  // and the producer
+constexpr int kRowWarps = 4;     // of heads
+constexpr int kRowThreads = 32 * kRowWarps + 32;  // and the producer
 constexpr int kRowStages = 3;
-constexpr int kRowHeads = 4;      // most heads of a unit
-constexpr int kMaskWords = 4;     // 128 rows a stage at most
+constexpr int kRowHeads = 4;     // most heads of a unit
+constexpr int kRowGroups = 8;    // most 16-row groups of a stage
 
-// What a stage holds: rows of conversation b and the unit's heads from h0 on,
-// `v0` the first by the order of those seen; rows that are there; chunks of the
-// piece before and after it, the slot of the piece's part; its position.
+// What a stage holds: groups of 16 rows of conversation b and the unit's heads
+// from h0 on; v0 the first's number among those seen, times 16; the rows of each
+// that are there and seen; chunks of the piece before and after it, the slot of
+// the piece's part; the token's position; groups.
 struct StageInfo {
-  int b, h0, v0, before, after, slot, pos;
-  unsigned mask[kMaskWords];
+  int b, h0, v0, before, after, slot, pos, groups;
+  unsigned short bits[kRowGroups];
 };
 
 template <int D>
 struct RowSmem {
-  // a row's heads, and 16 bytes that move the next row to other banks; a stage
-  // has 16 rows of four heads, 32 of two, 64 of one (twice that at d = 64)
-  static constexpr int kHalfBytes = 16 * kRowHeads * 256 + 128 * 16;  // keys, or values
+  static constexpr int kHalfBytes = 16 * kRowHeads * 256;  // keys, or values
   static constexpr int kStage = 2 * kHalfBytes;
-  static constexpr int kBytes = kRowStages * kStage;
-  static constexpr int kAlloc = kBytes + 128;
+  static constexpr int kAlloc = kRowStages * kStage + 1024;  // slack for alignment
+};
+
+struct RowMaps {
+  CUtensorMap k, v;  // (d, page_rows, Hkv, pages), box 64 x 16 x heads x 1
 };
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -502,9 +508,40 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Chunks of one unit of a conversation that sees n private rows.
+// Chunks (stages) of one unit of a conversation that sees n groups.
 __device__ __forceinline__ int chunks_of(const StepArgs& a, int n) {
-  return (n + a.stage_rows - 1) / a.stage_rows;
+  return (n + a.stage_groups - 1) / a.stage_groups;
+}
+
+// The new token's rotated key and its value to its row, heads h0 .. h0 + heads
+// - 1, by one warp: before that warp loads the row.
+template <int D>
+__device__ __forceinline__ void write_row(const StepArgs& a, const Turns& f, int b, const StepOf& s,
+                                          int pos, int h0, int heads) {
+  constexpr int HALF = D / 2;
+  const int lane = threadIdx.x & 31;
+  const long long from = (static_cast<long long>(b) * a.Hkv + h0) * D;
+  const long long to = (((static_cast<long long>(s.page) << a.pt.page_log2) +
+                         (s.row & ((1 << a.pt.page_log2) - 1))) * a.Hkv + h0) * D;
+  float2 cs[HALF / 32];
+#pragma unroll
+  for (int e = 0; e < HALF / 32; ++e) cs[e] = rope_cs_turns(f.t[lane + 32 * e], pos);
+  for (int h = 0; h < heads; ++h)
+#pragma unroll
+    for (int e = 0; e < HALF / 32; ++e) {
+      const int j = h * D + lane + 32 * e;
+      float y0, y1;
+      rope_pair(__bfloat162float(a.k_new[from + j]), __bfloat162float(a.k_new[from + j + HALF]),
+                cs[e], y0, y1);
+      a.k_pages[to + j] = __float2bfloat16_rn(y0);
+      a.k_pages[to + j + HALF] = __float2bfloat16_rn(y1);
+    }
+  for (int e = lane * 8; e < heads * D; e += 256)
+    *reinterpret_cast<uint4*>(a.v_pages + to + e) =
+        __ldg(reinterpret_cast<const uint4*>(a.v_new + from + e));
+  __threadfence();
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+  __syncwarp();
 }
 
 // kWide: groups of more than four query heads.  The first product's A has the
@@ -512,10 +549,11 @@ __device__ __forceinline__ int chunks_of(const StepArgs& a, int n) {
 // the third ones in rows 4 .. where the group leaves those free, else they are
 // a product of their own.
 template <int D, bool kWide>
-__global__ void __launch_bounds__(kRowThreads, 2)
-    step_rows_kernel(const __grid_constant__ StepArgs a, const __grid_constant__ Turns f) {
+__global__ void __maxnreg__(112)
+    step_rows_kernel(const __grid_constant__ RowMaps maps, const __grid_constant__ StepArgs a,
+                     const __grid_constant__ Turns f) {
   using L = RowSmem<D>;
-  constexpr int HALF = D / 2, KS = D / 16;  // steps of 16 dims
+  constexpr int KS = D / 16;  // steps of 16 dims
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kRowStages], empty[kRowStages];
   __shared__ StageInfo info[kRowStages];
@@ -523,14 +561,14 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   __shared__ int run_b, abort_flag;
   __shared__ long long run_off;
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t abort_s = smem_u32(&abort_flag);
   if (tid == 0) {
     abort_flag = 0;
     for (int s = 0; s < kRowStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 4 * kRowGroups);
+      mbar_init(&empty[s], kRowWarps);
     }
     fence_mbar_init();
   }
@@ -580,29 +618,31 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   }
   __syncthreads();
   const int n_chunks = static_cast<int>(hi - lo);
-  const int head_bytes = D * 2;
+  const int head_bytes = 2048, half_bytes = a.heads * head_bytes;  // 16 rows of 64 dims
+  const int group_bytes = (D / 64) * half_bytes;
 
-  if (warp == 4 * kRowGroups) {
+  if (warp == kRowWarps) {
     // ------------------------------------------------------------ producer --
     int b = run_b, n = 0;  // chunks handed on
     bool ok = n_chunks > 0;
     int unit = 0, c0 = 0;
+    StepOf s{};
     if (ok) {
-      const int per_unit = chunks_of(a, step_of(a, b).n);
+      s = step_of(a, b);
+      const int per_unit = chunks_of(a, s.n);
       unit = static_cast<int>(run_off / per_unit);
       c0 = static_cast<int>(run_off - static_cast<long long>(unit) * per_unit);
     }
     while (ok && n < n_chunks) {
-      const StepOf s = step_of(a, b);
       const int all = chunks_of(a, s.n);
       if (all == 0) {  // idle
-        ++b;
+        s = step_of(a, ++b);
         continue;
       }
-      const int pos = position_of(a, b, s.row);
-      const int h0 = unit * a.heads, heads = min(a.heads, a.Hkv - h0);
-      const int row_bytes = heads * head_bytes, stride = row_bytes + 16;
+      const int pos = position_of(a, b, s.row), h0 = unit * a.heads;
       const int c1 = min(all, c0 + n_chunks - n);
+      // the next conversation's, before they are needed
+      const StepOf next = unit + 1 == a.units && b + 1 < a.B ? step_of(a, b + 1) : s;
       // the piece's slot: the run's first piece, its last one, or a whole unit
       const bool opens = n == 0 && c0 > 0, closes = c1 < all;
       const int slot = opens || (closes && n == 0) ? 2 * blockIdx.x
@@ -610,109 +650,65 @@ __global__ void __launch_bounds__(kRowThreads, 2)
                                                    : 2 * a.row_ctas + b * a.units + unit;
       const int* pages = a.pt.table + static_cast<long long>(b) * a.pt.max_pages;
       const int mask = (1 << a.pt.page_log2) - 1;
+      // a chunk's groups, a lane each: its first row, and that row's page
+      auto row_of = [&](int c) {
+        const int i = c * a.stage_groups + lane;
+        return lane < a.stage_groups && i < s.n ? s.group(i) * 16 : -1;
+      };
+      auto look_up = [&](int r) { return r < 0 ? -1 : __ldg(pages + (r >> a.pt.page_log2)); };
+      int row = row_of(c0), page = look_up(row);
       for (int c = c0; c < c1; ++c, ++n) {
-        const int st = n % kRowStages, v0 = c * a.stage_rows;
-        // the rows' places, a lane each, 32 at a time
-        long long at[kMaskWords];
-        unsigned there[kMaskWords], copied[kMaskWords];
-#pragma unroll
-        for (int w = 0; w < kMaskWords; ++w) {
-          const int i = w * 32 + lane, v = v0 + i;
-          at[w] = -1;
-          if (i < a.stage_rows && v < s.n) {
-            const int r = s.seen(v), page = __ldg(pages + (r >> a.pt.page_log2));
-            if (is_page(page, a.pt.n_pages))
-              at[w] = (((static_cast<long long>(page) << a.pt.page_log2) + (r & mask)) * a.Hkv +
-                       h0) * D;
+        const int st = n % kRowStages;
+        const int row_next = c + 1 < c1 ? row_of(c + 1) : -1, page_next = look_up(row_next);
+        const bool there = row >= 0 && is_page(page, a.pt.n_pages);
+        unsigned bits = 0;
+        if (there) {
+          bits = 0xffffu;
+          if (row + 15 > s.row || (row + 15 >= s.low && row < s.high)) {
+            bits = 0;
+            for (int i = 0; i < 16; ++i) bits |= static_cast<unsigned>(s.sees(row + i)) << i;
           }
-          there[w] = __ballot_sync(0xffffffffu, at[w] >= 0);
-          const bool copy = at[w] >= 0 && v < s.n - 1;  // (the last one is the new token)
-          copied[w] = __ballot_sync(0xffffffffu, copy);
-          if (!copy) at[w] = -1;
         }
+        if (c + 1 == all) write_row<D>(a, f, b, s, pos, h0, min(a.heads, a.Hkv - h0));
         if (n >= kRowStages) {
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], (n / kRowStages - 1) & 1, abort_s,
                                                  a.status, kDevErrTimeoutTma));
           if (!ok) break;
         }
-        uint8_t* const ks = smem + st * L::kStage;
-        uint8_t* const vs = ks + L::kHalfBytes;
-        const int rows = min(a.stage_rows, s.n - v0), last = s.n - 1 - v0;
-        if (last < a.stage_rows) {  // the new token: its row here, and in its page
-          const long long from = (static_cast<long long>(b) * a.Hkv + h0) * D;
-          const long long to = (((static_cast<long long>(s.page) << a.pt.page_log2) +
-                                 (s.row & mask)) * a.Hkv + h0) * D;
-          float2 cs[HALF / 32];
-#pragma unroll
-          for (int e = 0; e < HALF / 32; ++e) cs[e] = rope_cs_turns(f.t[lane + 32 * e], pos);
-          __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(ks + last * stride);
-          for (int h = 0; h < heads; ++h)
-#pragma unroll
-            for (int e = 0; e < HALF / 32; ++e) {
-              const int j = h * D + lane + 32 * e;
-              float y0, y1;
-              rope_pair(__bfloat162float(a.k_new[from + j]),
-                        __bfloat162float(a.k_new[from + j + HALF]), cs[e], y0, y1);
-              const __nv_bfloat16 z0 = __float2bfloat16_rn(y0), z1 = __float2bfloat16_rn(y1);
-              kr[j] = z0;
-              kr[j + HALF] = z1;
-              a.k_pages[to + j] = z0;
-              a.k_pages[to + j + HALF] = z1;
-            }
-          for (int e = lane * 8; e < heads * D; e += 256) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.v_new + from + e));
-            *reinterpret_cast<uint4*>(vs + last * stride + e * 2) = v;
-            *reinterpret_cast<uint4*>(a.v_pages + to + e) = v;
-          }
-        }
-        // values of rows that are not there, up to a whole group of 16: 0 times
-        // what the stage last held need not be 0
-        bool holes = false;
-#pragma unroll
-        for (int w = 0; w < kMaskWords; ++w) {
-          const int upto = min(max(((rows + 15) & ~15) - 32 * w, 0), 32);
-          holes |= static_cast<unsigned>((1ull << upto) - 1) != there[w];
-        }
-        if (holes)
-          for (int i = 0; i < ((rows + 15) & ~15); ++i) {
-            if (there[i >> 5] >> (i & 31) & 1) continue;
-            for (int e = lane * 16; e < row_bytes; e += 512)
-              *reinterpret_cast<uint4*>(vs + i * stride + e) = make_uint4(0u, 0u, 0u, 0u);
-          }
-        // (before a later copy into what was written here)
-        if (holes || last < a.stage_rows) fence_proxy_async_smem();
-        __syncwarp();
+        const unsigned groups = __ballot_sync(0xffffffffu, there);
+        StageInfo& o = info[st];
+        if (lane < kRowGroups) o.bits[lane] = static_cast<unsigned short>(bits);
         if (lane == 0) {
-          StageInfo& o = info[st];
           o.b = b;
           o.h0 = h0;
-          o.v0 = v0;
+          o.v0 = c * a.stage_groups * 16;
           o.before = c - c0;
           o.after = c1 - 1 - c;
           o.slot = slot;
           o.pos = pos;
-          int copies = 0;
-#pragma unroll
-          for (int w = 0; w < kMaskWords; ++w) {
-            o.mask[w] = there[w];
-            copies += __popc(copied[w]);
-          }
-          mbar_arrive_expect_tx(&full[st], 2 * copies * row_bytes);
+          o.groups = min(a.stage_groups, s.n - c * a.stage_groups);
         }
         __syncwarp();
-#pragma unroll
-        for (int w = 0; w < kMaskWords; ++w)
-          if (at[w] >= 0) {
-            const int i = w * 32 + lane;
-            bulk_load(ks + i * stride, a.k_pages + at[w], row_bytes, &full[st]);
-            bulk_load(vs + i * stride, a.v_pages + at[w], row_bytes, &full[st]);
-          }
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], 2 * __popc(groups) * group_bytes);
         __syncwarp();
+        if (there) {
+          uint8_t* const ks = smem + st * L::kStage + lane * group_bytes;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            tma_load_4d(ks + h * half_bytes, &maps.k, &full[st], h * 64, row & mask, h0, page);
+            tma_load_4d(ks + L::kHalfBytes + h * half_bytes, &maps.v, &full[st], h * 64, row & mask,
+                        h0, page);
+          }
+        }
+        __syncwarp();
+        row = row_next;
+        page = page_next;
       }
       c0 = 0;
       if (++unit == a.units) {
         unit = 0;
         ++b;
+        s = next;
       }
     }
     pdl_release();
@@ -722,30 +718,30 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     __syncwarp();
   } else {
     // --------------------------------------------------------------- heads --
-    const int group = warp >> 2, w4 = warp & 3;
-    const int q8 = lane >> 2, t4 = lane & 3;     // query row, pair of columns
+    const int q8 = lane >> 2, t4 = lane & 3;  // query row, pair of columns
+    const int h = warp % a.heads, sub = warp / a.heads;  // (idle beyond the last group)
     bool ok = true;
     float m = -INFINITY, l = 0.f;
     float o[D / 16][4];  // O^T: dims 16i + q8 (+ 8), queries 2 t4 (+ 1)
     // the queries' terms as A: rows 0-7 (first terms, and third in rows 4-7),
     // rows 8-15 (second ones)
     uint32_t qa[KS][2], qb[KS][2], qc[kWide ? KS : 1][2];
+    // chunks of 16 bytes of a row's 64 dims lie by the row's last three bits
+    const int krow = (lane & 7) + (lane >> 4) * 8, kcol = (lane >> 3) & 1;
     for (int n = 0; n < n_chunks && ok; ++n) {
       const int st = n % kRowStages;
       ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (n / kRowStages) & 1, abort_s, a.status,
                                              kDevErrTimeoutSoftmax));
       if (!ok) break;
       const StageInfo& in = info[st];
-      const int before = vld(in.before), after = vld(in.after), h0 = vld(in.h0), b = vld(in.b);
-      const int heads = min(a.heads, a.Hkv - h0);
-      const int h = w4 % a.heads, sub = w4 / a.heads;  // (idle beyond the last head or group)
-      const bool works = before % kRowGroups == group && h < heads && sub < a.subs;
+      const int h0 = vld(in.h0);
+      const bool works = h0 + h < a.Hkv && sub < a.subs;
       if (works) {
-        const int g = h0 + h;
-        if (before < kRowGroups) {  // ---- the group's first chunk of a piece: its queries
+        const int g = h0 + h, b = vld(in.b);
+        if (vld(in.before) == 0) {  // ---- a piece's first chunk: its queries
           const int pos = vld(in.pos);
           const __nv_bfloat16* x = a.q + (static_cast<long long>(b) * a.Hq + g * a.G) * D;
-          const int third = kWide ? q8 : q8 - 4;  // the query whose third term the row holds
+          const int third = q8 - 4;  // the query whose third term the row holds (not kWide)
           const bool has = q8 < a.G, more = !kWide && third >= 0 && third < a.G;
           const uint32_t* xq = reinterpret_cast<const uint32_t*>(x + (has ? q8 : more ? third : 0) * D);
           uint32_t raw[KS][2];
@@ -789,34 +785,37 @@ __global__ void __launch_bounds__(kRowThreads, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
         }
-        const int stride = heads * head_bytes + 16;
-        const uint32_t ks = smem_u32(smem + st * L::kStage) + h * head_bytes;
-        const uint32_t vs = ks + L::kHalfBytes;
-        for (int r0 = sub * 16; r0 < a.stage_rows; r0 += a.subs * 16) {
-          const unsigned bits = static_cast<unsigned>(
-                                    *reinterpret_cast<const volatile unsigned*>(&in.mask[r0 >> 5]) >>
-                                    (r0 & 31)) & 0xffffu;
-          if (bits == 0) continue;  // (uniform over the warp)
-          // ---- S [query terms, 16 keys]
-          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint32_t ka = ks + (r0 + (lane & 7) + (lane >> 4) * 8) * stride + ((lane >> 3) & 1) * 16;
+        const int groups = vld(in.groups);
+        const uint32_t ks = smem_u32(smem + st * L::kStage) + h * head_bytes + krow * 128;
+        bool cleared = false;
+        for (int i = sub; i < groups; i += a.subs) {
+          const unsigned bits = *reinterpret_cast<const volatile unsigned short*>(&in.bits[i]);
+          const uint32_t kg = ks + i * group_bytes, vg = kg + L::kHalfBytes;
+          float x4[4] = {0.f, 0.f, 0.f, 0.f};  // query q8, keys 2 t4, + 1, + 8, + 9
+          if (bits) {  // (uniform over the warp)
+            // ---- S [query terms, 16 keys]
+            float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            uint32_t kb[4];
-            ldsm_x4(ka + k * 32, kb);
-            mma_bf16_16816(s0, qa[k][0], qb[k][0], qa[k][1], qb[k][1], kb[0], kb[1]);
-            mma_bf16_16816(s1, qa[k][0], qb[k][0], qa[k][1], qb[k][1], kb[2], kb[3]);
-            if (kWide) {
-              mma_bf16_16816(s0, qc[k][0], 0u, qc[k][1], 0u, kb[0], kb[1]);
-              mma_bf16_16816(s1, qc[k][0], 0u, qc[k][1], 0u, kb[2], kb[3]);
+            for (int k = 0; k < KS; ++k) {
+              uint32_t kb[4];
+              ldsm_x4(kg + (k >> 2) * half_bytes +
+                          ((((2 * (k & 3) + kcol) ^ (lane & 7))) << 4), kb);
+              mma_bf16_16816(s0, qa[k][0], qb[k][0], qa[k][1], qb[k][1], kb[0], kb[1]);
+              mma_bf16_16816(s1, qa[k][0], qb[k][0], qa[k][1], qb[k][1], kb[2], kb[3]);
+              if (kWide) {
+                mma_bf16_16816(s0, qc[k][0], 0u, qc[k][1], 0u, kb[0], kb[1]);
+                mma_bf16_16816(s1, qc[k][0], 0u, qc[k][1], 0u, kb[2], kb[3]);
+              }
             }
-          }
-          // this thread: query q8, keys 2 t4, + 1, + 8, + 9
-          float x4[4] = {s0[0] + s0[2], s0[1] + s0[3], s1[0] + s1[2], s1[1] + s1[3]};
-          if (!kWide) {  // (rows 4-7 hold third terms)
+            x4[0] = s0[0] + s0[2];
+            x4[1] = s0[1] + s0[3];
+            x4[2] = s1[0] + s1[2];
+            x4[3] = s1[1] + s1[3];
+            if (!kWide) {  // (rows 4-7 hold third terms)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x4[e] += __shfl_xor_sync(0xffffffffu, e < 2 ? s0[e] : s1[e - 2], 16);
+              for (int e = 0; e < 4; ++e)
+                x4[e] += __shfl_xor_sync(0xffffffffu, e < 2 ? s0[e] : s1[e - 2], 16);
+            }
           }
           const bool live = q8 < a.G;
 #pragma unroll
@@ -827,10 +826,11 @@ __global__ void __launch_bounds__(kRowThreads, 2)
           if (a.logits && live) {
             float* lg = a.logits +
                         ((static_cast<long long>(b) * a.Hkv + g) * a.G + q8) * a.cap + vld(in.v0) +
-                        r0 + 2 * t4;
+                        i * 16 + 2 * t4;
             *reinterpret_cast<float2*>(lg) = make_float2(x4[0], x4[1]);
             *reinterpret_cast<float2*>(lg + 8) = make_float2(x4[2], x4[3]);
           }
+          if (!bits) continue;
           float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -844,11 +844,11 @@ __global__ void __launch_bounds__(kRowThreads, 2)
             const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t4);
             const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              o[i][0] *= a0;
-              o[i][1] *= a1;
-              o[i][2] *= a0;
-              o[i][3] *= a1;
+            for (int j = 0; j < D / 16; ++j) {
+              o[j][0] *= a0;
+              o[j][1] *= a1;
+              o[j][2] *= a0;
+              o[j][3] *= a1;
             }
           }
           const float mr = m == -INFINITY ? 0.f : m;
@@ -856,17 +856,31 @@ __global__ void __launch_bounds__(kRowThreads, 2)
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4[e] = exp2_approx(x4[e] - mr);
           l += (e4[0] + e4[1]) + (e4[2] + e4[3]);
+          if (bits != 0xffffu) {
+            // values of rows that are not seen may be anything, and 0 times them
+            // need not be 0
+            if (!(bits >> (lane & 15) & 1)) {
+              const uint32_t at = vg + ((lane & 15) - krow) * 128 + (lane >> 4) * 64;
+#pragma unroll
+              for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  sts_u4(at + k * half_bytes + e * 16, make_uint4(0u, 0u, 0u, 0u));
+            }
+            cleared = true;
+            __syncwarp();
+          }
           // ---- O^T += V^T P^T: P^T as B has the layout of S
           const uint32_t p0 = pack_bf16x2(e4[0], e4[1]), p1 = pack_bf16x2(e4[2], e4[3]);
-          const uint32_t va = vs + (r0 + (lane & 7) + (lane >> 4) * 8) * stride + ((lane >> 3) & 1) * 16;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
+          for (int j = 0; j < D / 16; ++j) {
             uint32_t vt[4];
-            ldsm_x4_t(va + i * 32, vt);
-            mma_bf16_16816(o[i], vt[0], vt[1], vt[2], vt[3], p0, p1);
+            ldsm_x4_t(vg + (j >> 2) * half_bytes + (((2 * (j & 3) + kcol) ^ (lane & 7)) << 4), vt);
+            mma_bf16_16816(o[j], vt[0], vt[1], vt[2], vt[3], p0, p1);
           }
         }
-        if (after < kRowGroups) {  // ---- the group's last chunk of the piece: its part
+        if (cleared) fence_proxy_async_smem();  // before a later load of what was cleared
+        if (vld(in.after) == 0) {  // ---- the piece's last chunk: its part
           float sum = l;
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -875,7 +889,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
           const float i0 = __shfl_sync(0xffffffffu, inv, 8 * t4);
           const float i1 = __shfl_sync(0xffffffffu, inv, 8 * t4 + 4);
           const long long part =
-              ((static_cast<long long>(vld(in.slot)) * kRowGroups + group) * a.subs + sub) * a.heads + h;
+              (static_cast<long long>(vld(in.slot)) * a.subs + sub) * a.heads + h;
           if (t4 == 0 && q8 < a.G) a.row_lse[part * a.G + q8] = any ? m + __log2f(sum) : -INFINITY;
           float* out = a.row_o + part * a.G * D;
 #pragma unroll
@@ -884,9 +898,9 @@ __global__ void __launch_bounds__(kRowThreads, 2)
             const float iq = e ? i1 : i0;
             if (q < a.G)
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                out[q * D + 16 * i + q8] = iq == 0.f ? 0.f : o[i][e] * iq;
-                out[q * D + 16 * i + q8 + 8] = iq == 0.f ? 0.f : o[i][2 + e] * iq;
+              for (int j = 0; j < D / 16; ++j) {
+                out[q * D + 16 * j + q8] = iq == 0.f ? 0.f : o[j][e] * iq;
+                out[q * D + 16 * j + q8 + 8] = iq == 0.f ? 0.f : o[j][2 + e] * iq;
               }
           }
         }
@@ -901,17 +915,21 @@ __global__ void __launch_bounds__(kRowThreads, 2)
 
 // --------------------------------------------------------------- finish ----
 constexpr int kFinishThreads = 512;
+constexpr int kFinishParts = 128;  // parts joined at a time
 
-// Block (rows, kv head, conversation): the parts' common log-sum-exp, a warp
-// per query head; the first block the output, some threads per column of four;
-// all the weights of their rows.
+// Blocks (., kv head, conversation): the parts' common log-sum-exp, a warp per
+// query head; then the first one the output, some threads per column of four,
+// the parts' weights and places settled before; the others the rows' weights.
 template <int D>
-__global__ void __launch_bounds__(kFinishThreads)
+__global__ void __launch_bounds__(kFinishThreads, 2)
     step_finish_kernel(const __grid_constant__ StepArgs a) {
   __shared__ float total[kMaxGroup];
   __shared__ float4 acc[kFinishThreads];
+  __shared__ float weight[kMaxGroup][kFinishParts];
+  __shared__ const float4* place[kMaxGroup][kFinishParts];
   pdl_wait();
   const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long start = __ldcg(a.starts + b), units = __ldcg(a.starts + a.B);
   const StepOf s = step_of(a, b);
   __nv_bfloat16* out = a.o + (static_cast<long long>(b) * a.Hq + g * a.G) * D;
   if (s.row < 0) {
@@ -919,39 +937,37 @@ __global__ void __launch_bounds__(kFinishThreads)
       for (int e = tid; e < a.G * D; e += kFinishThreads) out[e] = __float2bfloat16_rn(0.f);
     return;
   }
-  if (blockIdx.x > 0 && static_cast<int>(blockIdx.x) * kFinishThreads >= s.n) return;
+  const int first = (static_cast<int>(blockIdx.x) - 1) * kFinishThreads;  // rows' blocks
+  if (first >= s.n * 16) return;
   // ---- the parts of the private rows: those of the runs that hold the unit
   const int unit = g / a.heads, h = g - unit * a.heads, all = chunks_of(a, s.n);
-  const long long chunk = (__ldcg(a.starts + a.B) + a.row_ctas - 1) / a.row_ctas;
-  const long long u0 = __ldcg(a.starts + b) + static_cast<long long>(unit) * all, u1 = u0 + all;
-  const int c0 = static_cast<int>(u0 / chunk), c1 = static_cast<int>((u1 - 1) / chunk);
-  const int per = kRowGroups * a.subs, n_row = (c1 - c0 + 1) * per;
-  auto row_part = [&](int i) -> long long {  // its index, or -1
-    const int c = c0 + i / per, k = i % per;
-    // (a group beyond the piece's chunks had none)
-    if (k / a.subs >= min(u1, (c + 1) * chunk) - max(u0, c * chunk)) return -1;
-    const long long slot = c0 == c1                     ? 2 * a.row_ctas + static_cast<long long>(b) * a.units + unit
+  const long long chunk = (units + a.row_ctas - 1) / a.row_ctas;
+  const long long u0 = start + static_cast<long long>(unit) * all;
+  const int c0 = static_cast<int>(u0 / chunk), c1 = static_cast<int>((u0 + all - 1) / chunk);
+  const int n_row = (c1 - c0 + 1) * a.subs;
+  auto row_part = [&](int i) -> long long {
+    const int c = c0 + i / a.subs, k = i % a.subs;
+    const long long slot = c0 == c1 ? 2 * a.row_ctas + static_cast<long long>(b) * a.units + unit
                            : c > c0 || u0 == c0 * chunk ? 2 * c
                                                         : 2 * c + 1;
-    return (slot * per + k) * a.heads + h;
+    return ((slot * a.subs + k) * a.heads + h) * a.G;
   };
   // ---- and of the cartridge, by the tile that holds the query's row
-  auto cart_seg = [&](int hh) { return g * a.row_tiles + (b * a.G + hh) / kTile; };
-  auto cart_count = [&](int hh) {
-    if (a.key_tiles == 0) return 0;
-    const int u = cart_seg(hh) * a.key_tiles;
-    return (u + a.key_tiles - 1) / a.cart_chunk - u / a.cart_chunk + 1;
+  auto cart_first = [&](int hh) {
+    return static_cast<long long>(g * a.row_tiles + (b * a.G + hh) / kTile) * a.cart_parts;
+  };
+  auto parts_of = [&](int hh) {
+    if (a.key_tiles == 0) return n_row;
+    const int u = (g * a.row_tiles + (b * a.G + hh) / kTile) * a.key_tiles;
+    return n_row + (u + a.key_tiles - 1) / a.cart_chunk - u / a.cart_chunk + 1;
   };
   auto lse_of = [&](int hh, int i) {
-    if (i >= n_row) {
-      const long long slot = static_cast<long long>(cart_seg(hh)) * a.cart_parts + i - n_row;
-      return __ldcg(a.cart_lse + slot * kTile + (b * a.G + hh) % kTile);
-    }
-    const long long part = row_part(i);
-    return part < 0 ? -INFINITY : __ldcg(a.row_lse + part * a.G + hh);
+    return i < n_row ? __ldcg(a.row_lse + row_part(i) + hh)
+                     : __ldcg(a.cart_lse + (cart_first(hh) + i - n_row) * kTile +
+                              (b * a.G + hh) % kTile);
   };
   if (warp < a.G) {
-    const int n = n_row + cart_count(warp);
+    const int n = parts_of(warp);
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i < n; i += 32) {
       const float x = lse_of(warp, i), top = fmaxf(m, x);
@@ -976,23 +992,32 @@ __global__ void __launch_bounds__(kFinishThreads)
     const int cols = a.G * (D / 4), each = kFinishThreads / cols;
     const int col = tid % cols, turn = tid / cols, hh = col / (D / 4), j = col % (D / 4);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (turn < each) {
-      const int n = n_row + cart_count(hh);
-      const long long cart0 = static_cast<long long>(cart_seg(hh)) * a.cart_parts;
-      const int row = (b * a.G + hh) % kTile;
-#pragma unroll 4
-      for (int i = turn; i < n; i += each) {
-        const float w = exp2_approx(lse_of(hh, i) - total[hh]);
-        if (w == 0.f) continue;
-        const float4* part =
-            i >= n_row ? reinterpret_cast<const float4*>(a.cart_o) +
-                             ((cart0 + i - n_row) * (D / 4) + j) * kTile + row
-                       : reinterpret_cast<const float4*>(a.row_o + (row_part(i) * a.G + hh) * D) + j;
-        const float4 v = __ldcg(part);
-        x.x = fmaf(w, v.x, x.x);
-        x.y = fmaf(w, v.y, x.y);
-        x.z = fmaf(w, v.z, x.z);
-        x.w = fmaf(w, v.w, x.w);
+    int most = 0;
+    for (int q = 0; q < a.G; ++q) most = max(most, parts_of(q));
+    for (int i0 = 0; i0 < most; i0 += kFinishParts) {
+      __syncthreads();
+      for (int e = tid; e < a.G * kFinishParts; e += kFinishThreads) {
+        const int q = e / kFinishParts, k = e % kFinishParts, i = i0 + k;
+        if (i >= parts_of(q)) continue;
+        weight[q][k] = exp2_approx(lse_of(q, i) - total[q]);
+        place[q][k] = reinterpret_cast<const float4*>(
+            i < n_row ? a.row_o + (row_part(i) + q) * D
+                      : a.cart_o + ((cart_first(q) + i - n_row) * (D / 4) * kTile +
+                                    (b * a.G + q) % kTile) * 4);
+      }
+      __syncthreads();
+      if (turn < each) {
+        const int n = min(parts_of(hh) - i0, kFinishParts);
+#pragma unroll 8
+        for (int k = turn; k < n; k += each) {
+          const float w = weight[hh][k];
+          const float4 v = __ldcg(place[hh][k] + (i0 + k < n_row ? j : j * kTile));
+          // (a part of no weight may hold anything)
+          x.x += w == 0.f ? 0.f : w * v.x;
+          x.y += w == 0.f ? 0.f : w * v.y;
+          x.z += w == 0.f ? 0.f : w * v.z;
+          x.w += w == 0.f ? 0.f : w * v.w;
+        }
       }
     }
     acc[tid] = x;
@@ -1008,14 +1033,16 @@ __global__ void __launch_bounds__(kFinishThreads)
       *reinterpret_cast<uint2*>(out + hh * D + 4 * j) =
           make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
     }
+    return;
   }
-  if (!a.weights) return;
   const long long bg = static_cast<long long>(b) * a.Hkv + g;
   float* w = a.weights + bg * a.weight_rows;
   const float* lg = a.logits + bg * a.G * a.cap;
-  for (int v = blockIdx.x * kFinishThreads + tid; v < s.n; v += gridDim.x * kFinishThreads) {
-    const int r = s.seen(v);
-    if (r < s.row && page_of(a.pt, b, r) < 0) continue;  // (not there: no logits)
+  const int step = (gridDim.x - 1) * kFinishThreads;
+#pragma unroll 2
+  for (int v = first + tid; v < s.n * 16; v += step) {
+    const int r = s.group(v >> 4) * 16 + (v & 15);
+    if (!s.sees(r)) continue;
     float x = 0.f;
     for (int hh = 0; hh < a.G; ++hh)
       x += exp2_approx(__ldcg(lg + static_cast<long long>(hh) * a.cap + v) - total[hh]);
@@ -1026,7 +1053,7 @@ __global__ void __launch_bounds__(kFinishThreads)
 struct StepWs {
   size_t cart_o, cart_lse, row_o, row_lse, starts, logits, total;
   int row_tiles, key_tiles, cart_chunk, cart_parts, cart_ctas;
-  int heads, units, subs, stage_rows, row_ctas;
+  int heads, units, subs, stage_groups, row_ctas;
 };
 // (every size goes by the GPU's multiprocessors: the grids do)
 StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
@@ -1050,14 +1077,14 @@ StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
   w.heads = (Hkv + w.units - 1) / w.units;
   w.units = (Hkv + w.heads - 1) / w.heads;
   w.subs = kRowHeads / w.heads;
-  w.stage_rows = 16 * w.subs * (d == 64 ? 2 : 1);
-  w.row_ctas = sms;
+  w.stage_groups = w.subs * (d == 64 ? 2 : 1);
+  // one CTA per SM beside the cartridge's, two without
+  w.row_ctas = p > 0 ? sms : 2 * sms;
   const size_t segments = static_cast<size_t>(Hkv) * w.row_tiles;
   w.cart_o = take(segments * w.cart_parts * kTile * d * 4);
   w.cart_lse = take(segments * w.cart_parts * kTile * 4);
   const size_t parts =
-      (2 * static_cast<size_t>(w.row_ctas) + static_cast<size_t>(B) * w.units) * kRowGroups * w.subs *
-      w.heads;
+      (2 * static_cast<size_t>(w.row_ctas) + static_cast<size_t>(B) * w.units) * w.subs * w.heads;
   w.row_o = take(parts * G * d * 4);
   w.row_lse = take(parts * G * 4);
   w.starts = take((static_cast<size_t>(B) + 1) * 8);
@@ -1103,15 +1130,24 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
+  const uint64_t page_rows = 1ull << a.pt.page_log2, row = static_cast<uint64_t>(a.Hkv) * D * 2;
+  const uint64_t dims[4] = {D, page_rows, static_cast<uint64_t>(a.Hkv),
+                            static_cast<uint64_t>(a.pt.n_pages)};
+  const uint64_t strides[3] = {row, D * 2, row * page_rows};
+  const uint32_t box[4] = {64, 16, static_cast<uint32_t>(a.heads), 1};
+  RowMaps maps;
+  if (!encode_bf16_map4(&maps.k, a.k_pages, dims, strides, box) ||
+      !encode_bf16_map4(&maps.v, a.v_pages, dims, strides, box))
+    return cudaErrorInvalidValue;
   const bool wide = a.G > 4;
   e = wide ? set_smem_once<step_rows_kernel<D, true>>(L::kAlloc)
            : set_smem_once<step_rows_kernel<D, false>>(L::kAlloc);
   if (e != cudaSuccess) return e;
   auto* rows = wide ? step_rows_kernel<D, true> : step_rows_kernel<D, false>;
   if (w.cart_ctas > 0) {
-    e = launch_dependent(rows, dim3(w.row_ctas), dim3(kRowThreads), L::kAlloc, st, a, f);
+    e = launch_dependent(rows, dim3(w.row_ctas), dim3(kRowThreads), L::kAlloc, st, maps, a, f);
   } else {
-    rows<<<w.row_ctas, kRowThreads, L::kAlloc, st>>>(a, f);
+    rows<<<w.row_ctas, kRowThreads, L::kAlloc, st>>>(maps, a, f);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
@@ -1119,8 +1155,8 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
   // for every 512 rows that a table can name
   int blocks = 1;
   if (a.weights)
-    blocks = std::max(1, std::min((a.cap + kFinishThreads - 1) / kFinishThreads,
-                                  4 * w.row_ctas / std::max(1, a.B * a.Hkv)));
+    blocks += std::max(1, std::min((a.cap + kFinishThreads - 1) / kFinishThreads,
+                                   4 * sm_count() / std::max(1, a.B * a.Hkv)));
   return launch_dependent(step_finish_kernel<D>, dim3(blocks, a.Hkv, a.B), dim3(kFinishThreads), 0,
                           st, a);
 }
@@ -1191,7 +1227,7 @@ int cart_attn_decode_paged(int B, int window, int sinks, int Hq, int Hkv, int d,
   a.heads = w.heads;
   a.units = w.units;
   a.subs = w.subs;
-  a.stage_rows = w.stage_rows;
+  a.stage_groups = w.stage_groups;
   a.row_ctas = w.row_ctas;
   a.starts = reinterpret_cast<long long*>(ws + w.starts);
   a.row_o = reinterpret_cast<float*>(ws + w.row_o);
