@@ -13,9 +13,9 @@
 //           of both per CTA, a warp per head and 16 rows: m16n8k16 products with
 //           the query's terms in the rows of A that a group of heads leaves free,
 //           and V^T as A of the second product, whose B has the layout that the
-//           first one leaves.  The producer warp writes the new token's rotated
-//           key and value to its row before it loads that.  All conversations'
-//           rows, one after the other, are cut into equal runs.
+//           first one leaves.  The warp that comes to the new token's row
+//           writes its head's rotated key and value to it and to the stage.  All
+//           conversations' rows, one after the other, are cut into equal runs.
 //   finish  joins a (conversation, kv head)'s parts by their log-sum-exps, and
 //           adds exp2(logit - log-sum-exp) of the group's heads to each row.
 #include <cuda_bf16.h>
@@ -31,6 +31,24 @@
 
 namespace cart {
 namespace {
+
+// Raises a kernel's shared-memory limit as set_smem_once does, and asks for the
+// largest shared part of an SM's first-level cache: two kernels share one there,
+// which fits only what the first of them was given.
+template <auto Kernel>
+cudaError_t set_shared_once(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) e = set_smem_once<Kernel>(bytes);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
+}
 
 constexpr int kMaxGroup = 8;  // query heads of a kv head
 // (a window or sinks beyond every place are that many)
@@ -52,8 +70,9 @@ struct StepArgs {
   // ---- rows: heads of a unit (of which a conversation has `units`), 16-row
   // groups that its warps take side by side, and of a stage, CTAs
   int heads, units, subs, stage_groups, row_ctas;
+  int finish_heads;          // heads of a block of the last kernel: `heads` or 1
   long long* starts;         // [B + 1]: chunks of a unit before each conversation's
-  float *row_o, *row_lse;    // [slots, subs, heads, G, d], [.., G]
+  float *row_o, *row_lse;    // [slots, turns * subs, heads, G, d], [.., G]
   int cap;                   // most private rows
   float* logits;             // [B, Hkv, G, cap], log2 domain, by the order of groups seen
 };
@@ -120,9 +139,10 @@ struct CartMaps {
   CUtensorMap k, v;
 };
 
-// (144 registers, and 112 of the rows' kernel: both fit each quarter of an SM)
+// (96 registers, and 104 of the rows' kernel: a quarter of an SM holds two of
+// these warps and three of those)
 template <int D>
-__global__ void __maxnreg__(144)
+__global__ void __maxnreg__(96)
     step_cart_kernel(const __grid_constant__ CartMaps maps, const __grid_constant__ StepArgs a,
                      const __grid_constant__ Turns f) {
   using L = CartSmem<D>;
@@ -321,34 +341,42 @@ __global__ void __maxnreg__(144)
         if (!ok) break;
         tc_fence_after();
         const uint32_t ts = tS + (s & 1) * kCartKeys + lane_off;
-        uint32_t r[2][32];
-        tmem_ld32(ts, r[0]);
-        tmem_ld32(ts + 32, r[1]);
-        tmem_ld_wait();
-        tmem_reg_fence(r[0]);
-        tmem_reg_fence(r[1]);
         // the row sees the keys up to `end` that are sinks or in its window
         const int k0 = t * kCartKeys;
-        const int end = min(a.p - k0, kCartKeys), from = first > k0 ? min(first - k0, kCartKeys) : 0;
+        const int end = first == 0x7fffffff ? 0 : min(a.p - k0, kCartKeys);
+        const int from = first > k0 ? min(first - k0, kCartKeys) : 0;
         const int sink = min(max(a.sinks - k0, 0), kCartKeys);
-        const bool none = first == 0x7fffffff;
-        if (__any_sync(0xffffffffu, end < kCartKeys || from > 0 || none)) {
+        const bool cut = __any_sync(0xffffffffu, end < kCartKeys || from > sink);
+        // (S is read twice, half a tile at a time, to spare registers)
+        auto load = [&](int half, uint32_t (&r)[32]) {
+          tmem_ld32(ts + 32 * half, r);
+          tmem_ld_wait();
+          tmem_reg_fence(r);
+          if (cut) {
 #pragma unroll
-          for (int c = 0; c < kCartKeys; ++c)
-            if (none || c >= end || (c < from && c >= sink))
-              r[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < 32; ++c) {
+              const int k = 32 * half + c;
+              if (k >= end || (k < from && k >= sink)) r[c] = __float_as_uint(-INFINITY);
+            }
+          }
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r[32];
+          load(half, r);
+          float mx[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            mx[q] = __uint_as_float(r[16 * q]);
+#pragma unroll
+            for (int c = 1; c < 15; c += 2)
+              mx[q] = fmax3(mx[q], __uint_as_float(r[16 * q + c]), __uint_as_float(r[16 * q + c + 1]));
+            mx[q] = fmaxf(mx[q], __uint_as_float(r[16 * q + 15]));
+          }
+          top = fmax3(top, mx[0], mx[1]);
         }
-        float mx[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mx[q] = __uint_as_float(r[q >> 1][(q & 1) * 16]);
-#pragma unroll
-          for (int c = 1; c < 15; c += 2)
-            mx[q] = fmax3(mx[q], __uint_as_float(r[q >> 1][(q & 1) * 16 + c]),
-                          __uint_as_float(r[q >> 1][(q & 1) * 16 + c + 1]));
-          mx[q] = fmaxf(mx[q], __uint_as_float(r[q >> 1][(q & 1) * 16 + 15]));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        top *= a.scale_log2;
         // (the maximum is renewed where it grows by more than 8: weights stay
         // below 2^8)
         float alpha = 1.f;
@@ -361,16 +389,19 @@ __global__ void __maxnreg__(144)
         const float mr = m == -INFINITY ? 0.f : m;  // (nothing seen yet: weights 0)
         const float2 nm2 = make_float2(-mr, -mr);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t pk[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 x =
-              __ffma2_rn(u2f2(r[c >> 4][2 * (c & 15)], r[c >> 4][2 * (c & 15) + 1]), sc2, nm2);
-          const float2 w = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-          sum[c & 1] = __fadd2_rn(sum[c & 1], w);
-          pk[c] = pack_bf16x2(w.x, w.y);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r[32], pk[16];
+          load(half, r);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float2 x = __ffma2_rn(u2f2(r[2 * c], r[2 * c + 1]), sc2, nm2);
+            const float2 w = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+            sum[c & 1] = __fadd2_rn(sum[c & 1], w);
+            pk[c] = pack_bf16x2(w.x, w.y);
+          }
+          tmem_st16(ts + 16 * half, pk);  // (over columns that have been read)
         }
-        tmem_st32(ts, pk);
         l = l * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
         if (__any_sync(0xffffffffu, rescale)) {
           ok = wait(&bars[kCPvDone], (s - 1) & 1, kDevErrTimeoutSoftmax);
@@ -461,7 +492,8 @@ __global__ void __maxnreg__(144)
 }
 
 // ----------------------------------------------------------------- rows ----
-constexpr int kRowWarps = 4;     // of heads
+constexpr int kRowTurns = 2;     // groups of four warps, which take a piece's chunks in turn
+constexpr int kRowWarps = 4 * kRowTurns;
 constexpr int kRowThreads = 32 * kRowWarps + 32;  // and the producer
 constexpr int kRowStages = 3;
 constexpr int kRowHeads = 4;     // most heads of a unit
@@ -470,9 +502,11 @@ constexpr int kRowGroups = 8;    // most 16-row groups of a stage
 // What a stage holds: groups of 16 rows of conversation b and the unit's heads
 // from h0 on; v0 the first's number among those seen, times 16; the rows of each
 // that are there and seen; chunks of the piece before and after it, the slot of
-// the piece's part; the token's position; groups.
+// the piece's part; the token's position; groups; the new row's number among
+// the stage's (-1: not here) and its place in the pool.
 struct StageInfo {
-  int b, h0, v0, before, after, slot, pos, groups;
+  int b, h0, v0, before, after, slot, pos, groups, fresh;
+  long long at;
   unsigned short bits[kRowGroups];
 };
 
@@ -513,34 +547,36 @@ __device__ __forceinline__ int chunks_of(const StepArgs& a, int n) {
   return (n + a.stage_groups - 1) / a.stage_groups;
 }
 
-// The new token's rotated key and its value to its row, heads h0 .. h0 + heads
-// - 1, by one warp: before that warp loads the row.
+// The new token's rotated key and its value, one head's, by a warp: to its row
+// of the pool, and to row r of the staged group, where what the pool held before
+// has landed.
 template <int D>
-__device__ __forceinline__ void write_row(const StepArgs& a, const Turns& f, int b, const StepOf& s,
-                                          int pos, int h0, int heads) {
+__device__ __forceinline__ void write_row(const StepArgs& a, const Turns& f, int b, int g, int pos,
+                                          long long at, uint32_t ks, uint32_t vs, int half_bytes,
+                                          int r) {
   constexpr int HALF = D / 2;
   const int lane = threadIdx.x & 31;
-  const long long from = (static_cast<long long>(b) * a.Hkv + h0) * D;
-  const long long to = (((static_cast<long long>(s.page) << a.pt.page_log2) +
-                         (s.row & ((1 << a.pt.page_log2) - 1))) * a.Hkv + h0) * D;
-  float2 cs[HALF / 32];
+  const long long from = (static_cast<long long>(b) * a.Hkv + g) * D, to = at + g * D;
+  auto staged = [&](int j) {  // place of element j
+    return (j >> 6) * half_bytes + r * 128 + ((((j & 63) >> 3) ^ (r & 7)) << 4) + (j & 7) * 2;
+  };
 #pragma unroll
-  for (int e = 0; e < HALF / 32; ++e) cs[e] = rope_cs_turns(f.t[lane + 32 * e], pos);
-  for (int h = 0; h < heads; ++h)
-#pragma unroll
-    for (int e = 0; e < HALF / 32; ++e) {
-      const int j = h * D + lane + 32 * e;
-      float y0, y1;
-      rope_pair(__bfloat162float(a.k_new[from + j]), __bfloat162float(a.k_new[from + j + HALF]),
-                cs[e], y0, y1);
-      a.k_pages[to + j] = __float2bfloat16_rn(y0);
-      a.k_pages[to + j + HALF] = __float2bfloat16_rn(y1);
-    }
-  for (int e = lane * 8; e < heads * D; e += 256)
-    *reinterpret_cast<uint4*>(a.v_pages + to + e) =
-        __ldg(reinterpret_cast<const uint4*>(a.v_new + from + e));
-  __threadfence();
-  asm volatile("fence.proxy.async.global;" ::: "memory");
+  for (int e = 0; e < HALF / 32; ++e) {
+    const int j = lane + 32 * e;
+    float y0, y1;
+    rope_pair(__bfloat162float(a.k_new[from + j]), __bfloat162float(a.k_new[from + j + HALF]),
+              rope_cs_turns(f.t[j], pos), y0, y1);
+    const __nv_bfloat16 z0 = __float2bfloat16_rn(y0), z1 = __float2bfloat16_rn(y1);
+    a.k_pages[to + j] = z0;
+    a.k_pages[to + j + HALF] = z1;
+    sts_u16(ks + staged(j), __bfloat16_as_ushort(z0));
+    sts_u16(ks + staged(j + HALF), __bfloat16_as_ushort(z1));
+  }
+  if (lane < D / 8) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.v_new + from + lane * 8));
+    *reinterpret_cast<uint4*>(a.v_pages + to + lane * 8) = v;
+    sts_u4(vs + staged(lane * 8), v);
+  }
   __syncwarp();
 }
 
@@ -549,7 +585,7 @@ __device__ __forceinline__ void write_row(const StepArgs& a, const Turns& f, int
 // the third ones in rows 4 .. where the group leaves those free, else they are
 // a product of their own.
 template <int D, bool kWide>
-__global__ void __maxnreg__(112)
+__global__ void __maxnreg__(104)
     step_rows_kernel(const __grid_constant__ RowMaps maps, const __grid_constant__ StepArgs a,
                      const __grid_constant__ Turns f) {
   using L = RowSmem<D>;
@@ -618,7 +654,8 @@ __global__ void __maxnreg__(112)
   }
   __syncthreads();
   const int n_chunks = static_cast<int>(hi - lo);
-  const int head_bytes = 2048, half_bytes = a.heads * head_bytes;  // 16 rows of 64 dims
+  constexpr int head_bytes = 2048;
+  const int half_bytes = a.heads * head_bytes;  // 16 rows of 64 dims
   const int group_bytes = (D / 64) * half_bytes;
 
   if (warp == kRowWarps) {
@@ -669,7 +706,6 @@ __global__ void __maxnreg__(112)
             for (int i = 0; i < 16; ++i) bits |= static_cast<unsigned>(s.sees(row + i)) << i;
           }
         }
-        if (c + 1 == all) write_row<D>(a, f, b, s, pos, h0, min(a.heads, a.Hkv - h0));
         if (n >= kRowStages) {
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], (n / kRowStages - 1) & 1, abort_s,
                                                  a.status, kDevErrTimeoutTma));
@@ -687,6 +723,9 @@ __global__ void __maxnreg__(112)
           o.slot = slot;
           o.pos = pos;
           o.groups = min(a.stage_groups, s.n - c * a.stage_groups);
+          o.fresh = c + 1 < all ? -1 : (s.n - 1 - c * a.stage_groups) * 16 + (s.row & 15);
+          o.at = ((static_cast<long long>(s.page) << a.pt.page_log2) + (s.row & mask)) *
+                 a.Hkv * D;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[st], 2 * __popc(groups) * group_bytes);
@@ -719,7 +758,8 @@ __global__ void __maxnreg__(112)
   } else {
     // --------------------------------------------------------------- heads --
     const int q8 = lane >> 2, t4 = lane & 3;  // query row, pair of columns
-    const int h = warp % a.heads, sub = warp / a.heads;  // (idle beyond the last group)
+    const int turn = warp >> 2, h = (warp & 3) % a.heads;
+    const int sub = (warp & 3) / a.heads;  // (idle beyond the last group)
     bool ok = true;
     float m = -INFINITY, l = 0.f;
     float o[D / 16][4];  // O^T: dims 16i + q8 (+ 8), queries 2 t4 (+ 1)
@@ -735,10 +775,11 @@ __global__ void __maxnreg__(112)
       if (!ok) break;
       const StageInfo& in = info[st];
       const int h0 = vld(in.h0);
-      const bool works = h0 + h < a.Hkv && sub < a.subs;
+      const int before = vld(in.before);
+      const bool works = before % kRowTurns == turn && h0 + h < a.Hkv && sub < a.subs;
       if (works) {
         const int g = h0 + h, b = vld(in.b);
-        if (vld(in.before) == 0) {  // ---- a piece's first chunk: its queries
+        if (before < kRowTurns) {  // ---- the first chunk of a piece: its queries
           const int pos = vld(in.pos);
           const __nv_bfloat16* x = a.q + (static_cast<long long>(b) * a.Hq + g * a.G) * D;
           const int third = q8 - 4;  // the query whose third term the row holds (not kWide)
@@ -785,7 +826,9 @@ __global__ void __maxnreg__(112)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
         }
-        const int groups = vld(in.groups);
+        const int groups = vld(in.groups), fresh = vld(in.fresh);
+        float* const lg = a.logits + ((static_cast<long long>(b) * a.Hkv + g) * a.G + q8) * a.cap +
+                          vld(in.v0) + 2 * t4;
         const uint32_t ks = smem_u32(smem + st * L::kStage) + h * head_bytes + krow * 128;
         bool cleared = false;
         for (int i = sub; i < groups; i += a.subs) {
@@ -793,28 +836,41 @@ __global__ void __maxnreg__(112)
           const uint32_t kg = ks + i * group_bytes, vg = kg + L::kHalfBytes;
           float x4[4] = {0.f, 0.f, 0.f, 0.f};  // query q8, keys 2 t4, + 1, + 8, + 9
           if (bits) {  // (uniform over the warp)
-            // ---- S [query terms, 16 keys]
-            float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+            if (fresh >> 4 == i) {
+              write_row<D>(a, f, b, g, vld(in.pos), *const_cast<const volatile long long*>(&in.at),
+                           kg - krow * 128, vg - krow * 128, half_bytes, fresh & 15);
+              cleared = true;
+            }
+            // ---- S [query terms, 16 keys], even and odd steps apart (the
+            // products of one chain wait for one another)
+            float s0[2][4], s1[2][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s0[0][e] = s0[1][e] = s1[0][e] = s1[1][e] = 0.f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
               uint32_t kb[4];
               ldsm_x4(kg + (k >> 2) * half_bytes +
                           ((((2 * (k & 3) + kcol) ^ (lane & 7))) << 4), kb);
-              mma_bf16_16816(s0, qa[k][0], qb[k][0], qa[k][1], qb[k][1], kb[0], kb[1]);
-              mma_bf16_16816(s1, qa[k][0], qb[k][0], qa[k][1], qb[k][1], kb[2], kb[3]);
+              mma_bf16_16816(s0[k & 1], qa[k][0], qb[k][0], qa[k][1], qb[k][1], kb[0], kb[1]);
+              mma_bf16_16816(s1[k & 1], qa[k][0], qb[k][0], qa[k][1], qb[k][1], kb[2], kb[3]);
               if (kWide) {
-                mma_bf16_16816(s0, qc[k][0], 0u, qc[k][1], 0u, kb[0], kb[1]);
-                mma_bf16_16816(s1, qc[k][0], 0u, qc[k][1], 0u, kb[2], kb[3]);
+                mma_bf16_16816(s0[k & 1], qc[k][0], 0u, qc[k][1], 0u, kb[0], kb[1]);
+                mma_bf16_16816(s1[k & 1], qc[k][0], 0u, qc[k][1], 0u, kb[2], kb[3]);
               }
             }
-            x4[0] = s0[0] + s0[2];
-            x4[1] = s0[1] + s0[3];
-            x4[2] = s1[0] + s1[2];
-            x4[3] = s1[1] + s1[3];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s0[0][e] += s0[1][e];
+              s1[0][e] += s1[1][e];
+            }
+            x4[0] = s0[0][0] + s0[0][2];
+            x4[1] = s0[0][1] + s0[0][3];
+            x4[2] = s1[0][0] + s1[0][2];
+            x4[3] = s1[0][1] + s1[0][3];
             if (!kWide) {  // (rows 4-7 hold third terms)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                x4[e] += __shfl_xor_sync(0xffffffffu, e < 2 ? s0[e] : s1[e - 2], 16);
+                x4[e] += __shfl_xor_sync(0xffffffffu, e < 2 ? s0[0][e] : s1[0][e - 2], 16);
             }
           }
           const bool live = q8 < a.G;
@@ -824,11 +880,8 @@ __global__ void __maxnreg__(112)
             x4[e] = live && (bits >> key & 1) ? x4[e] * a.scale_log2 : -INFINITY;
           }
           if (a.logits && live) {
-            float* lg = a.logits +
-                        ((static_cast<long long>(b) * a.Hkv + g) * a.G + q8) * a.cap + vld(in.v0) +
-                        i * 16 + 2 * t4;
-            *reinterpret_cast<float2*>(lg) = make_float2(x4[0], x4[1]);
-            *reinterpret_cast<float2*>(lg + 8) = make_float2(x4[2], x4[3]);
+            *reinterpret_cast<float2*>(lg + i * 16) = make_float2(x4[0], x4[1]);
+            *reinterpret_cast<float2*>(lg + i * 16 + 8) = make_float2(x4[2], x4[3]);
           }
           if (!bits) continue;
           float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
@@ -879,8 +932,8 @@ __global__ void __maxnreg__(112)
             mma_bf16_16816(o[j], vt[0], vt[1], vt[2], vt[3], p0, p1);
           }
         }
-        if (cleared) fence_proxy_async_smem();  // before a later load of what was cleared
-        if (vld(in.after) == 0) {  // ---- the piece's last chunk: its part
+        if (cleared) fence_proxy_async_smem();  // before a later load of what was written
+        if (vld(in.after) < kRowTurns) {  // ---- the last chunk of the piece: its part
           float sum = l;
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -889,7 +942,7 @@ __global__ void __maxnreg__(112)
           const float i0 = __shfl_sync(0xffffffffu, inv, 8 * t4);
           const float i1 = __shfl_sync(0xffffffffu, inv, 8 * t4 + 4);
           const long long part =
-              (static_cast<long long>(vld(in.slot)) * a.subs + sub) * a.heads + h;
+              ((static_cast<long long>(vld(in.slot)) * kRowTurns + turn) * a.subs + sub) * a.heads + h;
           if (t4 == 0 && q8 < a.G) a.row_lse[part * a.G + q8] = any ? m + __log2f(sum) : -INFINITY;
           float* out = a.row_o + part * a.G * D;
 #pragma unroll
@@ -915,62 +968,70 @@ __global__ void __maxnreg__(112)
 
 // --------------------------------------------------------------- finish ----
 constexpr int kFinishThreads = 512;
-constexpr int kFinishParts = 128;  // parts joined at a time
+constexpr int kFinishParts = 32;                      // parts joined at a time
+constexpr int kFinishHeads = kRowHeads * kMaxGroup;   // most query heads of a block
 
-// Blocks (., kv head, conversation): the parts' common log-sum-exp, a warp per
-// query head; then the first one the output, some threads per column of four,
-// the parts' weights and places settled before; the others the rows' weights.
+// Blocks (., heads, conversation), the heads a unit's or one: the parts' common
+// log-sum-exp, a warp per query head; then the first block the output, some
+// threads per column of four, the parts' weights and places settled before; the
+// others the rows' weights.
 template <int D>
 __global__ void __launch_bounds__(kFinishThreads, 2)
     step_finish_kernel(const __grid_constant__ StepArgs a) {
-  __shared__ float total[kMaxGroup];
+  __shared__ float total[kFinishHeads];
   __shared__ float4 acc[kFinishThreads];
-  __shared__ float weight[kMaxGroup][kFinishParts];
-  __shared__ const float4* place[kMaxGroup][kFinishParts];
+  __shared__ float weight[kFinishHeads][kFinishParts];
+  __shared__ const float4* place[kFinishHeads][kFinishParts];
   pdl_wait();
-  const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long start = __ldcg(a.starts + b), units = __ldcg(a.starts + a.B);
+  const int g0 = blockIdx.y * a.finish_heads, b = blockIdx.z;
+  const int heads = min(a.finish_heads, a.Hkv - g0), nq = heads * a.G;  // query heads
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long start = __ldcg(a.starts + b), chunks = __ldcg(a.starts + a.B);
   const StepOf s = step_of(a, b);
-  __nv_bfloat16* out = a.o + (static_cast<long long>(b) * a.Hq + g * a.G) * D;
+  __nv_bfloat16* out = a.o + (static_cast<long long>(b) * a.Hq + g0 * a.G) * D;
   if (s.row < 0) {
     if (blockIdx.x == 0)
-      for (int e = tid; e < a.G * D; e += kFinishThreads) out[e] = __float2bfloat16_rn(0.f);
+      for (int e = tid; e < nq * D; e += kFinishThreads) out[e] = __float2bfloat16_rn(0.f);
     return;
   }
   const int first = (static_cast<int>(blockIdx.x) - 1) * kFinishThreads;  // rows' blocks
   if (first >= s.n * 16) return;
   // ---- the parts of the private rows: those of the runs that hold the unit
-  const int unit = g / a.heads, h = g - unit * a.heads, all = chunks_of(a, s.n);
-  const long long chunk = (units + a.row_ctas - 1) / a.row_ctas;
-  const long long u0 = start + static_cast<long long>(unit) * all;
-  const int c0 = static_cast<int>(u0 / chunk), c1 = static_cast<int>((u0 + all - 1) / chunk);
-  const int n_row = (c1 - c0 + 1) * a.subs;
-  auto row_part = [&](int i) -> long long {
-    const int c = c0 + i / a.subs, k = i % a.subs;
+  const int unit = g0 / a.heads, all = chunks_of(a, s.n), per = kRowTurns * a.subs;
+  const long long chunk = (chunks + a.row_ctas - 1) / a.row_ctas;
+  const long long u0 = start + static_cast<long long>(unit) * all, u1 = u0 + all;
+  const int c0 = static_cast<int>(u0 / chunk), c1 = static_cast<int>((u1 - 1) / chunk);
+  const int n_row = (c1 - c0 + 1) * per;
+  auto row_part = [&](int q, int i) -> long long {  // its row, or -1
+    const int c = c0 + i / per, k = i % per;
+    // (warps whose turn is beyond the piece's chunks had none)
+    if (k / a.subs >= min(u1, (c + 1) * chunk) - max(u0, c * chunk)) return -1;
     const long long slot = c0 == c1 ? 2 * a.row_ctas + static_cast<long long>(b) * a.units + unit
                            : c > c0 || u0 == c0 * chunk ? 2 * c
                                                         : 2 * c + 1;
-    return ((slot * a.subs + k) * a.heads + h) * a.G;
+    return ((slot * per + k) * a.heads + g0 - unit * a.heads) * a.G + q;
   };
   // ---- and of the cartridge, by the tile that holds the query's row
-  auto cart_first = [&](int hh) {
-    return static_cast<long long>(g * a.row_tiles + (b * a.G + hh) / kTile) * a.cart_parts;
-  };
-  auto parts_of = [&](int hh) {
+  auto cart_row = [&](int q) { return b * a.G + q % a.G; };
+  auto cart_seg = [&](int q) { return (g0 + q / a.G) * a.row_tiles + cart_row(q) / kTile; };
+  auto parts_of = [&](int q) {
     if (a.key_tiles == 0) return n_row;
-    const int u = (g * a.row_tiles + (b * a.G + hh) / kTile) * a.key_tiles;
+    const int u = cart_seg(q) * a.key_tiles;
     return n_row + (u + a.key_tiles - 1) / a.cart_chunk - u / a.cart_chunk + 1;
   };
-  auto lse_of = [&](int hh, int i) {
-    return i < n_row ? __ldcg(a.row_lse + row_part(i) + hh)
-                     : __ldcg(a.cart_lse + (cart_first(hh) + i - n_row) * kTile +
-                              (b * a.G + hh) % kTile);
+  auto lse_of = [&](int q, int i) {
+    if (i >= n_row)
+      return __ldcg(a.cart_lse +
+                    (static_cast<long long>(cart_seg(q)) * a.cart_parts + i - n_row) * kTile +
+                    cart_row(q) % kTile);
+    const long long part = row_part(q, i);
+    return part < 0 ? -INFINITY : __ldcg(a.row_lse + part);
   };
-  if (warp < a.G) {
-    const int n = parts_of(warp);
+  for (int q = warp; q < nq; q += kFinishThreads / 32) {
+    const int n = parts_of(q);
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i < n; i += 32) {
-      const float x = lse_of(warp, i), top = fmaxf(m, x);
+      const float x = lse_of(q, i), top = fmaxf(m, x);
       if (top != -INFINITY || x != x) {
         l = l * exp2_approx(m - top) + exp2_approx(x - top);
         m = top;
@@ -985,68 +1046,80 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
       m = top;
     }
     // (no logit above -inf: every weight is 0)
-    if (lane == 0) total[warp] = l == 0.f ? INFINITY : m + __log2f(l);
+    if (lane == 0) total[q] = l == 0.f ? INFINITY : m + __log2f(l);
   }
   __syncthreads();
   if (blockIdx.x == 0) {
-    const int cols = a.G * (D / 4), each = kFinishThreads / cols;
-    const int col = tid % cols, turn = tid / cols, hh = col / (D / 4), j = col % (D / 4);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     int most = 0;
-    for (int q = 0; q < a.G; ++q) most = max(most, parts_of(q));
-    for (int i0 = 0; i0 < most; i0 += kFinishParts) {
-      __syncthreads();
-      for (int e = tid; e < a.G * kFinishParts; e += kFinishThreads) {
-        const int q = e / kFinishParts, k = e % kFinishParts, i = i0 + k;
-        if (i >= parts_of(q)) continue;
-        weight[q][k] = exp2_approx(lse_of(q, i) - total[q]);
-        place[q][k] = reinterpret_cast<const float4*>(
-            i < n_row ? a.row_o + (row_part(i) + q) * D
-                      : a.cart_o + ((cart_first(q) + i - n_row) * (D / 4) * kTile +
-                                    (b * a.G + q) % kTile) * 4);
-      }
-      __syncthreads();
-      if (turn < each) {
-        const int n = min(parts_of(hh) - i0, kFinishParts);
+    for (int q = 0; q < nq; ++q) most = max(most, parts_of(q));
+    const int cols = nq * (D / 4), each = max(kFinishThreads / cols, 1);
+    const int turn = tid / cols;  // (below `each`, or idle; 0 where there are more columns)
+    for (int col0 = 0; col0 < cols; col0 += kFinishThreads) {
+      const int col = col0 + (each > 1 ? tid % cols : tid);
+      const int q = col / (D / 4), j = col % (D / 4);
+      const bool mine = turn < each && col < cols;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 < most; i0 += kFinishParts) {
+        if (col0 == 0 || most > kFinishParts) {  // (else it is there already)
+          __syncthreads();
+          for (int e = tid; e < nq * kFinishParts; e += kFinishThreads) {
+            const int qq = e / kFinishParts, k = e % kFinishParts, i = i0 + k;
+            if (i >= parts_of(qq)) continue;
+            weight[qq][k] = exp2_approx(lse_of(qq, i) - total[qq]);
+            place[qq][k] = reinterpret_cast<const float4*>(
+                i < n_row ? a.row_o + max(row_part(qq, i), 0ll) * D
+                          : a.cart_o + ((static_cast<long long>(cart_seg(qq)) * a.cart_parts + i -
+                                         n_row) * (D / 4) * kTile + cart_row(qq) % kTile) * 4);
+          }
+          __syncthreads();
+        }
+        if (mine) {
+          const int n = min(parts_of(q) - i0, kFinishParts);
 #pragma unroll 8
-        for (int k = turn; k < n; k += each) {
-          const float w = weight[hh][k];
-          const float4 v = __ldcg(place[hh][k] + (i0 + k < n_row ? j : j * kTile));
-          // (a part of no weight may hold anything)
-          x.x += w == 0.f ? 0.f : w * v.x;
-          x.y += w == 0.f ? 0.f : w * v.y;
-          x.z += w == 0.f ? 0.f : w * v.z;
-          x.w += w == 0.f ? 0.f : w * v.w;
+          for (int k = turn; k < n; k += each) {
+            const float w = weight[q][k];
+            const float4 v = __ldcg(place[q][k] + (i0 + k < n_row ? j : j * kTile));
+            // (a part of no weight may hold anything)
+            x.x += w == 0.f ? 0.f : w * v.x;
+            x.y += w == 0.f ? 0.f : w * v.y;
+            x.z += w == 0.f ? 0.f : w * v.z;
+            x.w += w == 0.f ? 0.f : w * v.w;
+          }
         }
       }
-    }
-    acc[tid] = x;
-    __syncthreads();
-    if (turn == 0) {
-      for (int k = 1; k < each; ++k) {
-        const float4 v = acc[k * cols + col];
-        x.x += v.x;
-        x.y += v.y;
-        x.z += v.z;
-        x.w += v.w;
+      if (each > 1) {
+        acc[tid] = x;
+        __syncthreads();
+        if (turn == 0)
+          for (int k = 1; k < each; ++k) {
+            const float4 v = acc[k * cols + col];
+            x.x += v.x;
+            x.y += v.y;
+            x.z += v.z;
+            x.w += v.w;
+          }
       }
-      *reinterpret_cast<uint2*>(out + hh * D + 4 * j) =
-          make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+      if (mine && turn == 0)
+        *reinterpret_cast<uint2*>(out + q * D + 4 * j) =
+            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
     }
     return;
   }
-  const long long bg = static_cast<long long>(b) * a.Hkv + g;
-  float* w = a.weights + bg * a.weight_rows;
-  const float* lg = a.logits + bg * a.G * a.cap;
+  const long long bg = static_cast<long long>(b) * a.Hkv + g0;
   const int step = (gridDim.x - 1) * kFinishThreads;
-#pragma unroll 2
   for (int v = first + tid; v < s.n * 16; v += step) {
     const int r = s.group(v >> 4) * 16 + (v & 15);
     if (!s.sees(r)) continue;
-    float x = 0.f;
-    for (int hh = 0; hh < a.G; ++hh)
-      x += exp2_approx(__ldcg(lg + static_cast<long long>(hh) * a.cap + v) - total[hh]);
-    w[r] = r < s.row ? w[r] + x : x;
+    for (int h = 0; h < heads; ++h) {
+      const float* lg = a.logits + (bg + h) * a.G * a.cap + v;
+      float* w = a.weights + (bg + h) * a.weight_rows + r;
+      const float old = r < s.row ? *w : 0.f;
+      float x = 0.f;
+#pragma unroll 4
+      for (int hh = 0; hh < a.G; ++hh)
+        x += exp2_approx(__ldcg(lg + static_cast<long long>(hh) * a.cap) - total[h * a.G + hh]);
+      *w = old + x;
+    }
   }
 }
 
@@ -1084,7 +1157,8 @@ StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
   w.cart_o = take(segments * w.cart_parts * kTile * d * 4);
   w.cart_lse = take(segments * w.cart_parts * kTile * 4);
   const size_t parts =
-      (2 * static_cast<size_t>(w.row_ctas) + static_cast<size_t>(B) * w.units) * w.subs * w.heads;
+      (2 * static_cast<size_t>(w.row_ctas) + static_cast<size_t>(B) * w.units) * kRowTurns *
+      w.subs * w.heads;
   w.row_o = take(parts * G * d * 4);
   w.row_lse = take(parts * G * 4);
   w.starts = take((static_cast<size_t>(B) + 1) * 8);
@@ -1116,7 +1190,7 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
   using L = RowSmem<D>;
   cudaError_t e = cudaSuccess;
   if (w.cart_ctas > 0) {
-    e = set_smem_once<step_cart_kernel<D>>(C::kAlloc);
+    e = set_shared_once<step_cart_kernel<D>>(C::kAlloc);
     if (e != cudaSuccess) return e;
     const uint64_t dims[4] = {D, static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(a.p), 1};
     const uint64_t row = static_cast<uint64_t>(a.Hkv) * D * 2;
@@ -1140,8 +1214,8 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
       !encode_bf16_map4(&maps.v, a.v_pages, dims, strides, box))
     return cudaErrorInvalidValue;
   const bool wide = a.G > 4;
-  e = wide ? set_smem_once<step_rows_kernel<D, true>>(L::kAlloc)
-           : set_smem_once<step_rows_kernel<D, false>>(L::kAlloc);
+  e = wide ? set_shared_once<step_rows_kernel<D, true>>(L::kAlloc)
+           : set_shared_once<step_rows_kernel<D, false>>(L::kAlloc);
   if (e != cudaSuccess) return e;
   auto* rows = wide ? step_rows_kernel<D, true> : step_rows_kernel<D, false>;
   if (w.cart_ctas > 0) {
@@ -1151,14 +1225,18 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  // blocks for the weights' rows: as many as the GPU takes at once, at most one
-  // for every 512 rows that a table can name
+  // blocks of the last kernel: a unit's heads each where that leaves enough of
+  // them, else one; and for the weights' rows as many as the GPU takes at once, at
+  // most one for every 512 rows that a table can name
+  StepArgs last = a;
+  last.finish_heads = a.B * a.units >= sm_count() ? a.heads : 1;
+  const int across = (a.Hkv + last.finish_heads - 1) / last.finish_heads;
   int blocks = 1;
   if (a.weights)
     blocks += std::max(1, std::min((a.cap + kFinishThreads - 1) / kFinishThreads,
-                                   4 * sm_count() / std::max(1, a.B * a.Hkv)));
-  return launch_dependent(step_finish_kernel<D>, dim3(blocks, a.Hkv, a.B), dim3(kFinishThreads), 0,
-                          st, a);
+                                   4 * sm_count() / std::max(1, a.B * across)));
+  return launch_dependent(step_finish_kernel<D>, dim3(blocks, across, a.B), dim3(kFinishThreads), 0,
+                          st, last);
 }
 
 }  // namespace
