@@ -8,16 +8,20 @@
 //           as tcgen05 products: 128 rows and 64 keys at a time, Q resident as
 //           two bf16 terms, S and O in TMEM.  All (kv head, row tile, key tile)
 //           triples are cut into equal runs, one per CTA.
-//   rows    the private rows, bound by HBM: 16 rows of up to four heads by one
-//           box each for keys and values and 64 dims, three stages of up to 16 KB
-//           of both per CTA, a warp per head and 16 rows: m16n8k16 products with
-//           the query's terms in the rows of A that a group of heads leaves free,
-//           and V^T as A of the second product, whose B has the layout that the
-//           first one leaves.  The warp that comes to the new token's row
-//           writes its head's rotated key and value to it and to the stage.  All
-//           conversations' rows, one after the other, are cut into equal runs.
-//   finish  joins a (conversation, kv head)'s parts by their log-sum-exps, and
-//           adds exp2(logit - log-sum-exp) of the group's heads to each row.
+//   rows    the cached private rows, bound by HBM: S^T = K Q^T and O^T = V^T P^T
+//           on tcgen05, so that the keys fill the 128 rows of a product and the
+//           few queries its columns.  A tile is 128 key rows, 32 of each of four
+//           kv heads (64 of two, 128 of one), its columns the queries of those
+//           heads as three bf16 terms each, which hold all 24 bits of f32; what a
+//           key's row meets of another head's queries is not read.  Warp w has
+//           the keys 32w .. 32w + 31 of a tile, one a thread, and a maximum, sums
+//           and an O^T of its own.  K and V tiles come through one ring of 96 KB.
+//           All conversations' rows, one after the other, are cut into equal
+//           runs, one per CTA.
+//   finish  the new token: its rotated key and its value to its row, its logits;
+//           joins them and a (conversation, kv head)'s parts by their log-sum-
+//           exps, and adds exp2(logit - log-sum-exp) of the group's heads to each
+//           row's weight.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -67,12 +71,12 @@ struct StepArgs {
   // ---- cart: row tiles, key tiles, tiles per CTA, most parts of a segment
   int row_tiles, key_tiles, cart_chunk, cart_parts;
   float *cart_o, *cart_lse;  // [Hkv * row_tiles, cart_parts, d / 4, 128] float4; [.., 128]
-  // ---- rows: heads of a unit (of which a conversation has `units`), 16-row
-  // groups that its warps take side by side, and of a stage, CTAs
-  int heads, units, subs, stage_groups, row_ctas;
+  // ---- rows: heads of a unit (of which a conversation has `units`), 32-row
+  // groups of a tile (heads * groups is 4), CTAs
+  int heads, units, groups, row_ctas;
   int finish_heads;          // heads of a block of the last kernel: `heads` or 1
   long long* starts;         // [B + 1]: chunks of a unit before each conversation's
-  float *row_o, *row_lse;    // [slots, turns * subs, heads, G, d], [.., G]
+  float *row_o, *row_lse;    // [slots, groups, heads, G, d], [.., G]
   int cap;                   // most private rows
   float* logits;             // [B, Hkv, G, cap], log2 domain, by the order of groups seen
 };
@@ -82,13 +86,13 @@ struct Turns {
 };
 
 // The step of conversation b: the row of its new token (-1: idle, or the row
-// has no page), that row's page; the rows it sees: those below `low` and from
-// `high` to `row`, in n groups of 16: those below g_low and from g_high on.
+// has no page), that row's page; the cached rows it sees: those below `low` and
+// from `high` to row - 1, in n groups of 32: those below g_low and from g_high on.
 struct StepOf {
   int row, page, low, high, g_low, g_high, n;
   bool lost;  // not idle, but without a page
   __device__ __forceinline__ int group(int i) const { return i < g_low ? i : i - g_low + g_high; }
-  __device__ __forceinline__ bool sees(int r) const { return r <= row && (r < low || r >= high); }
+  __device__ __forceinline__ bool sees(int r) const { return r < row && (r < low || r >= high); }
 };
 __device__ __forceinline__ StepOf step_of(const StepArgs& a, int b) {
   StepOf s;
@@ -98,9 +102,9 @@ __device__ __forceinline__ StepOf step_of(const StepArgs& a, int b) {
   s.row = s.page < 0 ? -1 : len;
   s.high = a.window > 0 ? max(s.row - a.window + 1, 0) : 0;
   s.low = min(max(a.sinks - a.p, 0), s.high);
-  s.g_high = s.high >> 4;
-  s.g_low = min((s.low + 15) >> 4, s.g_high);
-  s.n = s.row < 0 ? 0 : s.g_low + (s.row >> 4) + 1 - s.g_high;
+  s.g_high = s.high >> 5;
+  s.g_low = min((s.low + 31) >> 5, s.g_high);
+  s.n = s.row < 0 ? 0 : s.g_low + max(((s.row + 31) >> 5) - s.g_high, 0);
   return s;
 }
 __device__ __forceinline__ int position_of(const StepArgs& a, int b, int row) {
@@ -115,16 +119,15 @@ template <int D>
 struct CartSmem {
   static constexpr int kQBytes = kTile * D * 2, kKBytes = kCartKeys * D * 2;
   static constexpr int kQ = 0;                 // two terms
-  static constexpr int kK = kQ + 2 * kQBytes;  // two slots
-  static constexpr int kV = kK + 2 * kKBytes;
-  static constexpr int kBytes = kV + kKBytes;
-  static constexpr int kAlloc = kBytes + 1024;  // slack for 1024-byte alignment
+  static constexpr int kK = kQ + 2 * kQBytes;
+  static constexpr int kV = kK + kKBytes;
+  static constexpr int kAlloc = kV + kKBytes;  // starts 1024-aligned (checked at entry)
 };
 
 enum CartBar {
-  kCKFull0 = 0,
-  kCKEmpty0 = kCKFull0 + 2,
-  kCVFull = kCKEmpty0 + 2,
+  kCKFull = 0,
+  kCKEmpty,
+  kCVFull,
   kCSFull0,                   // S of buffer x is in TMEM
   kCPFull0 = kCSFull0 + 2,    // its weights are (128 arrivals); by buffer, since those
                               // of the next tile may come before these are waited for
@@ -139,17 +142,19 @@ struct CartMaps {
   CUtensorMap k, v;
 };
 
-// (96 registers, and 104 of the rows' kernel: a quarter of an SM holds two of
-// these warps and three of those)
+// (128 registers, as the rows' kernel: a quarter of an SM holds two warps of each)
 template <int D>
-__global__ void __maxnreg__(96)
+__global__ void __maxnreg__(128)
     step_cart_kernel(const __grid_constant__ CartMaps maps, const __grid_constant__ StepArgs a,
                      const __grid_constant__ Turns f) {
   using L = CartSmem<D>;
   constexpr int HALF = D / 2;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t step_smem[];
+  uint8_t* const smem = step_smem;
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(a.status, kDevErrSmemLayout);
+    return;
+  }
   __shared__ uint64_t bars[kCBars];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, first_s;
@@ -247,20 +252,18 @@ __global__ void __maxnreg__(96)
         int s = step;
         for (int t = t0; t < t1 && ok; ++t) {
           if (!seen(t)) continue;
-          const int x = s & 1;
-          if (s >= 2)
-            ok = mbar_wait(&bars[kCKEmpty0 + x], ((s >> 1) - 1) & 1, abort_s, a.status,
-                           kDevErrTimeoutTma);
+          if (s >= 1)
+            ok = mbar_wait(&bars[kCKEmpty], (s - 1) & 1, abort_s, a.status, kDevErrTimeoutTma);
           if (!ok) break;
-          mbar_arrive_expect_tx(&bars[kCKFull0 + x], L::kKBytes);
+          mbar_arrive_expect_tx(&bars[kCKFull], L::kKBytes);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(smem + L::kK + x * L::kKBytes + h * 8192, &maps.k, &bars[kCKFull0 + x],
-                        h * 64, g, t * kCartKeys, 0);
+            tma_load_4d(smem + L::kK + h * 8192, &maps.k, &bars[kCKFull], h * 64, g, t * kCartKeys,
+                        0);
           if (s >= 1)
             ok = mbar_wait(&bars[kCPvDone], (s - 1) & 1, abort_s, a.status, kDevErrTimeoutTma);
           if (!ok) {
-            mbar_wait(&bars[kCKFull0 + x], (s >> 1) & 1, 0u, nullptr, 0);
+            mbar_wait(&bars[kCKFull], s & 1, 0u, nullptr, 0);
             break;
           }
           mbar_arrive_expect_tx(&bars[kCVFull], L::kKBytes);
@@ -272,8 +275,7 @@ __global__ void __maxnreg__(96)
         }
         // (whatever went wrong: the last copies land before the CTA ends)
         if (s > step) {
-          mbar_wait(&bars[kCKFull0 + ((s - 1) & 1)], ((s - 1) >> 1) & 1, 0u, nullptr, 0);
-          if (s >= 2) mbar_wait(&bars[kCKFull0 + (s & 1)], ((s - 2) >> 1) & 1, 0u, nullptr, 0);
+          mbar_wait(&bars[kCKFull], (s - 1) & 1, 0u, nullptr, 0);
           mbar_wait(&bars[kCVFull], (s - 1) & 1, 0u, nullptr, 0);
         }
       }
@@ -289,28 +291,27 @@ __global__ void __maxnreg__(96)
       const uint64_t dK = sdesc_sw128(smem_u32(smem + L::kK), 16u, 1024u);
       const uint64_t dV = sdesc_sw128(smem_u32(smem + L::kV), 8192u, 1024u);
       auto issue_s = [&](int s) {
-        const uint64_t dk = desc_add(dK, (s & 1) * L::kKBytes);
 #pragma unroll
         for (int m = 1; m >= 0; --m)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             umma_bf16_ss_w(tS + (s & 1) * kCartKeys,
                            desc_add(dQ, m * L::kQBytes + (k >> 2) * 16384 + (k & 3) * 32),
-                           desc_add(dk, (k >> 2) * 8192 + (k & 3) * 32), idS,
+                           desc_add(dK, (k >> 2) * 8192 + (k & 3) * 32), idS,
                            m == 1 && k == 0 ? 0u : 1u);
         umma_commit_w(&bars[kCSFull0 + (s & 1)]);
-        umma_commit_w(&bars[kCKEmpty0 + (s & 1)]);
+        umma_commit_w(&bars[kCKEmpty]);
       };
       for (int t = 0; t < n && ok; ++t) {
         const int s = step + t;
         if (t == 0) {
-          ok = wait(&bars[kCKFull0 + (s & 1)], (s >> 1) & 1);
+          ok = wait(&bars[kCKFull], s & 1);
           if (!ok) break;
           tc_fence_after();
           issue_s(s);
         }
         if (t + 1 < n) {  // over the weights of tile t - 1, read by the product before
-          ok = wait(&bars[kCKFull0 + ((s + 1) & 1)], ((s + 1) >> 1) & 1);
+          ok = wait(&bars[kCKFull], (s + 1) & 1);
           if (!ok) break;
           tc_fence_after();
           issue_s(s + 1);
@@ -492,130 +493,105 @@ __global__ void __maxnreg__(96)
 }
 
 // ----------------------------------------------------------------- rows ----
-constexpr int kRowTurns = 2;     // groups of four warps, which take a piece's chunks in turn
-constexpr int kRowWarps = 4 * kRowTurns;
-constexpr int kRowThreads = 32 * kRowWarps + 32;  // and the producer
-constexpr int kRowStages = 3;
-constexpr int kRowHeads = 4;     // most heads of a unit
-constexpr int kRowGroups = 8;    // most 16-row groups of a stage
+constexpr int kRowThreads = 192;   // four warps of keys, TMA warp, MMA warp
+constexpr int kRowHeads = 4;       // most heads of a unit
+constexpr int kTerms = 3;          // of a query
+constexpr int kHeadColumns = kTerms * kMaxGroup;
+constexpr int kTileInfos = 4;
 
-// What a stage holds: groups of 16 rows of conversation b and the unit's heads
-// from h0 on; v0 the first's number among those seen, times 16; the rows of each
-// that are there and seen; chunks of the piece before and after it, the slot of
-// the piece's part; the token's position; groups; the new row's number among
-// the stage's (-1: not here) and its place in the pool.
-struct StageInfo {
-  int b, h0, v0, before, after, slot, pos, groups, fresh;
-  long long at;
-  unsigned short bits[kRowGroups];
+// What the roles know of a tile: conversation, first head, first key's number
+// among the groups seen, times 32; whether it opens and closes a piece, the slot
+// of the piece's parts, the token's position; the rows of each group that are
+// there and seen.
+struct TileInfo {
+  int b, h0, v0, opens, closes, slot, pos;
+  unsigned bits[kRowHeads];
 };
 
 template <int D>
 struct RowSmem {
-  static constexpr int kHalfBytes = 16 * kRowHeads * 256;  // keys, or values
-  static constexpr int kStage = 2 * kHalfBytes;
-  static constexpr int kAlloc = kRowStages * kStage + 1024;  // slack for alignment
+  static constexpr int kTileBytes = kTile * D * 2;          // a K or V tile
+  static constexpr int kSlots = 3 * 128 / D;                // of the ring
+  static constexpr int kQHalf = kRowHeads * kHeadColumns * 128;  // 64 dims of all columns
+  static constexpr int kP = kSlots * kTileBytes;  // weights: two buffers, 1 KB a warp
+  // (a product reads 16 rows of weights, eight of them behind the warp's)
+  static constexpr int kQ = kP + 2 * 4096;
+  static constexpr int kAlloc = kQ + (D / 64) * kQHalf;  // starts 1024-aligned
+};
+
+enum RowBar {
+  kRFull0 = 0,                  // ring slot has landed (6 slots at most)
+  kREmpty0 = kRFull0 + 6,
+  kRInfoFull0 = kREmpty0 + 6,   // info of a tile
+  kRInfoEmpty0 = kRInfoFull0 + kTileInfos,  // four warps and the MMA warp have read it
+  kRQReady = kRInfoEmpty0 + kTileInfos,     // a piece's queries are staged (128 arrivals)
+  kRSFull0,                     // S^T of buffer x is in TMEM
+  kRPFull0 = kRSFull0 + 2,      // its weights are in shared memory (128 arrivals)
+  kRPvDone = kRPFull0 + 2,      // O^T has a tile's
+  kRODone,                      // ... a piece's last tile's
+  kRExchange,                   // the four warps have left their factors (4 arrivals)
+  kRDrain,
+  kRBars
 };
 
 struct RowMaps {
-  CUtensorMap k, v;  // (d, page_rows, Hkv, pages), box 64 x 16 x heads x 1
+  CUtensorMap k, v;  // (d, page_rows, Hkv, pages), box 64 x 32 x heads, or 64 x 16 x 1
 };
 
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                               uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Tiles of one unit of a conversation that sees n groups.
+__device__ __forceinline__ int tiles_of(const StepArgs& a, int n) {
+  return (n + a.groups - 1) / a.groups;
 }
 
-// Chunks (stages) of one unit of a conversation that sees n groups.
-__device__ __forceinline__ int chunks_of(const StepArgs& a, int n) {
-  return (n + a.stage_groups - 1) / a.stage_groups;
+// The largest of a warp's values (NaN left out).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// The new token's rotated key and its value, one head's, by a warp: to its row
-// of the pool, and to row r of the staged group, where what the pool held before
-// has landed.
 template <int D>
-__device__ __forceinline__ void write_row(const StepArgs& a, const Turns& f, int b, int g, int pos,
-                                          long long at, uint32_t ks, uint32_t vs, int half_bytes,
-                                          int r) {
-  constexpr int HALF = D / 2;
-  const int lane = threadIdx.x & 31;
-  const long long from = (static_cast<long long>(b) * a.Hkv + g) * D, to = at + g * D;
-  auto staged = [&](int j) {  // place of element j
-    return (j >> 6) * half_bytes + r * 128 + ((((j & 63) >> 3) ^ (r & 7)) << 4) + (j & 7) * 2;
-  };
-#pragma unroll
-  for (int e = 0; e < HALF / 32; ++e) {
-    const int j = lane + 32 * e;
-    float y0, y1;
-    rope_pair(__bfloat162float(a.k_new[from + j]), __bfloat162float(a.k_new[from + j + HALF]),
-              rope_cs_turns(f.t[j], pos), y0, y1);
-    const __nv_bfloat16 z0 = __float2bfloat16_rn(y0), z1 = __float2bfloat16_rn(y1);
-    a.k_pages[to + j] = z0;
-    a.k_pages[to + j + HALF] = z1;
-    sts_u16(ks + staged(j), __bfloat16_as_ushort(z0));
-    sts_u16(ks + staged(j + HALF), __bfloat16_as_ushort(z1));
-  }
-  if (lane < D / 8) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.v_new + from + lane * 8));
-    *reinterpret_cast<uint4*>(a.v_pages + to + lane * 8) = v;
-    sts_u4(vs + staged(lane * 8), v);
-  }
-  __syncwarp();
-}
-
-// kWide: groups of more than four query heads.  The first product's A has the
-// queries' first terms in rows 0 .. G - 1 and their second ones in rows 8 ..;
-// the third ones in rows 4 .. where the group leaves those free, else they are
-// a product of their own.
-template <int D, bool kWide>
-__global__ void __maxnreg__(104)
+__global__ void __maxnreg__(128)
     step_rows_kernel(const __grid_constant__ RowMaps maps, const __grid_constant__ StepArgs a,
                      const __grid_constant__ Turns f) {
   using L = RowSmem<D>;
-  constexpr int KS = D / 16;  // steps of 16 dims
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[kRowStages], empty[kRowStages];
-  __shared__ StageInfo info[kRowStages];
-  __shared__ long long scan[kRowThreads / 32];
+  constexpr int HALF = D / 2, NS = L::kSlots;
+  extern __shared__ __align__(1024) uint8_t step_smem[];
+  uint8_t* const smem = step_smem;
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(a.status, kDevErrSmemLayout);
+    return;
+  }
+  __shared__ uint64_t bars[kRBars];
+  __shared__ TileInfo info[kTileInfos];
+  __shared__ float factor[2][4][kMaxGroup];  // what each warp's O^T is multiplied by
+  __shared__ int rescale[2][4];
+  __shared__ long long scan[kRowThreads / 32], run_off;
+  __shared__ uint32_t tmem_slot;
   __shared__ int run_b, abort_flag;
-  __shared__ long long run_off;
-  uint8_t* const smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t abort_s = smem_u32(&abort_flag);
   if (tid == 0) {
     abort_flag = 0;
-    for (int s = 0; s < kRowStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kRowWarps);
-    }
+    for (int s = 0; s < kRBars; ++s)
+      mbar_init(&bars[s], s == kRQReady || s == kRPFull0 || s == kRPFull0 + 1 ? 128
+                          : s >= kRInfoEmpty0 && s < kRInfoEmpty0 + kTileInfos ? 5
+                          : s == kRExchange                                    ? 4
+                                                                               : 1);
     fence_mbar_init();
   }
-  // ---- the chunks of all conversations, and this CTA's run of them
+  if (warp == 5) {
+    tmem_alloc(&tmem_slot, 256);
+    tmem_relinquish();
+  }
+  // ---- the tiles of all conversations, and this CTA's run of them
   const int per = (a.B + kRowThreads - 1) / kRowThreads;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const StepOf s = step_of(a, b);
     if (s.lost && blockIdx.x == 0) atomicOr(a.status, kDevErrNoPage);
-    mine += static_cast<long long>(chunks_of(a, s.n)) * a.units;
+    mine += static_cast<long long>(tiles_of(a, s.n)) * a.units;
   }
   long long x = mine;
 #pragma unroll
@@ -624,7 +600,10 @@ __global__ void __maxnreg__(104)
     if (lane >= o) x += y;
   }
   if (lane == 31) scan[warp] = x;
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
   long long total = 0, start = x - mine;
 #pragma unroll
   for (int w = 0; w < kRowThreads / 32; ++w) {
@@ -637,7 +616,7 @@ __global__ void __maxnreg__(104)
     long long at = start;
     int b = b0;
     for (;; ++b) {
-      const long long n = static_cast<long long>(chunks_of(a, step_of(a, b).n)) * a.units;
+      const long long n = static_cast<long long>(tiles_of(a, step_of(a, b).n)) * a.units;
       if (lo < at + n) break;
       at += n;
     }
@@ -648,102 +627,126 @@ __global__ void __maxnreg__(104)
     long long at = start;
     for (int b = b0; b < b1; ++b) {
       a.starts[b] = at;
-      at += static_cast<long long>(chunks_of(a, step_of(a, b).n)) * a.units;
+      at += static_cast<long long>(tiles_of(a, step_of(a, b).n)) * a.units;
     }
     if (tid == 0) a.starts[a.B] = total;
   }
   __syncthreads();
-  const int n_chunks = static_cast<int>(hi - lo);
-  constexpr int head_bytes = 2048;
-  const int half_bytes = a.heads * head_bytes;  // 16 rows of 64 dims
-  const int group_bytes = (D / 64) * half_bytes;
+  const int n_tiles = static_cast<int>(hi - lo);
+  // TMEM: two buffers of S^T, then the four O^T (16 columns each, 8 of them used)
+  const uint32_t tS = tmem, tO = tmem + 192;
+  constexpr int kSBuffer = 96;
 
-  if (warp == kRowWarps) {
+  if (warp == 4) {
     // ------------------------------------------------------------ producer --
-    int b = run_b, n = 0;  // chunks handed on
-    bool ok = n_chunks > 0;
-    int unit = 0, c0 = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_s, a.status, kDevErrTimeoutTma));
+    };
+    int b = run_b, n = 0, loads = 0;  // tiles handed on, ring slots filled
+    bool ok = n_tiles > 0;
+    int unit = 0, t0 = 0;
     StepOf s{};
     if (ok) {
       s = step_of(a, b);
-      const int per_unit = chunks_of(a, s.n);
+      const int per_unit = tiles_of(a, s.n);
       unit = static_cast<int>(run_off / per_unit);
-      c0 = static_cast<int>(run_off - static_cast<long long>(unit) * per_unit);
+      t0 = static_cast<int>(run_off - static_cast<long long>(unit) * per_unit);
     }
-    while (ok && n < n_chunks) {
-      const int all = chunks_of(a, s.n);
-      if (all == 0) {  // idle
+    // boxes: a group's 32 rows of all heads, or, in pages of 16, 16 rows of one
+    const bool small = a.pt.page_log2 == 4;
+    const int lanes = small ? 2 * a.groups : a.groups;  // that issue boxes
+    const int group_of = small ? lane >> 1 : lane;
+    const int lane_bytes = a.heads * (small ? 2048 : 4096) * (D / 64);
+    const int mask = (1 << a.pt.page_log2) - 1;
+    while (ok && n < n_tiles) {
+      const int all = tiles_of(a, s.n);
+      if (all == 0) {  // idle, or nothing cached
         s = step_of(a, ++b);
         continue;
       }
       const int pos = position_of(a, b, s.row), h0 = unit * a.heads;
-      const int c1 = min(all, c0 + n_chunks - n);
+      const int t1 = min(all, t0 + n_tiles - n);
       // the next conversation's, before they are needed
       const StepOf next = unit + 1 == a.units && b + 1 < a.B ? step_of(a, b + 1) : s;
       // the piece's slot: the run's first piece, its last one, or a whole unit
-      const bool opens = n == 0 && c0 > 0, closes = c1 < all;
-      const int slot = opens || (closes && n == 0) ? 2 * blockIdx.x
-                       : closes                    ? 2 * blockIdx.x + 1
-                                                   : 2 * a.row_ctas + b * a.units + unit;
+      const bool from_before = n == 0 && t0 > 0, goes_on = t1 < all;
+      const int slot = from_before || (goes_on && n == 0) ? 2 * blockIdx.x
+                       : goes_on                          ? 2 * blockIdx.x + 1
+                                         : 2 * a.row_ctas + b * a.units + unit;
       const int* pages = a.pt.table + static_cast<long long>(b) * a.pt.max_pages;
-      const int mask = (1 << a.pt.page_log2) - 1;
-      // a chunk's groups, a lane each: its first row, and that row's page
-      auto row_of = [&](int c) {
-        const int i = c * a.stage_groups + lane;
-        return lane < a.stage_groups && i < s.n ? s.group(i) * 16 : -1;
+      // a tile's boxes, a lane each: first row, and that row's page
+      auto row_of = [&](int t) {
+        const int i = t * a.groups + group_of;
+        return lane < lanes && i < s.n ? s.group(i) * 32 + (small ? (lane & 1) * 16 : 0) : -1;
       };
-      auto look_up = [&](int r) { return r < 0 ? -1 : __ldg(pages + (r >> a.pt.page_log2)); };
-      int row = row_of(c0), page = look_up(row);
-      for (int c = c0; c < c1; ++c, ++n) {
-        const int st = n % kRowStages;
-        const int row_next = c + 1 < c1 ? row_of(c + 1) : -1, page_next = look_up(row_next);
+      auto look_up = [&](int r) {  // (the second half of the last group may be past the table)
+        return r < 0 || (r >> a.pt.page_log2) >= a.pt.max_pages
+                   ? -1
+                   : __ldg(pages + (r >> a.pt.page_log2));
+      };
+      int row = row_of(t0), page = look_up(row);
+      for (int t = t0; t < t1; ++t, ++n) {
+        const int row_next = t + 1 < t1 ? row_of(t + 1) : -1, page_next = look_up(row_next);
         const bool there = row >= 0 && is_page(page, a.pt.n_pages);
+        const int rows = small ? 16 : 32;
         unsigned bits = 0;
         if (there) {
-          bits = 0xffffu;
-          if (row + 15 > s.row || (row + 15 >= s.low && row < s.high)) {
+          bits = rows == 32 ? 0xffffffffu : 0xffffu;
+          if (row + rows > s.row || (row + rows > s.low && row < s.high)) {
             bits = 0;
-            for (int i = 0; i < 16; ++i) bits |= static_cast<unsigned>(s.sees(row + i)) << i;
+            for (int i = 0; i < rows; ++i) bits |= static_cast<unsigned>(s.sees(row + i)) << i;
           }
         }
-        if (n >= kRowStages) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], (n / kRowStages - 1) & 1, abort_s,
-                                                 a.status, kDevErrTimeoutTma));
+        if (small) bits |= __shfl_down_sync(0xffffffffu, bits, 1) << 16;  // (even lanes')
+        const unsigned boxes = __ballot_sync(0xffffffffu, there);
+        const int ti = n % kTileInfos;
+        if (n >= kTileInfos) {
+          ok = wait(&bars[kRInfoEmpty0 + ti], (n / kTileInfos - 1) & 1);
           if (!ok) break;
         }
-        const unsigned groups = __ballot_sync(0xffffffffu, there);
-        StageInfo& o = info[st];
-        if (lane < kRowGroups) o.bits[lane] = static_cast<unsigned short>(bits);
+        TileInfo& o = info[ti];
+        if (lane < lanes && (!small || !(lane & 1))) o.bits[group_of] = bits;
         if (lane == 0) {
           o.b = b;
           o.h0 = h0;
-          o.v0 = c * a.stage_groups * 16;
-          o.before = c - c0;
-          o.after = c1 - 1 - c;
+          o.v0 = t * a.groups * 32;
+          o.opens = t == t0;
+          o.closes = t + 1 == t1;
           o.slot = slot;
           o.pos = pos;
-          o.groups = min(a.stage_groups, s.n - c * a.stage_groups);
-          o.fresh = c + 1 < all ? -1 : (s.n - 1 - c * a.stage_groups) * 16 + (s.row & 15);
-          o.at = ((static_cast<long long>(s.page) << a.pt.page_log2) + (s.row & mask)) *
-                 a.Hkv * D;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], 2 * __popc(groups) * group_bytes);
-        __syncwarp();
-        if (there) {
-          uint8_t* const ks = smem + st * L::kStage + lane * group_bytes;
+        if (lane == 0) mbar_arrive(&bars[kRInfoFull0 + ti]);
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            tma_load_4d(ks + h * half_bytes, &maps.k, &full[st], h * 64, row & mask, h0, page);
-            tma_load_4d(ks + L::kHalfBytes + h * half_bytes, &maps.v, &full[st], h * 64, row & mask,
-                        h0, page);
+        for (int kv = 0; kv < 2; ++kv, ++loads) {
+          const int sl = loads % NS;
+          if (loads >= NS) {
+            ok = wait(&bars[kREmpty0 + sl], (loads / NS - 1) & 1);
+            if (!ok) break;
           }
+          if (lane == 0) mbar_arrive_expect_tx(&bars[kRFull0 + sl], __popc(boxes) * lane_bytes);
+          __syncwarp();
+          if (there) {
+            uint8_t* const to = smem + sl * L::kTileBytes + group_of * a.heads * 4096;
+            const CUtensorMap* m = kv ? &maps.v : &maps.k;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+              if (!small) {
+                tma_load_4d(to + h * 16384, m, &bars[kRFull0 + sl], h * 64, row & mask, h0, page);
+              } else {
+                for (int i = 0; i < a.heads; ++i)
+                  tma_load_4d(to + h * 16384 + i * 4096 + (lane & 1) * 2048, m, &bars[kRFull0 + sl],
+                              h * 64, 0, h0 + i, page);
+              }
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
         row = row_next;
         page = page_next;
       }
-      c0 = 0;
+      t0 = 0;
       if (++unit == a.units) {
         unit = 0;
         ++b;
@@ -752,216 +755,311 @@ __global__ void __maxnreg__(104)
     }
     pdl_release();
     if (lane == 0)  // the last copies land before the CTA ends
-      for (int i = max(n - kRowStages, 0); i < n; ++i)
-        mbar_wait(&full[i % kRowStages], (i / kRowStages) & 1, 0u, nullptr, 0);
+      for (int i = max(loads - NS, 0); i < loads; ++i)
+        mbar_wait(&bars[kRFull0 + i % NS], (i / NS) & 1, 0u, nullptr, 0);
+    __syncwarp();
+  } else if (warp == 5) {
+    // ----------------------------------------------------------------- MMA --
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_s, a.status, kDevErrTimeoutMma));
+    };
+    const uint32_t idS = idesc_bf16(128, a.heads == 1 ? 32 : a.heads * kHeadColumns, false, false);
+    const uint32_t idO = idesc_bf16(128, 16, true, false);
+    const uint64_t dK = sdesc_sw128(smem_u32(smem), 16u, 1024u);
+    // (64 dims: the product's upper 64 rows are the next warp's values, unread)
+    const uint64_t dV = sdesc_sw128(smem_u32(smem), D == 128 ? 16384u : 4096u, 1024u);
+    const uint64_t dQ = sdesc_sw128(smem_u32(smem + L::kQ), 16u, 1024u);
+    const uint64_t dP = sdesc_sw128(smem_u32(smem + L::kP), 16u, 1024u);
+    auto issue_s = [&](int n) {
+      const int e = 2 * n, sl = e % NS;
+      if (!wait(&bars[kRFull0 + sl], (e / NS) & 1)) return false;
+      tc_fence_after();
+      const uint64_t dk = desc_add(dK, sl * L::kTileBytes);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        umma_bf16_ss_w(tS + (n & 1) * kSBuffer, desc_add(dk, (k >> 2) * 16384 + (k & 3) * 32),
+                       desc_add(dQ, (k >> 2) * L::kQHalf + (k & 3) * 32), idS, k > 0 ? 1u : 0u);
+      umma_commit_w(&bars[kRSFull0 + (n & 1)]);
+      umma_commit_w(&bars[kREmpty0 + sl]);
+      return true;
+    };
+    bool ok = n_tiles > 0;
+    int pieces = 0;
+    // the tile's flags: bit 0 opens, bit 1 closes a piece
+    auto flags_of = [&](int n) {
+      const int ti = n % kTileInfos;
+      if (!wait(&bars[kRInfoFull0 + ti], (n / kTileInfos) & 1)) return -1;
+      const int fl = vld(info[ti].opens) | vld(info[ti].closes) << 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kRInfoEmpty0 + ti]);
+      return fl;
+    };
+    int fl = ok ? flags_of(0) : -1;
+    for (int n = 0; n < n_tiles && ok; ++n) {
+      ok = fl >= 0;
+      if (!ok) break;
+      const int now = fl;
+      if (now & 1) {  // a piece's first tile: its queries
+        ok = wait(&bars[kRQReady], pieces & 1) && issue_s(n);
+        ++pieces;
+        if (!ok) break;
+      }
+      if (n + 1 < n_tiles) {
+        fl = flags_of(n + 1);
+        ok = fl >= 0;
+        if (!ok) break;
+        // (of the same piece: over the S^T before, whose weights have been used)
+        if (!(fl & 1)) ok = issue_s(n + 1);
+        if (!ok) break;
+      }
+      const int e = 2 * n + 1, sl = e % NS;
+      ok = wait(&bars[kRFull0 + sl], (e / NS) & 1) && wait(&bars[kRPFull0 + (n & 1)], (n >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t dv = desc_add(dV, sl * L::kTileBytes), dp = desc_add(dP, (n & 1) * 4096);
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          umma_bf16_ss_w(tO + w * 16, desc_add(dv, w * 4096 + k * 2048),
+                         desc_add(dp, w * 1024 + k * 32), idO, (now & 1) && k == 0 ? 0u : 1u);
+      umma_commit_w(&bars[kREmpty0 + sl]);
+      umma_commit_w(&bars[kRPvDone]);
+      if (now & 2) umma_commit_w(&bars[kRODone]);
+    }
+    // every product issued above completes before the CTA ends
+    umma_commit_w(&bars[kRDrain]);
+    mbar_wait(&bars[kRDrain], 0, 0u, nullptr, 0);
     __syncwarp();
   } else {
-    // --------------------------------------------------------------- heads --
-    const int q8 = lane >> 2, t4 = lane & 3;  // query row, pair of columns
-    const int turn = warp >> 2, h = (warp & 3) % a.heads;
-    const int sub = (warp & 3) / a.heads;  // (idle beyond the last group)
+    // ---------------------------------------------------------------- keys --
+    auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t err) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_s, a.status, err));
+    };
+    const int h = warp % a.heads, grp = warp / a.heads;
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     bool ok = true;
-    float m = -INFINITY, l = 0.f;
-    float o[D / 16][4];  // O^T: dims 16i + q8 (+ 8), queries 2 t4 (+ 1)
-    // the queries' terms as A: rows 0-7 (first terms, and third in rows 4-7),
-    // rows 8-15 (second ones)
-    uint32_t qa[KS][2], qb[KS][2], qc[kWide ? KS : 1][2];
-    // chunks of 16 bytes of a row's 64 dims lie by the row's last three bits
-    const int krow = (lane & 7) + (lane >> 4) * 8, kcol = (lane >> 3) & 1;
-    for (int n = 0; n < n_chunks && ok; ++n) {
-      const int st = n % kRowStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (n / kRowStages) & 1, abort_s, a.status,
-                                             kDevErrTimeoutSoftmax));
+    float m[kMaxGroup], l[kMaxGroup];  // the warp's maxima, the thread's sums
+    int exchanges = 0, pieces = 0;
+    for (int n = 0; n < n_tiles && ok; ++n) {
+      const int ti = n % kTileInfos, x = n & 1;
+      ok = wait(&bars[kRInfoFull0 + ti], (n / kTileInfos) & 1, kDevErrTimeoutSoftmax);
       if (!ok) break;
-      const StageInfo& in = info[st];
-      const int h0 = vld(in.h0);
-      const int before = vld(in.before);
-      const bool works = before % kRowTurns == turn && h0 + h < a.Hkv && sub < a.subs;
-      if (works) {
-        const int g = h0 + h, b = vld(in.b);
-        if (before < kRowTurns) {  // ---- the first chunk of a piece: its queries
-          const int pos = vld(in.pos);
-          const __nv_bfloat16* x = a.q + (static_cast<long long>(b) * a.Hq + g * a.G) * D;
-          const int third = q8 - 4;  // the query whose third term the row holds (not kWide)
-          const bool has = q8 < a.G, more = !kWide && third >= 0 && third < a.G;
-          const uint32_t* xq = reinterpret_cast<const uint32_t*>(x + (has ? q8 : more ? third : 0) * D);
-          uint32_t raw[KS][2];
+      const TileInfo& in = info[ti];
+      const int b = vld(in.b), h0 = vld(in.h0), v0 = vld(in.v0), slot = vld(in.slot);
+      const bool opens = vld(in.opens), closes = vld(in.closes);
+      const unsigned bits = *const_cast<const volatile unsigned*>(&in.bits[grp]);
+      const int g = h0 + h;
+      if (opens) {
+        // ---- the piece's queries: four threads a row, over all terms (the last
+        // piece's products have read theirs: its last S^T is there)
+        const int pos = vld(in.pos);
+        const int qi = tid >> 2, part = tid & 3, qh = qi / kMaxGroup, qq = qi % kMaxGroup;
+        if (qh < a.heads && qq < a.G && h0 + qh < a.Hkv) {
+          const __nv_bfloat16* src =
+              a.q + (static_cast<long long>(b) * a.Hq + (h0 + qh) * a.G + qq) * D;
+          const uint32_t qs = smem_u32(smem + L::kQ);
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
+          for (int c = 0; c < HALF / 32; ++c) {  // pairs 8j .. 8j + 7
+            const int j = part * (HALF / 32) + c;
+            const uint4 l4 = __ldg(reinterpret_cast<const uint4*>(src + 8 * j));
+            const uint4 h4 = __ldg(reinterpret_cast<const uint4*>(src + HALF + 8 * j));
+            const uint32_t pl[4] = {l4.x, l4.y, l4.z, l4.w}, ph[4] = {h4.x, h4.y, h4.z, h4.w};
+            uint32_t yl[kTerms][4], yh[kTerms][4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) raw[k][e] = has || more ? __ldg(xq + 8 * k + 4 * e + t4) : 0u;
+            for (int k = 0; k < 4; ++k) {
+              const float2 fl = bf16x2_to_float2(pl[k]), fh = bf16x2_to_float2(ph[k]);
+              float2 u, w;
+              rope_pair(fl.x, fh.x, rope_cs_turns(f.t[8 * j + 2 * k], pos), u.x, w.x);
+              rope_pair(fl.y, fh.y, rope_cs_turns(f.t[8 * j + 2 * k + 1], pos), u.y, w.y);
 #pragma unroll
-          for (int k = 0; k < KS / 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = 16 * k + 8 * e + 2 * t4;
-              const float2 lo2 = bf16x2_to_float2(raw[k][e]), hi2 = bf16x2_to_float2(raw[k + KS / 2][e]);
-              float2 y, z;
-              rope_pair(lo2.x, hi2.x, rope_cs_turns(f.t[j], pos), y.x, z.x);
-              rope_pair(lo2.y, hi2.y, rope_cs_turns(f.t[j + 1], pos), y.y, z.y);
-              uint32_t ty[3], tz[3];
-#pragma unroll
-              for (int s = 0; s < 3; ++s) {
-                ty[s] = pack_bf16x2(y.x, y.y);
-                tz[s] = pack_bf16x2(z.x, z.y);
-                const float2 dy = bf16x2_to_float2(ty[s]), dz = bf16x2_to_float2(tz[s]);
-                y.x -= dy.x;
-                y.y -= dy.y;
-                z.x -= dz.x;
-                z.y -= dz.y;
-              }
-              qa[k][e] = more ? ty[2] : ty[0];
-              qa[k + KS / 2][e] = more ? tz[2] : tz[0];
-              qb[k][e] = more ? 0u : ty[1];
-              qb[k + KS / 2][e] = more ? 0u : tz[1];
-              if (kWide) {
-                qc[k][e] = ty[2];
-                qc[k + KS / 2][e] = tz[2];
-              }
-            }
-          m = -INFINITY;
-          l = 0.f;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-        }
-        const int groups = vld(in.groups), fresh = vld(in.fresh);
-        float* const lg = a.logits + ((static_cast<long long>(b) * a.Hkv + g) * a.G + q8) * a.cap +
-                          vld(in.v0) + 2 * t4;
-        const uint32_t ks = smem_u32(smem + st * L::kStage) + h * head_bytes + krow * 128;
-        bool cleared = false;
-        for (int i = sub; i < groups; i += a.subs) {
-          const unsigned bits = *reinterpret_cast<const volatile unsigned short*>(&in.bits[i]);
-          const uint32_t kg = ks + i * group_bytes, vg = kg + L::kHalfBytes;
-          float x4[4] = {0.f, 0.f, 0.f, 0.f};  // query q8, keys 2 t4, + 1, + 8, + 9
-          if (bits) {  // (uniform over the warp)
-            if (fresh >> 4 == i) {
-              write_row<D>(a, f, b, g, vld(in.pos), *const_cast<const volatile long long*>(&in.at),
-                           kg - krow * 128, vg - krow * 128, half_bytes, fresh & 15);
-              cleared = true;
-            }
-            // ---- S [query terms, 16 keys], even and odd steps apart (the
-            // products of one chain wait for one another)
-            float s0[2][4], s1[2][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s0[0][e] = s0[1][e] = s1[0][e] = s1[1][e] = 0.f;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              uint32_t kb[4];
-              ldsm_x4(kg + (k >> 2) * half_bytes +
-                          ((((2 * (k & 3) + kcol) ^ (lane & 7))) << 4), kb);
-              mma_bf16_16816(s0[k & 1], qa[k][0], qb[k][0], qa[k][1], qb[k][1], kb[0], kb[1]);
-              mma_bf16_16816(s1[k & 1], qa[k][0], qb[k][0], qa[k][1], qb[k][1], kb[2], kb[3]);
-              if (kWide) {
-                mma_bf16_16816(s0[k & 1], qc[k][0], 0u, qc[k][1], 0u, kb[0], kb[1]);
-                mma_bf16_16816(s1[k & 1], qc[k][0], 0u, qc[k][1], 0u, kb[2], kb[3]);
+              for (int s = 0; s < kTerms; ++s) {  // what the terms before leave, exactly
+                yl[s][k] = pack_bf16x2(u.x, u.y);
+                yh[s][k] = pack_bf16x2(w.x, w.y);
+                const float2 du = bf16x2_to_float2(yl[s][k]), dw = bf16x2_to_float2(yh[s][k]);
+                u.x -= du.x;
+                u.y -= du.y;
+                w.x -= dw.x;
+                w.y -= dw.y;
               }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s0[0][e] += s0[1][e];
-              s1[0][e] += s1[1][e];
+            for (int s = 0; s < kTerms; ++s) {
+              const int col = qh * kHeadColumns + s * kMaxGroup + qq;  // a row of 128 bytes
+              sts_u4(qs + sw128_offset(col, j), make_uint4(yl[s][0], yl[s][1], yl[s][2], yl[s][3]));
+              sts_u4(qs + (D == 128 ? L::kQHalf + sw128_offset(col, j) : sw128_offset(col, j + 4)),
+                     make_uint4(yh[s][0], yh[s][1], yh[s][2], yh[s][3]));
             }
-            x4[0] = s0[0][0] + s0[0][2];
-            x4[1] = s0[0][1] + s0[0][3];
-            x4[2] = s1[0][0] + s1[0][2];
-            x4[3] = s1[0][1] + s1[0][3];
-            if (!kWide) {  // (rows 4-7 hold third terms)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                x4[e] += __shfl_xor_sync(0xffffffffu, e < 2 ? s0[0][e] : s1[0][e - 2], 16);
-            }
-          }
-          const bool live = q8 < a.G;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = 2 * t4 + (e & 1) + 8 * (e >> 1);
-            x4[e] = live && (bits >> key & 1) ? x4[e] * a.scale_log2 : -INFINITY;
-          }
-          if (a.logits && live) {
-            *reinterpret_cast<float2*>(lg + i * 16) = make_float2(x4[0], x4[1]);
-            *reinterpret_cast<float2*>(lg + i * 16 + 8) = make_float2(x4[2], x4[3]);
-          }
-          if (!bits) continue;
-          float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          float alpha = 1.f;
-          if (top > m + 8.f) {  // (the maximum is renewed where it grows by more than 8)
-            alpha = exp2_approx(m - top);
-            m = top;
-          }
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
-            l *= alpha;
-            const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t4);
-            const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-              o[j][0] *= a0;
-              o[j][1] *= a1;
-              o[j][2] *= a0;
-              o[j][3] *= a1;
-            }
-          }
-          const float mr = m == -INFINITY ? 0.f : m;
-          float e4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) e4[e] = exp2_approx(x4[e] - mr);
-          l += (e4[0] + e4[1]) + (e4[2] + e4[3]);
-          if (bits != 0xffffu) {
-            // values of rows that are not seen may be anything, and 0 times them
-            // need not be 0
-            if (!(bits >> (lane & 15) & 1)) {
-              const uint32_t at = vg + ((lane & 15) - krow) * 128 + (lane >> 4) * 64;
-#pragma unroll
-              for (int k = 0; k < D / 64; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  sts_u4(at + k * half_bytes + e * 16, make_uint4(0u, 0u, 0u, 0u));
-            }
-            cleared = true;
-            __syncwarp();
-          }
-          // ---- O^T += V^T P^T: P^T as B has the layout of S
-          const uint32_t p0 = pack_bf16x2(e4[0], e4[1]), p1 = pack_bf16x2(e4[2], e4[3]);
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            uint32_t vt[4];
-            ldsm_x4_t(vg + (j >> 2) * half_bytes + (((2 * (j & 3) + kcol) ^ (lane & 7)) << 4), vt);
-            mma_bf16_16816(o[j], vt[0], vt[1], vt[2], vt[3], p0, p1);
           }
         }
-        if (cleared) fence_proxy_async_smem();  // before a later load of what was written
-        if (vld(in.after) < kRowTurns) {  // ---- the last chunk of the piece: its part
-          float sum = l;
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          const bool any = sum > 0.f || sum != sum;
-          const float inv = any ? 1.f / sum : 0.f;
-          const float i0 = __shfl_sync(0xffffffffu, inv, 8 * t4);
-          const float i1 = __shfl_sync(0xffffffffu, inv, 8 * t4 + 4);
-          const long long part =
-              ((static_cast<long long>(vld(in.slot)) * kRowTurns + turn) * a.subs + sub) * a.heads + h;
-          if (t4 == 0 && q8 < a.G) a.row_lse[part * a.G + q8] = any ? m + __log2f(sum) : -INFINITY;
-          float* out = a.row_o + part * a.G * D;
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kRQReady]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int q = 2 * t4 + e;
-            const float iq = e ? i1 : i0;
-            if (q < a.G)
-#pragma unroll
-              for (int j = 0; j < D / 16; ++j) {
-                out[q * D + 16 * j + q8] = iq == 0.f ? 0.f : o[j][e] * iq;
-                out[q * D + 16 * j + q8 + 8] = iq == 0.f ? 0.f : o[j][2 + e] * iq;
-              }
-          }
+        for (int q = 0; q < kMaxGroup; ++q) {
+          m[q] = -INFINITY;
+          l[q] = 0.f;
         }
       }
+      ok = wait(&bars[kRSFull0 + x], (n >> 1) & 1, kDevErrTimeoutSoftmax);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[32];
+      tmem_ld32(tS + x * kSBuffer + h * kHeadColumns + lane_off, r);
+      tmem_ld_wait();
+      tmem_reg_fence(r);
+      const bool seen = bits >> lane & 1;
+      float s[kMaxGroup];
+#pragma unroll
+      for (int q = 0; q < kMaxGroup; ++q) {
+        const float v = __uint_as_float(r[q]) +
+                        (__uint_as_float(r[8 + q]) + __uint_as_float(r[16 + q]));
+        s[q] = seen ? v * a.scale_log2 : -INFINITY;
+      }
+      if (a.logits && g < a.Hkv) {
+        float* lg = a.logits + (static_cast<long long>(b) * a.Hkv + g) * a.G * a.cap + v0 +
+                    grp * 32 + lane;
+        if (v0 + grp * 32 + lane < a.cap)
+#pragma unroll
+          for (int q = 0; q < kMaxGroup; ++q)
+            if (q < a.G) lg[static_cast<long long>(q) * a.cap] = s[q];
+      }
+      // ---- maxima, renewed where they grow by more than 8 (the weights stay below
+      // 2^8): every O^T spans the lanes of all warps, so the factors are exchanged
+      bool grows = false;
+#pragma unroll
+      for (int q = 0; q < kMaxGroup; ++q) {
+        if (q >= a.G) break;
+        const float top = warp_max(s[q]);
+        if (top > m[q] + 8.f) {
+          const float alpha = exp2_approx(m[q] - top);
+          m[q] = top;
+          l[q] *= alpha;
+          if (lane == 0) factor[x][warp][q] = alpha;
+          grows = true;
+        } else if (lane == 0) {
+          factor[x][warp][q] = 1.f;
+        }
+      }
+      if (lane == 0) {
+        rescale[x][warp] = grows && !opens;
+        mbar_arrive(&bars[kRExchange]);
+      }
+      float p[kMaxGroup];
+#pragma unroll
+      for (int q = 0; q < kMaxGroup; ++q) {
+        p[q] = q < a.G ? exp2_approx(s[q] - (m[q] == -INFINITY ? 0.f : m[q])) : 0.f;
+        l[q] += q < a.G ? p[q] : 0.f;
+      }
+      // ---- weights as B: row q of 128 bytes, this key's two bytes
+      {
+        const uint32_t ps = smem_u32(smem + L::kP) + x * 4096 + warp * 1024;
+#pragma unroll
+        for (int q = 0; q < kMaxGroup; ++q)
+          sts_u16(ps + q * 128 + (((lane >> 3) ^ q) << 4) + (lane & 7) * 2,
+                  __bfloat16_as_ushort(__float2bfloat16_rn(p[q])));
+      }
+      if (bits != 0xffffffffu) {
+        // values of rows that are not seen may be anything, and 0 times them need
+        // not be 0
+        const int e = 2 * n + 1, sl = e % NS;
+        ok = wait(&bars[kRFull0 + sl], (e / NS) & 1, kDevErrTimeoutSoftmax);
+        if (!ok) break;
+        if (!seen) {
+          const uint32_t at = smem_u32(smem + sl * L::kTileBytes) + warp * 4096 + lane * 128;
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              sts_u4(at + k * 16384 + c * 16, make_uint4(0u, 0u, 0u, 0u));
+        }
+      }
+      ok = wait(&bars[kRExchange], exchanges & 1, kDevErrTimeoutSoftmax);
+      ++exchanges;
+      if (!ok) break;
+      int any = 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) any |= vld(rescale[x][w]);
+      if (any) {
+        // (the product before the last one is done: S^T of this tile came after it)
+        ok = wait(&bars[kRPvDone], (n - 1) & 1, kDevErrTimeoutSoftmax);
+        if (!ok) break;
+        tc_fence_after();
+        for (int w = 0; w < 4; ++w) {
+          if (!vld(rescale[x][w])) continue;
+          uint32_t o[16];
+          tmem_ld16(tO + w * 16 + lane_off, o);
+          tmem_ld_wait();
+          tmem_reg_fence16(o);
+#pragma unroll
+          for (int q = 0; q < kMaxGroup; ++q)
+            if (q < a.G)
+              o[q] = __float_as_uint(__uint_as_float(o[q]) *
+                                     *const_cast<const volatile float*>(&factor[x][w][q]));
+          tmem_st16(tO + w * 16 + lane_off, o);
+        }
+        tmem_st_wait();
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&bars[kRPFull0 + x]);
+      if (closes) {
+        // ---- the piece's parts: one of each warp, by all four (lane = dim)
+        float mine[kMaxGroup];
+#pragma unroll
+        for (int q = 0; q < kMaxGroup; ++q) {
+          float sum = l[q];
+#pragma unroll
+          for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+          mine[q] = sum;
+        }
+        // (this tile's factors are read: everyone has passed its exchange, and
+        // arrives here after it has read them)
+        __syncwarp();
+        if (lane == 0) {
+          const long long row = ((static_cast<long long>(slot) * a.groups + grp) * a.heads + h) * a.G;
+#pragma unroll
+          for (int q = 0; q < kMaxGroup; ++q) {
+            const bool some = mine[q] > 0.f || mine[q] != mine[q];
+            factor[x ^ 1][warp][q] = some ? 1.f / mine[q] : 0.f;
+            if (q < a.G && g < a.Hkv)
+              a.row_lse[row + q] = some ? m[q] + __log2f(mine[q]) : -INFINITY;
+          }
+          mbar_arrive(&bars[kRExchange]);
+        }
+        ok = wait(&bars[kRODone], pieces & 1, kDevErrTimeoutEpilogue) &&
+             wait(&bars[kRExchange], exchanges & 1, kDevErrTimeoutEpilogue);
+        ++exchanges;
+        ++pieces;
+        if (!ok) break;
+        tc_fence_after();
+        const int dim = warp * 32 + lane;
+        for (int w = 0; w < 4; ++w) {
+          const int wh = w % a.heads, wg = w / a.heads;
+          uint32_t o[16];
+          tmem_ld16(tO + w * 16 + lane_off, o);
+          tmem_ld_wait();
+          tmem_reg_fence16(o);
+          if (h0 + wh < a.Hkv && dim < D) {
+            float* out = a.row_o +
+                         ((static_cast<long long>(slot) * a.groups + wg) * a.heads + wh) * a.G * D +
+                         dim;
+#pragma unroll
+            for (int q = 0; q < kMaxGroup; ++q) {
+              const float inv = *const_cast<const volatile float*>(&factor[x ^ 1][w][q]);
+              if (q < a.G) out[q * D] = inv == 0.f ? 0.f : __uint_as_float(o[q]) * inv;
+            }
+          }
+        }
+        tc_fence_before();
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      if (lane == 0) mbar_arrive(&bars[kRInfoEmpty0 + ti]);
     }
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc(tmem, 256);
   // the last kernel waits for this one alone: it has waited for the cartridge's
   pdl_wait();
 }
@@ -971,45 +1069,85 @@ constexpr int kFinishThreads = 512;
 constexpr int kFinishParts = 32;                      // parts joined at a time
 constexpr int kFinishHeads = kRowHeads * kMaxGroup;   // most query heads of a block
 
-// Blocks (., heads, conversation), the heads a unit's or one: the parts' common
-// log-sum-exp, a warp per query head; then the first block the output, some
-// threads per column of four, the parts' weights and places settled before; the
-// others the rows' weights.
+// Blocks (., heads, conversation), the heads a unit's or one: the new token's
+// logits, a warp per query head, before what the other kernels leave is waited
+// for; then the parts' common log-sum-exp; then the first block the new row, the
+// output, some threads per column of four, the parts' weights and places settled
+// before, and the others the cached rows' weights.
 template <int D>
 __global__ void __launch_bounds__(kFinishThreads, 2)
-    step_finish_kernel(const __grid_constant__ StepArgs a) {
-  __shared__ float total[kFinishHeads];
+    step_finish_kernel(const __grid_constant__ StepArgs a, const __grid_constant__ Turns f) {
+  constexpr int HALF = D / 2;
+  __shared__ float fresh[kFinishHeads], total[kFinishHeads];
   __shared__ float4 acc[kFinishThreads];
   __shared__ float weight[kFinishHeads][kFinishParts];
   __shared__ const float4* place[kFinishHeads][kFinishParts];
-  pdl_wait();
   const int g0 = blockIdx.y * a.finish_heads, b = blockIdx.z;
   const int heads = min(a.finish_heads, a.Hkv - g0), nq = heads * a.G;  // query heads
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long start = __ldcg(a.starts + b), chunks = __ldcg(a.starts + a.B);
   const StepOf s = step_of(a, b);
   __nv_bfloat16* out = a.o + (static_cast<long long>(b) * a.Hq + g0 * a.G) * D;
   if (s.row < 0) {
     if (blockIdx.x == 0)
       for (int e = tid; e < nq * D; e += kFinishThreads) out[e] = __float2bfloat16_rn(0.f);
+    pdl_wait();
     return;
   }
   const int first = (static_cast<int>(blockIdx.x) - 1) * kFinishThreads;  // rows' blocks
-  if (first >= s.n * 16) return;
-  // ---- the parts of the private rows: those of the runs that hold the unit
-  const int unit = g0 / a.heads, all = chunks_of(a, s.n), per = kRowTurns * a.subs;
-  const long long chunk = (chunks + a.row_ctas - 1) / a.row_ctas;
-  const long long u0 = start + static_cast<long long>(unit) * all, u1 = u0 + all;
-  const int c0 = static_cast<int>(u0 / chunk), c1 = static_cast<int>((u1 - 1) / chunk);
-  const int n_row = (c1 - c0 + 1) * per;
-  auto row_part = [&](int q, int i) -> long long {  // its row, or -1
-    const int c = c0 + i / per, k = i % per;
-    // (warps whose turn is beyond the piece's chunks had none)
-    if (k / a.subs >= min(u1, (c + 1) * chunk) - max(u0, c * chunk)) return -1;
+  if (first >= s.n * 32) {
+    pdl_wait();
+    return;
+  }
+  // ---- the new token: its key as the cache holds it, its logits
+  const long long from = (static_cast<long long>(b) * a.Hkv + g0) * D;
+  {
+    const int pos = position_of(a, b, s.row);
+    float2 cs[HALF / 32];
+#pragma unroll
+    for (int e = 0; e < HALF / 32; ++e) cs[e] = rope_cs_turns(f.t[lane + 32 * e], pos);
+    const long long at = ((static_cast<long long>(s.page) << a.pt.page_log2) +
+                          (s.row & ((1 << a.pt.page_log2) - 1))) * a.Hkv * D + g0 * D;
+    for (int q = warp; q < nq; q += kFinishThreads / 32) {
+      const int h = q / a.G;
+      const __nv_bfloat16* k = a.k_new + from + h * D;
+      const __nv_bfloat16* x = a.q + (static_cast<long long>(b) * a.Hq + g0 * a.G + q) * D;
+      float dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < HALF / 32; ++e) {
+        const int j = lane + 32 * e;
+        float k0, k1, q0, q1;
+        rope_pair(__bfloat162float(k[j]), __bfloat162float(k[j + HALF]), cs[e], k0, k1);
+        rope_pair(__bfloat162float(x[j]), __bfloat162float(x[j + HALF]), cs[e], q0, q1);
+        const __nv_bfloat16 z0 = __float2bfloat16_rn(k0), z1 = __float2bfloat16_rn(k1);
+        if (blockIdx.x == 0 && q % a.G == 0) {
+          a.k_pages[at + h * D + j] = z0;
+          a.k_pages[at + h * D + j + HALF] = z1;
+        }
+        dot = fmaf(q0, __bfloat162float(z0), fmaf(q1, __bfloat162float(z1), dot));
+      }
+#pragma unroll
+      for (int w = 16; w; w >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, w);
+      if (lane == 0) fresh[q] = dot * a.scale_log2;
+    }
+    if (blockIdx.x == 0 && tid < heads * (D / 8))
+      *reinterpret_cast<uint4*>(a.v_pages + at + tid * 8) =
+          __ldg(reinterpret_cast<const uint4*>(a.v_new + from + tid * 8));
+  }
+  pdl_wait();
+  const long long start = __ldcg(a.starts + b), tiles = __ldcg(a.starts + a.B);
+  // ---- the parts of the cached rows: those of the runs that hold the unit
+  const int unit = g0 / a.heads, all = tiles_of(a, s.n);
+  const long long chunk = max((tiles + a.row_ctas - 1) / a.row_ctas, 1ll);
+  const long long u0 = start + static_cast<long long>(unit) * all;
+  const int c0 = static_cast<int>(u0 / chunk);
+  const int c1 = all > 0 ? static_cast<int>((u0 + all - 1) / chunk) : c0 - 1;
+  const int n_row = (c1 - c0 + 1) * a.groups;
+  auto row_part = [&](int q, int i) -> long long {
+    const int c = c0 + i / a.groups, k = i % a.groups;
     const long long slot = c0 == c1 ? 2 * a.row_ctas + static_cast<long long>(b) * a.units + unit
                            : c > c0 || u0 == c0 * chunk ? 2 * c
                                                         : 2 * c + 1;
-    return ((slot * per + k) * a.heads + g0 - unit * a.heads) * a.G + q;
+    return ((slot * a.groups + k) * a.heads + g0 - unit * a.heads) * a.G + q;
   };
   // ---- and of the cartridge, by the tile that holds the query's row
   auto cart_row = [&](int q) { return b * a.G + q % a.G; };
@@ -1020,18 +1158,15 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
     return n_row + (u + a.key_tiles - 1) / a.cart_chunk - u / a.cart_chunk + 1;
   };
   auto lse_of = [&](int q, int i) {
-    if (i >= n_row)
-      return __ldcg(a.cart_lse +
-                    (static_cast<long long>(cart_seg(q)) * a.cart_parts + i - n_row) * kTile +
-                    cart_row(q) % kTile);
-    const long long part = row_part(q, i);
-    return part < 0 ? -INFINITY : __ldcg(a.row_lse + part);
+    return i < n_row ? __ldcg(a.row_lse + row_part(q, i))
+                     : __ldcg(a.cart_lse + (static_cast<long long>(cart_seg(q)) * a.cart_parts + i -
+                                            n_row) * kTile + cart_row(q) % kTile);
   };
   for (int q = warp; q < nq; q += kFinishThreads / 32) {
     const int n = parts_of(q);
     float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < n; i += 32) {
-      const float x = lse_of(q, i), top = fmaxf(m, x);
+    for (int i = lane; i <= n; i += 32) {
+      const float x = i < n ? lse_of(q, i) : fresh[q], top = fmaxf(m, x);
       if (top != -INFINITY || x != x) {
         l = l * exp2_approx(m - top) + exp2_approx(x - top);
         m = top;
@@ -1049,7 +1184,14 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
     if (lane == 0) total[q] = l == 0.f ? INFINITY : m + __log2f(l);
   }
   __syncthreads();
+  const long long bg = static_cast<long long>(b) * a.Hkv + g0;
   if (blockIdx.x == 0) {
+    if (a.weights && tid < heads) {
+      float x = 0.f;
+      for (int hh = 0; hh < a.G; ++hh)
+        x += exp2_approx(fresh[tid * a.G + hh] - total[tid * a.G + hh]);
+      a.weights[(bg + tid) * a.weight_rows + s.row] = x;
+    }
     int most = 0;
     for (int q = 0; q < nq; ++q) most = max(most, parts_of(q));
     const int cols = nq * (D / 4), each = max(kFinishThreads / cols, 1);
@@ -1067,7 +1209,7 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
             if (i >= parts_of(qq)) continue;
             weight[qq][k] = exp2_approx(lse_of(qq, i) - total[qq]);
             place[qq][k] = reinterpret_cast<const float4*>(
-                i < n_row ? a.row_o + max(row_part(qq, i), 0ll) * D
+                i < n_row ? a.row_o + row_part(qq, i) * D
                           : a.cart_o + ((static_cast<long long>(cart_seg(qq)) * a.cart_parts + i -
                                          n_row) * (D / 4) * kTile + cart_row(qq) % kTile) * 4);
           }
@@ -1099,21 +1241,31 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
             x.w += v.w;
           }
       }
-      if (mine && turn == 0)
+      if (mine && turn == 0) {
+        const float w = exp2_approx(fresh[q] - total[q]);  // of the new token
+        const uint2 v2 =
+            __ldg(reinterpret_cast<const uint2*>(a.v_new + from + q / a.G * D + 4 * j));
+        const float2 lo = bf16x2_to_float2(v2.x), hi = bf16x2_to_float2(v2.y);
+        if (w != 0.f) {
+          x.x = fmaf(w, lo.x, x.x);
+          x.y = fmaf(w, lo.y, x.y);
+          x.z = fmaf(w, hi.x, x.z);
+          x.w = fmaf(w, hi.y, x.w);
+        }
         *reinterpret_cast<uint2*>(out + q * D + 4 * j) =
             make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+      }
     }
     return;
   }
-  const long long bg = static_cast<long long>(b) * a.Hkv + g0;
   const int step = (gridDim.x - 1) * kFinishThreads;
-  for (int v = first + tid; v < s.n * 16; v += step) {
-    const int r = s.group(v >> 4) * 16 + (v & 15);
+  for (int v = first + tid; v < s.n * 32; v += step) {
+    const int r = s.group(v >> 5) * 32 + (v & 31);
     if (!s.sees(r)) continue;
     for (int h = 0; h < heads; ++h) {
       const float* lg = a.logits + (bg + h) * a.G * a.cap + v;
       float* w = a.weights + (bg + h) * a.weight_rows + r;
-      const float old = r < s.row ? *w : 0.f;
+      const float old = *w;
       float x = 0.f;
 #pragma unroll 4
       for (int hh = 0; hh < a.G; ++hh)
@@ -1126,7 +1278,7 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
 struct StepWs {
   size_t cart_o, cart_lse, row_o, row_lse, starts, logits, total;
   int row_tiles, key_tiles, cart_chunk, cart_parts, cart_ctas;
-  int heads, units, subs, stage_groups, row_ctas;
+  int heads, units, groups, row_ctas;
 };
 // (every size goes by the GPU's multiprocessors: the grids do)
 StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
@@ -1146,19 +1298,15 @@ StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
     w.cart_ctas = (tiles + w.cart_chunk - 1) / w.cart_chunk;
     w.cart_parts = (w.key_tiles + w.cart_chunk - 1) / w.cart_chunk + 1;
   }
-  w.units = (Hkv + kRowHeads - 1) / kRowHeads;
-  w.heads = (Hkv + w.units - 1) / w.units;
+  w.heads = Hkv > 2 ? 4 : Hkv;  // (a unit's heads beyond the last one are not read)
   w.units = (Hkv + w.heads - 1) / w.heads;
-  w.subs = kRowHeads / w.heads;
-  w.stage_groups = w.subs * (d == 64 ? 2 : 1);
-  // one CTA per SM beside the cartridge's, two without
-  w.row_ctas = p > 0 ? sms : 2 * sms;
+  w.groups = kRowHeads / w.heads;
+  w.row_ctas = sms;
   const size_t segments = static_cast<size_t>(Hkv) * w.row_tiles;
   w.cart_o = take(segments * w.cart_parts * kTile * d * 4);
   w.cart_lse = take(segments * w.cart_parts * kTile * 4);
   const size_t parts =
-      (2 * static_cast<size_t>(w.row_ctas) + static_cast<size_t>(B) * w.units) * kRowTurns *
-      w.subs * w.heads;
+      (2 * static_cast<size_t>(w.row_ctas) + static_cast<size_t>(B) * w.units) * kRowHeads;
   w.row_o = take(parts * G * d * 4);
   w.row_lse = take(parts * G * 4);
   w.starts = take((static_cast<size_t>(B) + 1) * 8);
@@ -1208,20 +1356,19 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
   const uint64_t dims[4] = {D, page_rows, static_cast<uint64_t>(a.Hkv),
                             static_cast<uint64_t>(a.pt.n_pages)};
   const uint64_t strides[3] = {row, D * 2, row * page_rows};
-  const uint32_t box[4] = {64, 16, static_cast<uint32_t>(a.heads), 1};
+  const bool small = page_rows == 16;
+  const uint32_t box[4] = {64, small ? 16u : 32u, small ? 1u : static_cast<uint32_t>(a.heads), 1};
   RowMaps maps;
   if (!encode_bf16_map4(&maps.k, a.k_pages, dims, strides, box) ||
       !encode_bf16_map4(&maps.v, a.v_pages, dims, strides, box))
     return cudaErrorInvalidValue;
-  const bool wide = a.G > 4;
-  e = wide ? set_shared_once<step_rows_kernel<D, true>>(L::kAlloc)
-           : set_shared_once<step_rows_kernel<D, false>>(L::kAlloc);
+  e = set_shared_once<step_rows_kernel<D>>(L::kAlloc);
   if (e != cudaSuccess) return e;
-  auto* rows = wide ? step_rows_kernel<D, true> : step_rows_kernel<D, false>;
   if (w.cart_ctas > 0) {
-    e = launch_dependent(rows, dim3(w.row_ctas), dim3(kRowThreads), L::kAlloc, st, maps, a, f);
+    e = launch_dependent(step_rows_kernel<D>, dim3(w.row_ctas), dim3(kRowThreads), L::kAlloc, st,
+                         maps, a, f);
   } else {
-    rows<<<w.row_ctas, kRowThreads, L::kAlloc, st>>>(maps, a, f);
+    step_rows_kernel<D><<<w.row_ctas, kRowThreads, L::kAlloc, st>>>(maps, a, f);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
@@ -1236,7 +1383,7 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
     blocks += std::max(1, std::min((a.cap + kFinishThreads - 1) / kFinishThreads,
                                    4 * sm_count() / std::max(1, a.B * across)));
   return launch_dependent(step_finish_kernel<D>, dim3(blocks, across, a.B), dim3(kFinishThreads), 0,
-                          st, last);
+                          st, last, f);
 }
 
 }  // namespace
@@ -1304,8 +1451,7 @@ int cart_attn_decode_paged(int B, int window, int sinks, int Hq, int Hkv, int d,
   a.cart_lse = reinterpret_cast<float*>(ws + w.cart_lse);
   a.heads = w.heads;
   a.units = w.units;
-  a.subs = w.subs;
-  a.stage_groups = w.stage_groups;
+  a.groups = w.groups;
   a.row_ctas = w.row_ctas;
   a.starts = reinterpret_cast<long long*>(ws + w.starts);
   a.row_o = reinterpret_cast<float*>(ws + w.row_o);
