@@ -2,7 +2,7 @@
 // private rows, with the attention weights that the rows get added up
 // (cart_attn_decode_paged).
 //
-// Three kernels, chained by programmatic dependent launch; the first two run at
+// Four kernels, chained by programmatic dependent launch; the first two run at
 // once, one CTA of each per SM:
 //   cart    the B * G stacked query rows of each kv head against the cartridge,
 //           as tcgen05 products: 128 rows and 64 keys at a time, Q resident as
@@ -18,10 +18,9 @@
 //           and an O^T of its own.  K and V tiles come through one ring of 96 KB.
 //           All conversations' rows, one after the other, are cut into equal
 //           runs, one per CTA.
-//   finish  the new token: its rotated key and its value to its row, its logits;
-//           joins them and a (conversation, kv head)'s parts by their log-sum-
-//           exps, and adds exp2(logit - log-sum-exp) of the group's heads to each
-//           row's weight.
+//   join    the new token: its rotated key and its value to its row, its logits;
+//           joins them and a (conversation, kv head)'s parts by their log-sum-exps.
+//   weights adds exp2(logit - log-sum-exp) of the group's heads to each row's.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -74,10 +73,11 @@ struct StepArgs {
   // ---- rows: heads of a unit (of which a conversation has `units`), 32-row
   // groups of a tile (heads * groups is 4), CTAs
   int heads, units, groups, row_ctas;
-  int finish_heads;          // heads of a block of the last kernel: `heads` or 1
+  int join_heads;            // heads of a block of the joining kernel: `heads` or 1
   long long* starts;         // [B + 1]: chunks of a unit before each conversation's
   float *row_o, *row_lse;    // [slots, groups, heads, G, d], [.., G]
   int cap;                   // most private rows
+  float* total;              // [B, Hq] log2 log-sum-exps over everything
   float* logits;             // [B, Hkv, G, cap], log2 domain, by the order of groups seen
 };
 
@@ -85,21 +85,19 @@ struct Turns {
   float2 t[kMaxHeadDim / 2];
 };
 
-// The step of conversation b: the row of its new token (-1: idle, or the row
-// has no page), that row's page; the cached rows it sees: those below `low` and
-// from `high` to row - 1, in n groups of 32: those below g_low and from g_high on.
+// The step of conversation b: the row of its new token (-1: idle, or its table
+// has no place for it); the cached rows that it sees: those below `low` and from
+// `high` to row - 1, in n groups of 32: those below g_low and from g_high on.
+// (Whether the row has a page is looked up where the token is taken.)
 struct StepOf {
-  int row, page, low, high, g_low, g_high, n;
-  bool lost;  // not idle, but without a page
+  int row, low, high, g_low, g_high, n;
   __device__ __forceinline__ int group(int i) const { return i < g_low ? i : i - g_low + g_high; }
   __device__ __forceinline__ bool sees(int r) const { return r < row && (r < low || r >= high); }
 };
 __device__ __forceinline__ StepOf step_of(const StepArgs& a, int b) {
   StepOf s;
   const int len = held_rows(a.pt, b);
-  s.page = len < 0 ? -1 : page_of(a.pt, b, len);
-  s.lost = len >= 0 && s.page < 0;
-  s.row = s.page < 0 ? -1 : len;
+  s.row = len < a.cap ? len : -1;
   s.high = a.window > 0 ? max(s.row - a.window + 1, 0) : 0;
   s.low = min(max(a.sinks - a.p, 0), s.high);
   s.g_high = s.high >> 5;
@@ -121,7 +119,8 @@ struct CartSmem {
   static constexpr int kQ = 0;                 // two terms
   static constexpr int kK = kQ + 2 * kQBytes;
   static constexpr int kV = kK + kKBytes;
-  static constexpr int kAlloc = kV + kKBytes;  // starts 1024-aligned (checked at entry)
+  static constexpr int kShared = kV + kKBytes;  // a CartShared
+  static constexpr int kAlloc = kShared + 128;  // starts 1024-aligned (checked at entry)
 };
 
 enum CartBar {
@@ -137,6 +136,14 @@ enum CartBar {
   kCDrain,
   kCBars
 };
+
+// (no static shared memory: it would take 1 KB before aligned tiles)
+struct CartShared {
+  uint64_t bars[kCBars];
+  uint32_t tmem;
+  int abort, first;
+};
+static_assert(sizeof(CartShared) <= 128, "cart barrier area");
 
 struct CartMaps {
   CUtensorMap k, v;
@@ -155,26 +162,25 @@ __global__ void __maxnreg__(128)
     if (threadIdx.x == 0) atomicOr(a.status, kDevErrSmemLayout);
     return;
   }
-  __shared__ uint64_t bars[kCBars];
-  __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, first_s;
+  CartShared& sh = *reinterpret_cast<CartShared*>(smem + L::kShared);
+  uint64_t* const bars = sh.bars;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t abort_s = smem_u32(&abort_flag);
+  const uint32_t abort_s = smem_u32(&sh.abort);
   pdl_release();  // (the rows run beside this kernel)
   if (threadIdx.x == 0) {
-    abort_flag = 0;
+    sh.abort = 0;
     for (int s = 0; s < kCBars; ++s)
       mbar_init(&bars[s], s == kCPFull0 || s == kCPFull0 + 1 ? 128 : 1);
     fence_mbar_init();
   }
   if (warp == 5) {
-    tmem_alloc(&tmem_slot, 256);
+    tmem_alloc(&sh.tmem, 256);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot, tO = tmem, tS = tmem + 128;
+  const uint32_t tmem = sh.tmem, tO = tmem, tS = tmem + 128;
   const int total = a.Hkv * a.row_tiles * a.key_tiles;
   const int lo = min(blockIdx.x * a.cart_chunk, total), hi = min(lo + a.cart_chunk, total);
   const int R = a.B * a.G;
@@ -185,7 +191,7 @@ __global__ void __maxnreg__(128)
     const int t1 = min(t0 + hi - u, a.key_tiles);
     const int g = seg / a.row_tiles, row0 = (seg - g * a.row_tiles) * kTile;
     // ---- the tile's queries, rotated, as two terms; what they see
-    if (threadIdx.x == 0) first_s = 0x7fffffff;
+    if (threadIdx.x == 0) sh.first = 0x7fffffff;
     __syncthreads();
     const int row = threadIdx.x, R0 = row0 + row;
     int first = 0x7fffffff;  // first key in the row's window
@@ -237,12 +243,12 @@ __global__ void __maxnreg__(128)
       fence_proxy_async_smem();
       if (a.window > 0) {
         const int w = __reduce_min_sync(0xffffffffu, first);
-        if (lane == 0) atomicMin(&first_s, w);
+        if (lane == 0) atomicMin(&sh.first, w);
       }
     }
     __syncthreads();
     // tiles that some row sees
-    const int low = a.window > 0 ? first_s : 0;
+    const int low = a.window > 0 ? *const_cast<volatile int*>(&sh.first) : 0;
     auto seen = [&](int t) { return t * kCartKeys < a.sinks || (t + 1) * kCartKeys > low; };
     int n = 0;
     for (int t = t0; t < t1; ++t) n += seen(t);
@@ -501,10 +507,9 @@ constexpr int kTileInfos = 4;
 
 // What the roles know of a tile: conversation, first head, first key's number
 // among the groups seen, times 32; whether it opens and closes a piece, the slot
-// of the piece's parts, the token's position; the rows of each group that are
-// there and seen.
+// of the piece's parts; the rows of each group that are there and seen.
 struct TileInfo {
-  int b, h0, v0, opens, closes, slot, pos;
+  int b, h0, v0, opens, closes, slot;
   unsigned bits[kRowHeads];
 };
 
@@ -513,10 +518,11 @@ struct RowSmem {
   static constexpr int kTileBytes = kTile * D * 2;          // a K or V tile
   static constexpr int kSlots = 3 * 128 / D;                // of the ring
   static constexpr int kQHalf = kRowHeads * kHeadColumns * 128;  // 64 dims of all columns
-  static constexpr int kP = kSlots * kTileBytes;  // weights: two buffers, 1 KB a warp
-  // (a product reads 16 rows of weights, eight of them behind the warp's)
-  static constexpr int kQ = kP + 2 * 4096;
-  static constexpr int kAlloc = kQ + (D / 64) * kQHalf;  // starts 1024-aligned
+  static constexpr int kP = kSlots * kTileBytes;  // weights: two buffers, 1 KB for two warps
+  // (a product reads 16 rows of weights, eight of them behind the warps')
+  static constexpr int kQ = kP + 2 * 2048;
+  static constexpr int kShared = kQ + (D / 64) * kQHalf;  // a RowShared
+  static constexpr int kAlloc = kShared + 3584;           // starts 1024-aligned
 };
 
 enum RowBar {
@@ -533,6 +539,18 @@ enum RowBar {
   kRDrain,
   kRBars
 };
+
+struct RowShared {
+  float2 angles[kTileInfos][kMaxHeadDim / 2];  // of a piece, beside its first tile's info
+  uint64_t bars[kRBars];
+  long long scan[kRowThreads / 32], run_off;
+  TileInfo info[kTileInfos];
+  float factor[2][4][kMaxGroup];  // what each warp's O^T is multiplied by
+  int rescale[2][4];
+  uint32_t tmem;
+  int run_b, abort;
+};
+static_assert(sizeof(RowShared) <= 3584, "rows barrier area");
 
 struct RowMaps {
   CUtensorMap k, v;  // (d, page_rows, Hkv, pages), box 64 x 32 x heads, or 64 x 16 x 1
@@ -562,17 +580,15 @@ __global__ void __maxnreg__(128)
     if (threadIdx.x == 0) atomicOr(a.status, kDevErrSmemLayout);
     return;
   }
-  __shared__ uint64_t bars[kRBars];
-  __shared__ TileInfo info[kTileInfos];
-  __shared__ float factor[2][4][kMaxGroup];  // what each warp's O^T is multiplied by
-  __shared__ int rescale[2][4];
-  __shared__ long long scan[kRowThreads / 32], run_off;
-  __shared__ uint32_t tmem_slot;
-  __shared__ int run_b, abort_flag;
+  RowShared& sh = *reinterpret_cast<RowShared*>(smem + L::kShared);
+  uint64_t* const bars = sh.bars;
+  TileInfo* const info = sh.info;
+  auto& factor = sh.factor;
+  auto& rescale = sh.rescale;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t abort_s = smem_u32(&abort_flag);
+  const uint32_t abort_s = smem_u32(&sh.abort);
   if (tid == 0) {
-    abort_flag = 0;
+    sh.abort = 0;
     for (int s = 0; s < kRBars; ++s)
       mbar_init(&bars[s], s == kRQReady || s == kRPFull0 || s == kRPFull0 + 1 ? 128
                           : s >= kRInfoEmpty0 && s < kRInfoEmpty0 + kTileInfos ? 5
@@ -581,7 +597,7 @@ __global__ void __maxnreg__(128)
     fence_mbar_init();
   }
   if (warp == 5) {
-    tmem_alloc(&tmem_slot, 256);
+    tmem_alloc(&sh.tmem, 256);
     tmem_relinquish();
   }
   // ---- the tiles of all conversations, and this CTA's run of them
@@ -589,9 +605,7 @@ __global__ void __maxnreg__(128)
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    const StepOf s = step_of(a, b);
-    if (s.lost && blockIdx.x == 0) atomicOr(a.status, kDevErrNoPage);
-    mine += static_cast<long long>(tiles_of(a, s.n)) * a.units;
+    mine += static_cast<long long>(tiles_of(a, step_of(a, b).n)) * a.units;
   }
   long long x = mine;
 #pragma unroll
@@ -599,16 +613,16 @@ __global__ void __maxnreg__(128)
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) scan[warp] = x;
+  if (lane == 31) sh.scan[warp] = x;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = sh.tmem;
   long long total = 0, start = x - mine;
 #pragma unroll
   for (int w = 0; w < kRowThreads / 32; ++w) {
-    start += w < warp ? scan[w] : 0;
-    total += scan[w];
+    start += w < warp ? sh.scan[w] : 0;
+    total += sh.scan[w];
   }
   const long long chunk = (total + a.row_ctas - 1) / a.row_ctas;
   const long long lo = min(blockIdx.x * chunk, total), hi = min(lo + chunk, total);
@@ -620,8 +634,8 @@ __global__ void __maxnreg__(128)
       if (lo < at + n) break;
       at += n;
     }
-    run_b = b;
-    run_off = lo - at;
+    sh.run_b = b;
+    sh.run_off = lo - at;
   }
   if (blockIdx.x == 0) {  // for the last kernel
     long long at = start;
@@ -642,15 +656,16 @@ __global__ void __maxnreg__(128)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_s, a.status, kDevErrTimeoutTma));
     };
-    int b = run_b, n = 0, loads = 0;  // tiles handed on, ring slots filled
+    int b = vld(sh.run_b), n = 0, loads = 0;  // tiles handed on, ring slots filled
     bool ok = n_tiles > 0;
     int unit = 0, t0 = 0;
     StepOf s{};
     if (ok) {
       s = step_of(a, b);
       const int per_unit = tiles_of(a, s.n);
-      unit = static_cast<int>(run_off / per_unit);
-      t0 = static_cast<int>(run_off - static_cast<long long>(unit) * per_unit);
+      const long long off0 = *const_cast<const volatile long long*>(&sh.run_off);
+      unit = static_cast<int>(off0 / per_unit);
+      t0 = static_cast<int>(off0 - static_cast<long long>(unit) * per_unit);
     }
     // boxes: a group's 32 rows of all heads, or, in pages of 16, 16 rows of one
     const bool small = a.pt.page_log2 == 4;
@@ -705,6 +720,9 @@ __global__ void __maxnreg__(128)
           if (!ok) break;
         }
         TileInfo& o = info[ti];
+        if (t == t0)  // the piece's angles
+#pragma unroll 1
+          for (int e = lane; e < HALF; e += 32) sh.angles[ti][e] = rope_cs_turns(f.t[e], pos);
         if (lane < lanes && (!small || !(lane & 1))) o.bits[group_of] = bits;
         if (lane == 0) {
           o.b = b;
@@ -713,7 +731,6 @@ __global__ void __maxnreg__(128)
           o.opens = t == t0;
           o.closes = t + 1 == t1;
           o.slot = slot;
-          o.pos = pos;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kRInfoFull0 + ti]);
@@ -816,13 +833,13 @@ __global__ void __maxnreg__(128)
       ok = wait(&bars[kRFull0 + sl], (e / NS) & 1) && wait(&bars[kRPFull0 + (n & 1)], (n >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const uint64_t dv = desc_add(dV, sl * L::kTileBytes), dp = desc_add(dP, (n & 1) * 4096);
+      const uint64_t dv = desc_add(dV, sl * L::kTileBytes), dp = desc_add(dP, (n & 1) * 2048);
 #pragma unroll
       for (int w = 0; w < 4; ++w)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           umma_bf16_ss_w(tO + w * 16, desc_add(dv, w * 4096 + k * 2048),
-                         desc_add(dp, w * 1024 + k * 32), idO, (now & 1) && k == 0 ? 0u : 1u);
+                         desc_add(dp, (w >> 1) * 1024 + (w & 1) * 64 + k * 32), idO, (now & 1) && k == 0 ? 0u : 1u);
       umma_commit_w(&bars[kREmpty0 + sl]);
       umma_commit_w(&bars[kRPvDone]);
       if (now & 2) umma_commit_w(&bars[kRODone]);
@@ -841,6 +858,57 @@ __global__ void __maxnreg__(128)
     bool ok = true;
     float m[kMaxGroup], l[kMaxGroup];  // the warp's maxima, the thread's sums
     int exchanges = 0, pieces = 0;
+    // A piece's queries: four threads a row, over all terms.  (The products of the
+    // piece before have read theirs: its last S^T is there.)
+    auto stage_queries = [&](int ti) {
+      const int b = vld(info[ti].b), h0 = vld(info[ti].h0);
+      const int qi = tid >> 2, part = tid & 3, qh = qi / kMaxGroup, qq = qi % kMaxGroup;
+      if (qh < a.heads && qq < a.G && h0 + qh < a.Hkv) {
+        const __nv_bfloat16* src =
+            a.q + (static_cast<long long>(b) * a.Hq + (h0 + qh) * a.G + qq) * D;
+        const uint32_t qs = smem_u32(smem + L::kQ);
+        uint4 l4[HALF / 32], h4[HALF / 32];
+#pragma unroll
+        for (int c = 0; c < HALF / 32; ++c) {  // pairs 8j .. 8j + 7
+          const int j = part * (HALF / 32) + c;
+          l4[c] = __ldg(reinterpret_cast<const uint4*>(src + 8 * j));
+          h4[c] = __ldg(reinterpret_cast<const uint4*>(src + HALF + 8 * j));
+        }
+#pragma unroll
+        for (int c = 0; c < HALF / 32; ++c) {
+          const int j = part * (HALF / 32) + c;
+          const uint32_t pl[4] = {l4[c].x, l4[c].y, l4[c].z, l4[c].w};
+          const uint32_t ph[4] = {h4[c].x, h4[c].y, h4[c].z, h4[c].w};
+          uint32_t yl[kTerms][4], yh[kTerms][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 fl = bf16x2_to_float2(pl[k]), fh = bf16x2_to_float2(ph[k]);
+            float2 u, w;
+            rope_pair(fl.x, fh.x, sh.angles[ti][8 * j + 2 * k], u.x, w.x);
+            rope_pair(fl.y, fh.y, sh.angles[ti][8 * j + 2 * k + 1], u.y, w.y);
+#pragma unroll
+            for (int s = 0; s < kTerms; ++s) {  // what the terms before leave, exactly
+              yl[s][k] = pack_bf16x2(u.x, u.y);
+              yh[s][k] = pack_bf16x2(w.x, w.y);
+              const float2 du = bf16x2_to_float2(yl[s][k]), dw = bf16x2_to_float2(yh[s][k]);
+              u.x -= du.x;
+              u.y -= du.y;
+              w.x -= dw.x;
+              w.y -= dw.y;
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < kTerms; ++s) {
+            const int col = qh * kHeadColumns + s * kMaxGroup + qq;  // a row of 128 bytes
+            sts_u4(qs + sw128_offset(col, j), make_uint4(yl[s][0], yl[s][1], yl[s][2], yl[s][3]));
+            sts_u4(qs + (D == 128 ? L::kQHalf + sw128_offset(col, j) : sw128_offset(col, j + 4)),
+                   make_uint4(yh[s][0], yh[s][1], yh[s][2], yh[s][3]));
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[kRQReady]);
+    };
     for (int n = 0; n < n_tiles && ok; ++n) {
       const int ti = n % kTileInfos, x = n & 1;
       ok = wait(&bars[kRInfoFull0 + ti], (n / kTileInfos) & 1, kDevErrTimeoutSoftmax);
@@ -851,49 +919,7 @@ __global__ void __maxnreg__(128)
       const unsigned bits = *const_cast<const volatile unsigned*>(&in.bits[grp]);
       const int g = h0 + h;
       if (opens) {
-        // ---- the piece's queries: four threads a row, over all terms (the last
-        // piece's products have read theirs: its last S^T is there)
-        const int pos = vld(in.pos);
-        const int qi = tid >> 2, part = tid & 3, qh = qi / kMaxGroup, qq = qi % kMaxGroup;
-        if (qh < a.heads && qq < a.G && h0 + qh < a.Hkv) {
-          const __nv_bfloat16* src =
-              a.q + (static_cast<long long>(b) * a.Hq + (h0 + qh) * a.G + qq) * D;
-          const uint32_t qs = smem_u32(smem + L::kQ);
-#pragma unroll
-          for (int c = 0; c < HALF / 32; ++c) {  // pairs 8j .. 8j + 7
-            const int j = part * (HALF / 32) + c;
-            const uint4 l4 = __ldg(reinterpret_cast<const uint4*>(src + 8 * j));
-            const uint4 h4 = __ldg(reinterpret_cast<const uint4*>(src + HALF + 8 * j));
-            const uint32_t pl[4] = {l4.x, l4.y, l4.z, l4.w}, ph[4] = {h4.x, h4.y, h4.z, h4.w};
-            uint32_t yl[kTerms][4], yh[kTerms][4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 fl = bf16x2_to_float2(pl[k]), fh = bf16x2_to_float2(ph[k]);
-              float2 u, w;
-              rope_pair(fl.x, fh.x, rope_cs_turns(f.t[8 * j + 2 * k], pos), u.x, w.x);
-              rope_pair(fl.y, fh.y, rope_cs_turns(f.t[8 * j + 2 * k + 1], pos), u.y, w.y);
-#pragma unroll
-              for (int s = 0; s < kTerms; ++s) {  // what the terms before leave, exactly
-                yl[s][k] = pack_bf16x2(u.x, u.y);
-                yh[s][k] = pack_bf16x2(w.x, w.y);
-                const float2 du = bf16x2_to_float2(yl[s][k]), dw = bf16x2_to_float2(yh[s][k]);
-                u.x -= du.x;
-                u.y -= du.y;
-                w.x -= dw.x;
-                w.y -= dw.y;
-              }
-            }
-#pragma unroll
-            for (int s = 0; s < kTerms; ++s) {
-              const int col = qh * kHeadColumns + s * kMaxGroup + qq;  // a row of 128 bytes
-              sts_u4(qs + sw128_offset(col, j), make_uint4(yl[s][0], yl[s][1], yl[s][2], yl[s][3]));
-              sts_u4(qs + (D == 128 ? L::kQHalf + sw128_offset(col, j) : sw128_offset(col, j + 4)),
-                     make_uint4(yh[s][0], yh[s][1], yh[s][2], yh[s][3]));
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&bars[kRQReady]);
+        if (n == 0) stage_queries(0);
 #pragma unroll
         for (int q = 0; q < kMaxGroup; ++q) {
           m[q] = -INFINITY;
@@ -952,10 +978,10 @@ __global__ void __maxnreg__(128)
       }
       // ---- weights as B: row q of 128 bytes, this key's two bytes
       {
-        const uint32_t ps = smem_u32(smem + L::kP) + x * 4096 + warp * 1024;
+        const uint32_t ps = smem_u32(smem + L::kP) + x * 2048 + (warp >> 1) * 1024;
 #pragma unroll
         for (int q = 0; q < kMaxGroup; ++q)
-          sts_u16(ps + q * 128 + (((lane >> 3) ^ q) << 4) + (lane & 7) * 2,
+          sts_u16(ps + q * 128 + ((((warp & 1) * 4 + (lane >> 3)) ^ q) << 4) + (lane & 7) * 2,
                   __bfloat16_as_ushort(__float2bfloat16_rn(p[q])));
       }
       if (bits != 0xffffffffu) {
@@ -1003,6 +1029,12 @@ __global__ void __maxnreg__(128)
       tc_fence_before();
       mbar_arrive(&bars[kRPFull0 + x]);
       if (closes) {
+        if (n + 1 < n_tiles) {  // the next piece's queries meanwhile
+          const int next = (n + 1) % kTileInfos;
+          ok = wait(&bars[kRInfoFull0 + next], ((n + 1) / kTileInfos) & 1, kDevErrTimeoutSoftmax);
+          if (!ok) break;
+          stage_queries(next);
+        }
         // ---- the piece's parts: one of each warp, by all four (lane = dim)
         float mine[kMaxGroup];
 #pragma unroll
@@ -1064,37 +1096,33 @@ __global__ void __maxnreg__(128)
   pdl_wait();
 }
 
-// --------------------------------------------------------------- finish ----
-constexpr int kFinishThreads = 512;
-constexpr int kFinishParts = 32;                      // parts joined at a time
-constexpr int kFinishHeads = kRowHeads * kMaxGroup;   // most query heads of a block
+// ----------------------------------------------------------------- join ----
+constexpr int kJoinThreads = 512;
+constexpr int kJoinParts = 32;                      // parts joined at a time
+constexpr int kJoinHeads = kRowHeads * kMaxGroup;   // most query heads of a block
 
-// Blocks (., heads, conversation), the heads a unit's or one: the new token's
+// Block (heads, conversation), the heads a unit's or one: the new token's row and
 // logits, a warp per query head, before what the other kernels leave is waited
-// for; then the parts' common log-sum-exp; then the first block the new row, the
-// output, some threads per column of four, the parts' weights and places settled
-// before, and the others the cached rows' weights.
+// for; then the parts' common log-sum-exp; then the output, some threads per
+// column of four, the parts' weights and places settled before.
 template <int D>
-__global__ void __launch_bounds__(kFinishThreads, 2)
-    step_finish_kernel(const __grid_constant__ StepArgs a, const __grid_constant__ Turns f) {
+__global__ void __launch_bounds__(kJoinThreads, 2)
+    step_join_kernel(const __grid_constant__ StepArgs a, const __grid_constant__ Turns f) {
   constexpr int HALF = D / 2;
-  __shared__ float fresh[kFinishHeads], total[kFinishHeads];
-  __shared__ float4 acc[kFinishThreads];
-  __shared__ float weight[kFinishHeads][kFinishParts];
-  __shared__ const float4* place[kFinishHeads][kFinishParts];
-  const int g0 = blockIdx.y * a.finish_heads, b = blockIdx.z;
-  const int heads = min(a.finish_heads, a.Hkv - g0), nq = heads * a.G;  // query heads
+  __shared__ float fresh[kJoinHeads], total[kJoinHeads];
+  __shared__ float4 acc[kJoinThreads];
+  __shared__ float weight[kJoinHeads][kJoinParts];
+  __shared__ const float4* place[kJoinHeads][kJoinParts];
+  const int g0 = blockIdx.x * a.join_heads, b = blockIdx.y;
+  const int heads = min(a.join_heads, a.Hkv - g0), nq = heads * a.G;  // query heads
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_release();
   const StepOf s = step_of(a, b);
+  const int page = s.row < 0 ? -1 : page_of(a.pt, b, s.row);
   __nv_bfloat16* out = a.o + (static_cast<long long>(b) * a.Hq + g0 * a.G) * D;
-  if (s.row < 0) {
-    if (blockIdx.x == 0)
-      for (int e = tid; e < nq * D; e += kFinishThreads) out[e] = __float2bfloat16_rn(0.f);
-    pdl_wait();
-    return;
-  }
-  const int first = (static_cast<int>(blockIdx.x) - 1) * kFinishThreads;  // rows' blocks
-  if (first >= s.n * 32) {
+  if (page < 0) {
+    if (g0 == 0 && tid == 0 && __ldg(a.pt.lens + b) >= 0) atomicOr(a.status, kDevErrNoPage);
+    for (int e = tid; e < nq * D; e += kJoinThreads) out[e] = __float2bfloat16_rn(0.f);
     pdl_wait();
     return;
   }
@@ -1105,9 +1133,9 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
     float2 cs[HALF / 32];
 #pragma unroll
     for (int e = 0; e < HALF / 32; ++e) cs[e] = rope_cs_turns(f.t[lane + 32 * e], pos);
-    const long long at = ((static_cast<long long>(s.page) << a.pt.page_log2) +
+    const long long at = ((static_cast<long long>(page) << a.pt.page_log2) +
                           (s.row & ((1 << a.pt.page_log2) - 1))) * a.Hkv * D + g0 * D;
-    for (int q = warp; q < nq; q += kFinishThreads / 32) {
+    for (int q = warp; q < nq; q += kJoinThreads / 32) {
       const int h = q / a.G;
       const __nv_bfloat16* k = a.k_new + from + h * D;
       const __nv_bfloat16* x = a.q + (static_cast<long long>(b) * a.Hq + g0 * a.G + q) * D;
@@ -1119,7 +1147,7 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
         rope_pair(__bfloat162float(k[j]), __bfloat162float(k[j + HALF]), cs[e], k0, k1);
         rope_pair(__bfloat162float(x[j]), __bfloat162float(x[j + HALF]), cs[e], q0, q1);
         const __nv_bfloat16 z0 = __float2bfloat16_rn(k0), z1 = __float2bfloat16_rn(k1);
-        if (blockIdx.x == 0 && q % a.G == 0) {
+        if (q % a.G == 0) {
           a.k_pages[at + h * D + j] = z0;
           a.k_pages[at + h * D + j + HALF] = z1;
         }
@@ -1129,7 +1157,7 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
       for (int w = 16; w; w >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, w);
       if (lane == 0) fresh[q] = dot * a.scale_log2;
     }
-    if (blockIdx.x == 0 && tid < heads * (D / 8))
+    if (tid < heads * (D / 8))
       *reinterpret_cast<uint4*>(a.v_pages + at + tid * 8) =
           __ldg(reinterpret_cast<const uint4*>(a.v_new + from + tid * 8));
   }
@@ -1162,7 +1190,7 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
                      : __ldcg(a.cart_lse + (static_cast<long long>(cart_seg(q)) * a.cart_parts + i -
                                             n_row) * kTile + cart_row(q) % kTile);
   };
-  for (int q = warp; q < nq; q += kFinishThreads / 32) {
+  for (int q = warp; q < nq; q += kJoinThreads / 32) {
     const int n = parts_of(q);
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i <= n; i += 32) {
@@ -1181,31 +1209,33 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
       m = top;
     }
     // (no logit above -inf: every weight is 0)
-    if (lane == 0) total[q] = l == 0.f ? INFINITY : m + __log2f(l);
+    if (lane == 0) {
+      total[q] = l == 0.f ? INFINITY : m + __log2f(l);
+      a.total[static_cast<long long>(b) * a.Hq + g0 * a.G + q] = total[q];
+    }
   }
   __syncthreads();
-  const long long bg = static_cast<long long>(b) * a.Hkv + g0;
-  if (blockIdx.x == 0) {
+  {
     if (a.weights && tid < heads) {
       float x = 0.f;
       for (int hh = 0; hh < a.G; ++hh)
         x += exp2_approx(fresh[tid * a.G + hh] - total[tid * a.G + hh]);
-      a.weights[(bg + tid) * a.weight_rows + s.row] = x;
+      a.weights[(static_cast<long long>(b) * a.Hkv + g0 + tid) * a.weight_rows + s.row] = x;
     }
     int most = 0;
     for (int q = 0; q < nq; ++q) most = max(most, parts_of(q));
-    const int cols = nq * (D / 4), each = max(kFinishThreads / cols, 1);
+    const int cols = nq * (D / 4), each = max(kJoinThreads / cols, 1);
     const int turn = tid / cols;  // (below `each`, or idle; 0 where there are more columns)
-    for (int col0 = 0; col0 < cols; col0 += kFinishThreads) {
+    for (int col0 = 0; col0 < cols; col0 += kJoinThreads) {
       const int col = col0 + (each > 1 ? tid % cols : tid);
       const int q = col / (D / 4), j = col % (D / 4);
       const bool mine = turn < each && col < cols;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = 0; i0 < most; i0 += kFinishParts) {
-        if (col0 == 0 || most > kFinishParts) {  // (else it is there already)
+      for (int i0 = 0; i0 < most; i0 += kJoinParts) {
+        if (col0 == 0 || most > kJoinParts) {  // (else it is there already)
           __syncthreads();
-          for (int e = tid; e < nq * kFinishParts; e += kFinishThreads) {
-            const int qq = e / kFinishParts, k = e % kFinishParts, i = i0 + k;
+          for (int e = tid; e < nq * kJoinParts; e += kJoinThreads) {
+            const int qq = e / kJoinParts, k = e % kJoinParts, i = i0 + k;
             if (i >= parts_of(qq)) continue;
             weight[qq][k] = exp2_approx(lse_of(qq, i) - total[qq]);
             place[qq][k] = reinterpret_cast<const float4*>(
@@ -1216,7 +1246,7 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
           __syncthreads();
         }
         if (mine) {
-          const int n = min(parts_of(q) - i0, kFinishParts);
+          const int n = min(parts_of(q) - i0, kJoinParts);
 #pragma unroll 8
           for (int k = turn; k < n; k += each) {
             const float w = weight[q][k];
@@ -1256,10 +1286,25 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
             make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
       }
     }
-    return;
   }
-  const int step = (gridDim.x - 1) * kFinishThreads;
-  for (int v = first + tid; v < s.n * 32; v += step) {
+}
+
+// -------------------------------------------------------------- weights ----
+constexpr int kWeightThreads = 256;
+
+// A cached row per thread, over the heads of a unit.  Bound by the logits' and
+// weights' traffic.
+__global__ void __launch_bounds__(kWeightThreads)
+    step_weights_kernel(const __grid_constant__ StepArgs a) {
+  const int g0 = blockIdx.y * a.heads, b = blockIdx.z, heads = min(a.heads, a.Hkv - g0);
+  const StepOf s = step_of(a, b);
+  const int page = s.row < 0 ? -1 : page_of(a.pt, b, s.row);
+  pdl_wait();
+  if (page < 0) return;
+  const long long bg = static_cast<long long>(b) * a.Hkv + g0;
+  const float* total = a.total + bg * a.G;
+  for (int v = blockIdx.x * kWeightThreads + threadIdx.x; v < s.n * 32;
+       v += gridDim.x * kWeightThreads) {
     const int r = s.group(v >> 5) * 32 + (v & 31);
     if (!s.sees(r)) continue;
     for (int h = 0; h < heads; ++h) {
@@ -1269,14 +1314,15 @@ __global__ void __launch_bounds__(kFinishThreads, 2)
       float x = 0.f;
 #pragma unroll 4
       for (int hh = 0; hh < a.G; ++hh)
-        x += exp2_approx(__ldcg(lg + static_cast<long long>(hh) * a.cap) - total[h * a.G + hh]);
+        x += exp2_approx(__ldcg(lg + static_cast<long long>(hh) * a.cap) -
+                         __ldcg(total + h * a.G + hh));
       *w = old + x;
     }
   }
 }
 
 struct StepWs {
-  size_t cart_o, cart_lse, row_o, row_lse, starts, logits, total;
+  size_t cart_o, cart_lse, row_o, row_lse, starts, logits, sums, total;
   int row_tiles, key_tiles, cart_chunk, cart_parts, cart_ctas;
   int heads, units, groups, row_ctas;
 };
@@ -1310,6 +1356,7 @@ StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
   w.row_o = take(parts * G * d * 4);
   w.row_lse = take(parts * G * 4);
   w.starts = take((static_cast<size_t>(B) + 1) * 8);
+  w.sums = take(static_cast<size_t>(B) * Hq * 4);
   w.logits = take(weights ? static_cast<size_t>(B) * Hq * cap * 4 : 0);
   w.total = off;
   return w;
@@ -1372,18 +1419,20 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  // blocks of the last kernel: a unit's heads each where that leaves enough of
-  // them, else one; and for the weights' rows as many as the GPU takes at once, at
-  // most one for every 512 rows that a table can name
-  StepArgs last = a;
-  last.finish_heads = a.B * a.units >= sm_count() ? a.heads : 1;
-  const int across = (a.Hkv + last.finish_heads - 1) / last.finish_heads;
-  int blocks = 1;
-  if (a.weights)
-    blocks += std::max(1, std::min((a.cap + kFinishThreads - 1) / kFinishThreads,
-                                   4 * sm_count() / std::max(1, a.B * across)));
-  return launch_dependent(step_finish_kernel<D>, dim3(blocks, across, a.B), dim3(kFinishThreads), 0,
-                          st, last, f);
+  // blocks of the joining kernel: a unit's heads each where that leaves enough of
+  // them for the GPU, else one
+  StepArgs join = a;
+  join.join_heads = a.B * a.units >= sm_count() ? a.heads : 1;
+  e = launch_dependent(step_join_kernel<D>,
+                       dim3((a.Hkv + join.join_heads - 1) / join.join_heads, a.B),
+                       dim3(kJoinThreads), 0, st, join, f);
+  if (e != cudaSuccess || !a.weights) return e;
+  // blocks for a unit's rows: as many as the GPU takes at once, at most one for
+  // every 256 rows that a table can name
+  const int blocks = std::max(1, std::min((a.cap + kWeightThreads - 1) / kWeightThreads,
+                                          8 * sm_count() / std::max(1, a.B * a.units)));
+  return launch_dependent(step_weights_kernel, dim3(blocks, a.units, a.B), dim3(kWeightThreads), 0,
+                          st, a);
 }
 
 }  // namespace
@@ -1457,6 +1506,7 @@ int cart_attn_decode_paged(int B, int window, int sinks, int Hq, int Hkv, int d,
   a.row_o = reinterpret_cast<float*>(ws + w.row_o);
   a.row_lse = reinterpret_cast<float*>(ws + w.row_lse);
   a.cap = max_pages * page_rows;
+  a.total = reinterpret_cast<float*>(ws + w.sums);
   a.logits = weights ? reinterpret_cast<float*>(ws + w.logits) : nullptr;
   const RopeFreqs f = make_rope_freqs(d, rope_theta);
   Turns turns{};
