@@ -3,11 +3,7 @@
 // (cart_attn_decode_paged).
 //
 // Four kernels, chained by programmatic dependent launch; the first two run at
-// once, one CTA of each per SM:
-//   cart    the B * G stacked query rows of each kv head against the cartridge,
-//           as tcgen05 products: 128 rows and 64 keys at a time, Q resident as
-//           two bf16 terms, S and O in TMEM.  All (kv head, row tile, key tile)
-//           triples are cut into equal runs, one per CTA.
+// once, on SMs of their own:
 //   rows    the cached private rows, bound by HBM: S^T = K Q^T and O^T = V^T P^T
 //           on tcgen05, so that the keys fill the 128 rows of a product and the
 //           few queries its columns.  A tile is 128 key rows, 32 of each of four
@@ -15,9 +11,14 @@
 //           heads as three bf16 terms each, which hold all 24 bits of f32; what a
 //           key's row meets of another head's queries is not read.  Warp w has
 //           the keys 32w .. 32w + 31 of a tile, one a thread, and a maximum, sums
-//           and an O^T of its own.  K and V tiles come through one ring of 96 KB.
+//           and an O^T of its own.  K and V tiles come through one ring of 192 KB.
 //           All conversations' rows, one after the other, are cut into equal
-//           runs, one per CTA.
+//           runs, one per CTA and SM.
+//   cart    the B * G stacked query rows of each kv head against the cartridge,
+//           as tcgen05 products: 128 rows and 64 keys at a time, Q resident as
+//           two bf16 terms, S and O in TMEM.  All (kv head, row tile, key tile)
+//           triples are cut into equal runs, one per CTA; two CTAs an SM, on the
+//           SMs that the rows' kernel, launched first, leaves.
 //   join    the new token: its rotated key and its value to its row, its logits;
 //           joins them and a (conversation, kv head)'s parts by their log-sum-exps.
 //   weights adds exp2(logit - log-sum-exp) of the group's heads to each row's.
@@ -36,8 +37,8 @@ namespace cart {
 namespace {
 
 // Raises a kernel's shared-memory limit as set_smem_once does, and asks for the
-// largest shared part of an SM's first-level cache: two kernels share one there,
-// which fits only what the first of them was given.
+// largest shared part of an SM's first-level cache: what the first CTA on an SM
+// was given decides whether a second one fits.
 template <auto Kernel>
 cudaError_t set_shared_once(int bytes) {
   static std::atomic<unsigned long long> done{0};
@@ -149,9 +150,8 @@ struct CartMaps {
   CUtensorMap k, v;
 };
 
-// (128 registers, as the rows' kernel: a quarter of an SM holds two warps of each)
 template <int D>
-__global__ void __maxnreg__(128)
+__global__ void __launch_bounds__(kCartThreads, 2)
     step_cart_kernel(const __grid_constant__ CartMaps maps, const __grid_constant__ StepArgs a,
                      const __grid_constant__ Turns f) {
   using L = CartSmem<D>;
@@ -166,12 +166,16 @@ __global__ void __maxnreg__(128)
   uint64_t* const bars = sh.bars;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t abort_s = smem_u32(&sh.abort);
-  pdl_release();  // (the rows run beside this kernel)
+  pdl_release();
   if (threadIdx.x == 0) {
     sh.abort = 0;
     for (int s = 0; s < kCBars; ++s)
       mbar_init(&bars[s], s == kCPFull0 || s == kCPFull0 + 1 ? 128 : 1);
     fence_mbar_init();
+  }
+  if (threadIdx.x == 128) {
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
   }
   if (warp == 5) {
     tmem_alloc(&sh.tmem, 256);
@@ -192,22 +196,31 @@ __global__ void __maxnreg__(128)
     const int g = seg / a.row_tiles, row0 = (seg - g * a.row_tiles) * kTile;
     // ---- the tile's queries, rotated, as two terms; what they see
     if (threadIdx.x == 0) sh.first = 0x7fffffff;
-    __syncthreads();
     const int row = threadIdx.x, R0 = row0 + row;
+    const bool inside = row < kTile && R0 < R;
+    const int b = inside ? R0 / a.G : 0;
+    StepOf s{};
+    s.row = -1;
+    if (inside) s = step_of(a, b);
+    const int pos = s.row >= 0 ? position_of(a, b, s.row) : 0;
+    const __nv_bfloat16* x = a.q + (static_cast<long long>(b) * a.Hq + g * a.G + R0 % a.G) * D;
+    // a conversation's heads have the same angles: where three or more share
+    // them, each works some out, in the space of the keys and values
+    float2* const angles = reinterpret_cast<float2*>(smem + L::kK) + (b - row0 / a.G) * HALF;
+    const bool shared = a.G >= 3;
+    if (shared && s.row >= 0) {
+      // (a conversation's first rows may be in the tile before)
+      const int r0 = max(b * a.G, row0), n = min((b + 1) * a.G, row0 + kTile) - r0;
+#pragma unroll 4
+      for (int j = R0 - r0; j < HALF; j += n) angles[j] = rope_cs_turns_fast(f.t[j], pos);
+    }
+    __syncthreads();
     int first = 0x7fffffff;  // first key in the row's window
     if (row < kTile) {
       const uint32_t qs = smem_u32(smem + L::kQ);
-      const bool inside = R0 < R;
-      const int b = inside ? R0 / a.G : 0;
-      StepOf s{};
-      s.row = -1;
-      if (inside) s = step_of(a, b);
       if (s.row >= 0) {
         first = a.window > 0 ? a.p + s.row - a.window + 1 : 0;
-        const int pos = position_of(a, b, s.row);
-        const __nv_bfloat16* x =
-            a.q + (static_cast<long long>(b) * a.Hq + g * a.G + R0 % a.G) * D;
-#pragma unroll
+#pragma unroll 2
         for (int c = 0; c < HALF / 8; ++c) {  // pairs 8c .. 8c + 7
           const uint4 l4 = __ldg(reinterpret_cast<const uint4*>(x + 8 * c));
           const uint4 h4 = __ldg(reinterpret_cast<const uint4*>(x + HALF + 8 * c));
@@ -216,9 +229,12 @@ __global__ void __maxnreg__(128)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 fl = bf16x2_to_float2(pl[k]), fh = bf16x2_to_float2(ph[k]);
+            const int j = 8 * c + 2 * k;
+            const float2 c0 = shared ? angles[j] : rope_cs_turns_fast(f.t[j], pos);
+            const float2 c1 = shared ? angles[j + 1] : rope_cs_turns_fast(f.t[j + 1], pos);
             float2 v, w;
-            rope_pair(fl.x, fh.x, rope_cs_turns_fast(f.t[8 * c + 2 * k], pos), v.x, w.x);
-            rope_pair(fl.y, fh.y, rope_cs_turns_fast(f.t[8 * c + 2 * k + 1], pos), v.y, w.y);
+            rope_pair(fl.x, fh.x, c0, v.x, w.x);
+            rope_pair(fl.y, fh.y, c1, v.y, w.y);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               yl[m][k] = pack_bf16x2(v.x, v.y);
@@ -496,6 +512,8 @@ __global__ void __maxnreg__(128)
   __syncthreads();
   tc_fence_after();
   if (warp == 5) tmem_dealloc(tmem, 256);
+  // the next kernel waits for this one alone: it has waited for the rows'
+  pdl_wait();
 }
 
 // ----------------------------------------------------------------- rows ----
@@ -516,7 +534,7 @@ struct TileInfo {
 template <int D>
 struct RowSmem {
   static constexpr int kTileBytes = kTile * D * 2;          // a K or V tile
-  static constexpr int kSlots = 3 * 128 / D;                // of the ring
+  static constexpr int kSlots = 6 * 128 / D;                // of the ring
   static constexpr int kQHalf = kRowHeads * kHeadColumns * 128;  // 64 dims of all columns
   static constexpr int kP = kSlots * kTileBytes;  // weights: two buffers, 1 KB for two warps
   // (a product reads 16 rows of weights, eight of them behind the warps')
@@ -526,9 +544,9 @@ struct RowSmem {
 };
 
 enum RowBar {
-  kRFull0 = 0,                  // ring slot has landed (6 slots at most)
-  kREmpty0 = kRFull0 + 6,
-  kRInfoFull0 = kREmpty0 + 6,   // info of a tile
+  kRFull0 = 0,                  // ring slot has landed (12 slots at most)
+  kREmpty0 = kRFull0 + 12,
+  kRInfoFull0 = kREmpty0 + 12,  // info of a tile
   kRInfoEmpty0 = kRInfoFull0 + kTileInfos,  // four warps and the MMA warp have read it
   kRQReady = kRInfoEmpty0 + kTileInfos,     // a piece's queries are staged (128 arrivals)
   kRSFull0,                     // S^T of buffer x is in TMEM
@@ -545,7 +563,8 @@ struct RowShared {
   uint64_t bars[kRBars];
   long long scan[kRowThreads / 32], run_off;
   TileInfo info[kTileInfos];
-  float factor[2][4][kMaxGroup];  // what each warp's O^T is multiplied by
+  float factor[2][4][kMaxGroup];  // what each warp's O^T is multiplied by, by tile
+  float inverse[4][kMaxGroup];    // ... in the end (a warp may be a tile ahead of another)
   int rescale[2][4];
   uint32_t tmem;
   int run_b, abort;
@@ -569,7 +588,7 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 template <int D>
-__global__ void __maxnreg__(128)
+__global__ void __launch_bounds__(kRowThreads, 1)
     step_rows_kernel(const __grid_constant__ RowMaps maps, const __grid_constant__ StepArgs a,
                      const __grid_constant__ Turns f) {
   using L = RowSmem<D>;
@@ -585,6 +604,7 @@ __global__ void __maxnreg__(128)
   TileInfo* const info = sh.info;
   auto& factor = sh.factor;
   auto& rescale = sh.rescale;
+  auto& inverse = sh.inverse;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t abort_s = smem_u32(&sh.abort);
   if (tid == 0) {
@@ -595,6 +615,11 @@ __global__ void __maxnreg__(128)
                           : s == kRExchange                                    ? 4
                                                                                : 1);
     fence_mbar_init();
+  }
+  pdl_release();  // (the cartridge's kernel runs beside this one)
+  if (tid == 128) {
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
   }
   if (warp == 5) {
     tmem_alloc(&sh.tmem, 256);
@@ -679,7 +704,7 @@ __global__ void __maxnreg__(128)
         s = step_of(a, ++b);
         continue;
       }
-      const int pos = position_of(a, b, s.row), h0 = unit * a.heads;
+      const int h0 = unit * a.heads;
       const int t1 = min(all, t0 + n_tiles - n);
       // the next conversation's, before they are needed
       const StepOf next = unit + 1 == a.units && b + 1 < a.B ? step_of(a, b + 1) : s;
@@ -714,38 +739,14 @@ __global__ void __maxnreg__(128)
         }
         if (small) bits |= __shfl_down_sync(0xffffffffu, bits, 1) << 16;  // (even lanes')
         const unsigned boxes = __ballot_sync(0xffffffffu, there);
-        const int ti = n % kTileInfos;
-        if (n >= kTileInfos) {
-          ok = wait(&bars[kRInfoEmpty0 + ti], (n / kTileInfos - 1) & 1);
-          if (!ok) break;
-        }
-        TileInfo& o = info[ti];
-        if (t == t0)  // the piece's angles
-#pragma unroll 1
-          for (int e = lane; e < HALF; e += 32) sh.angles[ti][e] = rope_cs_turns(f.t[e], pos);
-        if (lane < lanes && (!small || !(lane & 1))) o.bits[group_of] = bits;
-        if (lane == 0) {
-          o.b = b;
-          o.h0 = h0;
-          o.v0 = t * a.groups * 32;
-          o.opens = t == t0;
-          o.closes = t + 1 == t1;
-          o.slot = slot;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kRInfoFull0 + ti]);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++loads) {
+        // a K or V tile into the next slot
+        auto load = [&](const CUtensorMap* m) {
           const int sl = loads % NS;
-          if (loads >= NS) {
-            ok = wait(&bars[kREmpty0 + sl], (loads / NS - 1) & 1);
-            if (!ok) break;
-          }
+          if (loads >= NS && !wait(&bars[kREmpty0 + sl], (loads / NS - 1) & 1)) return false;
           if (lane == 0) mbar_arrive_expect_tx(&bars[kRFull0 + sl], __popc(boxes) * lane_bytes);
           __syncwarp();
           if (there) {
             uint8_t* const to = smem + sl * L::kTileBytes + group_of * a.heads * 4096;
-            const CUtensorMap* m = kv ? &maps.v : &maps.k;
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
               if (!small) {
@@ -758,7 +759,34 @@ __global__ void __maxnreg__(128)
             }
           }
           __syncwarp();
+          ++loads;
+          return true;
+        };
+        ok = load(&maps.k);
+        if (!ok) break;
+        const int ti = n % kTileInfos;
+        if (n >= kTileInfos) {
+          ok = wait(&bars[kRInfoEmpty0 + ti], (n / kTileInfos - 1) & 1);
+          if (!ok) break;
         }
+        TileInfo& o = info[ti];
+        if (lane < lanes && (!small || !(lane & 1))) o.bits[group_of] = bits;
+        if (lane == 0) {
+          o.b = b;
+          o.h0 = h0;
+          o.v0 = t * a.groups * 32;
+          o.opens = t == t0;
+          o.closes = t + 1 == t1;
+          o.slot = slot;
+        }
+        if (t == t0) {  // the piece's angles
+          const int pos = position_of(a, b, s.row);
+#pragma unroll 1
+          for (int e = lane; e < HALF; e += 32) sh.angles[ti][e] = rope_cs_turns(f.t[e], pos);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kRInfoFull0 + ti]);
+        ok = load(&maps.v);
         if (!ok) break;
         row = row_next;
         page = page_next;
@@ -770,7 +798,6 @@ __global__ void __maxnreg__(128)
         s = next;
       }
     }
-    pdl_release();
     if (lane == 0)  // the last copies land before the CTA ends
       for (int i = max(loads - NS, 0); i < loads; ++i)
         mbar_wait(&bars[kRFull0 + i % NS], (i / NS) & 1, 0u, nullptr, 0);
@@ -1044,15 +1071,14 @@ __global__ void __maxnreg__(128)
           for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
           mine[q] = sum;
         }
-        // (this tile's factors are read: everyone has passed its exchange, and
-        // arrives here after it has read them)
+        // (the last piece's are read: everyone has come to this tile's exchange)
         __syncwarp();
         if (lane == 0) {
           const long long row = ((static_cast<long long>(slot) * a.groups + grp) * a.heads + h) * a.G;
 #pragma unroll
           for (int q = 0; q < kMaxGroup; ++q) {
             const bool some = mine[q] > 0.f || mine[q] != mine[q];
-            factor[x ^ 1][warp][q] = some ? 1.f / mine[q] : 0.f;
+            inverse[warp][q] = some ? 1.f / mine[q] : 0.f;
             if (q < a.G && g < a.Hkv)
               a.row_lse[row + q] = some ? m[q] + __log2f(mine[q]) : -INFINITY;
           }
@@ -1077,7 +1103,7 @@ __global__ void __maxnreg__(128)
                          dim;
 #pragma unroll
             for (int q = 0; q < kMaxGroup; ++q) {
-              const float inv = *const_cast<const volatile float*>(&factor[x ^ 1][w][q]);
+              const float inv = *const_cast<const volatile float*>(&inverse[w][q]);
               if (q < a.G) out[q * D] = inv == 0.f ? 0.f : __uint_as_float(o[q]) * inv;
             }
           }
@@ -1092,8 +1118,6 @@ __global__ void __maxnreg__(128)
   __syncthreads();
   tc_fence_after();
   if (warp == 5) tmem_dealloc(tmem, 256);
-  // the last kernel waits for this one alone: it has waited for the cartridge's
-  pdl_wait();
 }
 
 // ----------------------------------------------------------------- join ----
@@ -1110,6 +1134,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
     step_join_kernel(const __grid_constant__ StepArgs a, const __grid_constant__ Turns f) {
   constexpr int HALF = D / 2;
   __shared__ float fresh[kJoinHeads], total[kJoinHeads];
+  __shared__ int cart_n[kJoinHeads];
+  __shared__ long long cart_at[kJoinHeads];
   __shared__ float4 acc[kJoinThreads];
   __shared__ float weight[kJoinHeads][kJoinParts];
   __shared__ const float4* place[kJoinHeads][kJoinParts];
@@ -1161,40 +1187,59 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       *reinterpret_cast<uint4*>(a.v_pages + at + tid * 8) =
           __ldg(reinterpret_cast<const uint4*>(a.v_new + from + tid * 8));
   }
-  pdl_wait();
-  const long long start = __ldcg(a.starts + b), tiles = __ldcg(a.starts + a.B);
-  // ---- the parts of the cached rows: those of the runs that hold the unit
+  // ---- parts of the cartridge, by the tile that holds the query's row (the first
+  // one's place in cart_lse, their number)
+  if (tid < nq) {
+    const int R = b * a.G + tid % a.G, seg = (g0 + tid / a.G) * a.row_tiles + R / kTile;
+    const int u = seg * a.key_tiles;
+    cart_n[tid] =
+        a.key_tiles > 0 ? (u + a.key_tiles - 1) / a.cart_chunk - u / a.cart_chunk + 1 : 0;
+    cart_at[tid] = static_cast<long long>(seg) * a.cart_parts * kTile + R % kTile;
+  }
   const int unit = g0 / a.heads, all = tiles_of(a, s.n);
-  const long long chunk = max((tiles + a.row_ctas - 1) / a.row_ctas, 1ll);
-  const long long u0 = start + static_cast<long long>(unit) * all;
-  const int c0 = static_cast<int>(u0 / chunk);
-  const int c1 = all > 0 ? static_cast<int>((u0 + all - 1) / chunk) : c0 - 1;
-  const int n_row = (c1 - c0 + 1) * a.groups;
+  const int groups_log2 = a.groups == 4 ? 2 : a.groups - 1;
+  pdl_wait();
+  // ---- and of the cached rows: those of the runs that hold the unit
+  const long long start = __ldcg(a.starts + b), tiles = __ldcg(a.starts + a.B);
+  const unsigned long long u0 = start + static_cast<long long>(unit) * all;
+  int c0, c1;  // runs
+  bool opens;  // the unit opens its first run
+  if (tiles <= 0x7fffffff) {
+    const unsigned chunk = max(static_cast<unsigned>(tiles + a.row_ctas - 1) / a.row_ctas, 1u);
+    c0 = static_cast<unsigned>(u0) / chunk;
+    c1 = all > 0 ? static_cast<unsigned>(u0 + all - 1) / chunk : c0 - 1;
+    opens = u0 == static_cast<unsigned long long>(c0) * chunk;
+  } else {
+    const unsigned long long chunk = (tiles + a.row_ctas - 1) / a.row_ctas;
+    c0 = static_cast<int>(u0 / chunk);
+    c1 = all > 0 ? static_cast<int>((u0 + all - 1) / chunk) : c0 - 1;
+    opens = u0 == c0 * chunk;
+  }
+  const int n_row = (c1 - c0 + 1) << groups_log2;
   auto row_part = [&](int q, int i) -> long long {
-    const int c = c0 + i / a.groups, k = i % a.groups;
+    const int c = c0 + (i >> groups_log2), k = i & (a.groups - 1);
     const long long slot = c0 == c1 ? 2 * a.row_ctas + static_cast<long long>(b) * a.units + unit
-                           : c > c0 || u0 == c0 * chunk ? 2 * c
-                                                        : 2 * c + 1;
-    return ((slot * a.groups + k) * a.heads + g0 - unit * a.heads) * a.G + q;
+                           : c > c0 || opens ? 2 * c
+                                             : 2 * c + 1;
+    return (((slot << groups_log2) + k) * a.heads + g0 - unit * a.heads) * a.G + q;
   };
-  // ---- and of the cartridge, by the tile that holds the query's row
-  auto cart_row = [&](int q) { return b * a.G + q % a.G; };
-  auto cart_seg = [&](int q) { return (g0 + q / a.G) * a.row_tiles + cart_row(q) / kTile; };
-  auto parts_of = [&](int q) {
-    if (a.key_tiles == 0) return n_row;
-    const int u = cart_seg(q) * a.key_tiles;
-    return n_row + (u + a.key_tiles - 1) / a.cart_chunk - u / a.cart_chunk + 1;
+  auto place_of = [&](int q, int i) {
+    return reinterpret_cast<const float4*>(
+        i < n_row ? a.row_o + row_part(q, i) * D
+                  : a.cart_o + ((cart_at[q] / kTile + i - n_row) * (D / 4) * kTile +
+                                cart_at[q] % kTile) * 4);
   };
   auto lse_of = [&](int q, int i) {
     return i < n_row ? __ldcg(a.row_lse + row_part(q, i))
-                     : __ldcg(a.cart_lse + (static_cast<long long>(cart_seg(q)) * a.cart_parts + i -
-                                            n_row) * kTile + cart_row(q) % kTile);
+                     : __ldcg(a.cart_lse + cart_at[q] + static_cast<long long>(i - n_row) * kTile);
   };
+  __syncthreads();
   for (int q = warp; q < nq; q += kJoinThreads / 32) {
-    const int n = parts_of(q);
+    const int n = n_row + cart_n[q];
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i <= n; i += 32) {
       const float x = i < n ? lse_of(q, i) : fresh[q], top = fmaxf(m, x);
+      if (i < min(n, kJoinParts)) weight[q][i] = x;  // (for below)
       if (top != -INFINITY || x != x) {
         l = l * exp2_approx(m - top) + exp2_approx(x - top);
         m = top;
@@ -1209,9 +1254,16 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       m = top;
     }
     // (no logit above -inf: every weight is 0)
+    const float all_of = l == 0.f ? INFINITY : m + __log2f(l);
     if (lane == 0) {
-      total[q] = l == 0.f ? INFINITY : m + __log2f(l);
-      a.total[static_cast<long long>(b) * a.Hq + g0 * a.G + q] = total[q];
+      total[q] = all_of;
+      a.total[static_cast<long long>(b) * a.Hq + g0 * a.G + q] = all_of;
+    }
+    // ---- the first parts' weights and places
+    __syncwarp();
+    for (int i = lane; i < min(n, kJoinParts); i += 32) {
+      weight[q][i] = exp2_approx(weight[q][i] - all_of);
+      place[q][i] = place_of(q, i);
     }
   }
   __syncthreads();
@@ -1223,7 +1275,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       a.weights[(static_cast<long long>(b) * a.Hkv + g0 + tid) * a.weight_rows + s.row] = x;
     }
     int most = 0;
-    for (int q = 0; q < nq; ++q) most = max(most, parts_of(q));
+    for (int q = 0; q < nq; ++q) most = max(most, n_row + cart_n[q]);
     const int cols = nq * (D / 4), each = max(kJoinThreads / cols, 1);
     const int turn = tid / cols;  // (below `each`, or idle; 0 where there are more columns)
     for (int col0 = 0; col0 < cols; col0 += kJoinThreads) {
@@ -1232,21 +1284,18 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       const bool mine = turn < each && col < cols;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int i0 = 0; i0 < most; i0 += kJoinParts) {
-        if (col0 == 0 || most > kJoinParts) {  // (else it is there already)
+        if (most > kJoinParts && (col0 > 0 || i0 > 0)) {  // (the first ones are there)
           __syncthreads();
           for (int e = tid; e < nq * kJoinParts; e += kJoinThreads) {
             const int qq = e / kJoinParts, k = e % kJoinParts, i = i0 + k;
-            if (i >= parts_of(qq)) continue;
+            if (i >= n_row + cart_n[qq]) continue;
             weight[qq][k] = exp2_approx(lse_of(qq, i) - total[qq]);
-            place[qq][k] = reinterpret_cast<const float4*>(
-                i < n_row ? a.row_o + row_part(qq, i) * D
-                          : a.cart_o + ((static_cast<long long>(cart_seg(qq)) * a.cart_parts + i -
-                                         n_row) * (D / 4) * kTile + cart_row(qq) % kTile) * 4);
+            place[qq][k] = place_of(qq, i);
           }
           __syncthreads();
         }
         if (mine) {
-          const int n = min(parts_of(q) - i0, kJoinParts);
+          const int n = min(n_row + cart_n[q] - i0, kJoinParts);
 #pragma unroll 8
           for (int k = turn; k < n; k += each) {
             const float w = weight[q][k];
@@ -1292,32 +1341,35 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
 // -------------------------------------------------------------- weights ----
 constexpr int kWeightThreads = 256;
 
-// A cached row per thread, over the heads of a unit.  Bound by the logits' and
-// weights' traffic.
+// A cached row of a kv head per thread.  Bound by the logits' and weights'
+// traffic.
 __global__ void __launch_bounds__(kWeightThreads)
     step_weights_kernel(const __grid_constant__ StepArgs a) {
-  const int g0 = blockIdx.y * a.heads, b = blockIdx.z, heads = min(a.heads, a.Hkv - g0);
+  const int g = blockIdx.y, b = blockIdx.z;
   const StepOf s = step_of(a, b);
   const int page = s.row < 0 ? -1 : page_of(a.pt, b, s.row);
+  const long long bg = static_cast<long long>(b) * a.Hkv + g;
+  const float* lg = a.logits + bg * a.G * a.cap;
+  float* w = a.weights + bg * a.weight_rows;
   pdl_wait();
   if (page < 0) return;
-  const long long bg = static_cast<long long>(b) * a.Hkv + g0;
-  const float* total = a.total + bg * a.G;
+  float total[kMaxGroup];
+#pragma unroll
+  for (int q = 0; q < kMaxGroup; ++q)
+    total[q] = q < a.G ? __ldcg(a.total + bg * a.G + q) : 0.f;
   for (int v = blockIdx.x * kWeightThreads + threadIdx.x; v < s.n * 32;
        v += gridDim.x * kWeightThreads) {
     const int r = s.group(v >> 5) * 32 + (v & 31);
     if (!s.sees(r)) continue;
-    for (int h = 0; h < heads; ++h) {
-      const float* lg = a.logits + (bg + h) * a.G * a.cap + v;
-      float* w = a.weights + (bg + h) * a.weight_rows + r;
-      const float old = *w;
-      float x = 0.f;
-#pragma unroll 4
-      for (int hh = 0; hh < a.G; ++hh)
-        x += exp2_approx(__ldcg(lg + static_cast<long long>(hh) * a.cap) -
-                         __ldcg(total + h * a.G + hh));
-      *w = old + x;
-    }
+    float x[kMaxGroup];
+#pragma unroll
+    for (int q = 0; q < kMaxGroup; ++q)
+      x[q] = q < a.G ? __ldcg(lg + static_cast<long long>(q) * a.cap + v) : 0.f;
+    const float old = w[r];
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < kMaxGroup; ++q) sum += q < a.G ? exp2_approx(x[q] - total[q]) : 0.f;
+    w[r] = old + sum;
   }
 }
 
@@ -1339,15 +1391,19 @@ StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
   w.row_tiles = (B * G + kTile - 1) / kTile;
   w.key_tiles = (p + kCartKeys - 1) / kCartKeys;
   const int tiles = Hkv * w.row_tiles * w.key_tiles;
+#ifndef CSMS
+#define CSMS 48
+#endif
+  const int cart_sms = std::min(CSMS, sms / 2 + 1);  // SMs of the cartridge's kernel
   if (tiles > 0) {
-    w.cart_chunk = (tiles + sms - 1) / sms;
+    w.cart_chunk = (tiles + 2 * cart_sms - 1) / (2 * cart_sms);
     w.cart_ctas = (tiles + w.cart_chunk - 1) / w.cart_chunk;
     w.cart_parts = (w.key_tiles + w.cart_chunk - 1) / w.cart_chunk + 1;
   }
   w.heads = Hkv > 2 ? 4 : Hkv;  // (a unit's heads beyond the last one are not read)
   w.units = (Hkv + w.heads - 1) / w.heads;
   w.groups = kRowHeads / w.heads;
-  w.row_ctas = sms;
+  w.row_ctas = std::max(sms - (tiles > 0 ? (w.cart_ctas + 1) / 2 : 0), 1);
   const size_t segments = static_cast<size_t>(Hkv) * w.row_tiles;
   w.cart_o = take(segments * w.cart_parts * kTile * d * 4);
   w.cart_lse = take(segments * w.cart_parts * kTile * 4);
@@ -1383,42 +1439,39 @@ template <int D>
 cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cudaStream_t st) {
   using C = CartSmem<D>;
   using L = RowSmem<D>;
-  cudaError_t e = cudaSuccess;
+  static_assert(L::kAlloc <= 232448 && C::kAlloc + L::kAlloc > 232448, "an SM for the rows alone");
+  static_assert(2 * (C::kAlloc + 1024) <= 233472, "two CTAs of the cartridge's kernel an SM");
+  const uint64_t page_rows = 1ull << a.pt.page_log2, row = static_cast<uint64_t>(a.Hkv) * D * 2;
+  const bool small = page_rows == 16;
+  RowMaps rows;
+  {
+    const uint64_t dims[4] = {D, page_rows, static_cast<uint64_t>(a.Hkv),
+                              static_cast<uint64_t>(a.pt.n_pages)};
+    const uint64_t strides[3] = {row, D * 2, row * page_rows};
+    const uint32_t box[4] = {64, small ? 16u : 32u, small ? 1u : static_cast<uint32_t>(a.heads), 1};
+    if (!encode_bf16_map4(&rows.k, a.k_pages, dims, strides, box) ||
+        !encode_bf16_map4(&rows.v, a.v_pages, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
+  cudaError_t e = set_shared_once<step_rows_kernel<D>>(L::kAlloc);
+  if (e != cudaSuccess) return e;
+  step_rows_kernel<D><<<w.row_ctas, kRowThreads, L::kAlloc, st>>>(rows, a, f);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   if (w.cart_ctas > 0) {
-    e = set_shared_once<step_cart_kernel<D>>(C::kAlloc);
-    if (e != cudaSuccess) return e;
     const uint64_t dims[4] = {D, static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(a.p), 1};
-    const uint64_t row = static_cast<uint64_t>(a.Hkv) * D * 2;
     const uint64_t strides[3] = {D * 2, row, row * a.p};
     const uint32_t box[4] = {64, 1, kCartKeys, 1};
-    CartMaps maps;
-    if (!encode_bf16_map4(&maps.k, a.kc, dims, strides, box) ||
-        !encode_bf16_map4(&maps.v, a.vc, dims, strides, box))
+    CartMaps cart;
+    if (!encode_bf16_map4(&cart.k, a.kc, dims, strides, box) ||
+        !encode_bf16_map4(&cart.v, a.vc, dims, strides, box))
       return cudaErrorInvalidValue;
-    step_cart_kernel<D><<<w.cart_ctas, kCartThreads, C::kAlloc, st>>>(maps, a, f);
-    e = cudaGetLastError();
+    e = set_shared_once<step_cart_kernel<D>>(C::kAlloc);
+    if (e == cudaSuccess)
+      e = launch_dependent(step_cart_kernel<D>, dim3(w.cart_ctas), dim3(kCartThreads), C::kAlloc, st,
+                           cart, a, f);
     if (e != cudaSuccess) return e;
   }
-  const uint64_t page_rows = 1ull << a.pt.page_log2, row = static_cast<uint64_t>(a.Hkv) * D * 2;
-  const uint64_t dims[4] = {D, page_rows, static_cast<uint64_t>(a.Hkv),
-                            static_cast<uint64_t>(a.pt.n_pages)};
-  const uint64_t strides[3] = {row, D * 2, row * page_rows};
-  const bool small = page_rows == 16;
-  const uint32_t box[4] = {64, small ? 16u : 32u, small ? 1u : static_cast<uint32_t>(a.heads), 1};
-  RowMaps maps;
-  if (!encode_bf16_map4(&maps.k, a.k_pages, dims, strides, box) ||
-      !encode_bf16_map4(&maps.v, a.v_pages, dims, strides, box))
-    return cudaErrorInvalidValue;
-  e = set_shared_once<step_rows_kernel<D>>(L::kAlloc);
-  if (e != cudaSuccess) return e;
-  if (w.cart_ctas > 0) {
-    e = launch_dependent(step_rows_kernel<D>, dim3(w.row_ctas), dim3(kRowThreads), L::kAlloc, st,
-                         maps, a, f);
-  } else {
-    step_rows_kernel<D><<<w.row_ctas, kRowThreads, L::kAlloc, st>>>(maps, a, f);
-    e = cudaGetLastError();
-  }
-  if (e != cudaSuccess) return e;
   // blocks of the joining kernel: a unit's heads each where that leaves enough of
   // them for the GPU, else one
   StepArgs join = a;
@@ -1427,11 +1480,11 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
                        dim3((a.Hkv + join.join_heads - 1) / join.join_heads, a.B),
                        dim3(kJoinThreads), 0, st, join, f);
   if (e != cudaSuccess || !a.weights) return e;
-  // blocks for a unit's rows: as many as the GPU takes at once, at most one for
+  // blocks for a head's rows: as many as the GPU takes at once, at most one for
   // every 256 rows that a table can name
   const int blocks = std::max(1, std::min((a.cap + kWeightThreads - 1) / kWeightThreads,
-                                          8 * sm_count() / std::max(1, a.B * a.units)));
-  return launch_dependent(step_weights_kernel, dim3(blocks, a.units, a.B), dim3(kWeightThreads), 0,
+                                          8 * sm_count() / std::max(1, a.B * a.Hkv)));
+  return launch_dependent(step_weights_kernel, dim3(blocks, a.Hkv, a.B), dim3(kWeightThreads), 0,
                           st, a);
 }
 
