@@ -2,7 +2,7 @@
 // private rows, with the attention weights that the rows get added up
 // (cart_attn_decode_paged).
 //
-// Four kernels, chained by programmatic dependent launch; the first two run at
+// Three kernels, chained by programmatic dependent launch; the first two run at
 // once, on SMs of their own:
 //   rows    the cached private rows, bound by HBM: S^T = K Q^T and O^T = V^T P^T
 //           on tcgen05, so that the keys fill the 128 rows of a product and the
@@ -20,8 +20,8 @@
 //           triples are cut into equal runs, one per CTA; two CTAs an SM, on the
 //           SMs that the rows' kernel, launched first, leaves.
 //   join    the new token: its rotated key and its value to its row, its logits;
-//           joins them and a (conversation, kv head)'s parts by their log-sum-exps.
-//   weights adds exp2(logit - log-sum-exp) of the group's heads to each row's.
+//           joins them and a (conversation, kv head)'s parts by their log-sum-exps;
+//           adds exp2(logit - log-sum-exp) of the group's heads to each row's weights.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -78,7 +78,6 @@ struct StepArgs {
   long long* starts;         // [B + 1]: chunks of a unit before each conversation's
   float *row_o, *row_lse;    // [slots, groups, heads, G, d], [.., G]
   int cap;                   // most private rows
-  float* total;              // [B, Hq] log2 log-sum-exps over everything
   float* logits;             // [B, Hkv, G, cap], log2 domain, by the order of groups seen
 };
 
@@ -194,47 +193,58 @@ __global__ void __launch_bounds__(kCartThreads, 2)
     const int seg = u / a.key_tiles, t0 = u - seg * a.key_tiles;
     const int t1 = min(t0 + hi - u, a.key_tiles);
     const int g = seg / a.row_tiles, row0 = (seg - g * a.row_tiles) * kTile;
-    // ---- the tile's queries, rotated, as two terms; what they see
+    // ---- the tile's queries, rotated, as two terms; what they see.  D / 16 threads
+    // have a row, pairs 8c .. 8c + 7 each; the angles, which a conversation's heads
+    // share, are worked out in the space of the keys and values, for as many rows
+    // at a time as have theirs there.
     if (threadIdx.x == 0) sh.first = 0x7fffffff;
-    const int row = threadIdx.x, R0 = row0 + row;
-    const bool inside = row < kTile && R0 < R;
-    const int b = inside ? R0 / a.G : 0;
-    StepOf s{};
-    s.row = -1;
-    if (inside) s = step_of(a, b);
-    const int pos = s.row >= 0 ? position_of(a, b, s.row) : 0;
-    const __nv_bfloat16* x = a.q + (static_cast<long long>(b) * a.Hq + g * a.G + R0 % a.G) * D;
-    // a conversation's heads have the same angles: where three or more share
-    // them, each works some out, in the space of the keys and values
-    float2* const angles = reinterpret_cast<float2*>(smem + L::kK) + (b - row0 / a.G) * HALF;
-    const bool shared = a.G >= 3;
-    if (shared && s.row >= 0) {
-      // (a conversation's first rows may be in the tile before)
-      const int r0 = max(b * a.G, row0), n = min((b + 1) * a.G, row0 + kTile) - r0;
+    constexpr int kChunks = HALF / 8, kAhead = 2;  // loads that a thread has in flight
+    const int rows = min(R - row0, kTile), turn_rows = a.G >= 3 ? kTile : 32;
+    static_assert((kTile / 3 + 2) * HALF * 8 <= 2 * L::kKBytes && 32 * HALF * 8 <= 2 * L::kKBytes,
+                  "angles of a turn's conversations");
+    float2* const angles = reinterpret_cast<float2*>(smem + L::kK);
+    const uint32_t qs = smem_u32(smem + L::kQ);
+    for (int r0 = 0; r0 < rows; r0 += turn_rows) {
+      const int n_rows = min(rows - r0, turn_rows), b0 = (row0 + r0) / a.G;
+      for (int e0 = threadIdx.x; e0 - static_cast<int>(threadIdx.x) < n_rows * kChunks;
+           e0 += kAhead * kCartThreads) {
+        uint4 l4[kAhead], h4[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int e = e0 + i * kCartThreads, r = row0 + r0 + e / kChunks;
+          if (e < n_rows * kChunks) {
+            const __nv_bfloat16* x =
+                a.q + (static_cast<long long>(r / a.G) * a.Hq + g * a.G + r % a.G) * D +
+                e % kChunks * 8;
+            l4[i] = __ldg(reinterpret_cast<const uint4*>(x));
+            h4[i] = __ldg(reinterpret_cast<const uint4*>(x + HALF));
+          }
+        }
+        if (e0 == static_cast<int>(threadIdx.x)) {
+          if (r0 > 0) __syncthreads();
+          const int n = (row0 + r0 + n_rows - 1) / a.G - b0 + 1;
 #pragma unroll 4
-      for (int j = R0 - r0; j < HALF; j += n) angles[j] = rope_cs_turns_fast(f.t[j], pos);
-    }
-    __syncthreads();
-    int first = 0x7fffffff;  // first key in the row's window
-    if (row < kTile) {
-      const uint32_t qs = smem_u32(smem + L::kQ);
-      if (s.row >= 0) {
-        first = a.window > 0 ? a.p + s.row - a.window + 1 : 0;
-#pragma unroll 2
-        for (int c = 0; c < HALF / 8; ++c) {  // pairs 8c .. 8c + 7
-          const uint4 l4 = __ldg(reinterpret_cast<const uint4*>(x + 8 * c));
-          const uint4 h4 = __ldg(reinterpret_cast<const uint4*>(x + HALF + 8 * c));
-          const uint32_t pl[4] = {l4.x, l4.y, l4.z, l4.w}, ph[4] = {h4.x, h4.y, h4.z, h4.w};
+          for (int k = threadIdx.x; k < n * HALF; k += kCartThreads) {
+            const int b = b0 + k / HALF;
+            angles[k] =
+                rope_cs_turns_fast(f.t[k % HALF], position_of(a, b, max(held_rows(a.pt, b), 0)));
+          }
+          __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int e = e0 + i * kCartThreads, r = r0 + e / kChunks, c = e % kChunks;
+          if (e >= n_rows * kChunks) continue;
+          const float2* cs = angles + ((row0 + r) / a.G - b0) * HALF + 8 * c;
+          const uint32_t pl[4] = {l4[i].x, l4[i].y, l4[i].z, l4[i].w};
+          const uint32_t ph[4] = {h4[i].x, h4[i].y, h4[i].z, h4[i].w};
           uint32_t yl[2][4], yh[2][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 fl = bf16x2_to_float2(pl[k]), fh = bf16x2_to_float2(ph[k]);
-            const int j = 8 * c + 2 * k;
-            const float2 c0 = shared ? angles[j] : rope_cs_turns_fast(f.t[j], pos);
-            const float2 c1 = shared ? angles[j + 1] : rope_cs_turns_fast(f.t[j + 1], pos);
             float2 v, w;
-            rope_pair(fl.x, fh.x, c0, v.x, w.x);
-            rope_pair(fl.y, fh.y, c1, v.y, w.y);
+            rope_pair(fl.x, fh.x, cs[2 * k], v.x, w.x);
+            rope_pair(fl.y, fh.y, cs[2 * k + 1], v.y, w.y);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               yl[m][k] = pack_bf16x2(v.x, v.y);
@@ -247,8 +257,8 @@ __global__ void __launch_bounds__(kCartThreads, 2)
             }
           }
           // (rows of 128 bytes, 64 elements; d = 128 has a second block)
-          const uint32_t o0 = sw128_offset(row, c);
-          const uint32_t o1 = D == 128 ? 16384u + sw128_offset(row, c) : sw128_offset(row, c + 4);
+          const uint32_t o0 = sw128_offset(r, c);
+          const uint32_t o1 = D == 128 ? 16384u + sw128_offset(r, c) : sw128_offset(r, c + 4);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             sts_u4(qs + m * L::kQBytes + o0, make_uint4(yl[m][0], yl[m][1], yl[m][2], yl[m][3]));
@@ -256,7 +266,15 @@ __global__ void __launch_bounds__(kCartThreads, 2)
           }
         }
       }
-      fence_proxy_async_smem();
+    }
+    fence_proxy_async_smem();
+    const int row = threadIdx.x;
+    int first = 0x7fffffff;  // first key in the row's window
+    if (row < kTile) {
+      if (row < rows) {
+        const StepOf s = step_of(a, (row0 + row) / a.G);
+        if (s.row >= 0) first = a.window > 0 ? a.p + s.row - a.window + 1 : 0;
+      }
       if (a.window > 0) {
         const int w = __reduce_min_sync(0xffffffffu, first);
         if (lane == 0) atomicMin(&sh.first, w);
@@ -481,7 +499,7 @@ __global__ void __launch_bounds__(kCartThreads, 2)
             tmem_ld_wait();
             tmem_reg_fence(o);
           }
-          if (R0 < R)
+          if (row < rows)
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               out[(c * 8 + e / 4) * kTile] =
@@ -524,10 +542,12 @@ constexpr int kHeadColumns = kTerms * kMaxGroup;
 constexpr int kTileInfos = 4;
 
 // What the roles know of a tile: conversation, first head, first key's number
-// among the groups seen, times 32; whether it opens and closes a piece, the slot
-// of the piece's parts; the rows of each group that are there and seen.
+// among the groups seen, times 32; whether it opens and closes a piece and is the
+// run's last (kNone: the run has none); the slot of the piece's parts; the rows of
+// each group that are there and seen.
+enum TileFlags { kOpens = 1, kCloses = 2, kLast = 4, kNone = 8 };
 struct TileInfo {
-  int b, h0, v0, opens, closes, slot;
+  int b, h0, v0, flags, slot;
   unsigned bits[kRowHeads];
 };
 
@@ -575,9 +595,21 @@ struct RowMaps {
   CUtensorMap k, v;  // (d, page_rows, Hkv, pages), box 64 x 32 x heads, or 64 x 16 x 1
 };
 
-// Tiles of one unit of a conversation that sees n groups.
+// Tiles of one unit of a conversation that sees n groups, and what they cost in
+// the schedule: the change from one unit's queries and sums to another's takes
+// about as long as that many tiles (kStart).
+#ifndef KSTART
+#define KSTART 4
+#endif
+constexpr int kStart = KSTART;
 __device__ __forceinline__ int tiles_of(const StepArgs& a, int n) {
   return (n + a.groups - 1) / a.groups;
+}
+__device__ __forceinline__ int cost_of(int tiles) { return tiles > 0 ? tiles + kStart : 0; }
+// x / y for x >= 0, y > 0; the 64-bit division takes several times as long as the
+// 32-bit one that nearly every schedule gets by with.
+__device__ __forceinline__ long long div_units(long long x, long long y) {
+  return ((x | y) >> 31) == 0 ? static_cast<unsigned>(x) / static_cast<unsigned>(y) : x / y;
 }
 
 // The largest of a warp's values (NaN left out).
@@ -587,7 +619,8 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-template <int D>
+// GQ: query heads of a kv head, 4 or 8 at most.
+template <int D, int GQ>
 __global__ void __launch_bounds__(kRowThreads, 1)
     step_rows_kernel(const __grid_constant__ RowMaps maps, const __grid_constant__ StepArgs a,
                      const __grid_constant__ Turns f) {
@@ -630,7 +663,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    mine += static_cast<long long>(tiles_of(a, step_of(a, b).n)) * a.units;
+    mine += static_cast<long long>(cost_of(tiles_of(a, step_of(a, b).n))) * a.units;
   }
   long long x = mine;
 #pragma unroll
@@ -649,13 +682,13 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     start += w < warp ? sh.scan[w] : 0;
     total += sh.scan[w];
   }
-  const long long chunk = (total + a.row_ctas - 1) / a.row_ctas;
+  const long long chunk = div_units(total + a.row_ctas - 1, a.row_ctas);
   const long long lo = min(blockIdx.x * chunk, total), hi = min(lo + chunk, total);
   if (lo < hi && start <= lo && lo < start + mine) {  // (one thread)
     long long at = start;
     int b = b0;
     for (;; ++b) {
-      const long long n = static_cast<long long>(tiles_of(a, step_of(a, b).n)) * a.units;
+      const long long n = static_cast<long long>(cost_of(tiles_of(a, step_of(a, b).n))) * a.units;
       if (lo < at + n) break;
       at += n;
     }
@@ -666,12 +699,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     long long at = start;
     for (int b = b0; b < b1; ++b) {
       a.starts[b] = at;
-      at += static_cast<long long>(tiles_of(a, step_of(a, b).n)) * a.units;
+      at += static_cast<long long>(cost_of(tiles_of(a, step_of(a, b).n))) * a.units;
     }
     if (tid == 0) a.starts[a.B] = total;
   }
   __syncthreads();
-  const int n_tiles = static_cast<int>(hi - lo);
   // TMEM: two buffers of S^T, then the four O^T (16 columns each, 8 of them used)
   const uint32_t tS = tmem, tO = tmem + 192;
   constexpr int kSBuffer = 96;
@@ -682,15 +714,16 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_s, a.status, kDevErrTimeoutTma));
     };
     int b = vld(sh.run_b), n = 0, loads = 0;  // tiles handed on, ring slots filled
-    bool ok = n_tiles > 0;
-    int unit = 0, t0 = 0;
+    long long left = hi - lo;                 // units to go
+    bool ok = true;
+    int unit = 0, at = 0;  // of the conversation, and in its cost
     StepOf s{};
-    if (ok) {
+    if (left > 0) {
       s = step_of(a, b);
-      const int per_unit = tiles_of(a, s.n);
-      const long long off0 = *const_cast<const volatile long long*>(&sh.run_off);
-      unit = static_cast<int>(off0 / per_unit);
-      t0 = static_cast<int>(off0 - static_cast<long long>(unit) * per_unit);
+      const int cost = cost_of(tiles_of(a, s.n));
+      const long long off = *const_cast<const volatile long long*>(&sh.run_off);
+      unit = static_cast<int>(div_units(off, cost));
+      at = static_cast<int>(off - static_cast<long long>(unit) * cost);
     }
     // boxes: a group's 32 rows of all heads, or, in pages of 16, 16 rows of one
     const bool small = a.pt.page_log2 == 4;
@@ -698,21 +731,35 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     const int group_of = small ? lane >> 1 : lane;
     const int lane_bytes = a.heads * (small ? 2048 : 4096) * (D / 64);
     const int mask = (1 << a.pt.page_log2) - 1;
-    while (ok && n < n_tiles) {
+    // (rows are read once a step; the cartridge, the logits and the parts stay in L2
+    // for it: 88 / 140 / 112 us without, 81 / 130 / 102 us with, at 96, 4 and 200
+    // conversations of 8, 8 and 4 kv heads)
+    const uint64_t policy = evict_first_policy();
+    while (ok && left > 0) {
       const int all = tiles_of(a, s.n);
       if (all == 0) {  // idle, or nothing cached
         s = step_of(a, ++b);
         continue;
       }
       const int h0 = unit * a.heads;
-      const int t1 = min(all, t0 + n_tiles - n);
+      const int end = static_cast<int>(min(static_cast<long long>(cost_of(all)), at + left));
+      const int t0 = max(at - kStart, 0), t1 = end - kStart;
+      left -= end - at;
+      // (what is left holds tiles if it is more than a start)
+      const bool more = left > kStart;
       // the next conversation's, before they are needed
       const StepOf next = unit + 1 == a.units && b + 1 < a.B ? step_of(a, b + 1) : s;
       // the piece's slot: the run's first piece, its last one, or a whole unit
-      const bool from_before = n == 0 && t0 > 0, goes_on = t1 < all;
-      const int slot = from_before || (goes_on && n == 0) ? 2 * blockIdx.x
-                       : goes_on                          ? 2 * blockIdx.x + 1
-                                         : 2 * a.row_ctas + b * a.units + unit;
+      const bool goes_on = t1 < all;
+      const int slot = t0 > 0 || (goes_on && n == 0) ? 2 * blockIdx.x
+                       : goes_on                     ? 2 * blockIdx.x + 1
+                                                     : 2 * a.row_ctas + b * a.units + unit;
+      if (t0 < t1) {  // its queries on their way to L2
+        const int heads = min(a.heads, a.Hkv - h0);
+        const char* q = reinterpret_cast<const char*>(
+            a.q + (static_cast<long long>(b) * a.Hq + h0 * a.G) * D);
+        for (int e = lane * 128; e < heads * a.G * D * 2; e += 32 * 128) prefetch_l2(q + e);
+      }
       const int* pages = a.pt.table + static_cast<long long>(b) * a.pt.max_pages;
       // a tile's boxes, a lane each: first row, and that row's page
       auto row_of = [&](int t) {
@@ -750,11 +797,12 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
               if (!small) {
-                tma_load_4d(to + h * 16384, m, &bars[kRFull0 + sl], h * 64, row & mask, h0, page);
+                tma_load_4d_hint(to + h * 16384, m, &bars[kRFull0 + sl], h * 64, row & mask, h0,
+                                 page, policy);
               } else {
                 for (int i = 0; i < a.heads; ++i)
-                  tma_load_4d(to + h * 16384 + i * 4096 + (lane & 1) * 2048, m, &bars[kRFull0 + sl],
-                              h * 64, 0, h0 + i, page);
+                  tma_load_4d_hint(to + h * 16384 + i * 4096 + (lane & 1) * 2048, m,
+                                   &bars[kRFull0 + sl], h * 64, 0, h0 + i, page, policy);
               }
             }
           }
@@ -775,8 +823,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           o.b = b;
           o.h0 = h0;
           o.v0 = t * a.groups * 32;
-          o.opens = t == t0;
-          o.closes = t + 1 == t1;
+          o.flags = (t == t0 ? kOpens : 0) | (t + 1 < t1 ? 0 : more ? kCloses : kCloses | kLast);
           o.slot = slot;
         }
         if (t == t0) {  // the piece's angles
@@ -791,12 +838,16 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         row = row_next;
         page = page_next;
       }
-      t0 = 0;
+      at = 0;
       if (++unit == a.units) {
         unit = 0;
         ++b;
         s = next;
       }
+    }
+    if (ok && n == 0 && lane == 0) {  // a run without tiles
+      info[0].flags = kNone;
+      mbar_arrive(&bars[kRInfoFull0]);
     }
     if (lane == 0)  // the last copies land before the CTA ends
       for (int i = max(loads - NS, 0); i < loads; ++i)
@@ -827,33 +878,31 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       umma_commit_w(&bars[kREmpty0 + sl]);
       return true;
     };
-    bool ok = n_tiles > 0;
+    bool ok = true;
     int pieces = 0;
-    // the tile's flags: bit 0 opens, bit 1 closes a piece
     auto flags_of = [&](int n) {
       const int ti = n % kTileInfos;
       if (!wait(&bars[kRInfoFull0 + ti], (n / kTileInfos) & 1)) return -1;
-      const int fl = vld(info[ti].opens) | vld(info[ti].closes) << 1;
+      const int fl = vld(info[ti].flags);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kRInfoEmpty0 + ti]);
       return fl;
     };
-    int fl = ok ? flags_of(0) : -1;
-    for (int n = 0; n < n_tiles && ok; ++n) {
-      ok = fl >= 0;
-      if (!ok) break;
+    int fl = flags_of(0);
+    for (int n = 0; ok; ++n) {
       const int now = fl;
-      if (now & 1) {  // a piece's first tile: its queries
+      if (now < 0 || (now & kNone)) break;
+      if (now & kOpens) {  // a piece's first tile: its queries
         ok = wait(&bars[kRQReady], pieces & 1) && issue_s(n);
         ++pieces;
         if (!ok) break;
       }
-      if (n + 1 < n_tiles) {
+      if (!(now & kLast)) {
         fl = flags_of(n + 1);
         ok = fl >= 0;
         if (!ok) break;
         // (of the same piece: over the S^T before, whose weights have been used)
-        if (!(fl & 1)) ok = issue_s(n + 1);
+        if (!(fl & kOpens)) ok = issue_s(n + 1);
         if (!ok) break;
       }
       const int e = 2 * n + 1, sl = e % NS;
@@ -866,10 +915,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           umma_bf16_ss_w(tO + w * 16, desc_add(dv, w * 4096 + k * 2048),
-                         desc_add(dp, (w >> 1) * 1024 + (w & 1) * 64 + k * 32), idO, (now & 1) && k == 0 ? 0u : 1u);
+                         desc_add(dp, (w >> 1) * 1024 + (w & 1) * 64 + k * 32), idO, (now & kOpens) && k == 0 ? 0u : 1u);
       umma_commit_w(&bars[kREmpty0 + sl]);
       umma_commit_w(&bars[kRPvDone]);
-      if (now & 2) umma_commit_w(&bars[kRODone]);
+      if (now & kCloses) umma_commit_w(&bars[kRODone]);
+      if (now & kLast) break;
     }
     // every product issued above completes before the CTA ends
     umma_commit_w(&bars[kRDrain]);
@@ -883,7 +933,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     const int h = warp % a.heads, grp = warp / a.heads;
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     bool ok = true;
-    float m[kMaxGroup], l[kMaxGroup];  // the warp's maxima, the thread's sums
+    float m[GQ], l[GQ];  // the warp's maxima, the thread's sums
     int exchanges = 0, pieces = 0;
     // A piece's queries: four threads a row, over all terms.  (The products of the
     // piece before have read theirs: its last S^T is there.)
@@ -936,19 +986,21 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(&bars[kRQReady]);
     };
-    for (int n = 0; n < n_tiles && ok; ++n) {
+    for (int n = 0; ok; ++n) {
       const int ti = n % kTileInfos, x = n & 1;
       ok = wait(&bars[kRInfoFull0 + ti], (n / kTileInfos) & 1, kDevErrTimeoutSoftmax);
       if (!ok) break;
       const TileInfo& in = info[ti];
+      const int flags = vld(in.flags);
+      if (flags & kNone) break;
       const int b = vld(in.b), h0 = vld(in.h0), v0 = vld(in.v0), slot = vld(in.slot);
-      const bool opens = vld(in.opens), closes = vld(in.closes);
+      const bool opens = flags & kOpens, closes = flags & kCloses;
       const unsigned bits = *const_cast<const volatile unsigned*>(&in.bits[grp]);
       const int g = h0 + h;
       if (opens) {
         if (n == 0) stage_queries(0);
 #pragma unroll
-        for (int q = 0; q < kMaxGroup; ++q) {
+        for (int q = 0; q < GQ; ++q) {
           m[q] = -INFINITY;
           l[q] = 0.f;
         }
@@ -961,55 +1013,53 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       tmem_ld_wait();
       tmem_reg_fence(r);
       const bool seen = bits >> lane & 1;
-      float s[kMaxGroup];
+      float s[GQ];
 #pragma unroll
-      for (int q = 0; q < kMaxGroup; ++q) {
+      for (int q = 0; q < GQ; ++q) {
         const float v = __uint_as_float(r[q]) +
                         (__uint_as_float(r[8 + q]) + __uint_as_float(r[16 + q]));
-        s[q] = seen ? v * a.scale_log2 : -INFINITY;
-      }
-      if (a.logits && g < a.Hkv) {
-        float* lg = a.logits + (static_cast<long long>(b) * a.Hkv + g) * a.G * a.cap + v0 +
-                    grp * 32 + lane;
-        if (v0 + grp * 32 + lane < a.cap)
-#pragma unroll
-          for (int q = 0; q < kMaxGroup; ++q)
-            if (q < a.G) lg[static_cast<long long>(q) * a.cap] = s[q];
+        s[q] = seen && q < a.G ? v * a.scale_log2 : -INFINITY;
       }
       // ---- maxima, renewed where they grow by more than 8 (the weights stay below
       // 2^8): every O^T spans the lanes of all warps, so the factors are exchanged
+      float top[GQ];
       bool grows = false;
 #pragma unroll
-      for (int q = 0; q < kMaxGroup; ++q) {
-        if (q >= a.G) break;
-        const float top = warp_max(s[q]);
-        if (top > m[q] + 8.f) {
-          const float alpha = exp2_approx(m[q] - top);
-          m[q] = top;
+      for (int q = 0; q < GQ; ++q) top[q] = warp_max(s[q]);
+#pragma unroll
+      for (int q = 0; q < GQ; ++q) grows |= top[q] > m[q] + 8.f;
+      if (grows) {
+#pragma unroll
+        for (int q = 0; q < GQ; ++q) {
+          const bool up = top[q] > m[q] + 8.f;
+          const float alpha = up ? exp2_approx(m[q] - top[q]) : 1.f;
+          m[q] = up ? top[q] : m[q];
           l[q] *= alpha;
-          if (lane == 0) factor[x][warp][q] = alpha;
-          grows = true;
-        } else if (lane == 0) {
-          factor[x][warp][q] = 1.f;
+          if (lane == q) factor[x][warp][q] = alpha;
         }
       }
+      __syncwarp();
       if (lane == 0) {
         rescale[x][warp] = grows && !opens;
         mbar_arrive(&bars[kRExchange]);
-      }
-      float p[kMaxGroup];
-#pragma unroll
-      for (int q = 0; q < kMaxGroup; ++q) {
-        p[q] = q < a.G ? exp2_approx(s[q] - (m[q] == -INFINITY ? 0.f : m[q])) : 0.f;
-        l[q] += q < a.G ? p[q] : 0.f;
       }
       // ---- weights as B: row q of 128 bytes, this key's two bytes
       {
         const uint32_t ps = smem_u32(smem + L::kP) + x * 2048 + (warp >> 1) * 1024;
 #pragma unroll
-        for (int q = 0; q < kMaxGroup; ++q)
+        for (int q = 0; q < GQ; ++q) {
+          const float p = exp2_approx(s[q] - (m[q] == -INFINITY ? 0.f : m[q]));
+          l[q] += p;
           sts_u16(ps + q * 128 + ((((warp & 1) * 4 + (lane >> 3)) ^ q) << 4) + (lane & 7) * 2,
-                  __bfloat16_as_ushort(__float2bfloat16_rn(p[q])));
+                  __bfloat16_as_ushort(__float2bfloat16_rn(p)));
+        }
+      }
+      if (a.logits && g < a.Hkv && v0 + grp * 32 + lane < a.cap) {
+        float* lg = a.logits + (static_cast<long long>(b) * a.Hkv + g) * a.G * a.cap + v0 +
+                    grp * 32 + lane;
+#pragma unroll
+        for (int q = 0; q < GQ; ++q)
+          if (q < a.G) lg[static_cast<long long>(q) * a.cap] = s[q];
       }
       if (bits != 0xffffffffu) {
         // values of rows that are not seen may be anything, and 0 times them need
@@ -1044,10 +1094,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           tmem_ld_wait();
           tmem_reg_fence16(o);
 #pragma unroll
-          for (int q = 0; q < kMaxGroup; ++q)
-            if (q < a.G)
-              o[q] = __float_as_uint(__uint_as_float(o[q]) *
-                                     *const_cast<const volatile float*>(&factor[x][w][q]));
+          for (int q = 0; q < GQ; ++q)
+            o[q] = __float_as_uint(__uint_as_float(o[q]) *
+                                   *const_cast<const volatile float*>(&factor[x][w][q]));
           tmem_st16(tO + w * 16 + lane_off, o);
         }
         tmem_st_wait();
@@ -1056,34 +1105,32 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       tc_fence_before();
       mbar_arrive(&bars[kRPFull0 + x]);
       if (closes) {
-        if (n + 1 < n_tiles) {  // the next piece's queries meanwhile
+        if (!(flags & kLast)) {  // the next piece's queries meanwhile
           const int next = (n + 1) % kTileInfos;
           ok = wait(&bars[kRInfoFull0 + next], ((n + 1) / kTileInfos) & 1, kDevErrTimeoutSoftmax);
           if (!ok) break;
           stage_queries(next);
         }
         // ---- the piece's parts: one of each warp, by all four (lane = dim)
-        float mine[kMaxGroup];
+        float sum = 0.f, most = 0.f;  // of query `lane`
 #pragma unroll
-        for (int q = 0; q < kMaxGroup; ++q) {
-          float sum = l[q];
+        for (int q = 0; q < GQ; ++q) {
+          float y = l[q];
 #pragma unroll
-          for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-          mine[q] = sum;
+          for (int w = 16; w; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
+          sum = lane == q ? y : sum;
+          most = lane == q ? m[q] : most;
         }
         // (the last piece's are read: everyone has come to this tile's exchange)
-        __syncwarp();
-        if (lane == 0) {
-          const long long row = ((static_cast<long long>(slot) * a.groups + grp) * a.heads + h) * a.G;
-#pragma unroll
-          for (int q = 0; q < kMaxGroup; ++q) {
-            const bool some = mine[q] > 0.f || mine[q] != mine[q];
-            inverse[warp][q] = some ? 1.f / mine[q] : 0.f;
-            if (q < a.G && g < a.Hkv)
-              a.row_lse[row + q] = some ? m[q] + __log2f(mine[q]) : -INFINITY;
-          }
-          mbar_arrive(&bars[kRExchange]);
+        if (lane < GQ) {
+          const bool some = sum > 0.f || sum != sum;
+          inverse[warp][lane] = some ? 1.f / sum : 0.f;
+          if (lane < a.G && g < a.Hkv)
+            a.row_lse[((static_cast<long long>(slot) * a.groups + grp) * a.heads + h) * a.G + lane] =
+                some ? most + __log2f(sum) : -INFINITY;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kRExchange]);
         ok = wait(&bars[kRODone], pieces & 1, kDevErrTimeoutEpilogue) &&
              wait(&bars[kRExchange], exchanges & 1, kDevErrTimeoutEpilogue);
         ++exchanges;
@@ -1102,7 +1149,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                          ((static_cast<long long>(slot) * a.groups + wg) * a.heads + wh) * a.G * D +
                          dim;
 #pragma unroll
-            for (int q = 0; q < kMaxGroup; ++q) {
+            for (int q = 0; q < GQ; ++q) {
               const float inv = *const_cast<const volatile float*>(&inverse[w][q]);
               if (q < a.G) out[q * D] = inv == 0.f ? 0.f : __uint_as_float(o[q]) * inv;
             }
@@ -1112,6 +1159,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kRInfoEmpty0 + ti]);
+      if (flags & kLast) break;
     }
   }
   tc_fence_before();
@@ -1128,7 +1176,8 @@ constexpr int kJoinHeads = kRowHeads * kMaxGroup;   // most query heads of a blo
 // Block (heads, conversation), the heads a unit's or one: the new token's row and
 // logits, a warp per query head, before what the other kernels leave is waited
 // for; then the parts' common log-sum-exp; then the output, some threads per
-// column of four, the parts' weights and places settled before.
+// column of four, the parts' weights and places settled before.  The cached rows'
+// weights are spread over further blocks, which repeat what leads to the log-sum-exp.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 2)
     step_join_kernel(const __grid_constant__ StepArgs a, const __grid_constant__ Turns f) {
@@ -1147,6 +1196,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
   const int page = s.row < 0 ? -1 : page_of(a.pt, b, s.row);
   __nv_bfloat16* out = a.o + (static_cast<long long>(b) * a.Hq + g0 * a.G) * D;
   if (page < 0) {
+    if (blockIdx.z > 0) {
+      pdl_wait();
+      return;
+    }
     if (g0 == 0 && tid == 0 && __ldg(a.pt.lens + b) >= 0) atomicOr(a.status, kDevErrNoPage);
     for (int e = tid; e < nq * D; e += kJoinThreads) out[e] = __float2bfloat16_rn(0.f);
     pdl_wait();
@@ -1173,7 +1226,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
         rope_pair(__bfloat162float(k[j]), __bfloat162float(k[j + HALF]), cs[e], k0, k1);
         rope_pair(__bfloat162float(x[j]), __bfloat162float(x[j + HALF]), cs[e], q0, q1);
         const __nv_bfloat16 z0 = __float2bfloat16_rn(k0), z1 = __float2bfloat16_rn(k1);
-        if (q % a.G == 0) {
+        if (q % a.G == 0 && blockIdx.z == 0) {
           a.k_pages[at + h * D + j] = z0;
           a.k_pages[at + h * D + j + HALF] = z1;
         }
@@ -1183,7 +1236,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       for (int w = 16; w; w >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, w);
       if (lane == 0) fresh[q] = dot * a.scale_log2;
     }
-    if (tid < heads * (D / 8))
+    if (tid < heads * (D / 8) && blockIdx.z == 0)
       *reinterpret_cast<uint4*>(a.v_pages + at + tid * 8) =
           __ldg(reinterpret_cast<const uint4*>(a.v_new + from + tid * 8));
   }
@@ -1196,25 +1249,17 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
         a.key_tiles > 0 ? (u + a.key_tiles - 1) / a.cart_chunk - u / a.cart_chunk + 1 : 0;
     cart_at[tid] = static_cast<long long>(seg) * a.cart_parts * kTile + R % kTile;
   }
-  const int unit = g0 / a.heads, all = tiles_of(a, s.n);
+  const int unit = g0 / a.heads, cost = cost_of(tiles_of(a, s.n));
   const int groups_log2 = a.groups == 4 ? 2 : a.groups - 1;
   pdl_wait();
   // ---- and of the cached rows: those of the runs that hold the unit
-  const long long start = __ldcg(a.starts + b), tiles = __ldcg(a.starts + a.B);
-  const unsigned long long u0 = start + static_cast<long long>(unit) * all;
-  int c0, c1;  // runs
-  bool opens;  // the unit opens its first run
-  if (tiles <= 0x7fffffff) {
-    const unsigned chunk = max(static_cast<unsigned>(tiles + a.row_ctas - 1) / a.row_ctas, 1u);
-    c0 = static_cast<unsigned>(u0) / chunk;
-    c1 = all > 0 ? static_cast<unsigned>(u0 + all - 1) / chunk : c0 - 1;
-    opens = u0 == static_cast<unsigned long long>(c0) * chunk;
-  } else {
-    const unsigned long long chunk = (tiles + a.row_ctas - 1) / a.row_ctas;
-    c0 = static_cast<int>(u0 / chunk);
-    c1 = all > 0 ? static_cast<int>((u0 + all - 1) / chunk) : c0 - 1;
-    opens = u0 == c0 * chunk;
-  }
+  const long long start = __ldcg(a.starts + b), units = __ldcg(a.starts + a.B);
+  const long long u0 = start + static_cast<long long>(unit) * cost;
+  const long long chunk = max(div_units(units + a.row_ctas - 1, a.row_ctas), 1ll);
+  // (a run may hold the unit's start alone)
+  const int c0 = static_cast<int>(div_units(u0 + kStart, chunk));
+  const int c1 = cost > 0 ? static_cast<int>(div_units(u0 + cost - 1, chunk)) : c0 - 1;
+  const bool opens = u0 <= c0 * chunk;  // the unit's first tile is its run's first
   const int n_row = (c1 - c0 + 1) << groups_log2;
   auto row_part = [&](int q, int i) -> long long {
     const int c = c0 + (i >> groups_log2), k = i & (a.groups - 1);
@@ -1257,7 +1302,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
     const float all_of = l == 0.f ? INFINITY : m + __log2f(l);
     if (lane == 0) {
       total[q] = all_of;
-      a.total[static_cast<long long>(b) * a.Hq + g0 * a.G + q] = all_of;
     }
     // ---- the first parts' weights and places
     __syncwarp();
@@ -1267,11 +1311,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
     }
   }
   __syncthreads();
-  {
-    if (a.weights && tid < heads) {
+  if (blockIdx.z == 0) {
+    if (a.weights && tid < heads) {  // of the new row
       float x = 0.f;
-      for (int hh = 0; hh < a.G; ++hh)
-        x += exp2_approx(fresh[tid * a.G + hh] - total[tid * a.G + hh]);
+      for (int q = tid * a.G; q < (tid + 1) * a.G; ++q) x += exp2_approx(fresh[q] - total[q]);
       a.weights[(static_cast<long long>(b) * a.Hkv + g0 + tid) * a.weight_rows + s.row] = x;
     }
     int most = 0;
@@ -1336,45 +1379,52 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       }
     }
   }
-}
-
-// -------------------------------------------------------------- weights ----
-constexpr int kWeightThreads = 256;
-
-// A cached row of a kv head per thread.  Bound by the logits' and weights'
-// traffic.
-__global__ void __launch_bounds__(kWeightThreads)
-    step_weights_kernel(const __grid_constant__ StepArgs a) {
-  const int g = blockIdx.y, b = blockIdx.z;
-  const StepOf s = step_of(a, b);
-  const int page = s.row < 0 ? -1 : page_of(a.pt, b, s.row);
-  const long long bg = static_cast<long long>(b) * a.Hkv + g;
-  const float* lg = a.logits + bg * a.G * a.cap;
-  float* w = a.weights + bg * a.weight_rows;
-  pdl_wait();
-  if (page < 0) return;
-  float total[kMaxGroup];
+  // ---- the cached rows' weights, four rows a thread; by the blocks behind the
+  // first where there are any
+  if (a.weights && (gridDim.z == 1 || blockIdx.z > 0)) {
+    const int parts = max(static_cast<int>(gridDim.z) - 1, 1);
+    const int part = max(static_cast<int>(blockIdx.z) - 1, 0);
+    const int G = a.G, per = s.n * 8;
+    const bool wide = (a.weight_rows & 3) == 0;
+#pragma unroll 1
+    for (int e = part * kJoinThreads + tid; e < heads * per; e += parts * kJoinThreads) {
+      const int h = e / per, v = (e - h * per) * 4, r = s.group(v >> 5) * 32 + (v & 31);
+      const long long bg = static_cast<long long>(b) * a.Hkv + g0 + h;
+      const float* lg = a.logits + bg * G * a.cap + v;
+      float* w = a.weights + bg * a.weight_rows + r;
+      const bool all = wide && s.sees(r) && s.sees(r + 3) && (r >= s.high || r + 3 < s.low);
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 x[kMaxGroup];
+      if (all) y = *reinterpret_cast<const float4*>(w);
 #pragma unroll
-  for (int q = 0; q < kMaxGroup; ++q)
-    total[q] = q < a.G ? __ldcg(a.total + bg * a.G + q) : 0.f;
-  for (int v = blockIdx.x * kWeightThreads + threadIdx.x; v < s.n * 32;
-       v += gridDim.x * kWeightThreads) {
-    const int r = s.group(v >> 5) * 32 + (v & 31);
-    if (!s.sees(r)) continue;
-    float x[kMaxGroup];
+      for (int q = 0; q < kMaxGroup; ++q)
+        if (q < G)
+          x[q] = __ldcg(reinterpret_cast<const float4*>(lg + static_cast<long long>(q) * a.cap));
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int q = 0; q < kMaxGroup; ++q)
-      x[q] = q < a.G ? __ldcg(lg + static_cast<long long>(q) * a.cap + v) : 0.f;
-    const float old = w[r];
-    float sum = 0.f;
+      for (int q = 0; q < kMaxGroup; ++q)
+        if (q < G) {
+          const float t = total[h * G + q];
+          sum.x += exp2_approx(x[q].x - t);
+          sum.y += exp2_approx(x[q].y - t);
+          sum.z += exp2_approx(x[q].z - t);
+          sum.w += exp2_approx(x[q].w - t);
+        }
+      if (all) {
+        *reinterpret_cast<float4*>(w) =
+            make_float4(y.x + sum.x, y.y + sum.y, y.z + sum.z, y.w + sum.w);
+      } else {
+        const float part[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
-    for (int q = 0; q < kMaxGroup; ++q) sum += q < a.G ? exp2_approx(x[q] - total[q]) : 0.f;
-    w[r] = old + sum;
+        for (int k = 0; k < 4; ++k)
+          if (s.sees(r + k)) w[k] += part[k];
+      }
+    }
   }
 }
 
 struct StepWs {
-  size_t cart_o, cart_lse, row_o, row_lse, starts, logits, sums, total;
+  size_t cart_o, cart_lse, row_o, row_lse, starts, logits, total;
   int row_tiles, key_tiles, cart_chunk, cart_parts, cart_ctas;
   int heads, units, groups, row_ctas;
 };
@@ -1392,18 +1442,21 @@ StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
   w.key_tiles = (p + kCartKeys - 1) / kCartKeys;
   const int tiles = Hkv * w.row_tiles * w.key_tiles;
 #ifndef CSMS
-#define CSMS 48
+#define CSMS 24
 #endif
   const int cart_sms = std::min(CSMS, sms / 2 + 1);  // SMs of the cartridge's kernel
   if (tiles > 0) {
-    w.cart_chunk = (tiles + 2 * cart_sms - 1) / (2 * cart_sms);
+#ifndef CCTAS
+#define CCTAS (2 * cart_sms)
+#endif
+    w.cart_chunk = (tiles + CCTAS - 1) / CCTAS;
     w.cart_ctas = (tiles + w.cart_chunk - 1) / w.cart_chunk;
     w.cart_parts = (w.key_tiles + w.cart_chunk - 1) / w.cart_chunk + 1;
   }
   w.heads = Hkv > 2 ? 4 : Hkv;  // (a unit's heads beyond the last one are not read)
   w.units = (Hkv + w.heads - 1) / w.heads;
   w.groups = kRowHeads / w.heads;
-  w.row_ctas = std::max(sms - (tiles > 0 ? (w.cart_ctas + 1) / 2 : 0), 1);
+  w.row_ctas = std::max(sms - (tiles > 0 ? std::min((w.cart_ctas + 1) / 2, cart_sms) : 0), 1);
   const size_t segments = static_cast<size_t>(Hkv) * w.row_tiles;
   w.cart_o = take(segments * w.cart_parts * kTile * d * 4);
   w.cart_lse = take(segments * w.cart_parts * kTile * 4);
@@ -1412,7 +1465,6 @@ StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
   w.row_o = take(parts * G * d * 4);
   w.row_lse = take(parts * G * 4);
   w.starts = take((static_cast<size_t>(B) + 1) * 8);
-  w.sums = take(static_cast<size_t>(B) * Hq * 4);
   w.logits = take(weights ? static_cast<size_t>(B) * Hq * cap * 4 : 0);
   w.total = off;
   return w;
@@ -1453,9 +1505,11 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
         !encode_bf16_map4(&rows.v, a.v_pages, dims, strides, box))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = set_shared_once<step_rows_kernel<D>>(L::kAlloc);
+  cudaError_t e = a.G > 4 ? set_shared_once<step_rows_kernel<D, 8>>(L::kAlloc)
+                          : set_shared_once<step_rows_kernel<D, 4>>(L::kAlloc);
   if (e != cudaSuccess) return e;
-  step_rows_kernel<D><<<w.row_ctas, kRowThreads, L::kAlloc, st>>>(rows, a, f);
+  auto* rows_kernel = a.G > 4 ? step_rows_kernel<D, 8> : step_rows_kernel<D, 4>;
+  rows_kernel<<<w.row_ctas, kRowThreads, L::kAlloc, st>>>(rows, a, f);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (w.cart_ctas > 0) {
@@ -1476,16 +1530,14 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
   // them for the GPU, else one
   StepArgs join = a;
   join.join_heads = a.B * a.units >= sm_count() ? a.heads : 1;
-  e = launch_dependent(step_join_kernel<D>,
-                       dim3((a.Hkv + join.join_heads - 1) / join.join_heads, a.B),
-                       dim3(kJoinThreads), 0, st, join, f);
-  if (e != cudaSuccess || !a.weights) return e;
-  // blocks for a head's rows: as many as the GPU takes at once, at most one for
-  // every 256 rows that a table can name
-  const int blocks = std::max(1, std::min((a.cap + kWeightThreads - 1) / kWeightThreads,
-                                          8 * sm_count() / std::max(1, a.B * a.Hkv)));
-  return launch_dependent(step_weights_kernel, dim3(blocks, a.Hkv, a.B), dim3(kWeightThreads), 0,
-                          st, a);
+  const int across = (a.Hkv + join.join_heads - 1) / join.join_heads;
+  // ... and as many for the rows' weights as the GPU takes at once, at most one for
+  // every 4 * kJoinThreads rows that a table can name
+  const int deep = a.weights ? std::max(1, std::min((a.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads),
+                                                    2 * sm_count() / (across * a.B) - 1) + 1)
+                             : 1;
+  return launch_dependent(step_join_kernel<D>, dim3(across, a.B, deep), dim3(kJoinThreads), 0, st,
+                          join, f);
 }
 
 }  // namespace
@@ -1559,7 +1611,6 @@ int cart_attn_decode_paged(int B, int window, int sinks, int Hq, int Hkv, int d,
   a.row_o = reinterpret_cast<float*>(ws + w.row_o);
   a.row_lse = reinterpret_cast<float*>(ws + w.row_lse);
   a.cap = max_pages * page_rows;
-  a.total = reinterpret_cast<float*>(ws + w.sums);
   a.logits = weights ? reinterpret_cast<float*>(ws + w.logits) : nullptr;
   const RopeFreqs f = make_rope_freqs(d, rope_theta);
   Turns turns{};
