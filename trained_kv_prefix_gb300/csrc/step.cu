@@ -581,13 +581,13 @@ enum RowBar {
 struct RowShared {
   float2 angles[kTileInfos][kMaxHeadDim / 2];  // of a piece, beside its first tile's info
   uint64_t bars[kRBars];
-  long long scan[kRowThreads / 32], run_off;
+  long long scan[kRowThreads / 32];
   TileInfo info[kTileInfos];
   float factor[2][4][kMaxGroup];  // what each warp's O^T is multiplied by, by tile
   float inverse[4][kMaxGroup];    // ... in the end (a warp may be a tile ahead of another)
   int rescale[2][4];
   uint32_t tmem;
-  int run_b, abort;
+  int run_b, run_unit, run_at, abort;  // (where the run begins)
 };
 static_assert(sizeof(RowShared) <= 3584, "rows barrier area");
 
@@ -692,8 +692,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       if (lo < at + n) break;
       at += n;
     }
+    const int cost = cost_of(tiles_of(a, step_of(a, b).n));
+    const long long off = lo - at;
     sh.run_b = b;
-    sh.run_off = lo - at;
+    sh.run_unit = static_cast<int>(div_units(off, cost));
+    sh.run_at = static_cast<int>(off - static_cast<long long>(sh.run_unit) * cost);
   }
   if (blockIdx.x == 0) {  // for the last kernel
     long long at = start;
@@ -720,10 +723,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     StepOf s{};
     if (left > 0) {
       s = step_of(a, b);
-      const int cost = cost_of(tiles_of(a, s.n));
-      const long long off = *const_cast<const volatile long long*>(&sh.run_off);
-      unit = static_cast<int>(div_units(off, cost));
-      at = static_cast<int>(off - static_cast<long long>(unit) * cost);
+      unit = vld(sh.run_unit);
+      at = vld(sh.run_at);
     }
     // boxes: a group's 32 rows of all heads, or, in pages of 16, 16 rows of one
     const bool small = a.pt.page_log2 == 4;
@@ -826,7 +827,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           o.flags = (t == t0 ? kOpens : 0) | (t + 1 < t1 ? 0 : more ? kCloses : kCloses | kLast);
           o.slot = slot;
         }
-        if (t == t0) {  // the piece's angles
+        if (t == t0 && n > 0) {  // the piece's angles (the key warps have the first one's)
           const int pos = position_of(a, b, s.row);
 #pragma unroll 1
           for (int e = lane; e < HALF; e += 32) sh.angles[ti][e] = rope_cs_turns(f.t[e], pos);
@@ -936,21 +937,29 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     float m[GQ], l[GQ];  // the warp's maxima, the thread's sums
     int exchanges = 0, pieces = 0;
     // A piece's queries: four threads a row, over all terms.  (The products of the
-    // piece before have read theirs: its last S^T is there.)
-    auto stage_queries = [&](int ti) {
-      const int b = vld(info[ti].b), h0 = vld(info[ti].h0);
+    // piece before have read theirs: its last S^T is there.)  The run's first ones
+    // are worked on while its pages are looked up, their angles here.
+    auto stage_queries = [&](int ti, int b, int h0, bool first) {
       const int qi = tid >> 2, part = tid & 3, qh = qi / kMaxGroup, qq = qi % kMaxGroup;
-      if (qh < a.heads && qq < a.G && h0 + qh < a.Hkv) {
+      const bool mine = qh < a.heads && qq < a.G && h0 + qh < a.Hkv;
+      uint4 l4[HALF / 32], h4[HALF / 32];
+      if (mine) {
         const __nv_bfloat16* src =
             a.q + (static_cast<long long>(b) * a.Hq + (h0 + qh) * a.G + qq) * D;
-        const uint32_t qs = smem_u32(smem + L::kQ);
-        uint4 l4[HALF / 32], h4[HALF / 32];
 #pragma unroll
         for (int c = 0; c < HALF / 32; ++c) {  // pairs 8j .. 8j + 7
           const int j = part * (HALF / 32) + c;
           l4[c] = __ldg(reinterpret_cast<const uint4*>(src + 8 * j));
           h4[c] = __ldg(reinterpret_cast<const uint4*>(src + HALF + 8 * j));
         }
+      }
+      if (first) {
+        if (tid < HALF)
+          sh.angles[ti][tid] = rope_cs_turns(f.t[tid], position_of(a, b, step_of(a, b).row));
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      }
+      if (mine) {
+        const uint32_t qs = smem_u32(smem + L::kQ);
 #pragma unroll
         for (int c = 0; c < HALF / 32; ++c) {
           const int j = part * (HALF / 32) + c;
@@ -986,6 +995,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(&bars[kRQReady]);
     };
+    if (lo < hi) stage_queries(0, vld(sh.run_b), vld(sh.run_unit) * a.heads, true);
     for (int n = 0; ok; ++n) {
       const int ti = n % kTileInfos, x = n & 1;
       ok = wait(&bars[kRInfoFull0 + ti], (n / kTileInfos) & 1, kDevErrTimeoutSoftmax);
@@ -998,7 +1008,6 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       const unsigned bits = *const_cast<const volatile unsigned*>(&in.bits[grp]);
       const int g = h0 + h;
       if (opens) {
-        if (n == 0) stage_queries(0);
 #pragma unroll
         for (int q = 0; q < GQ; ++q) {
           m[q] = -INFINITY;
@@ -1109,7 +1118,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           const int next = (n + 1) % kTileInfos;
           ok = wait(&bars[kRInfoFull0 + next], ((n + 1) / kTileInfos) & 1, kDevErrTimeoutSoftmax);
           if (!ok) break;
-          stage_queries(next);
+          stage_queries(next, vld(info[next].b), vld(info[next].h0), false);
         }
         // ---- the piece's parts: one of each warp, by all four (lane = dim)
         float sum = 0.f, most = 0.f;  // of query `lane`
@@ -1325,6 +1334,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       const int col = col0 + (each > 1 ? tid % cols : tid);
       const int q = col / (D / 4), j = col % (D / 4);
       const bool mine = turn < each && col < cols;
+      const uint2 v2 = mine && turn == 0 ? __ldg(reinterpret_cast<const uint2*>(
+                                               a.v_new + from + q / a.G * D + 4 * j))
+                                         : make_uint2(0u, 0u);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int i0 = 0; i0 < most; i0 += kJoinParts) {
         if (most > kJoinParts && (col0 > 0 || i0 > 0)) {  // (the first ones are there)
@@ -1365,8 +1377,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       }
       if (mine && turn == 0) {
         const float w = exp2_approx(fresh[q] - total[q]);  // of the new token
-        const uint2 v2 =
-            __ldg(reinterpret_cast<const uint2*>(a.v_new + from + q / a.G * D + 4 * j));
         const float2 lo = bf16x2_to_float2(v2.x), hi = bf16x2_to_float2(v2.y);
         if (w != 0.f) {
           x.x = fmaf(w, lo.x, x.x);
