@@ -597,11 +597,9 @@ struct RowMaps {
 
 // Tiles of one unit of a conversation that sees n groups, and what they cost in
 // the schedule: the change from one unit's queries and sums to another's takes
-// about as long as that many tiles (kStart).
-#ifndef KSTART
-#define KSTART 4
-#endif
-constexpr int kStart = KSTART;
+// about as long as that many tiles (1 / 2 / 3 / 5: 89.3 / 88.1 / 89.6 / 88.1 us at 96
+// conversations, 112 / 111 / 109.7 / 109.6 us at 200).
+constexpr int kStart = 4;
 __device__ __forceinline__ int tiles_of(const StepArgs& a, int n) {
   return (n + a.groups - 1) / a.groups;
 }
@@ -1438,6 +1436,37 @@ struct StepWs {
   int row_tiles, key_tiles, cart_chunk, cart_parts, cart_ctas;
   int heads, units, groups, row_ctas;
 };
+
+// Key tiles of a run of the cartridge's kernel: as many SMs are its as let both
+// kernels end together, going by what they were seen to take side by side, the
+// tables half full (`row_bytes`: their keys and values).  A run of c tiles takes
+// 17 us + 8 us a piece + 2 us a tile; the rows 8 us + their bytes at 0.05 TB/s an
+// SM, 6.3 TB/s at most.  So runs that divide a row tile's key tiles are preferred:
+// at 96 conversations, 768 tiles in segments of 32, 22 / 24 / 28 SMs took 88 / 78 /
+// 80 us in all, at 200 (704 in segments of 16) 20 / 22 / 24 took 96 / 94.5 / 96.7,
+// at 4 of up to 32k rows (1024 in segments of 128) 16 / 26 / 48 took 131 / 117 / 123.
+int cart_chunk_of(int tiles, int key_tiles, double row_bytes, int sms) {
+  int best = tiles;
+  double best_us = 0.0, best_cart = 0.0;
+  for (int c = 1; c < std::max(sms, 2); c += c < 2 ? 1 : 2) {
+    const int chunk = (tiles + 2 * c - 1) / (2 * c);
+    const int pieces = key_tiles % chunk == 0 ? 1
+                       : chunk % key_tiles == 0 ? chunk / key_tiles
+                                                : chunk / key_tiles + 2;
+    const int left = sms - ((tiles + chunk - 1) / chunk + 1) / 2;
+    const double cart = 17.0 + 8.0 * pieces + 2.0 * chunk;
+    const double rows = 8.0 + row_bytes * 1e-6 / std::min(0.05 * std::max(left, 1), 6.3);
+    const double us = std::max(cart, rows);
+    if (c == 1 || us < best_us || (us == best_us && cart < best_cart)) {
+      best = chunk;
+      best_us = us;
+      best_cart = cart;
+    }
+    if (chunk == 1) break;
+  }
+  return best;
+}
+
 // (every size goes by the GPU's multiprocessors: the grids do)
 StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
   StepWs w{};
@@ -1451,22 +1480,15 @@ StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
   w.row_tiles = (B * G + kTile - 1) / kTile;
   w.key_tiles = (p + kCartKeys - 1) / kCartKeys;
   const int tiles = Hkv * w.row_tiles * w.key_tiles;
-#ifndef CSMS
-#define CSMS 24
-#endif
-  const int cart_sms = std::min(CSMS, sms / 2 + 1);  // SMs of the cartridge's kernel
   if (tiles > 0) {
-#ifndef CCTAS
-#define CCTAS (2 * cart_sms)
-#endif
-    w.cart_chunk = (tiles + CCTAS - 1) / CCTAS;
+    w.cart_chunk = cart_chunk_of(tiles, w.key_tiles, static_cast<double>(B) * Hkv * d * 2 * cap, sms);
     w.cart_ctas = (tiles + w.cart_chunk - 1) / w.cart_chunk;
     w.cart_parts = (w.key_tiles + w.cart_chunk - 1) / w.cart_chunk + 1;
   }
   w.heads = Hkv > 2 ? 4 : Hkv;  // (a unit's heads beyond the last one are not read)
   w.units = (Hkv + w.heads - 1) / w.heads;
   w.groups = kRowHeads / w.heads;
-  w.row_ctas = std::max(sms - (tiles > 0 ? std::min((w.cart_ctas + 1) / 2, cart_sms) : 0), 1);
+  w.row_ctas = std::max(sms - (w.cart_ctas + 1) / 2, 1);
   const size_t segments = static_cast<size_t>(Hkv) * w.row_tiles;
   w.cart_o = take(segments * w.cart_parts * kTile * d * 4);
   w.cart_lse = take(segments * w.cart_parts * kTile * 4);
