@@ -281,11 +281,25 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveLoads = 4;      // 16-byte pieces of K, and of V, per thread in flight
-constexpr int kMoveKeys = 4096;    // weights of the rows between held in shared memory
+// T threads a block.  The weights of the rows between, while the least of those
+// that stay is looked for; then a list of rows that stay.
+template <int T>
+struct MoveShared {
+  static constexpr int kRows = 4 * T, kKeys = (T == 256 ? 6 : 10) * kRows;
+  static constexpr int kLoads = 512 / T;  // 16-byte pieces of K, and of V, a thread and turn
+  union {
+    uint32_t keys[kKeys];
+    struct {
+      long long src[kRows], dst[kRows];  // (dst < 0: stays where it is)
+      int row[kRows];
+      float weight[kRows];
+    } list;
+  };
+  uint32_t hist[256], sums[T / 32], pick[2];
+};
 
 // Inclusive prefix sum of v over the block, and the sum.  Every thread calls it.
+template <int T>
 __device__ __forceinline__ uint2 move_scan(uint32_t v, uint32_t* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t x = v;
@@ -299,7 +313,7 @@ __device__ __forceinline__ uint2 move_scan(uint32_t v, uint32_t* sums) {
   __syncthreads();
   uint32_t before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kMoveThreads / 32; ++w) {
+  for (int w = 0; w < T / 32; ++w) {
     before += w < warp ? sums[w] : 0;
     all += sums[w];
   }
@@ -308,15 +322,21 @@ __device__ __forceinline__ uint2 move_scan(uint32_t v, uint32_t* sums) {
 
 // Block (layer, conversation, kv head): the weight of the last row that stays
 // by a search over its 32 bits, eight at a time from the top (a histogram of
-// the rows that agree so far), then the rows in order, 256 at a time.  Row i of
-// those that stay is never before place i, so a run of rows may be written
-// once all of it has been read, whatever is read later.
-__global__ void __launch_bounds__(kMoveThreads)
+// the rows that agree so far), then the rows in order: a list of those that
+// stay, T rows looked at a time, then its moves.  Row i of those that stay is
+// never before place i, so a row may be written once all up to it have been
+// read, whatever is read later: a turn's rows are asked for before those of the
+// turn before are written.  Bound by HBM where there are many blocks: 16 layers of
+// 64 conversations and 8 kv heads from up to 1100 rows to 512 take 339 us, as long
+// as a copy of the rows that move; by latency where there are few.  (The bounds'
+// second part is left open for 256 threads: a 1 there costs 10%.)
+template <int T>
+__global__ void __launch_bounds__(T, T == 512 ? 2 : 0)
     evict_move_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ uint32_t keys[kMoveKeys];
-  __shared__ uint32_t hist[256], sums[kMoveThreads / 32], pick[2];
-  __shared__ long long src[kMoveThreads], dst[kMoveThreads];
-  __shared__ float held_w[kMoveThreads];
+  extern __shared__ __align__(16) char move_smem[];
+  MoveShared<T>& sh = *reinterpret_cast<MoveShared<T>*>(move_smem);
+  constexpr int kLoads = MoveShared<T>::kLoads;
+  uint32_t* const sums = sh.sums;
   pdl_wait();
   pdl_release();
   const int g = blockIdx.x % a.Hkv, lb = blockIdx.x / a.Hkv;
@@ -332,32 +352,33 @@ __global__ void __launch_bounds__(kMoveThreads)
   bool any = false;
   if (stay > 0) {
     any = true;
-    const bool cached = m1 - m0 <= kMoveKeys;
+    const bool cached = m1 - m0 <= MoveShared<T>::kKeys;
     uint32_t left = stay, prefix = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
-      hist[tid] = 0;
+      if (tid < 256) sh.hist[tid] = 0;
       __syncthreads();
       const uint32_t above = shift == 24 ? 0 : 0xffffffffu << (shift + 8);
-      for (int i = m0 + tid; i < m1; i += kMoveThreads) {
+#pragma unroll 4
+      for (int i = m0 + tid; i < m1; i += T) {
         uint32_t key;
         if (shift == 24 || !cached) {
           key = weight_key(w[i]);
-          if (cached) keys[i - m0] = key;
+          if (cached) sh.keys[i - m0] = key;
         } else {
-          key = keys[i - m0];
+          key = sh.keys[i - m0];
         }
-        if ((key & above) == prefix) atomicAdd(hist + (key >> shift & 255), 1);
+        if ((key & above) == prefix) atomicAdd(sh.hist + (key >> shift & 255), 1);
       }
       __syncthreads();
-      const uint32_t mine = hist[255 - tid];
-      const uint32_t upto = move_scan(mine, sums).x;
+      const uint32_t mine = tid < 256 ? sh.hist[255 - tid] : 0;
+      const uint32_t upto = move_scan<T>(mine, sums).x;
       if (upto >= left && upto - mine < left) {
-        pick[0] = 255 - tid;
-        pick[1] = left - (upto - mine);
+        sh.pick[0] = 255 - tid;
+        sh.pick[1] = left - (upto - mine);
       }
       __syncthreads();
-      prefix |= pick[0] << shift;
-      left = pick[1];
+      prefix |= sh.pick[0] << shift;
+      left = sh.pick[1];
     }
     cut = prefix;
     ties = left;
@@ -373,66 +394,102 @@ __global__ void __launch_bounds__(kMoveThreads)
   // (the pages of the rows before are as they were)
   const int begin = q.first & ~mask;
   above = begin;
-  for (int r0 = begin; r0 < q.len; r0 += kMoveThreads) {
-    const int r = r0 + tid;
-    bool more = false, same = false;
-    float x = 0.f;
-    if (r < q.len) {
-      if (w) x = w[r];
-      if (r < m0 || r >= m1) {
-        more = true;
-      } else if (any) {
-        const uint32_t key = weight_key(x);
-        more = key > cut;
-        same = key == cut;
+  auto& list = sh.list;
+  float ahead = w && begin + tid < q.len ? w[begin + tid] : 0.f;
+  for (int r0 = begin; r0 < q.len;) {
+    const int base = static_cast<int>(above + min(equal, ties));  // the list's first place
+    int n = 0;
+    for (; r0 < q.len && n + T <= MoveShared<T>::kRows; r0 += T) {
+      const int r = r0 + tid;
+      const float x = ahead;
+      if (w && r + T < q.len) ahead = w[r + T];
+      bool more = false, same = false;
+      if (r < q.len) {
+        if (r < m0 || r >= m1) {
+          more = true;
+        } else if (any) {
+          const uint32_t key = weight_key(x);
+          more = key > cut;
+          same = key == cut;
+        }
       }
+      // both counts in one scan: at most T of each
+      const uint2 s =
+          move_scan<T>(static_cast<uint32_t>(more) | static_cast<uint32_t>(same) << 16, sums);
+      const uint32_t more_to = above + (s.x & 0xffff), same_to = equal + (s.x >> 16);
+      if (more || (same && same_to <= ties)) {
+        const int i = static_cast<int>(more_to + min(same_to, ties)) - 1 - base;
+        list.row[i] = r;
+        list.weight[i] = x;
+      }
+      above += s.y & 0xffff;
+      equal += s.y >> 16;
+      n = static_cast<int>(above + min(equal, ties)) - base;
     }
-    // both counts in one scan: at most 256 of each
-    const uint2 s = move_scan(static_cast<uint32_t>(more) | static_cast<uint32_t>(same) << 16, sums);
-    const uint32_t more_to = above + (s.x & 0xffff), same_to = equal + (s.x >> 16);
-    const bool stays = more || (same && same_to <= ties);
-    const int base = static_cast<int>(above + min(equal, ties));
-    above += s.y & 0xffff;
-    equal += s.y >> 16;
-    const int n = static_cast<int>(above + min(equal, ties)) - base;
-    if (stays) {
-      const int z = static_cast<int>(more_to + min(same_to, ties)) - 1;  // its place
+    __syncthreads();
+    for (int i = tid; i < n; i += T) {
+      const int r = list.row[i], z = base + i;
       const int page = __ldg(from_row + (r >> a.pt.page_log2));
       const int now = __ldcg(to_row + (z >> a.pt.page_log2));
       const bool moves = z != r || now != page;
-      src[z - base] = page * a.page_bytes + static_cast<long long>(r & mask) * a.row_bytes;
-      dst[z - base] =
+      list.src[i] = page * a.page_bytes + static_cast<long long>(r & mask) * a.row_bytes;
+      list.dst[i] =
           moves ? now * a.page_bytes + static_cast<long long>(z & mask) * a.row_bytes : -1;
-      held_w[z - base] = x;
+      if (w) w[z] = list.weight[i];
     }
     __syncthreads();
-    if (w && tid < n) w[base + tid] = held_w[tid];
-    for (int t0 = 0; t0 < n * per; t0 += kMoveThreads * kMoveLoads) {
-      uint4 rk[kMoveLoads], rv[kMoveLoads];
-      long long to[kMoveLoads];
+    // ---- the moves, a turn's loads ahead of the stores of the turn before
+    uint4 rk[2][kLoads], rv[2][kLoads];
+    long long to[2][kLoads];
+    int i = tid / per, c = tid - i * per;  // (of the next piece)
+    const int di = T / per, dc = T - di * per;
+    auto load = [&](int x) {
 #pragma unroll
-      for (int u = 0; u < kMoveLoads; ++u) {
-        const int t = t0 + u * kMoveThreads + tid;
-        to[u] = -1;
-        if (t < n * per) {
-          const int i = t / per, c = (t - i * per) * 16;
-          if (dst[i] >= 0) {
-            to[u] = dst[i] + c;
-            rk[u] = __ldcg(reinterpret_cast<const uint4*>(kp + src[i] + c));
-            rv[u] = __ldcg(reinterpret_cast<const uint4*>(vp + src[i] + c));
-          }
+      for (int u = 0; u < kLoads; ++u) {
+        to[x][u] = i < n ? list.dst[i] : -1;
+        if (to[x][u] >= 0) {
+          const long long at = list.src[i] + c * 16;
+          to[x][u] += c * 16;
+          rk[x][u] = __ldcg(reinterpret_cast<const uint4*>(kp + at));
+          rv[x][u] = __ldcg(reinterpret_cast<const uint4*>(vp + at));
+        }
+        i += di;
+        c += dc;
+        if (c >= per) {
+          c -= per;
+          ++i;
         }
       }
-      __syncthreads();
+    };
+    auto store = [&](int x) {
 #pragma unroll
-      for (int u = 0; u < kMoveLoads; ++u)
-        if (to[u] >= 0) {
-          *reinterpret_cast<uint4*>(kp + to[u]) = rk[u];
-          *reinterpret_cast<uint4*>(vp + to[u]) = rv[u];
+      for (int u = 0; u < kLoads; ++u)
+        if (to[x][u] >= 0) {
+          *reinterpret_cast<uint4*>(kp + to[x][u]) = rk[x][u];
+          *reinterpret_cast<uint4*>(vp + to[x][u]) = rv[x][u];
         }
+    };
+    const int turns = (n * per + T * kLoads - 1) / (T * kLoads);
+    load(0);
+    for (int t = 0; t < turns; t += 2) {
+      load(1);
+      __syncthreads();  // turn t - 1 has been read by all
+      store(0);
+      load(0);
+      __syncthreads();
+      store(1);
     }
-    __syncthreads();  // the lists are free again
+    __syncthreads();  // the list is free again
   }
+}
+
+template <int T>
+cudaError_t launch_moves(unsigned blocks, cudaStream_t st, const EvictArgs& a) {
+  constexpr int bytes = sizeof(MoveShared<T>);
+  const cudaError_t e = set_smem_once<evict_move_kernel<T>>(bytes);
+  return e == cudaSuccess
+             ? launch_dependent(evict_move_kernel<T>, dim3(blocks), dim3(T), bytes, st, a)
+             : e;
 }
 
 // The new tables and lengths, a warp per conversation.
@@ -554,8 +611,12 @@ int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtype, void* 
   evict_plan_kernel<<<kMetaCtas, kMetaThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = launch_dependent(evict_move_kernel, dim3(static_cast<unsigned>(blocks * Hkv)),
-                         dim3(kMoveThreads), 0, st, a);
+    // Blocks that the SMs take two at a time have more threads: 177 us against 284
+    // with 192 blocks and up to 20000 rows (17.1 against 18.5 us with 12 of 200);
+    // with 8192 blocks and 1100 rows 457 against 339.
+    e = blocks * Hkv <= 2 * sm_count()
+            ? launch_moves<512>(static_cast<unsigned>(blocks * Hkv), st, a)
+            : launch_moves<256>(static_cast<unsigned>(blocks * Hkv), st, a);
   if (e == cudaSuccess)
     e = launch_dependent(evict_tables_kernel, dim3((B + 7) / 8), dim3(256), 0, st, a);
   return e == cudaSuccess ? CART_OK : CART_ERR_CUDA;
