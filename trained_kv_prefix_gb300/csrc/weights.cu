@@ -576,21 +576,45 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
 }
 
 // --------------------------------------------------------------- finish ----
-// A key per thread: its parts by column tile, in order.
-__global__ void __launch_bounds__(256) weigh_finish_kernel(const __grid_constant__ WeighArgs a) {
+// A key per thread: its parts by column tile, in order.  Bound by the parts' reads:
+// the column tiles that see a key tile are worked out once a block.
+constexpr int kFinishThreads = 2 * kTile;
+
+__global__ void __launch_bounds__(kFinishThreads)
+    weigh_finish_kernel(const __grid_constant__ WeighArgs a) {
+  // what column tile q0 + e sees of the block's key tiles
+  __shared__ uint8_t sees[kFinishThreads];
   pdl_wait();
-  const int slot = blockIdx.x * 256 + threadIdx.x, g = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, slot0 = blockIdx.x * kFinishThreads, slot = slot0 + tid;
+  const int g = blockIdx.y, b = blockIdx.z;
   const int rows = max(held_rows(a.pt, b), 0);
+  const int first = slot0 / kTile;  // key tiles: the cartridge's, then the rows'
   const bool own = slot >= a.n_ct * kTile;
   const int r = own ? slot - a.n_ct * kTile : slot;
-  if (r >= (own ? rows : a.p)) return;
+  const bool there = r < (own ? rows : a.p);
   const long long bg = static_cast<long long>(b) * a.Hkv + g;
+  const int mine = 1 << (slot / kTile - first);
   float w = 0.f;
-  for (int qt = 0; qt < a.n_qt; ++qt) {
-    const Tiles tl = column_tiles(a, rows, qt);
-    if (tl.n > 0 && tl.has(own, r / kTile))
-      w += __ldcg(a.part + (bg * a.n_qt + qt) * a.slots + slot);
+  for (int q0 = 0; q0 < a.n_qt; q0 += kFinishThreads) {
+    const int n = min(a.n_qt - q0, kFinishThreads);
+    __syncthreads();
+    if (tid < n) {
+      const Tiles tl = column_tiles(a, rows, q0 + tid);
+      int bits = 0;
+      for (int k = 0; k < kFinishThreads / kTile; ++k) {
+        const int t = first + k;
+        if (tl.n > 0 && tl.has(t >= a.n_ct, t >= a.n_ct ? t - a.n_ct : t)) bits |= 1 << k;
+      }
+      sees[tid] = static_cast<uint8_t>(bits);
+    }
+    __syncthreads();
+    if (!there) continue;
+    const float* part = a.part + (bg * a.n_qt + q0) * a.slots + slot;
+#pragma unroll 8
+    for (int e = 0; e < n; ++e)
+      if (sees[e] & mine) w += __ldcg(part + static_cast<long long>(e) * a.slots);
   }
+  if (!there) return;
   float* to = own ? a.weights + bg * a.weight_rows + r : a.cart + bg * a.p + r;
   *to = a.accumulate && (!own || r < rows - a.T) ? *to + w : w;
 }
@@ -678,7 +702,8 @@ cudaError_t launch_weigh(const WeighArgs& a, const void* kc, const void* k_pages
                          dim3(static_cast<unsigned>(std::min<long long>(sms, most))),
                          dim3(kWeighThreads), L::kAlloc, st, maps, a);
   if (e == cudaSuccess && a.part)
-    e = launch_dependent(weigh_finish_kernel, dim3((a.slots + 255) / 256, a.Hkv, a.B), dim3(256), 0,
+    e = launch_dependent(weigh_finish_kernel, dim3((a.slots + kFinishThreads - 1) / kFinishThreads, a.Hkv, a.B),
+                         dim3(kFinishThreads), 0,
                          st, a);
   return e;
 }
