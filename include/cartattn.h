@@ -514,7 +514,8 @@ CART_API int cart_pages_append(int B, int n, int total, const int* cu_seqlens, i
  *          before its first row are not there, and what q and lse hold for them
  *          is not read
  *   lse    [B, Hq, queries] f32: their natural-log log-sum-exps, as
- *          cart_attn_fwd returns them
+ *          cart_attn_fwd returns them (-inf: every logit was; the query gives
+ *          no weight)
  *   pos    position of query 0 (NULL: its place)
  *   kc     [p, Hkv, d] bf16 (NULL when p == 0)
  *   weights, and cart [B, Hkv, p] f32 for the cartridge's rows (NULL when
@@ -524,8 +525,8 @@ CART_API int cart_pages_append(int B, int n, int total, const int* cu_seqlens, i
  *          it is added, but for the rows of the queries themselves (from
  *          lens[b] - queries on), which are set.  Rows that have no page count
  *          as seen by no query.  Rows from lens[b] on are left as they are.
- * The rotated queries enter the products as two bf16 terms (2^-16 of their
- * value), the sums are f32.  A key that a query does not see gets nothing from
+ * The rotated queries enter the products as three bf16 terms (all 24 bits of
+ * their f32 values), the sums are f32.  A key that a query does not see gets nothing from
  * it, whatever either holds.
  * Workspace: cart_attn_weights_workspace_size().                          */
 CART_API size_t cart_attn_weights_workspace_size(int B, int queries, int Hq, int Hkv, int d, int p,
@@ -585,7 +586,10 @@ CART_API int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtyp
  * not finite makes the logits of those that see it NaN or infinite.
  * An idle conversation (lens < 0) has o = 0 and nothing written, and so has one
  * whose row lens[b] has no page, which sets device status bit 7.
- * The rotated queries enter the products with private rows as two bf16 terms.
+ * The rotated queries enter the products with private rows, which the weights
+ * come from, as three bf16 terms (all 24 bits of their f32 values), those with
+ * the cartridge as two (2^-16 of the value); the weights of the values are
+ * rounded to bf16, their sums f32.
  * Workspace: cart_attn_decode_paged_workspace_size(), `weights` 1 where they are
  * kept.                                                                    */
 CART_API size_t cart_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int d, int p,
@@ -607,10 +611,10 @@ CART_API const char* cart_status_string(int status);
  * warps, 3: the epilogue), when a work schedule is inconsistent (bit 4), or
  * when the dynamic shared memory does not start 1024-byte aligned (bit 5;
  * the kernel then does nothing), when a packed segment table breaks its
- * rules (bit 6), or when a drafted token's row has no page (bit 7).
- * Synchronizes the current device.  Writes
- * the bits to *bits_out (may be NULL); returns CART_OK, CART_ERR_TIMEOUT when
- * any bit is set, or CART_ERR_CUDA. */
+ * rules (bit 6), or when a drafted, appended or decoded token's row has no
+ * page (bit 7).  Synchronizes the current device.  Writes the bits to
+ * *bits_out (may be NULL); returns CART_OK, CART_ERR_TIMEOUT when any bit is
+ * set, or CART_ERR_CUDA. */
 CART_API int cart_device_status(unsigned* bits_out, int clear);
 
 /* cart_release -- destroys the current device's helper stream and events

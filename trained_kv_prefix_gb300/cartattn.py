@@ -815,7 +815,7 @@ def cart_pages_evict(k_pages, v_pages, table, lens, refs, weights, keep, *, firs
         _fits(conversations=B, max_pages=M, pages=N, weight_rows=W, first=first, recent=recent)
     i32 = torch.int32
     # one layer's pool goes with one layer's weights
-    held = (layers, B, Hkv, W) if k_pages.dim() == 5 else (B, Hkv, W)
+    held = (layers, B, Hkv, W) if len(k_pages.shape) == 5 else (B, Hkv, W)
     args = (B, layers, Hkv, d, dt, kp, vp, N, P, _arg("table", table, i32, (B, M), dev), M,
             _arg("lens", lens, i32, (B,), dev), _arg("refs", refs, i32, (N,), dev),
             None if weights is None else _arg("weights", weights, torch.float32, held, dev), W,

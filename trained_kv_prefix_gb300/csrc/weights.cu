@@ -202,9 +202,11 @@ __global__ void __launch_bounds__(kPrepThreads)
       *reinterpret_cast<uint4*>(y) = make_uint4(yl[s][0], yl[s][1], yl[s][2], yl[s][3]);
       *reinterpret_cast<uint4*>(y + HALF) = make_uint4(yh[s][0], yh[s][1], yh[s][2], yh[s][3]);
     }
-    if (j0 == 0)
-      a.nlse2[col] = -1.4426950408889634f *
-                     __ldg(a.lse + (static_cast<long long>(b) * a.Hq + h) * a.T + t0 + t);
+    if (j0 == 0) {
+      const float lse = __ldg(a.lse + (static_cast<long long>(b) * a.Hq + h) * a.T + t0 + t);
+      // (-inf: every logit was, and the query gives no weight)
+      a.nlse2[col] = lse == -INFINITY ? -INFINITY : -1.4426950408889634f * lse;
+    }
   }
 }
 
