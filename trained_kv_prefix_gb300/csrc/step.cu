@@ -15,10 +15,10 @@
 //           All conversations' rows, one after the other, are cut into equal
 //           runs, one per CTA and SM.
 //   cart    the B * G stacked query rows of each kv head against the cartridge,
-//           as tcgen05 products: 128 rows and 64 keys at a time, Q resident as
-//           two bf16 terms, S and O in TMEM.  All (kv head, row tile, key tile)
-//           triples are cut into equal runs, one per CTA; two CTAs an SM, on the
-//           SMs that the rows' kernel, launched first, leaves.
+//           as tcgen05 products: 128 rows and 48 keys at a time, Q resident as
+//           two bf16 terms, S and O in TMEM.  The key tiles of each (kv head, row
+//           tile) are cut into equal pieces, one or more per CTA; two CTAs an SM,
+//           on the SMs that the rows' kernel, launched first, leaves.
 //   join    the new token: its rotated key and its value to its row, its logits;
 //           joins them and a (conversation, kv head)'s parts by their log-sum-exps;
 //           adds exp2(logit - log-sum-exp) of the group's heads to each row's weights.
@@ -68,8 +68,9 @@ struct StepArgs {
   float* weights;  // [B, Hkv, weight_rows], or null
   int weight_rows;
   uint32_t* status;
-  // ---- cart: row tiles, key tiles, tiles per CTA, most parts of a segment
-  int row_tiles, key_tiles, cart_chunk, cart_parts;
+  // ---- cart: row tiles, key tiles, pieces that the key tiles of a (kv head, row
+  // tile) are cut into, pieces of a CTA
+  int row_tiles, key_tiles, cart_parts, cart_each;
   float *cart_o, *cart_lse;  // [Hkv * row_tiles, cart_parts, d / 4, 128] float4; [.., 128]
   // ---- rows: heads of a unit (of which a conversation has `units`), 32-row
   // groups of a tile (heads * groups is 4), CTAs
@@ -111,26 +112,28 @@ __device__ __forceinline__ int position_of(const StepArgs& a, int b, int row) {
 
 // ----------------------------------------------------------------- cart ----
 constexpr int kCartThreads = 192;  // four softmax warps, TMA warp, MMA warp
-constexpr int kCartKeys = 64;      // keys of a tile
+constexpr int kCartKeys = 48;      // keys of a tile
+constexpr int kCartSColumns = 64;  // of TMEM, from one buffer of S to the next
 
 template <int D>
 struct CartSmem {
   static constexpr int kQBytes = kTile * D * 2, kKBytes = kCartKeys * D * 2;
   static constexpr int kQ = 0;                 // two terms
-  static constexpr int kK = kQ + 2 * kQBytes;
-  static constexpr int kV = kK + kKBytes;
-  static constexpr int kShared = kV + kKBytes;  // a CartShared
-  static constexpr int kAlloc = kShared + 128;  // starts 1024-aligned (checked at entry)
+  static constexpr int kK = kQ + 2 * kQBytes;  // two of each
+  static constexpr int kV = kK + 2 * kKBytes;
+  static constexpr int kShared = kV + 2 * kKBytes;  // a CartShared
+  static constexpr int kAlloc = kShared + 256;  // starts 1024-aligned (checked at entry)
 };
 
 enum CartBar {
-  kCKFull = 0,
-  kCKEmpty,
-  kCVFull,
-  kCSFull0,                   // S of buffer x is in TMEM
+  kCKFull0 = 0,               // keys of buffer x have landed
+  kCKEmpty0 = kCKFull0 + 2,   // ... have been read
+  kCVFull0 = kCKEmpty0 + 2,   // values, the same
+  kCVEmpty0 = kCVFull0 + 2,
+  kCSFull0 = kCVEmpty0 + 2,   // S of buffer x is in TMEM
   kCPFull0 = kCSFull0 + 2,    // its weights are (128 arrivals); by buffer, since those
                               // of the next tile may come before these are waited for
-  kCPvDone = kCPFull0 + 2,    // O has them, and V has been read
+  kCPvDone = kCPFull0 + 2,    // O has a tile's
   kCODone,                    // O has those of the piece's last tile (waits for this one
                               // may come two tiles after the last for the one before)
   kCDrain,
@@ -143,7 +146,7 @@ struct CartShared {
   uint32_t tmem;
   int abort, first;
 };
-static_assert(sizeof(CartShared) <= 128, "cart barrier area");
+static_assert(sizeof(CartShared) <= 256, "cart barrier area");
 
 struct CartMaps {
   CUtensorMap k, v;
@@ -184,14 +187,15 @@ __global__ void __launch_bounds__(kCartThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem, tO = tmem, tS = tmem + 128;
-  const int total = a.Hkv * a.row_tiles * a.key_tiles;
-  const int lo = min(blockIdx.x * a.cart_chunk, total), hi = min(lo + a.cart_chunk, total);
+  const int total = a.Hkv * a.row_tiles * a.cart_parts;
+  const int lo = min(blockIdx.x * a.cart_each, total), hi = min(lo + a.cart_each, total);
   const int R = a.B * a.G;
   int step = 0, pieces = 0;  // tiles walked, and pieces that had any, in every role
   bool ok = true;
-  for (int u = lo; u < hi;) {
-    const int seg = u / a.key_tiles, t0 = u - seg * a.key_tiles;
-    const int t1 = min(t0 + hi - u, a.key_tiles);
+  const int least = a.key_tiles / a.cart_parts, over = a.key_tiles - least * a.cart_parts;
+  for (int u = lo; u < hi; ++u) {
+    const int seg = u / a.cart_parts, part = u - seg * a.cart_parts;
+    const int t0 = part * least + min(part, over), t1 = t0 + least + (part < over);
     const int g = seg / a.row_tiles, row0 = (seg - g * a.row_tiles) * kTile;
     // ---- the tile's queries, rotated, as two terms; what they see.  D / 16 threads
     // have a row, pairs 8c .. 8c + 7 each; the angles, which a conversation's heads
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(kCartThreads, 2)
     if (threadIdx.x == 0) sh.first = 0x7fffffff;
     constexpr int kChunks = HALF / 8, kAhead = 2;  // loads that a thread has in flight
     const int rows = min(R - row0, kTile), turn_rows = a.G >= 3 ? kTile : 32;
-    static_assert((kTile / 3 + 2) * HALF * 8 <= 2 * L::kKBytes && 32 * HALF * 8 <= 2 * L::kKBytes,
+    static_assert((kTile / 3 + 2) * HALF * 8 <= 4 * L::kKBytes && 32 * HALF * 8 <= 4 * L::kKBytes,
                   "angles of a turn's conversations");
     float2* const angles = reinterpret_cast<float2*>(smem + L::kK);
     const uint32_t qs = smem_u32(smem + L::kQ);
@@ -292,31 +296,33 @@ __global__ void __launch_bounds__(kCartThreads, 2)
         int s = step;
         for (int t = t0; t < t1 && ok; ++t) {
           if (!seen(t)) continue;
-          if (s >= 1)
-            ok = mbar_wait(&bars[kCKEmpty], (s - 1) & 1, abort_s, a.status, kDevErrTimeoutTma);
+          const int x = s & 1;
+          const uint32_t last = ((s >> 1) - 1) & 1;
+          if (s >= 2)
+            ok = mbar_wait(&bars[kCKEmpty0 + x], last, abort_s, a.status, kDevErrTimeoutTma);
           if (!ok) break;
-          mbar_arrive_expect_tx(&bars[kCKFull], L::kKBytes);
+          mbar_arrive_expect_tx(&bars[kCKFull0 + x], L::kKBytes);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(smem + L::kK + h * 8192, &maps.k, &bars[kCKFull], h * 64, g, t * kCartKeys,
-                        0);
-          if (s >= 1)
-            ok = mbar_wait(&bars[kCPvDone], (s - 1) & 1, abort_s, a.status, kDevErrTimeoutTma);
+            tma_load_4d(smem + L::kK + x * L::kKBytes + h * kCartKeys * 128, &maps.k,
+                        &bars[kCKFull0 + x], h * 64, g, t * kCartKeys, 0);
+          if (s >= 2)
+            ok = mbar_wait(&bars[kCVEmpty0 + x], last, abort_s, a.status, kDevErrTimeoutTma);
           if (!ok) {
-            mbar_wait(&bars[kCKFull], s & 1, 0u, nullptr, 0);
+            mbar_wait(&bars[kCKFull0 + x], (s >> 1) & 1, 0u, nullptr, 0);
             break;
           }
-          mbar_arrive_expect_tx(&bars[kCVFull], L::kKBytes);
+          mbar_arrive_expect_tx(&bars[kCVFull0 + x], L::kKBytes);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(smem + L::kV + h * 8192, &maps.v, &bars[kCVFull], h * 64, g,
-                        t * kCartKeys, 0);
+            tma_load_4d(smem + L::kV + x * L::kKBytes + h * kCartKeys * 128, &maps.v,
+                        &bars[kCVFull0 + x], h * 64, g, t * kCartKeys, 0);
           ++s;
         }
         // (whatever went wrong: the last copies land before the CTA ends)
-        if (s > step) {
-          mbar_wait(&bars[kCKFull], (s - 1) & 1, 0u, nullptr, 0);
-          mbar_wait(&bars[kCVFull], (s - 1) & 1, 0u, nullptr, 0);
+        for (int i = max(s - 2, step); i < s; ++i) {
+          mbar_wait(&bars[kCKFull0 + (i & 1)], (i >> 1) & 1, 0u, nullptr, 0);
+          mbar_wait(&bars[kCVFull0 + (i & 1)], (i >> 1) & 1, 0u, nullptr, 0);
         }
       }
       __syncwarp();
@@ -329,40 +335,44 @@ __global__ void __launch_bounds__(kCartThreads, 2)
       const uint32_t idPV = idesc_bf16(128, D, false, true);
       const uint64_t dQ = sdesc_sw128(smem_u32(smem + L::kQ), 16u, 1024u);
       const uint64_t dK = sdesc_sw128(smem_u32(smem + L::kK), 16u, 1024u);
-      const uint64_t dV = sdesc_sw128(smem_u32(smem + L::kV), 8192u, 1024u);
+      const uint64_t dV = sdesc_sw128(smem_u32(smem + L::kV), kCartKeys * 128u, 1024u);
       auto issue_s = [&](int s) {
+        const uint64_t dk = desc_add(dK, (s & 1) * L::kKBytes);
 #pragma unroll
         for (int m = 1; m >= 0; --m)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            umma_bf16_ss_w(tS + (s & 1) * kCartKeys,
+            umma_bf16_ss_w(tS + (s & 1) * kCartSColumns,
                            desc_add(dQ, m * L::kQBytes + (k >> 2) * 16384 + (k & 3) * 32),
-                           desc_add(dK, (k >> 2) * 8192 + (k & 3) * 32), idS,
+                           desc_add(dk, (k >> 2) * kCartKeys * 128 + (k & 3) * 32), idS,
                            m == 1 && k == 0 ? 0u : 1u);
         umma_commit_w(&bars[kCSFull0 + (s & 1)]);
-        umma_commit_w(&bars[kCKEmpty]);
+        umma_commit_w(&bars[kCKEmpty0 + (s & 1)]);
       };
       for (int t = 0; t < n && ok; ++t) {
         const int s = step + t;
         if (t == 0) {
-          ok = wait(&bars[kCKFull], s & 1);
+          ok = wait(&bars[kCKFull0 + (s & 1)], (s >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           issue_s(s);
         }
         if (t + 1 < n) {  // over the weights of tile t - 1, read by the product before
-          ok = wait(&bars[kCKFull], (s + 1) & 1);
+          ok = wait(&bars[kCKFull0 + ((s + 1) & 1)], ((s + 1) >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           issue_s(s + 1);
         }
-        ok = wait(&bars[kCVFull], s & 1) && wait(&bars[kCPFull0 + (s & 1)], (s >> 1) & 1);
+        ok = wait(&bars[kCVFull0 + (s & 1)], (s >> 1) & 1) &&
+             wait(&bars[kCPFull0 + (s & 1)], (s >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < kCartKeys / 16; ++k)
-          umma_bf16_ts_w(tO, tS + (s & 1) * kCartKeys + k * 8, desc_add(dV, k * 2048), idPV,
+          umma_bf16_ts_w(tO, tS + (s & 1) * kCartSColumns + k * 8,
+                         desc_add(dV, (s & 1) * L::kKBytes + k * 2048), idPV,
                          t > 0 || k > 0 ? 1u : 0u);
+        umma_commit_w(&bars[kCVEmpty0 + (s & 1)]);
         umma_commit_w(&bars[kCPvDone]);
         if (t == n - 1) umma_commit_w(&bars[kCODone]);
       }
@@ -381,42 +391,36 @@ __global__ void __launch_bounds__(kCartThreads, 2)
         ok = wait(&bars[kCSFull0 + (s & 1)], (s >> 1) & 1, kDevErrTimeoutSoftmax);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t ts = tS + (s & 1) * kCartKeys + lane_off;
+        const uint32_t ts = tS + (s & 1) * kCartSColumns + lane_off;
         // the row sees the keys up to `end` that are sinks or in its window
         const int k0 = t * kCartKeys;
         const int end = first == 0x7fffffff ? 0 : min(a.p - k0, kCartKeys);
         const int from = first > k0 ? min(first - k0, kCartKeys) : 0;
         const int sink = min(max(a.sinks - k0, 0), kCartKeys);
         const bool cut = __any_sync(0xffffffffu, end < kCartKeys || from > sink);
-        // (S is read twice, half a tile at a time, to spare registers)
-        auto load = [&](int half, uint32_t (&r)[32]) {
-          tmem_ld32(ts + 32 * half, r);
+        float v[kCartKeys];
+        {
+          uint32_t r[32], z[16];
+          tmem_ld32(ts, r);
+          tmem_ld16(ts + 32, z);
           tmem_ld_wait();
           tmem_reg_fence(r);
-          if (cut) {
+          tmem_reg_fence16(z);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int k = 32 * half + c;
-              if (k >= end || (k < from && k >= sink)) r[c] = __float_as_uint(-INFINITY);
-            }
-          }
-        };
-        float top = -INFINITY;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r[32];
-          load(half, r);
-          float mx[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            mx[q] = __uint_as_float(r[16 * q]);
-#pragma unroll
-            for (int c = 1; c < 15; c += 2)
-              mx[q] = fmax3(mx[q], __uint_as_float(r[16 * q + c]), __uint_as_float(r[16 * q + c + 1]));
-            mx[q] = fmaxf(mx[q], __uint_as_float(r[16 * q + 15]));
-          }
-          top = fmax3(top, mx[0], mx[1]);
+          for (int c = 0; c < kCartKeys; ++c) v[c] = __uint_as_float(c < 32 ? r[c & 31] : z[c & 15]);
         }
+        if (cut) {
+#pragma unroll
+          for (int c = 0; c < kCartKeys; ++c)
+            if (c >= end || (c < from && c >= sink)) v[c] = -INFINITY;
+        }
+        float mx[2] = {v[0], v[1]};
+#pragma unroll
+        for (int c = 2; c < kCartKeys - 2; c += 4) {
+          mx[0] = fmax3(mx[0], v[c], v[c + 1]);
+          mx[1] = fmax3(mx[1], v[c + 2], v[c + 3]);
+        }
+        float top = fmax3(fmaxf(mx[0], mx[1]), v[kCartKeys - 2], v[kCartKeys - 1]);
         top *= a.scale_log2;
         // (the maximum is renewed where it grows by more than 8: weights stay
         // below 2^8)
@@ -430,19 +434,16 @@ __global__ void __launch_bounds__(kCartThreads, 2)
         const float mr = m == -INFINITY ? 0.f : m;  // (nothing seen yet: weights 0)
         const float2 nm2 = make_float2(-mr, -mr);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pk[kCartKeys / 2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r[32], pk[16];
-          load(half, r);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float2 x = __ffma2_rn(u2f2(r[2 * c], r[2 * c + 1]), sc2, nm2);
-            const float2 w = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-            sum[c & 1] = __fadd2_rn(sum[c & 1], w);
-            pk[c] = pack_bf16x2(w.x, w.y);
-          }
-          tmem_st16(ts + 16 * half, pk);  // (over columns that have been read)
+        for (int c = 0; c < kCartKeys / 2; ++c) {
+          const float2 x = __ffma2_rn(make_float2(v[2 * c], v[2 * c + 1]), sc2, nm2);
+          const float2 w = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+          sum[c & 1] = __fadd2_rn(sum[c & 1], w);
+          pk[c] = pack_bf16x2(w.x, w.y);
         }
+        tmem_st16(ts, pk);  // (over columns that have been read)
+        tmem_st16(ts + kCartKeys / 2 - 16, pk + kCartKeys / 2 - 16);
         l = l * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
         if (__any_sync(0xffffffffu, rescale)) {
           ok = wait(&bars[kCPvDone], (s - 1) & 1, kDevErrTimeoutSoftmax);
@@ -468,12 +469,13 @@ __global__ void __launch_bounds__(kCartThreads, 2)
         // them need not be 0
         const int z0 = max(a.sinks - k0, 0), z1 = min(low - k0, kCartKeys);
         if (z0 < z1) {
-          ok = wait(&bars[kCVFull], s & 1, kDevErrTimeoutSoftmax);
+          ok = wait(&bars[kCVFull0 + (s & 1)], (s >> 1) & 1, kDevErrTimeoutSoftmax);
           if (!ok) break;
-          const uint32_t vs = smem_u32(smem + L::kV);
+          const uint32_t vs = smem_u32(smem + L::kV + (s & 1) * L::kKBytes);
           for (int e = row; e < (z1 - z0) * (D / 8); e += 128) {
             const int j = z0 + e / (D / 8), c = e % (D / 8);
-            sts_u4(vs + (c >> 3) * 8192 + j * 128 + (c & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+            sts_u4(vs + (c >> 3) * kCartKeys * 128 + j * 128 + (c & 7) * 16,
+                   make_uint4(0u, 0u, 0u, 0u));
           }
           fence_proxy_async_smem();
         }
@@ -483,8 +485,7 @@ __global__ void __launch_bounds__(kCartThreads, 2)
         ++i;
       }
       // ---- the piece's part: column blocks of four by row
-      const int part = blockIdx.x - seg * a.key_tiles / a.cart_chunk;
-      const long long slot = static_cast<long long>(seg) * a.cart_parts + part;
+      const long long slot = u;
       if (ok && n > 0) ok = wait(&bars[kCODone], pieces & 1, kDevErrTimeoutEpilogue);
       if (ok) {
         tc_fence_after();
@@ -514,7 +515,6 @@ __global__ void __launch_bounds__(kCartThreads, 2)
     }
     step += n;
     pieces += n > 0;
-    u += t1 - t0;
     // every role is done with the piece's Q, barriers and O; one that gave up
     // ends them all
     ok = !__syncthreads_or(!ok);
@@ -1190,7 +1190,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
     step_join_kernel(const __grid_constant__ StepArgs a, const __grid_constant__ Turns f) {
   constexpr int HALF = D / 2;
   __shared__ float fresh[kJoinHeads], total[kJoinHeads];
-  __shared__ int cart_n[kJoinHeads];
   __shared__ long long cart_at[kJoinHeads];
   __shared__ float4 acc[kJoinThreads];
   __shared__ float weight[kJoinHeads][kJoinParts];
@@ -1247,13 +1246,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       *reinterpret_cast<uint4*>(a.v_pages + at + tid * 8) =
           __ldg(reinterpret_cast<const uint4*>(a.v_new + from + tid * 8));
   }
-  // ---- parts of the cartridge, by the tile that holds the query's row (the first
-  // one's place in cart_lse, their number)
+  // ---- parts of the cartridge, by the tile that holds the query's row: the first
+  // one's place in cart_lse
   if (tid < nq) {
     const int R = b * a.G + tid % a.G, seg = (g0 + tid / a.G) * a.row_tiles + R / kTile;
-    const int u = seg * a.key_tiles;
-    cart_n[tid] =
-        a.key_tiles > 0 ? (u + a.key_tiles - 1) / a.cart_chunk - u / a.cart_chunk + 1 : 0;
     cart_at[tid] = static_cast<long long>(seg) * a.cart_parts * kTile + R % kTile;
   }
   const int unit = g0 / a.heads, cost = cost_of(tiles_of(a, s.n));
@@ -1267,7 +1263,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
   const int c0 = static_cast<int>(div_units(u0 + kStart, chunk));
   const int c1 = cost > 0 ? static_cast<int>(div_units(u0 + cost - 1, chunk)) : c0 - 1;
   const bool opens = u0 <= c0 * chunk;  // the unit's first tile is its run's first
-  const int n_row = (c1 - c0 + 1) << groups_log2;
+  const int n_row = (c1 - c0 + 1) << groups_log2, n = n_row + a.cart_parts;
   auto row_part = [&](int q, int i) -> long long {
     const int c = c0 + (i >> groups_log2), k = i & (a.groups - 1);
     const long long slot = c0 == c1 ? 2 * a.row_ctas + static_cast<long long>(b) * a.units + unit
@@ -1287,7 +1283,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
   };
   __syncthreads();
   for (int q = warp; q < nq; q += kJoinThreads / 32) {
-    const int n = n_row + cart_n[q];
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i <= n; i += 32) {
       const float x = i < n ? lse_of(q, i) : fresh[q], top = fmaxf(m, x);
@@ -1324,8 +1319,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       for (int q = tid * a.G; q < (tid + 1) * a.G; ++q) x += exp2_approx(fresh[q] - total[q]);
       a.weights[(static_cast<long long>(b) * a.Hkv + g0 + tid) * a.weight_rows + s.row] = x;
     }
-    int most = 0;
-    for (int q = 0; q < nq; ++q) most = max(most, n_row + cart_n[q]);
     const int cols = nq * (D / 4), each = max(kJoinThreads / cols, 1);
     const int turn = tid / cols;  // (below `each`, or idle; 0 where there are more columns)
     for (int col0 = 0; col0 < cols; col0 += kJoinThreads) {
@@ -1336,21 +1329,21 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
                                                a.v_new + from + q / a.G * D + 4 * j))
                                          : make_uint2(0u, 0u);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = 0; i0 < most; i0 += kJoinParts) {
-        if (most > kJoinParts && (col0 > 0 || i0 > 0)) {  // (the first ones are there)
+      for (int i0 = 0; i0 < n; i0 += kJoinParts) {
+        if (n > kJoinParts && (col0 > 0 || i0 > 0)) {  // (the first ones are there)
           __syncthreads();
           for (int e = tid; e < nq * kJoinParts; e += kJoinThreads) {
             const int qq = e / kJoinParts, k = e % kJoinParts, i = i0 + k;
-            if (i >= n_row + cart_n[qq]) continue;
+            if (i >= n) continue;
             weight[qq][k] = exp2_approx(lse_of(qq, i) - total[qq]);
             place[qq][k] = place_of(qq, i);
           }
           __syncthreads();
         }
         if (mine) {
-          const int n = min(n_row + cart_n[q] - i0, kJoinParts);
+          const int here = min(n - i0, kJoinParts);
 #pragma unroll 8
-          for (int k = turn; k < n; k += each) {
+          for (int k = turn; k < here; k += each) {
             const float w = weight[q][k];
             const float4 v = __ldcg(place[q][k] + (i0 + k < n_row ? j : j * kTile));
             // (a part of no weight may hold anything)
@@ -1433,36 +1426,40 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
 
 struct StepWs {
   size_t cart_o, cart_lse, row_o, row_lse, starts, logits, total;
-  int row_tiles, key_tiles, cart_chunk, cart_parts, cart_ctas;
+  int row_tiles, key_tiles, cart_parts, cart_each, cart_ctas;
   int heads, units, groups, row_ctas;
 };
 
-// Key tiles of a run of the cartridge's kernel: as many SMs are its as let both
-// kernels end together, going by what they were seen to take side by side, the
-// tables half full (`row_bytes`: their keys and values).  A run of c tiles takes
-// 17 us + 8 us a piece + 2 us a tile; the rows 8 us + their bytes at 0.05 TB/s an
-// SM, 6.3 TB/s at most.  So runs that divide a row tile's key tiles are preferred:
-// at 96 conversations, 768 tiles in segments of 32, 22 / 24 / 28 SMs took 88 / 78 /
-// 80 us in all, at 200 (704 in segments of 16) 20 / 22 / 24 took 96 / 94.5 / 96.7,
-// at 4 of up to 32k rows (1024 in segments of 128) 16 / 26 / 48 took 131 / 117 / 123.
-int cart_chunk_of(int tiles, int key_tiles, double row_bytes, int sms) {
-  int best = tiles;
+struct CartCut {
+  int parts, each;
+};
+// Pieces that the key tiles of a (kv head, row tile), a segment, are cut into, and
+// how many a CTA has: as many SMs are the cartridge's kernel's as let both kernels
+// end together, going by what they were seen to take side by side, the tables half
+// full (`row_bytes`: their keys and values).  A CTA takes 16 us + 8 us a piece + 1.1
+// us a tile; the rows 8 us + their bytes at 0.05 TB/s an SM, 6.3 TB/s at most; and
+// a piece 0.3 us where it is joined.  In all, at 96 conversations (24 segments of 43
+// tiles), 1 / 2 / 3 / 4 pieces of one a CTA took 87.4 / 75.3 / 78.3 / 83 us, at 200 (44
+// of 22) 93 / 99 / 116 / 145, at 4 of up to 32k rows (8 of 171) 3 / 5 / 7 126 / 119.4 /
+// 119.1, at one of 200 (8 of 11) 1 / 3 / 5 / 11 26.8 / 20.5 / 19.5 / 21.1.
+CartCut cart_cut(int segments, int key_tiles, double row_bytes, int sms) {
+  CartCut best{1, segments};
   double best_us = 0.0, best_cart = 0.0;
-  for (int c = 1; c < std::max(sms, 2); c += c < 2 ? 1 : 2) {
-    const int chunk = (tiles + 2 * c - 1) / (2 * c);
-    const int pieces = key_tiles % chunk == 0 ? 1
-                       : chunk % key_tiles == 0 ? chunk / key_tiles
-                                                : chunk / key_tiles + 2;
-    const int left = sms - ((tiles + chunk - 1) / chunk + 1) / 2;
-    const double cart = 17.0 + 8.0 * pieces + 2.0 * chunk;
-    const double rows = 8.0 + row_bytes * 1e-6 / std::min(0.05 * std::max(left, 1), 6.3);
-    const double us = std::max(cart, rows);
-    if (c == 1 || us < best_us || (us == best_us && cart < best_cart)) {
-      best = chunk;
-      best_us = us;
-      best_cart = cart;
+  const int most = std::max(2 * (sms - 1), 1);  // CTAs
+  for (int n = 1; n <= key_tiles && n <= std::max(most / segments, 4); ++n) {
+    const int tiles = (key_tiles + n - 1) / n, pieces = segments * n;
+    for (int each = (pieces + most - 1) / most; each <= pieces; ++each) {
+      const int ctas = (pieces + each - 1) / each, left = sms - (ctas + 1) / 2;
+      const double cart = 16.0 + each * (8.0 + 1.1 * tiles);
+      const double rows = 8.0 + row_bytes * 1e-6 / std::min(0.05 * std::max(left, 1), 6.3);
+      const double us = std::max(cart, rows) + 0.3 * n;
+      if (best_us == 0.0 || us < best_us || (us == best_us && cart < best_cart)) {
+        best = CartCut{n, each};
+        best_us = us;
+        best_cart = cart;
+      }
+      if (cart > best_us) break;  // (and longer with more each)
     }
-    if (chunk == 1) break;
   }
   return best;
 }
@@ -1479,11 +1476,13 @@ StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
   const int sms = std::max(sm_count(), 1), G = Hq / Hkv;
   w.row_tiles = (B * G + kTile - 1) / kTile;
   w.key_tiles = (p + kCartKeys - 1) / kCartKeys;
-  const int tiles = Hkv * w.row_tiles * w.key_tiles;
-  if (tiles > 0) {
-    w.cart_chunk = cart_chunk_of(tiles, w.key_tiles, static_cast<double>(B) * Hkv * d * 2 * cap, sms);
-    w.cart_ctas = (tiles + w.cart_chunk - 1) / w.cart_chunk;
-    w.cart_parts = (w.key_tiles + w.cart_chunk - 1) / w.cart_chunk + 1;
+  if (w.key_tiles > 0) {
+    const int segments = Hkv * w.row_tiles;
+    const CartCut cut =
+        cart_cut(segments, w.key_tiles, static_cast<double>(B) * Hkv * d * 2 * cap, sms);
+    w.cart_parts = cut.parts;
+    w.cart_each = cut.each;
+    w.cart_ctas = (segments * cut.parts + cut.each - 1) / cut.each;
   }
   w.heads = Hkv > 2 ? 4 : Hkv;  // (a unit's heads beyond the last one are not read)
   w.units = (Hkv + w.heads - 1) / w.heads;
@@ -1631,8 +1630,8 @@ int cart_attn_decode_paged(int B, int window, int sinks, int Hq, int Hkv, int d,
   a.status = device_status_ptr();
   a.row_tiles = w.row_tiles;
   a.key_tiles = w.key_tiles;
-  a.cart_chunk = w.cart_chunk;
   a.cart_parts = w.cart_parts;
+  a.cart_each = w.cart_each;
   a.cart_o = reinterpret_cast<float*>(ws + w.cart_o);
   a.cart_lse = reinterpret_cast<float*>(ws + w.cart_lse);
   a.heads = w.heads;
