@@ -285,7 +285,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // that stay is looked for; then a list of rows that stay.
 template <int T>
 struct MoveShared {
-  static constexpr int kRows = 4 * T, kKeys = (T == 256 ? 6 : 10) * kRows;
+  static constexpr int kRows = 6 * T, kKeys = (T == 256 ? 6 : 7) * kRows;
   static constexpr int kLoads = 512 / T;  // 16-byte pieces of K, and of V, a thread and turn
   union {
     uint32_t keys[kKeys];
@@ -323,11 +323,11 @@ __device__ __forceinline__ uint2 move_scan(uint32_t v, uint32_t* sums) {
 // Block (layer, conversation, kv head): the weight of the last row that stays
 // by a search over its 32 bits, eight at a time from the top (a histogram of
 // the rows that agree so far), then the rows in order: a list of those that
-// stay, T rows looked at a time, then its moves.  Row i of those that stay is
+// stay, 4 T rows looked at a time, then its moves.  Row i of those that stay is
 // never before place i, so a row may be written once all up to it have been
 // read, whatever is read later: a turn's rows are asked for before those of the
 // turn before are written.  Bound by HBM where there are many blocks: 16 layers of
-// 64 conversations and 8 kv heads from up to 1100 rows to 512 take 339 us, as long
+// 64 conversations and 8 kv heads from up to 1100 rows to 512 take 338 us, as long
 // as a copy of the rows that move; by latency where there are few.  (The bounds'
 // second part is left open for 256 threads: a 1 there costs 10%.)
 template <int T>
@@ -348,6 +348,18 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 0)
   const int last = w ? min(a.recent, q.keep - q.first) : q.keep - q.first;
   const int m0 = q.first, m1 = q.len - last;        // the rows between
   const int stay = q.keep - q.first - last;         // and how many of them stay
+  // the weights of four rows (r a multiple of 4)
+  const bool wide = (a.weight_rows & 3) == 0;
+  auto weights_at = [&](int r) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!w || r >= q.len) return x;
+    if (wide) return *reinterpret_cast<const float4*>(w + r);
+    x.x = w[r];
+    if (r + 1 < q.len) x.y = w[r + 1];
+    if (r + 2 < q.len) x.z = w[r + 2];
+    if (r + 3 < q.len) x.w = w[r + 3];
+    return x;
+  };
   uint32_t cut = 0xffffffffu, ties = 0;  // rows of a higher key stay, and so many of this key
   bool any = false;
   if (stay > 0) {
@@ -358,16 +370,24 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 0)
       if (tid < 256) sh.hist[tid] = 0;
       __syncthreads();
       const uint32_t above = shift == 24 ? 0 : 0xffffffffu << (shift + 8);
-#pragma unroll 4
-      for (int i = m0 + tid; i < m1; i += T) {
-        uint32_t key;
-        if (shift == 24 || !cached) {
-          key = weight_key(w[i]);
-          if (cached) sh.keys[i - m0] = key;
-        } else {
-          key = sh.keys[i - m0];
-        }
+      auto count = [&](uint32_t key) {
         if ((key & above) == prefix) atomicAdd(sh.hist + (key >> shift & 255), 1);
+      };
+      if (shift == 24 || !cached) {
+#pragma unroll 2
+        for (int i = (m0 & ~3) + 4 * tid; i < m1; i += 4 * T) {
+          const float4 x = weights_at(i);
+          const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (i + u < m0 || i + u >= m1) continue;
+            const uint32_t key = weight_key(y[u]);
+            if (cached) sh.keys[i + u - m0] = key;
+            count(key);
+          }
+        }
+      } else {
+        for (int i = tid; i < m1 - m0; i += T) count(sh.keys[i]);
       }
       __syncthreads();
       const uint32_t mine = tid < 256 ? sh.hist[255 - tid] : 0;
@@ -395,32 +415,40 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 0)
   const int begin = q.first & ~mask;
   above = begin;
   auto& list = sh.list;
-  float ahead = w && begin + tid < q.len ? w[begin + tid] : 0.f;
+  float4 ahead = weights_at(begin + 4 * tid);
   for (int r0 = begin; r0 < q.len;) {
     const int base = static_cast<int>(above + min(equal, ties));  // the list's first place
     int n = 0;
-    for (; r0 < q.len && n + T <= MoveShared<T>::kRows; r0 += T) {
-      const int r = r0 + tid;
-      const float x = ahead;
-      if (w && r + T < q.len) ahead = w[r + T];
-      bool more = false, same = false;
-      if (r < q.len) {
-        if (r < m0 || r >= m1) {
-          more = true;
+    for (; r0 < q.len && n + 4 * T <= MoveShared<T>::kRows; r0 += 4 * T) {
+      const int r = r0 + 4 * tid;
+      const float x[4] = {ahead.x, ahead.y, ahead.z, ahead.w};
+      ahead = weights_at(r + 4 * T);
+      uint32_t more = 0, same = 0;  // by row
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (r + u >= q.len) continue;
+        if (r + u < m0 || r + u >= m1) {
+          more |= 1u << u;
         } else if (any) {
-          const uint32_t key = weight_key(x);
-          more = key > cut;
-          same = key == cut;
+          const uint32_t key = weight_key(x[u]);
+          more |= static_cast<uint32_t>(key > cut) << u;
+          same |= static_cast<uint32_t>(key == cut) << u;
         }
       }
-      // both counts in one scan: at most T of each
-      const uint2 s =
-          move_scan<T>(static_cast<uint32_t>(more) | static_cast<uint32_t>(same) << 16, sums);
-      const uint32_t more_to = above + (s.x & 0xffff), same_to = equal + (s.x >> 16);
-      if (more || (same && same_to <= ties)) {
-        const int i = static_cast<int>(more_to + min(same_to, ties)) - 1 - base;
-        list.row[i] = r;
-        list.weight[i] = x;
+      // both counts in one scan: at most 4 T of each
+      const uint32_t mine = __popc(more) | __popc(same) << 16;
+      const uint2 s = move_scan<T>(mine, sums);
+      uint32_t more_to = above + ((s.x - mine) & 0xffff), same_to = equal + ((s.x - mine) >> 16);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool is_more = more >> u & 1, is_same = same >> u & 1;
+        more_to += is_more;
+        same_to += is_same;
+        if (is_more || (is_same && same_to <= ties)) {
+          const int i = static_cast<int>(more_to + min(same_to, ties)) - 1 - base;
+          list.row[i] = r + u;
+          list.weight[i] = x[u];
+        }
       }
       above += s.y & 0xffff;
       equal += s.y >> 16;
@@ -611,9 +639,9 @@ int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtype, void* 
   evict_plan_kernel<<<kMetaCtas, kMetaThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    // Blocks that the SMs take two at a time have more threads: 177 us against 284
-    // with 192 blocks and up to 20000 rows (17.1 against 18.5 us with 12 of 200);
-    // with 8192 blocks and 1100 rows 457 against 339.
+    // Blocks that the SMs take two at a time have more threads: 160 us against 183
+    // with 192 blocks and up to 20000 rows (19.8 against 18.5 with 12 of 200); with
+    // 8192 blocks and 1100 rows 372 against 338.
     e = blocks * Hkv <= 2 * sm_count()
             ? launch_moves<512>(static_cast<unsigned>(blocks * Hkv), st, a)
             : launch_moves<256>(static_cast<unsigned>(blocks * Hkv), st, a);
