@@ -101,6 +101,13 @@ struct StepOf {
   int row, low, high, g_low, g_high, n;
   __device__ __forceinline__ int group(int i) const { return i < g_low ? i : i - g_low + g_high; }
   __device__ __forceinline__ bool sees(int r) const { return r < row && (r < low || r >= high); }
+  // ... rows r .. r + 31, a bit each
+  __device__ __forceinline__ unsigned sees32(int r) const {
+    auto below = [&](int x) {
+      return x - r >= 32 ? 0xffffffffu : x > r ? (1u << (x - r)) - 1 : 0u;
+    };
+    return below(row) & (below(low) | ~below(high));
+  }
 };
 __device__ __forceinline__ StepOf step_of(const StepArgs& a, int b) {
   StepOf s;
@@ -764,19 +771,6 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       left -= end - at;
       // (what is left holds tiles if it is more than a start)
       const bool more = left > kStart;
-      // the next conversation's, before they are needed
-      const StepOf next = unit + 1 == a.units && b + 1 < a.B ? step_of(a, b + 1) : s;
-      // the piece's slot: the run's first piece, its last one, or a whole unit
-      const bool goes_on = t1 < all;
-      const int slot = t0 > 0 || (goes_on && n == 0) ? 2 * blockIdx.x
-                       : goes_on                     ? 2 * blockIdx.x + 1
-                                                     : 2 * a.row_ctas + b * a.units + unit;
-      if (t0 < t1) {  // its queries on their way to L2
-        const int heads = min(a.heads, a.Hkv - h0);
-        const char* q = reinterpret_cast<const char*>(
-            a.q + (static_cast<long long>(b) * a.Hq + h0 * a.G) * D);
-        for (int e = lane * 128; e < heads * a.G * D * 2; e += 32 * 128) prefetch_l2(q + e);
-      }
       const int* pages = a.pt.table + static_cast<long long>(b) * a.pt.max_pages;
       // a tile's boxes, a lane each: first row, and that row's page
       auto row_of = [&](int t) {
@@ -789,18 +783,23 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                    : __ldg(pages + (r >> a.pt.page_log2));
       };
       int row = row_of(t0), page = look_up(row);
+      // the next conversation's, before they are needed
+      const StepOf next = unit + 1 == a.units && b + 1 < a.B ? step_of(a, b + 1) : s;
+      // the piece's slot: the run's first piece, its last one, or a whole unit
+      const bool goes_on = t1 < all;
+      const int slot = t0 > 0 || (goes_on && n == 0) ? 2 * blockIdx.x
+                       : goes_on                     ? 2 * blockIdx.x + 1
+                                                     : 2 * a.row_ctas + b * a.units + unit;
+      if (t0 < t1 && n > 0) {  // its queries on their way to L2 (the run's first are asked for)
+        const int heads = min(a.heads, a.Hkv - h0);
+        const char* q = reinterpret_cast<const char*>(
+            a.q + (static_cast<long long>(b) * a.Hq + h0 * a.G) * D);
+        for (int e = lane * 128; e < heads * a.G * D * 2; e += 32 * 128) prefetch_l2(q + e);
+      }
       for (int t = t0; t < t1; ++t, ++n) {
         const int row_next = t + 1 < t1 ? row_of(t + 1) : -1, page_next = look_up(row_next);
         const bool there = row >= 0 && is_page(page, a.pt.n_pages);
-        const int rows = small ? 16 : 32;
-        unsigned bits = 0;
-        if (there) {
-          bits = rows == 32 ? 0xffffffffu : 0xffffu;
-          if (row + rows > s.row || (row + rows > s.low && row < s.high)) {
-            bits = 0;
-            for (int i = 0; i < rows; ++i) bits |= static_cast<unsigned>(s.sees(row + i)) << i;
-          }
-        }
+        unsigned bits = there ? s.sees32(row) & (small ? 0xffffu : 0xffffffffu) : 0u;
         if (small) bits |= __shfl_down_sync(0xffffffffu, bits, 1) << 16;  // (even lanes')
         const unsigned boxes = __ballot_sync(0xffffffffu, there);
         // a K or V tile into the next slot
