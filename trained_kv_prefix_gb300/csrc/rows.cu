@@ -342,11 +342,8 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 0)
   MoveShared<T>& sh = *reinterpret_cast<MoveShared<T>*>(move_smem);
   constexpr int kLoads = MoveShared<T>::kLoads;
   uint32_t* const sums = sh.sums;
-  pdl_wait();
-  pdl_release();
   const int g = blockIdx.x % a.Hkv, lb = blockIdx.x / a.Hkv;
   const int b = lb % a.B, layer = lb / a.B, tid = threadIdx.x;
-  if (!__ldcg(a.go + b)) return;
   const Budget q = budget_of(a, b);
   float* w = a.weights ? a.weights + (static_cast<long long>(lb) * a.Hkv + g) * a.weight_rows
                        : nullptr;
@@ -367,7 +364,7 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 0)
   };
   uint32_t cut = 0xffffffffu, ties = 0;  // rows of a higher key stay, and so many of this key
   bool any = false;
-  if (stay > 0) {
+  if (stay > 0 && q.len > q.keep) {  // (needs nothing of the plan, and runs beside it)
     any = true;
     const bool cached = m1 - m0 <= MoveShared<T>::kKeys;
     uint32_t left = stay, prefix = 0;
@@ -408,6 +405,9 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 0)
     cut = prefix;
     ties = left;
   }
+  pdl_wait();
+  pdl_release();
+  if (!__ldcg(a.go + b)) return;
   const int* from_row = a.pt.table + static_cast<long long>(b) * a.pt.max_pages;
   const int* to_row = a.to + static_cast<long long>(b) * a.pt.max_pages;
   const int mask = (1 << a.pt.page_log2) - 1;
