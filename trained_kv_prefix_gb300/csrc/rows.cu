@@ -47,7 +47,7 @@ __device__ __forceinline__ int segment_of(const int* cu, int B, int t) {
 
 // Four tokens of the token axis per block: their page rows and angles first,
 // then 16-byte pieces, a key's with those d/2 further on.  Bound by HBM: 48
-// prompts of up to 2000 tokens of 8 x 128 take 73 us, 58 at a copy's rate.  Many
+// prompts of up to 2000 tokens of 8 x 128 take 73 us, at 85% of a copy's rate.  Many
 // small blocks carry it (32 registers, eight blocks an SM): with pieces asked for
 // before their places are known 88 us, keys and values in blocks of their own 85,
 // two tokens a block 112, eight 71 (but 27 tokens 7.5 us against 6.2).
@@ -332,7 +332,7 @@ __device__ __forceinline__ uint2 move_scan(uint32_t v, uint32_t* sums) {
 // never before place i, so a row may be written once all up to it have been
 // read, whatever is read later: a turn's rows are asked for before those of the
 // turn before are written.  Bound by HBM where there are many blocks: 16 layers of
-// 64 conversations and 8 kv heads from up to 1100 rows to 512 take 338 us, as long
+// 64 conversations and 8 kv heads from up to 1100 rows to 512 take 334 us, as long
 // as a copy of the rows that move; by latency where there are few.  (The bounds'
 // second part is left open for 256 threads: a 1 there costs 10%.)
 template <int T>
@@ -644,9 +644,9 @@ int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtype, void* 
   evict_plan_kernel<<<kMetaCtas, kMetaThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    // Blocks that the SMs take two at a time have more threads: 160 us against 183
-    // with 192 blocks and up to 20000 rows (19.8 against 18.5 with 12 of 200); with
-    // 8192 blocks and 1100 rows 372 against 338.
+    // Blocks that the SMs take two at a time have more threads: 153 us against 175
+    // with 192 blocks and up to 20000 rows (16.4 against 15.7 with 12 of 200); with
+    // 8192 blocks and 1100 rows 370 against 334.
     e = blocks * Hkv <= 2 * sm_count()
             ? launch_moves<512>(static_cast<unsigned>(blocks * Hkv), st, a)
             : launch_moves<256>(static_cast<unsigned>(blocks * Hkv), st, a);
