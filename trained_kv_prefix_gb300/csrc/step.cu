@@ -1208,7 +1208,9 @@ constexpr int kJoinHeads = kRowHeads * kMaxGroup;   // most query heads of a blo
 // logits (L2), one after the other; 12 us behind the last row of those
 // conversations.  (Blocks of a head each: 128 threads 88.0, 256 95, 512 102.7; of four
 // heads 512 threads 88.5 us in all, at an earlier state.)
-template <int D>
+// GQ as above: the fewer registers for four take 1.6 us off the 76.2 of 96
+// conversations.
+template <int D, int GQ>
 __global__ void __launch_bounds__(kJoinThreads, 2)
     step_join_kernel(const __grid_constant__ StepArgs a, const __grid_constant__ Turns f) {
   constexpr int HALF = D / 2;
@@ -1418,15 +1420,15 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       float* w = a.weights + bg * a.weight_rows + r;
       const bool all = wide && s.sees(r) && s.sees(r + 3) && (r >= s.high || r + 3 < s.low);
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      float4 x[kMaxGroup];
+      float4 x[GQ];
       if (all) y = *reinterpret_cast<const float4*>(w);
 #pragma unroll
-      for (int q = 0; q < kMaxGroup; ++q)
+      for (int q = 0; q < GQ; ++q)
         if (q < G)
           x[q] = __ldcg(reinterpret_cast<const float4*>(lg + static_cast<long long>(q) * a.cap));
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int q = 0; q < kMaxGroup; ++q)
+      for (int q = 0; q < GQ; ++q)
         if (q < G) {
           const float t = total[h * G + q];
           sum.x += exp2_approx(x[q].x - t);
@@ -1590,7 +1592,7 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
   const int deep = a.weights ? std::max(1, std::min((a.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads),
                                                     2 * sm_count() / (across * a.B) - 1) + 1)
                              : 1;
-  return launch_dependent(step_join_kernel<D>, dim3(across, a.B, deep), dim3(kJoinThreads), 0, st,
+  return launch_dependent(a.G > 4 ? step_join_kernel<D, 8> : step_join_kernel<D, 4>, dim3(across, a.B, deep), dim3(kJoinThreads), 0, st,
                           join, f);
 }
 
