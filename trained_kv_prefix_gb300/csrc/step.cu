@@ -931,7 +931,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           umma_bf16_ss_w(tO + w * 16, desc_add(dv, w * 4096 + k * 2048),
-                         desc_add(dp, (w >> 1) * 1024 + (w & 1) * 64 + k * 32), idO, (now & kOpens) && k == 0 ? 0u : 1u);
+                         desc_add(dp, (w >> 1) * 1024 + (w & 1) * 64 + k * 32), idO,
+                         (now & kOpens) && k == 0 ? 0u : 1u);
       umma_commit_w(&bars[kREmpty0 + sl]);
       umma_commit_w(&bars[kRPvDone]);
       if (now & kCloses) umma_commit_w(&bars[kRODone]);
@@ -1471,7 +1472,9 @@ CartCut cart_cut(int segments, int key_tiles, double row_bytes, int sms) {
   CartCut best{1, segments};
   double best_us = 0.0, best_cart = 0.0;
   const int most = std::max(2 * (sms - 1), 1);  // CTAs
-  for (int n = 1; n <= key_tiles && n <= std::max(most / segments, 4); ++n) {
+  // (where a CTA has several segments anyway, whole ones: less to join)
+  const int finest = segments >= 4 * most ? 1 : std::max(most / segments, 4);
+  for (int n = 1; n <= std::min(key_tiles, finest); ++n) {
     const int tiles = (key_tiles + n - 1) / n, pieces = segments * n;
     for (int each = (pieces + most - 1) / most; each <= pieces; ++each) {
       const int ctas = (pieces + each - 1) / each, left = sms - (ctas + 1) / 2;
@@ -1578,8 +1581,8 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
       return cudaErrorInvalidValue;
     e = set_shared_once<step_cart_kernel<D>>(C::kAlloc);
     if (e == cudaSuccess)
-      e = launch_dependent(step_cart_kernel<D>, dim3(w.cart_ctas), dim3(kCartThreads), C::kAlloc, st,
-                           cart, a, f);
+      e = launch_dependent(step_cart_kernel<D>, dim3(w.cart_ctas), dim3(kCartThreads), C::kAlloc,
+                           st, cart, a, f);
     if (e != cudaSuccess) return e;
   }
   // blocks of the joining kernel: a unit's heads each where that leaves enough of
@@ -1589,11 +1592,12 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
   const int across = (a.Hkv + join.join_heads - 1) / join.join_heads;
   // ... and as many for the rows' weights as the GPU takes at once, at most one for
   // every 4 * kJoinThreads rows that a table can name
-  const int deep = a.weights ? std::max(1, std::min((a.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads),
-                                                    2 * sm_count() / (across * a.B) - 1) + 1)
-                             : 1;
-  return launch_dependent(a.G > 4 ? step_join_kernel<D, 8> : step_join_kernel<D, 4>, dim3(across, a.B, deep), dim3(kJoinThreads), 0, st,
-                          join, f);
+  const int deep =
+      a.weights ? std::max(1, std::min((a.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads),
+                                       2 * sm_count() / (across * a.B) - 1) + 1)
+                : 1;
+  return launch_dependent(a.G > 4 ? step_join_kernel<D, 8> : step_join_kernel<D, 4>,
+                          dim3(across, a.B, deep), dim3(kJoinThreads), 0, st, join, f);
 }
 
 }  // namespace
