@@ -103,7 +103,9 @@ __device__ __forceinline__ Tiles column_tiles(const WeighArgs& a, int rows, int 
   }
   return tiles_of(a, a.p + rows - a.T + i0, a.p + rows - a.T + i1);
 }
-// A segment of n tiles is n + kStartUnits units of the schedule.
+// A segment of n tiles is n + kStartUnits units of the schedule (0 / 1 / 2 / 4: whole
+// prompts 147.5 / 144.4 / 143.2 / 143.0 us, 32 queries of 64 conversations 167 / 166.3 /
+// 166.3 / 165.3).
 constexpr int kStartUnits = 2;
 __device__ __forceinline__ int segment_units(int n) { return n > 0 ? n + kStartUnits : 0; }
 
