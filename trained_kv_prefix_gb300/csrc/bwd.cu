@@ -133,7 +133,10 @@ __device__ __forceinline__ void store_row_out(void* base, long long off, const f
 // Q and dO have rings of their own: a Q slot is released by dK(u), a dO
 // slot by dV(u).  Q gets three slots, so a Q tile is copied while two full
 // steps of MMAs run; dO gets two (its first reader, dP^T, comes later in the
-// step).  The step's -lse2 entries travel with Q, its -D entries with dO.
+// step).  A row vector travels with the tile whose release its last readers
+// come before: the step's -lse2 entries, read in the P phase, with dO (dV(u)
+// waits for every thread's P^T); its -D entries, read in the dS phase beside
+// dV(u), with Q (dK(u) waits for every thread's dS^T).
 // The layout fills the 227 KB limit, so it relies on the dynamic shared
 // memory starting 1024-byte aligned (checked at entry; no static shared
 // variables).
@@ -147,9 +150,9 @@ struct DkdvSmem {
   static constexpr int kV = kK + kTileBytes;                  // resident V
   static constexpr int kQ0 = kV + kTileBytes;                 // Q ring
   static constexpr int kDo0 = kQ0 + kDkdvQSlots * kTileBytes;  // dO ring
-  static constexpr int kVecL = kDo0 + kDkdvDoSlots * kTileBytes;  // -lse2 [128] per Q slot
-  static constexpr int kVecD = kVecL + kDkdvQSlots * 512;         // -D [128] per dO slot
-  static constexpr int kBar = kVecD + kDkdvDoSlots * 512;
+  static constexpr int kVecL = kDo0 + kDkdvDoSlots * kTileBytes;  // -lse2 [128] per dO slot
+  static constexpr int kVecD = kVecL + kDkdvDoSlots * 512;        // -D [128] per Q slot
+  static constexpr int kBar = kVecD + kDkdvQSlots * 512;
   static constexpr int kBytes = kBar + 256;
   static constexpr int kAlloc = kBytes;
   static_assert(kAlloc <= 232448, "dK/dV shared memory above the 227 KB limit");
@@ -329,8 +332,8 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
 
   if (warp == 16) {
     // ------------------------------------------------------------ producer --
-    // One lane: per step the Q tile with the step's 128 entries of -lse2,
-    // then the dO tile with its 128 entries of -D (TMA for the tiles, plain
+    // One lane: per step the Q tile with the step's 128 entries of -D, then
+    // the dO tile with its 128 entries of -lse2 (TMA for the tiles, plain
     // bulk copies from the padded row vectors), each pair completing on its
     // ring slot's full barrier.
     if (lane == 0 && U > 0) {
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
         for (int hc = 0; hc < D / 64; ++hc)
           tma_load_4d(sQ + hc * 16384, &mQ, &bars[kQFull0 + sq], hc * 64, h,
                       it.row0 + it.qt * kTile, it.blk);
-        bulk_load(vecL + sq * 128, a.nlse2 + vo, 512, &bars[kQFull0 + sq]);
+        bulk_load(vecD + sq * 128, a.nDvec + vo, 512, &bars[kQFull0 + sq]);
         issued_q = u + 1;
         if (u >= SD) {
           ok = mbar_wait(&bars[kDoEmpty0 + sd], ((u / SD) - 1) & 1, abort_s, a.status,
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
         for (int hc = 0; hc < D / 64; ++hc)
           tma_load_4d(sdO + hc * 16384, &mdO, &bars[kDoFull0 + sd], hc * 64, h,
                       it.row0 + it.qt * kTile, it.blk);
-        bulk_load(vecD + sd * 128, a.nDvec + vo, 512, &bars[kDoFull0 + sd]);
+        bulk_load(vecL + sd * 128, a.nlse2 + vo, 512, &bars[kDoFull0 + sd]);
         issued_do = u + 1;
       }
       if (!ok) {
@@ -522,8 +525,10 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
     uint32_t phq = 0, phd = 0;
     for (int u = 0; u < U && ok; ++u) {
       ok = mbar_wait(&bars[kStFull], u & 1, abort_s, a.status, kDevErrTimeoutSoftmax);
-      // the step's -lse2 entries landed with Q (kQFull already complete: the
-      // MMAs behind kStFull waited for it); waiting makes them visible
+      // the step's -lse2 entries land with dO; its -D entries, and the query
+      // tile beside them, landed with Q (kQFull already complete: the MMAs
+      // behind kStFull waited for it); waiting makes them visible
+      if (ok) ok = mbar_wait(&bars[kDoFull0 + sd], phd, abort_s, a.status, kDevErrTimeoutSoftmax);
       if (ok) ok = mbar_wait(&bars[kQFull0 + sq], phq, abort_s, a.status, kDevErrTimeoutSoftmax);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -539,8 +544,8 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
       // producer leaves the step's tile next to its Q slot)
       const int qt_u = (window > 0 && cart) ? *reinterpret_cast<volatile int*>(step_qt + sq) : qt;
       const int qhi = window > 0 ? max(0, min(32, i_hi - qt_u * kTile - wg * 32 + 1)) : 32;
-      const uint32_t lse_s = smem_u32(vecL + sq * 128 + wg * 32);
-      const uint32_t dv_s = smem_u32(vecD + sd * 128 + wg * 32);
+      const uint32_t lse_s = smem_u32(vecL + sd * 128 + wg * 32);
+      const uint32_t dv_s = smem_u32(vecD + sq * 128 + wg * 32);
       uint32_t r[32];
       tmem_ld32(tst, r);
       tmem_ld_wait();
@@ -577,9 +582,6 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
         mbar_arrive(&bars[kPtFull]);
       }
       ok = mbar_wait(&bars[kDpTFull], u & 1, abort_s, a.status, kDevErrTimeoutSoftmax);
-      // the step's -D entries landed with dO (kDoFull already complete: the
-      // MMAs behind kDpTFull waited for it); waiting makes them visible
-      if (ok) ok = mbar_wait(&bars[kDoFull0 + sd], phd, abort_s, a.status, kDevErrTimeoutSoftmax);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
