@@ -86,7 +86,8 @@ struct StepArgs {
   long long* starts;         // [B + 1]: chunks of a unit before each conversation's
   float *row_o, *row_lse;    // [slots, groups, heads, G, d], [.., G]
   int cap;                   // most private rows
-  float* logits;             // [B, Hkv, G, cap], log2 domain, by the order of groups seen
+  int logit_rows;            // ... in whole groups of 32, as they are written and read
+  float* logits;             // [B, Hkv, G, logit_rows], log2 domain, by the order of groups seen
 };
 
 struct Turns {
@@ -1079,12 +1080,12 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                   __bfloat16_as_ushort(__float2bfloat16_rn(p)));
         }
       }
-      if (a.logits && g < a.Hkv && v0 + grp * 32 + lane < a.cap) {
-        float* lg = a.logits + (static_cast<long long>(b) * a.Hkv + g) * a.G * a.cap + v0 +
+      if (a.logits && g < a.Hkv && v0 + grp * 32 + lane < a.logit_rows) {
+        float* lg = a.logits + (static_cast<long long>(b) * a.Hkv + g) * a.G * a.logit_rows + v0 +
                     grp * 32 + lane;
 #pragma unroll
         for (int q = 0; q < GQ; ++q)
-          if (q < a.G) lg[static_cast<long long>(q) * a.cap] = s[q];
+          if (q < a.G) lg[static_cast<long long>(q) * a.logit_rows] = s[q];
       }
       if (bits != 0xffffffffu) {
         // values of rows that are not seen may be anything, and 0 times them need
@@ -1417,7 +1418,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
     for (int e = part * kJoinThreads + tid; e < heads * per; e += parts * kJoinThreads) {
       const int h = e / per, v = (e - h * per) * 4, r = s.group(v >> 5) * 32 + (v & 31);
       const long long bg = static_cast<long long>(b) * a.Hkv + g0 + h;
-      const float* lg = a.logits + bg * G * a.cap + v;
+      const float* lg = a.logits + bg * G * a.logit_rows + v;
       float* w = a.weights + bg * a.weight_rows + r;
       const bool all = wide && s.sees(r) && s.sees(r + 3) && (r >= s.high || r + 3 < s.low);
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1426,7 +1427,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
 #pragma unroll
       for (int q = 0; q < GQ; ++q)
         if (q < G)
-          x[q] = __ldcg(reinterpret_cast<const float4*>(lg + static_cast<long long>(q) * a.cap));
+          x[q] = __ldcg(
+              reinterpret_cast<const float4*>(lg + static_cast<long long>(q) * a.logit_rows));
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int q = 0; q < GQ; ++q)
@@ -1453,7 +1455,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
 struct StepWs {
   size_t cart_o, cart_lse, row_o, row_lse, starts, logits, total;
   int row_tiles, key_tiles, cart_parts, cart_each, cart_ctas;
-  int heads, units, groups, row_ctas;
+  int heads, units, groups, row_ctas, logit_rows;
 };
 
 struct CartCut {
@@ -1524,7 +1526,8 @@ StepWs step_ws(int B, int Hq, int Hkv, int d, int p, int cap, bool weights) {
   w.row_o = take(parts * G * d * 4);
   w.row_lse = take(parts * G * 4);
   w.starts = take((static_cast<size_t>(B) + 1) * 8);
-  w.logits = take(weights ? static_cast<size_t>(B) * Hq * cap * 4 : 0);
+  w.logit_rows = (cap + 31) & ~31;
+  w.logits = take(weights ? static_cast<size_t>(B) * Hq * w.logit_rows * 4 : 0);
   w.total = off;
   return w;
 }
@@ -1672,6 +1675,7 @@ int cart_attn_decode_paged(int B, int window, int sinks, int Hq, int Hkv, int d,
   a.row_o = reinterpret_cast<float*>(ws + w.row_o);
   a.row_lse = reinterpret_cast<float*>(ws + w.row_lse);
   a.cap = max_pages * page_rows;
+  a.logit_rows = w.logit_rows;
   a.logits = weights ? reinterpret_cast<float*>(ws + w.logits) : nullptr;
   const RopeFreqs f = make_rope_freqs(d, rope_theta);
   Turns turns{};
