@@ -586,10 +586,11 @@ CART_API int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtyp
  * not finite makes the logits of those that see it NaN or infinite.
  * An idle conversation (lens < 0) has o = 0 and nothing written, and so has one
  * whose row lens[b] has no page, which sets device status bit 7.
- * The rotated queries enter the products with private rows, which the weights
- * come from, as three bf16 terms (all 24 bits of their f32 values), those with
- * the cartridge as two (2^-16 of the value); the weights of the values are
- * rounded to bf16, their sums f32.
+ * The rotated queries enter the products with private rows as three bf16 terms
+ * (all 24 bits of their f32 values), those with the cartridge as two (2^-16 of
+ * the value): where there is a cartridge, the log-sum-exp that the weights are
+ * relative to is as exact as these.  The softmax weights of the values enter as
+ * two bf16 terms (2^-15 of the weight); sums are f32.
  * Workspace: cart_attn_decode_paged_workspace_size(), `weights` 1 where they are
  * kept.                                                                    */
 CART_API size_t cart_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int d, int p,

@@ -16,7 +16,8 @@
 //           runs, one per CTA and SM.
 //   cart    the B * G stacked query rows of each kv head against the cartridge,
 //           as tcgen05 products: 128 rows and 48 keys at a time, Q resident as
-//           two bf16 terms, S and O in TMEM.  The key tiles of each (kv head, row
+//           two bf16 terms (2^-16 of it, and the hardware's sine and cosine, 5e-7;
+//           with a third, two CTAs do not fit an SM), S and O in TMEM.  The key tiles of each (kv head, row
 //           tile) are cut into equal pieces, one or more per CTA; two CTAs an SM,
 //           on the SMs that the rows' kernel, launched first, leaves.
 //   join    the new token: its rotated key and its value to its row, its logits;
@@ -93,6 +94,20 @@ struct StepArgs {
 struct Turns {
   float2 t[kMaxHeadDim / 2];
 };
+
+// Softmax weights of values enter the products as two bf16 terms, good to 2^-15 of
+// them, so that outputs are as exact as their own rounding to bf16 allows (0.0017 of
+// them in all; 0.0023 with one term, at the same speed to within 3%).  The first is
+// cut off below the weight, so that both are above 0 where it is, and a value that
+// is infinite stays so.
+__device__ __forceinline__ float below(float w) { return w * 0x1.fffffep-1f; }
+// ... of two weights, each term's in a word
+__device__ __forceinline__ void split_weights(float2 w, uint32_t& first, uint32_t& second) {
+  const float2 y = __fmul2_rn(w, make_float2(0x1.fffffep-1f, 0x1.fffffep-1f));
+  first = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
+  const float2 f = bf16x2_to_float2(first);
+  second = pack_bf16x2(w.x - f.x, w.y - f.y);
+}
 
 // The step of conversation b: the row of its new token (-1: idle, or its table
 // has no place for it); the cached rows that it sees: those below `low` and from
@@ -387,10 +402,12 @@ __global__ void __launch_bounds__(kCartThreads, 2)
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < kCartKeys / 16; ++k)
-          umma_bf16_ts_w(tO, tS + (s & 1) * kCartSColumns + k * 8,
-                         desc_add(dV, (s & 1) * L::kKBytes + k * 2048), idPV,
-                         t > 0 || k > 0 ? 1u : 0u);
+        for (int m = 1; m >= 0; --m)  // (the smaller terms first)
+#pragma unroll
+          for (int k = 0; k < kCartKeys / 16; ++k)
+            umma_bf16_ts_w(tO, tS + (s & 1) * kCartSColumns + m * (kCartKeys / 2) + k * 8,
+                           desc_add(dV, (s & 1) * L::kKBytes + k * 2048), idPV,
+                           t > 0 || m == 0 || k > 0 ? 1u : 0u);
         umma_commit_w(&bars[kCVEmpty0 + (s & 1)]);
         umma_commit_w(&bars[kCPvDone]);
         if (t == n - 1) umma_commit_w(&bars[kCODone]);
@@ -453,16 +470,16 @@ __global__ void __launch_bounds__(kCartThreads, 2)
         const float mr = m == -INFINITY ? 0.f : m;  // (nothing seen yet: weights 0)
         const float2 nm2 = make_float2(-mr, -mr);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t pk[kCartKeys / 2];
+        uint32_t pk[kCartKeys];  // first terms, second terms
 #pragma unroll
         for (int c = 0; c < kCartKeys / 2; ++c) {
           const float2 x = __ffma2_rn(make_float2(v[2 * c], v[2 * c + 1]), sc2, nm2);
           const float2 w = make_float2(exp2_approx(x.x), exp2_approx(x.y));
           sum[c & 1] = __fadd2_rn(sum[c & 1], w);
-          pk[c] = pack_bf16x2(w.x, w.y);
+          split_weights(w, pk[c], pk[kCartKeys / 2 + c]);
         }
-        tmem_st16(ts, pk);  // (over columns that have been read)
-        tmem_st16(ts + kCartKeys / 2 - 16, pk + kCartKeys / 2 - 16);
+        tmem_st32(ts, pk);  // (over columns that have been read)
+        tmem_st16(ts + 32, pk + 32);
         l = l * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
         if (__any_sync(0xffffffffu, rescale)) {
           ok = wait(&bars[kCPvDone], (s - 1) & 1, kDevErrTimeoutSoftmax);
@@ -575,11 +592,12 @@ struct RowSmem {
   static constexpr int kTileBytes = kTile * D * 2;          // a K or V tile
   static constexpr int kSlots = 6 * 128 / D;                // of the ring
   static constexpr int kQHalf = kRowHeads * kHeadColumns * 128;  // 64 dims of all columns
-  static constexpr int kP = kSlots * kTileBytes;  // weights: two buffers, 1 KB for two warps
-  // (a product reads 16 rows of weights, eight of them behind the warps')
-  static constexpr int kQ = kP + 2 * 2048;
+  // weights: two buffers, 2 KB for two warps, eight rows of each term (a product
+  // has at least 16 columns: the second term costs none)
+  static constexpr int kP = kSlots * kTileBytes;
+  static constexpr int kQ = kP + 2 * 4096;
   static constexpr int kShared = kQ + (D / 64) * kQHalf;  // a RowShared
-  static constexpr int kAlloc = kShared + 3584;           // starts 1024-aligned
+  static constexpr int kAlloc = kShared + 3072;           // starts 1024-aligned
 };
 
 enum RowBar {
@@ -608,7 +626,7 @@ struct RowShared {
   uint32_t tmem;
   int run_b, run_unit, run_at, abort;  // (where the run begins)
 };
-static_assert(sizeof(RowShared) <= 3584, "rows barrier area");
+static_assert(sizeof(RowShared) <= 3072, "rows barrier area");
 
 struct RowMaps {
   CUtensorMap k, v;  // (d, page_rows, Hkv, pages), box 64 x 32 x heads, or 64 x 16 x 1
@@ -731,7 +749,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     if (tid == 0) a.starts[a.B] = total;
   }
   __syncthreads();
-  // TMEM: two buffers of S^T, then the four O^T (16 columns each, 8 of them used)
+  // TMEM: two buffers of S^T, then the four O^T (16 columns each, eight of a term)
   const uint32_t tS = tmem, tO = tmem + 192;
   constexpr int kSBuffer = 96;
 
@@ -926,13 +944,13 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       ok = wait(&bars[kRFull0 + sl], (e / NS) & 1) && wait(&bars[kRPFull0 + (n & 1)], (n >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const uint64_t dv = desc_add(dV, sl * L::kTileBytes), dp = desc_add(dP, (n & 1) * 2048);
+      const uint64_t dv = desc_add(dV, sl * L::kTileBytes), dp = desc_add(dP, (n & 1) * 4096);
 #pragma unroll
       for (int w = 0; w < 4; ++w)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           umma_bf16_ss_w(tO + w * 16, desc_add(dv, w * 4096 + k * 2048),
-                         desc_add(dp, (w >> 1) * 1024 + (w & 1) * 64 + k * 32), idO,
+                         desc_add(dp, (w >> 1) * 2048 + (w & 1) * 64 + k * 32), idO,
                          (now & kOpens) && k == 0 ? 0u : 1u);
       umma_commit_w(&bars[kREmpty0 + sl]);
       umma_commit_w(&bars[kRPvDone]);
@@ -1069,15 +1087,19 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         rescale[x][warp] = grows && !opens;
         mbar_arrive(&bars[kRExchange]);
       }
-      // ---- weights as B: row q of 128 bytes, this key's two bytes
+      // ---- weights as B: row q of 128 bytes, and q + 8, this key's two bytes
       {
-        const uint32_t ps = smem_u32(smem + L::kP) + x * 2048 + (warp >> 1) * 1024;
+        const uint32_t ps = smem_u32(smem + L::kP) + x * 4096 + (warp >> 1) * 2048;
 #pragma unroll
         for (int q = 0; q < GQ; ++q) {
           const float p = exp2_approx(s[q] - (m[q] == -INFINITY ? 0.f : m[q]));
           l[q] += p;
-          sts_u16(ps + q * 128 + ((((warp & 1) * 4 + (lane >> 3)) ^ q) << 4) + (lane & 7) * 2,
-                  __bfloat16_as_ushort(__float2bfloat16_rn(p)));
+          const uint32_t at =
+              ps + q * 128 + ((((warp & 1) * 4 + (lane >> 3)) ^ q) << 4) + (lane & 7) * 2;
+          const uint32_t first = __float_as_uint(below(p)) >> 16;
+          sts_u16(at, static_cast<uint16_t>(first));
+          sts_u16(at + 1024, __bfloat16_as_ushort(
+                                 __float2bfloat16_rn(p - __uint_as_float(first << 16))));
         }
       }
       if (a.logits && g < a.Hkv && v0 + grp * 32 + lane < a.logit_rows) {
@@ -1120,9 +1142,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           tmem_ld_wait();
           tmem_reg_fence16(o);
 #pragma unroll
-          for (int q = 0; q < GQ; ++q)
-            o[q] = __float_as_uint(__uint_as_float(o[q]) *
-                                   *const_cast<const volatile float*>(&factor[x][w][q]));
+          for (int q = 0; q < GQ; ++q) {
+            const float f = *const_cast<const volatile float*>(&factor[x][w][q]);
+            o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+            o[8 + q] = __float_as_uint(__uint_as_float(o[8 + q]) * f);
+          }
           tmem_st16(tO + w * 16 + lane_off, o);
         }
         tmem_st_wait();
@@ -1177,7 +1201,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll
             for (int q = 0; q < GQ; ++q) {
               const float inv = *const_cast<const volatile float*>(&inverse[w][q]);
-              if (q < a.G) out[q * D] = inv == 0.f ? 0.f : __uint_as_float(o[q]) * inv;
+              if (q < a.G)
+                out[q * D] =
+                    inv == 0.f ? 0.f : (__uint_as_float(o[q]) + __uint_as_float(o[8 + q])) * inv;
             }
           }
         }
