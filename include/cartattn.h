@@ -592,7 +592,8 @@ CART_API int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtyp
  * relative to is as exact as these.  The softmax weights of the values enter as
  * two bf16 terms (2^-15 of the weight); sums are f32.
  * Workspace: cart_attn_decode_paged_workspace_size(), `weights` 1 where they are
- * kept.                                                                    */
+ * kept; the work is cut for the current device's multiprocessors, so the size is
+ * that device's.                                                           */
 CART_API size_t cart_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int d, int p,
                                                       int page_rows, int max_pages, int weights);
 CART_API int cart_attn_decode_paged(int B, int window, int sinks, int Hq, int Hkv, int d, int p,

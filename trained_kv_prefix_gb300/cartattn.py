@@ -833,10 +833,22 @@ def cart_pages_evict(k_pages, v_pages, table, lens, refs, weights, keep, *, firs
     return done
 
 
-@functools.lru_cache(maxsize=1024)
-def decode_paged_workspace_size(B, Hq, Hkv, d, p, page_rows, max_pages, weights) -> int:
+@functools.lru_cache(maxsize=1024)  # (by device: the work is cut for its multiprocessors)
+def _decode_paged_size(device, B, Hq, Hkv, d, p, page_rows, max_pages, weights) -> int:
     return int(lib().cart_attn_decode_paged_workspace_size(B, Hq, Hkv, d, p, page_rows, max_pages,
                                                            1 if weights else 0))
+
+
+def decode_paged_workspace_size(B, Hq, Hkv, d, p, page_rows, max_pages, weights) -> int:
+    """Of the current device."""
+    if torch.cuda.is_available():
+        size, device = _decode_paged_size, torch.cuda.current_device()
+    else:  # (what is asked for without one says nothing of a later one's)
+        size, device = _decode_paged_size.__wrapped__, None
+    return size(device, B, Hq, Hkv, d, p, page_rows, max_pages, weights)
+
+
+decode_paged_workspace_size.cache_clear = _decode_paged_size.cache_clear
 
 
 def cart_attn_decode_paged(q, k_new, v_new, kc, vc, k_pages, v_pages, table, lens, *, pos=None,
@@ -875,8 +887,8 @@ def cart_attn_decode_paged(q, k_new, v_new, kc, vc, k_pages, v_pages, table, len
             op = o.data_ptr()
         else:
             op = _arg("o", o, bf, q.shape, dev)
-        ws, wp, wn = _scratch(on, workspace, decode_paged_workspace_size(
-            B, Hq, Hkv, d, p, P, M, weights is not None))
+        ws, wp, wn = _scratch(on, workspace, _decode_paged_size(
+            dev.index, B, Hq, Hkv, d, p, P, M, weights is not None))
         rc = (_lib or lib()).cart_attn_decode_paged(
             B, window, sinks, Hq, Hkv, d, p, d ** -0.5 if scale is None else scale, theta, *args, op,
             wp, wn, on.handle)

@@ -17,9 +17,10 @@
 //   cart    the B * G stacked query rows of each kv head against the cartridge,
 //           as tcgen05 products: 128 rows and 48 keys at a time, Q resident as
 //           two bf16 terms (2^-16 of it, and the hardware's sine and cosine, 5e-7;
-//           with a third, two CTAs do not fit an SM), S and O in TMEM.  The key tiles of each (kv head, row
-//           tile) are cut into equal pieces, one or more per CTA; two CTAs an SM,
-//           on the SMs that the rows' kernel, launched first, leaves.
+//           with a third, two CTAs do not fit an SM), S and O in TMEM.  The key
+//           tiles of each (kv head, row tile) are cut into equal pieces, one or more
+//           per CTA; two CTAs an SM, on the SMs that the rows' kernel, launched
+//           first, leaves.
 //   join    the new token: its rotated key and its value to its row, its logits;
 //           joins them and a (conversation, kv head)'s parts by their log-sum-exps;
 //           adds exp2(logit - log-sum-exp) of the group's heads to each row's weights.
