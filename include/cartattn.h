@@ -586,6 +586,7 @@ CART_API int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtyp
  * not finite makes the logits of those that see it NaN or infinite.
  * An idle conversation (lens < 0) has o = 0 and nothing written, and so has one
  * whose row lens[b] has no page, which sets device status bit 7.
+ * o may be q itself; outputs overlap nothing else that the call is given.
  * The rotated queries enter the products with private rows as three bf16 terms
  * (all 24 bits of their f32 values), those with the cartridge as two (2^-16 of
  * the value): where there is a cartridge, the log-sum-exp that the weights are

@@ -1622,11 +1622,16 @@ cudaError_t launch_step(const StepArgs& a, const StepWs& w, const Turns& f, cuda
   join.join_heads = a.B * a.units >= sm_count() ? a.heads : 1;
   const int across = (a.Hkv + join.join_heads - 1) / join.join_heads;
   // ... and as many for the rows' weights as the GPU takes at once, at most one for
-  // every 4 * kJoinThreads rows that a table can name
+  // every 4 * kJoinThreads rows that a table can name; none where the output takes
+  // the queries' place, which they would read after it is written
+  const auto at = [](const __nv_bfloat16* x) { return reinterpret_cast<uintptr_t>(x); };
+  const uintptr_t bytes = static_cast<uintptr_t>(a.B) * a.Hq * D * 2;
+  const bool in_place = at(a.o) < at(a.q) + bytes && at(a.q) < at(a.o) + bytes;
   const int deep =
-      a.weights ? std::max(1, std::min((a.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads),
-                                       2 * sm_count() / (across * a.B) - 1) + 1)
-                : 1;
+      a.weights && !in_place
+          ? std::max(1, std::min((a.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads),
+                                 2 * sm_count() / (across * a.B) - 1) + 1)
+          : 1;
   return launch_dependent(a.G > 4 ? step_join_kernel<D, 8> : step_join_kernel<D, 4>,
                           dim3(across, a.B, deep), dim3(kJoinThreads), 0, st, join, f);
 }
