@@ -548,9 +548,9 @@ CART_API int cart_attn_weights(int B, int queries, int window, int sinks, int Hq
  *          rows between that have most weight, ties to the lower row, NaN
  *          counting as most
  *   weights [layers, B, Hkv, weight_rows] f32, or NULL: the last rows stay
- *   done   [B] int32 (output): 1, or 0 where the conversation holds more than
- *          keep[b] rows and was left as it is: a page of its rows is not there,
- *          or there were too few free pages
+ *   done   [B] int32 (output; may be keep itself): 1, or 0 where the
+ *          conversation holds more than keep[b] rows and was left as it is: a
+ *          page of its rows is not there, or there were too few free pages
  * The rows that stay keep their order: the i-th of them becomes row i, and its
  * weight weights[..][i]; rows and weights behind are left as they were.  Pages
  * that rows would be moved into and that are shared (refs > 1) are not written:

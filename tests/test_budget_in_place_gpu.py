@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_budget_gpu import _i32, make_step
+from tests.test_budget_gpu import _f32, _i32, make_evict, make_step
 from trained_kv_prefix_gb300 import cartattn as ca
 
 pytestmark = pytest.mark.gpu
@@ -37,3 +37,21 @@ def test_step_writes_over_its_queries(heads):
             got.append((o.clone(), w))
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
         assert ca.device_status(clear=True) == (1 << 7 if B == 3 else 0)
+
+
+def test_evict_writes_done_over_keep():
+    """Many blocks that read keep while others are through."""
+    pools, table, lens, refs, w = make_evict(43, 9, 12, 8, 64, 16,
+                                             (300, 250, 7, 120, 400, -1, 33, 64, 500), spare=2)
+    table[3, 1] = -1                            # a page that is not there
+    keep = (100, 250, 9, 40, 39, 5, -1, 1, 0)
+    got = []
+    for place in (False, True):
+        g = [x.cuda() for x in pools]
+        gt, gl, gr, gw, k = _i32(table), _i32(lens), _i32(refs), _f32(w), _i32(keep)
+        done = ca.cart_pages_evict(*g, gt, gl, gr, gw, k, first=3, recent=9,
+                                   done=k if place else None)
+        got.append((done, *g, gt, gl, gr, gw))
+    assert got[0][0].tolist() == [1, 1, 1, 0, 1, 1, 1, 1, 1]
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(*got))
+    assert ca.device_status(clear=True) == 0

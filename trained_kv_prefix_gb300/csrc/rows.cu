@@ -254,10 +254,7 @@ __global__ void __cluster_dims__(kMetaCtas, 1, 1) __launch_bounds__(kMetaThreads
     const Budget q = budget_of(a, b);
     const int n = __ldcg(a.need + b), base = __ldcg(a.base + b);
     const bool go = n >= 0 && (n == 0 || base + n <= n_free);
-    if (lane == 0) {
-      a.go[b] = go;
-      a.done[b] = go || n == kIdle;
-    }
+    if (lane == 0) a.go[b] = go;
     if (!go) continue;
     const int* row = a.pt.table + static_cast<long long>(b) * a.pt.max_pages;
     int* to = a.to + static_cast<long long>(b) * a.pt.max_pages;
@@ -525,12 +522,17 @@ cudaError_t launch_moves(unsigned blocks, cudaStream_t st, const EvictArgs& a) {
              : e;
 }
 
-// The new tables and lengths, a warp per conversation.
+// The new tables, lengths and `done` (written behind the last read of keep, whose
+// place it may have), a warp per conversation.
 __global__ void __launch_bounds__(256) evict_tables_kernel(const __grid_constant__ EvictArgs a) {
   pdl_wait();
   const int b = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (b >= a.B || !__ldcg(a.go + b)) return;
-  const int keep = __ldg(a.keep + b), end = pages_for(a, keep);
+  if (b >= a.B) return;
+  const bool go = __ldcg(a.go + b);
+  const int keep = __ldcg(a.keep + b), end = pages_for(a, keep);
+  __syncwarp();
+  if (lane == 0) a.done[b] = go || __ldcg(a.need + b) == kIdle;
+  if (!go) return;
   int* row = a.table + static_cast<long long>(b) * a.pt.max_pages;
   const int* to = a.to + static_cast<long long>(b) * a.pt.max_pages;
   for (int k = lane; k < a.pt.max_pages; k += 32) row[k] = k < end ? __ldcg(to + k) : -1;
