@@ -635,9 +635,10 @@ struct RowMaps {
 
 // Tiles of one unit of a conversation that sees n groups, and what they cost in
 // the schedule: the change from one unit's queries and sums to another's takes
-// about as long as that many tiles (1 / 2 / 3 / 5: 89.3 / 88.1 / 89.6 / 88.1 us at 96
-// conversations, 112 / 111 / 109.7 / 109.6 us at 200).
-constexpr int kStart = 4;
+// about as long as that many tiles (2 / 3 / 4 / 5 / 6, in all: 68.8 / 68.9 / 69.9 / 70.4
+// / 70.6 us at 96 conversations, 115.3 / 115.1 / 114.9 / 114.3 / 113.6 at 4 long ones,
+// 89.6 / 88.6 / 89.2 / 90.4 / 90.1 at 200 in a window).
+constexpr int kStart = 3;
 __device__ __forceinline__ int tiles_of(const StepArgs& a, int n) {
   return (n + a.groups - 1) / a.groups;
 }

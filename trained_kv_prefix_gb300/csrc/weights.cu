@@ -103,10 +103,10 @@ __device__ __forceinline__ Tiles column_tiles(const WeighArgs& a, int rows, int 
   }
   return tiles_of(a, a.p + rows - a.T + i0, a.p + rows - a.T + i1);
 }
-// A segment of n tiles is n + kStartUnits units of the schedule (0 / 1 / 2 / 4: whole
-// prompts 147.5 / 144.4 / 143.2 / 143.0 us, 32 queries of 64 conversations 167 / 166.3 /
-// 166.3 / 165.3).
-constexpr int kStartUnits = 2;
+// A segment of n tiles is n + kStartUnits units of the schedule (0 / 1 / 2 / 3 / 4:
+// whole prompts 150.5 / 147.4 / 146.9 / 147.2 / 145.8 us, 32 queries of 64 conversations
+// 170.5 / 170.1 / 170.9 / 169.3 / 168.8).
+constexpr int kStartUnits = 4;
 __device__ __forceinline__ int segment_units(int n) { return n > 0 ? n + kStartUnits : 0; }
 
 struct Turns {
