@@ -1494,7 +1494,10 @@ struct CartCut {
 // end together, going by what they were seen to take side by side, the tables half
 // full (`row_bytes`: their keys and values).  A CTA takes 16 us + 8 us a piece + 1.1
 // us a tile; the rows 8 us + their bytes at 0.05 TB/s an SM, 6.3 TB/s at most; and
-// a piece 0.3 us where it is joined.  In all, at 96 conversations (24 segments of 43
+// a piece 0.3 us where it is joined.  The cartridge's own time counts a quarter
+// beside: a table may hold far fewer rows than it names, and SMs that the rows do
+// not need cost them nothing (96 conversations of up to 1500 rows, tables of 2048 to
+// 32768: 68 us, 85 without that quarter).  In all, at 96 conversations (24 segments of 43
 // tiles), 1 / 2 / 3 / 4 pieces of one a CTA took 87.4 / 75.3 / 78.3 / 83 us, at 200 (44
 // of 22) 93 / 99 / 116 / 145, at 4 of up to 32k rows (8 of 171) 3 / 5 / 7 126 / 119.4 /
 // 119.1, at one of 200 (8 of 11) 1 / 3 / 5 / 11 26.8 / 20.5 / 19.5 / 21.1.
@@ -1510,13 +1513,13 @@ CartCut cart_cut(int segments, int key_tiles, double row_bytes, int sms) {
       const int ctas = (pieces + each - 1) / each, left = sms - (ctas + 1) / 2;
       const double cart = 16.0 + each * (8.0 + 1.1 * tiles);
       const double rows = 8.0 + row_bytes * 1e-6 / std::min(0.05 * std::max(left, 1), 6.3);
-      const double us = std::max(cart, rows) + 0.3 * n;
+      const double us = std::max(cart, rows) + 0.25 * cart + 0.3 * n;
       if (best_us == 0.0 || us < best_us || (us == best_us && cart < best_cart)) {
         best = CartCut{n, each};
         best_us = us;
         best_cart = cart;
       }
-      if (cart > best_us) break;  // (and longer with more each)
+      if (1.25 * cart > best_us) break;  // (and longer with more each)
     }
   }
   return best;
