@@ -1,8 +1,8 @@
 """The order that the dK / dV kernel's shared-memory rings rely on, read from
-its source: a ring slot is loaded again once the product that the ring's release
-follows has read it, so every other reader has to be ahead of the arrival that
-this product waits for.  (A reader behind it sees the slot's next contents now
-and then, which no result can be relied on to show.)"""
+its source: a ring slot is loaded again once its empty barrier has all arrivals,
+so every reader has to be ahead of an arrival of its own there, or of the one that
+the product which arrives there is issued behind.  (A reader behind it sees the
+slot's next contents now and then, which no result can be relied on to show.)"""
 import os
 import re
 
@@ -27,16 +27,23 @@ def ring_of(kernel, vec):
     return rings[0]
 
 
-def release_waits_for(kernel, ring):
-    """The barrier of the last wait before the product that releases the ring."""
+def release(kernel, ring):
+    """What a reading warp does last before a slot of the ring can be loaded again:
+    its own arrival on the empty barrier, where that counts the 16 warps beside the
+    product, or the arrival that the releasing product is issued behind."""
+    own = f"mbar_arrive(&bars[k{ring}Empty0 + "
+    if f"mbar_init(&bars[k{ring}Empty0 + s], 17)" in kernel:
+        assert kernel.count(own) == 1
+        return own
+    assert f"mbar_init(&bars[k{ring}Empty0 + s], 1)" in kernel and own not in kernel
     at = kernel.index(f"umma_commit_w(&bars[k{ring}Empty0 + ")
     waits = [m for m in re.finditer(r"ok = wait\(&bars\[(kPtFull|kDsFull)\]", kernel) if m.start() < at]
-    return waits[-1].group(1)
+    return f"mbar_arrive(&bars[{waits[-1].group(1)}])"
 
 
 @pytest.mark.parametrize("vec,address", [("vecL", "lse_s"), ("vecD", "dv_s")])
 def test_row_vectors_are_read_before_their_slot_is_released(kernel, vec, address):
-    arrive = kernel.index(f"mbar_arrive(&bars[{release_waits_for(kernel, ring_of(kernel, vec))}])")
+    arrive = kernel.index(release(kernel, ring_of(kernel, vec)))
     reads = [m.start() for m in re.finditer(r"lds128\(" + address, kernel)]
     assert reads and max(reads) < arrive
 

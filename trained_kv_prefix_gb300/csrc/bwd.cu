@@ -131,12 +131,12 @@ __device__ __forceinline__ void store_row_out(void* base, long long off, const f
 // it, dP^T(u+1) overwrites dS^T(u) after dK(u) (one CTA's MMAs run in issue
 // order).
 // Q and dO have rings of their own: a Q slot is released by dK(u), a dO
-// slot by dV(u).  Q gets three slots, so a Q tile is copied while two full
+// slot by dV(u) and by every warp of the dS phase, which reads the slot's -D
+// beside dV(u) (with -D in Q's slots, whose dK(u) follows all dS arrivals, and
+// -lse2 in dO's, 221.8 us of self-study and 663 us of packed training against
+// 220.7 and 658).  Q gets three slots, so a Q tile is copied while two full
 // steps of MMAs run; dO gets two (its first reader, dP^T, comes later in the
-// step).  A row vector travels with the tile whose release its last readers
-// come before: the step's -lse2 entries, read in the P phase, with dO (dV(u)
-// waits for every thread's P^T); its -D entries, read in the dS phase beside
-// dV(u), with Q (dK(u) waits for every thread's dS^T).
+// step).  The step's -lse2 entries travel with Q, its -D entries with dO.
 // The layout fills the 227 KB limit, so it relies on the dynamic shared
 // memory starting 1024-byte aligned (checked at entry; no static shared
 // variables).
@@ -150,9 +150,9 @@ struct DkdvSmem {
   static constexpr int kV = kK + kTileBytes;                  // resident V
   static constexpr int kQ0 = kV + kTileBytes;                 // Q ring
   static constexpr int kDo0 = kQ0 + kDkdvQSlots * kTileBytes;  // dO ring
-  static constexpr int kVecL = kDo0 + kDkdvDoSlots * kTileBytes;  // -lse2 [128] per dO slot
-  static constexpr int kVecD = kVecL + kDkdvDoSlots * 512;        // -D [128] per Q slot
-  static constexpr int kBar = kVecD + kDkdvQSlots * 512;
+  static constexpr int kVecL = kDo0 + kDkdvDoSlots * kTileBytes;  // -lse2 [128] per Q slot
+  static constexpr int kVecD = kVecL + kDkdvQSlots * 512;         // -D [128] per dO slot
+  static constexpr int kBar = kVecD + kDkdvDoSlots * 512;
   static constexpr int kBytes = kBar + 256;
   static constexpr int kAlloc = kBytes;
   static_assert(kAlloc <= 232448, "dK/dV shared memory above the 227 KB limit");
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
     }
     for (int s = 0; s < SD; ++s) {
       mbar_init(&bars[kDoFull0 + s], 1);
-      mbar_init(&bars[kDoEmpty0 + s], 1);
+      mbar_init(&bars[kDoEmpty0 + s], 17);  // dV(u) and the 16 warps
     }
     mbar_init(&bars[kStFull], 1);
     mbar_init(&bars[kPtFull], 512);
@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
 
   if (warp == 16) {
     // ------------------------------------------------------------ producer --
-    // One lane: per step the Q tile with the step's 128 entries of -D, then
-    // the dO tile with its 128 entries of -lse2 (TMA for the tiles, plain
+    // One lane: per step the Q tile with the step's 128 entries of -lse2,
+    // then the dO tile with its 128 entries of -D (TMA for the tiles, plain
     // bulk copies from the padded row vectors), each pair completing on its
     // ring slot's full barrier.
     if (lane == 0 && U > 0) {
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
         for (int hc = 0; hc < D / 64; ++hc)
           tma_load_4d(sQ + hc * 16384, &mQ, &bars[kQFull0 + sq], hc * 64, h,
                       it.row0 + it.qt * kTile, it.blk);
-        bulk_load(vecD + sq * 128, a.nDvec + vo, 512, &bars[kQFull0 + sq]);
+        bulk_load(vecL + sq * 128, a.nlse2 + vo, 512, &bars[kQFull0 + sq]);
         issued_q = u + 1;
         if (u >= SD) {
           ok = mbar_wait(&bars[kDoEmpty0 + sd], ((u / SD) - 1) & 1, abort_s, a.status,
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
         for (int hc = 0; hc < D / 64; ++hc)
           tma_load_4d(sdO + hc * 16384, &mdO, &bars[kDoFull0 + sd], hc * 64, h,
                       it.row0 + it.qt * kTile, it.blk);
-        bulk_load(vecL + sd * 128, a.nlse2 + vo, 512, &bars[kDoFull0 + sd]);
+        bulk_load(vecD + sd * 128, a.nDvec + vo, 512, &bars[kDoFull0 + sd]);
         issued_do = u + 1;
       }
       if (!ok) {
@@ -525,10 +525,8 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
     uint32_t phq = 0, phd = 0;
     for (int u = 0; u < U && ok; ++u) {
       ok = mbar_wait(&bars[kStFull], u & 1, abort_s, a.status, kDevErrTimeoutSoftmax);
-      // the step's -lse2 entries land with dO; its -D entries, and the query
-      // tile beside them, landed with Q (kQFull already complete: the MMAs
-      // behind kStFull waited for it); waiting makes them visible
-      if (ok) ok = mbar_wait(&bars[kDoFull0 + sd], phd, abort_s, a.status, kDevErrTimeoutSoftmax);
+      // the step's -lse2 entries landed with Q (kQFull already complete: the
+      // MMAs behind kStFull waited for it); waiting makes them visible
       if (ok) ok = mbar_wait(&bars[kQFull0 + sq], phq, abort_s, a.status, kDevErrTimeoutSoftmax);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -544,8 +542,8 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
       // producer leaves the step's tile next to its Q slot)
       const int qt_u = (window > 0 && cart) ? *reinterpret_cast<volatile int*>(step_qt + sq) : qt;
       const int qhi = window > 0 ? max(0, min(32, i_hi - qt_u * kTile - wg * 32 + 1)) : 32;
-      const uint32_t lse_s = smem_u32(vecL + sd * 128 + wg * 32);
-      const uint32_t dv_s = smem_u32(vecD + sq * 128 + wg * 32);
+      const uint32_t lse_s = smem_u32(vecL + sq * 128 + wg * 32);
+      const uint32_t dv_s = smem_u32(vecD + sd * 128 + wg * 32);
       uint32_t r[32];
       tmem_ld32(tst, r);
       tmem_ld_wait();
@@ -582,6 +580,9 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
         mbar_arrive(&bars[kPtFull]);
       }
       ok = mbar_wait(&bars[kDpTFull], u & 1, abort_s, a.status, kDevErrTimeoutSoftmax);
+      // the step's -D entries landed with dO (kDoFull already complete: the
+      // MMAs behind kDpTFull waited for it); waiting makes them visible
+      if (ok) ok = mbar_wait(&bars[kDoFull0 + sd], phd, abort_s, a.status, kDevErrTimeoutSoftmax);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -600,6 +601,9 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
         pd[2 * c4] = pack_bf16x2(ds0.x, ds0.y);
         pd[2 * c4 + 1] = pack_bf16x2(ds1.x, ds1.y);
       }
+      // the slot's -D entries have been read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kDoEmpty0 + sd]);
       // dS^T packed over the first 16 of this group's dP^T columns (read)
       tmem_st16(tdp, pd);
       tmem_st_wait();
