@@ -481,6 +481,10 @@ CART_API int cart_pages_compact(int B, int layers, int Hkv, int d, cart_dtype dt
  *             max_pages * page_rows.  Kept by conversation and row, not by
  *             page: fork, reserve and compact leave them as they are (a caller
  *             that forks copies its weights along).
+ * Of the calls that take several new tokens of a conversation, none has positions
+ * apart from places: cart_attn_decode_tree rotates at p + lens[b], which after an
+ * eviction is not the token's position, and nothing tells it so.  A conversation
+ * whose rows were evicted goes on by cart_attn_decode_paged, a token at a time.
  * Hq / Hkv is 1 to 8 here, any of them, and d 64 or 128.
  * Workspaces as above: no initial value, nothing outlives the call, calls that
  * may overlap need workspaces of their own.                                */
@@ -515,7 +519,8 @@ CART_API int cart_pages_append(int B, int n, int total, const int* cu_seqlens, i
  *          is not read
  *   lse    [B, Hq, queries] f32: their natural-log log-sum-exps, as
  *          cart_attn_fwd returns them (-inf: every logit was; the query gives
- *          no weight)
+ *          no weight).  Those of an attention with sinks beside a window are the
+ *          caller's to find: cart_attn_fwd has none.
  *   pos    position of query 0 (NULL: its place)
  *   kc     [p, Hkv, d] bf16 (NULL when p == 0)
  *   weights, and cart [B, Hkv, p] f32 for the cartridge's rows (NULL when
@@ -528,7 +533,11 @@ CART_API int cart_pages_append(int B, int n, int total, const int* cu_seqlens, i
  * The rotated queries enter the products as three bf16 terms (all 24 bits of
  * their f32 values), the sums are f32.  A key that a query does not see gets nothing from
  * it, whatever either holds.
- * Workspace: cart_attn_weights_workspace_size().                          */
+ * Workspace: cart_attn_weights_workspace_size().  It has a f32 for each key that
+ * the tables can name and each 128 columns (queries * Hq / Hkv) of a kv head: with
+ * the queries' terms 1.9 GB for 32768 over as many keys, 8 heads of 4.  A long
+ * prompt is weighed in chunks, the rows that are there growing with them and
+ * accumulate 1 from the second on.                                        */
 CART_API size_t cart_attn_weights_workspace_size(int B, int queries, int Hq, int Hkv, int d, int p,
                                                  int page_rows, int max_pages);
 CART_API int cart_attn_weights(int B, int queries, int window, int sinks, int Hq, int Hkv, int d,
@@ -553,9 +562,10 @@ CART_API int cart_attn_weights(int B, int queries, int window, int sinks, int Hq
  *          page of its rows is not there, or there were too few free pages
  * The rows that stay keep their order: the i-th of them becomes row i, and its
  * weight weights[..][i]; rows and weights behind are left as they were.  Pages
- * that rows would be moved into and that are shared (refs > 1) are not written:
- * a free one takes the place of each (lowest first, conversations in order; one
- * that finds too few, and all later ones that need any, are left).  Pages
+ * from that of row `first` to that of row keep[b] - 1 that are shared (refs > 1)
+ * are not written, whether or not a row in them changes its place: a free one takes
+ * the place of each (lowest first, conversations in order; one that finds too few,
+ * and all later ones that need any, are left).  Pages
  * behind the last of keep[b] rows are given back.  What is given back, or loses
  * its last holder, is free from the next call on.  lens[b] becomes keep[b].
  *   k_pages, v_pages: all layers, CART_BF16 or CART_F32; a head's row, d
@@ -593,8 +603,10 @@ CART_API int cart_pages_evict(int B, int layers, int Hkv, int d, cart_dtype dtyp
  * relative to is as exact as these.  The softmax weights of the values enter as
  * two bf16 terms (2^-15 of the weight); sums are f32.
  * Workspace: cart_attn_decode_paged_workspace_size(), `weights` 1 where they are
- * kept; the work is cut for the current device's multiprocessors, so the size is
- * that device's.                                                           */
+ * kept, which takes 4 * Hq bytes for every row that the tables can name; the work
+ * is cut for the current device's multiprocessors, so the size is that device's.
+ * (Where neither weights, sinks nor positions apart from places are wanted, the tree
+ * of one node is the faster call for a few conversations.)                 */
 CART_API size_t cart_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int d, int p,
                                                       int page_rows, int max_pages, int weights);
 CART_API int cart_attn_decode_paged(int B, int window, int sinks, int Hq, int Hkv, int d, int p,

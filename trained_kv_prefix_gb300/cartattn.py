@@ -762,7 +762,8 @@ def cart_attn_weights(q, lse, kc, k_pages, table, lens, weights, cart=None, *, p
     max_pages * page_rows) gets the private rows', cart ``[B, Hkv, p]`` f32
     (None: a new one) the cartridge's.  ``accumulate``: added to what they hold
     (a new cart's 0), the queries' own rows set.  pos ``[B]`` int32: position of
-    query 0; window and sinks by places (see the header).  Returns ``(weights,
+    query 0; window and sinks by places (see the header).  The workspace grows
+    with queries x keys: long prompts are weighed in chunks.  Returns ``(weights,
     cart)``."""
     B, T, Hq, d = q.shape
     p, Hkv = kc.shape[0], kc.shape[1]
@@ -861,8 +862,8 @@ def cart_attn_decode_paged(q, k_new, v_new, kc, vc, k_pages, v_pages, table, len
     int32: the token's position (None: p + lens[b]; rows that were evicted leave
     it ahead of that).  ``weights`` ``[B, Hkv, rows]`` f32 (rows >= max_pages *
     page_rows) gets what the token gives each row added, and row lens[b] set.
-    window and sinks by places (see the header).  Returns o ``[B, Hq, d]``
-    bf16, 0 for idle conversations."""
+    window and sinks by places (see the header).  o may be q itself.  Returns o
+    ``[B, Hq, d]`` bf16, 0 for idle conversations."""
     B, Hq, d = q.shape
     Hkv, p = k_new.shape[1], kc.shape[0]
     N, P = k_pages.shape[0], k_pages.shape[1]

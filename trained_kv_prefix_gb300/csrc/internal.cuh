@@ -35,7 +35,11 @@ cudaError_t set_smem_once(int bytes) {
 // Launches kern<<<grid, block, smem, st>>>(args...) as the programmatic
 // dependent of the previous kernel on st: it may start while that kernel
 // still runs, and calls pdl_wait() (ptx.cuh) in every thread before it
-// touches global memory, so the stream order of memory effects is kept.
+// touches what that kernel writes, or writes what that kernel reads, so the
+// stream order of memory effects is kept.  (What it may touch before that is
+// bound by the first kernel of the chain, which is launched plainly and so
+// has everything before the call behind it: step.cu and rows.cu read inputs
+// of the call there, and say so.)
 template <typename... KArgs, typename... Args>
 cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t st, Args&&... args) {

@@ -58,9 +58,9 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
 // dependent of the previous kernel on its stream may start before that
 // kernel ends; pdl_wait() returns once it (and so, transitively, all earlier
 // work on the stream) has completed with its writes visible, and is a no-op
-// for a plain launch.  Every thread of such a kernel calls it before its
-// first global-memory access.  pdl_release() lets this grid's own dependent
-// launch (it still waits for this grid before touching memory).
+// for a plain launch.  Every thread of such a kernel calls it before it
+// touches what an earlier kernel of its chain writes, or writes what one reads.
+// pdl_release() lets this grid's own dependent launch.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -329,8 +329,8 @@ __device__ __forceinline__ uint2 move_scan(uint32_t v, uint32_t* sums) {
 // never before place i, so a row may be written once all up to it have been
 // read, whatever is read later: a turn's rows are asked for before those of the
 // turn before are written.  Bound by HBM where there are many blocks: 16 layers of
-// 64 conversations and 8 kv heads from up to 1100 rows to 512 take 334 us, as long
-// as a copy of the rows that move; by latency where there are few.  (The bounds'
+// 64 conversations and 8 kv heads from up to 1100 rows to 512 take 330 us, as long
+// as a copy of the 2.2 GB that moves; by latency where there are few.  (The bounds'
 // second part is left open for 256 threads: a 1 there costs 10%.)
 template <int T>
 __global__ void __launch_bounds__(T, T == 512 ? 2 : 0)
@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 0)
   };
   uint32_t cut = 0xffffffffu, ties = 0;  // rows of a higher key stay, and so many of this key
   bool any = false;
-  if (stay > 0 && q.len > q.keep) {  // (needs nothing of the plan, and runs beside it)
+  // (needs nothing of the plan, which writes nothing that it reads, and runs beside it)
+  if (stay > 0 && q.len > q.keep) {
     any = true;
     const bool cached = m1 - m0 <= MoveShared<T>::kKeys;
     uint32_t left = stay, prefix = 0;

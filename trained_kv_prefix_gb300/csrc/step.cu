@@ -25,12 +25,20 @@
 //           joins them and a (conversation, kv head)'s parts by their log-sum-exps;
 //           adds exp2(logit - log-sum-exp) of the group's heads to each row's weights.
 //
+// The rows' kernel is launched plainly and starts behind all that came before the
+// call: so cart, and join ahead of its wait, may read the call's inputs, and join may
+// write what no other kernel of the call looks at: the new row (the rows' kernel
+// loads it with its neighbours and takes nothing from it) and the outputs of
+// conversations that sit the step out (o may be q: nothing is taken from their
+// queries either).  Launched as a dependent itself, it would leave cart and join
+// racing what came before the call.
+//
 // The whole, 32 query heads over 8, d 128, with weights: 96 conversations of up to
-// 1500 rows over a cartridge of 2048 in 75 us, of which 46 are the bytes' at a
-// copy's rate.  Stamps of that call: the first loads leave after 4.7 us (schedule,
-// pages), the first S^T is there at 7; the rows end at 57 (5.8 TB/s from the first
-// load on, at 128 SMs), the cartridge by then; the log-sum-exps are joined at 63, the
-// weights and outputs out at 70.
+// 1500 rows over a cartridge of 2048 in 68 us, 61 without weights, of which 46 are the
+// bytes' at a copy's rate.  Stamps of an earlier form that took 75 us: the first loads
+// leave after 4.7 us (schedule, pages), the first S^T is there at 7; the rows end at 57
+// (5.8 TB/s from the first load on, at 128 SMs), the cartridge by then; the log-sum-exps
+// are joined at 63, the weights and outputs out at 70.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -1499,7 +1507,7 @@ struct CartCut {
 // not need cost them nothing (96 conversations of up to 1500 rows, tables of 2048 to
 // 32768: 68 us, 85 without that quarter).  In all, at 96 conversations (24 segments of 43
 // tiles), 1 / 2 / 3 / 4 pieces of one a CTA took 87.4 / 75.3 / 78.3 / 83 us, at 200 (44
-// of 22) 93 / 99 / 116 / 145, at 4 of up to 32k rows (8 of 171) 3 / 5 / 7 126 / 119.4 /
+// of 22) 93 / 99 / 116 / 145, at 4 of up to 49k rows (8 of 171) 3 / 5 / 7 126 / 119.4 /
 // 119.1, at one of 200 (8 of 11) 1 / 3 / 5 / 11 26.8 / 20.5 / 19.5 / 21.1.
 CartCut cart_cut(int segments, int key_tiles, double row_bytes, int sms) {
   CartCut best{1, segments};

@@ -25,9 +25,9 @@
 //           window leaves tiles out: the columns' parts added up in order.
 //
 // Bound by the tensor pipe.  32 heads over 8, d 128: the last 32 queries of 64
-// conversations over 4096 and up to 1031 keys take 165 us, weigh 157 of them (the
+// conversations over 4096 and up to 1031 keys take 164 us, weigh 155 of them (the
 // three products of the keys that are seen at 1470 TFLOP/s); 1024 queries of 4 over
-// 2048 and up to 1200 keys 145 us: prep 18 (100 MB of terms written), weigh 120
+// 2048 and up to 1200 keys 141 us: prep 18 (100 MB of terms written), weigh 120
 // (1460 TFLOP/s), finish 9.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
