@@ -516,7 +516,7 @@ CART_API int cart_pages_append(int B, int n, int total, const int* cu_seqlens, i
  *   q      [B, queries, Hq, d] bf16, NOT rotated: query i of conversation b has
  *          place p + lens[b] - queries + i (end-aligned); those that would lie
  *          before its first row are not there, and what q and lse hold for them
- *          is not read
+ *          does not matter
  *   lse    [B, Hq, queries] f32: their natural-log log-sum-exps, as
  *          cart_attn_fwd returns them (-inf: every logit was; the query gives
  *          no weight).  Those of an attention with sinks beside a window are the
